@@ -561,6 +561,175 @@ lq_status lq_attention_decode_rice(int lattice, const uint32_t* k_stream_dev, si
                                    int q_heads, int head_dim, const void* q_dev, int qdtype, float* out_dev,
                                    void* workspace_dev, size_t workspace_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Serving a batch of requests from a paged 8-bit KV cache.
+ *
+ * The cache is a pool of num_blocks blocks of block_size tokens (16, 32, 64 or
+ * 128), shared by all requests:
+ *   codes  int8    [num_blocks x kv_heads x block_size x head_dim], one for K, one for V
+ *   scales float32 [num_blocks x kv_heads], >= 0: a cached value is code * scale
+ * Slot s is token s % block_size of block s / block_size.  Request i's blocks,
+ * in token order, are row i of a block table (int32, -1 where there is none);
+ * a batch's new tokens are numbered request after request, cu_new / cu_q
+ * [batch + 1] the prefix sums of their counts.  head_dim is a multiple of 16 up
+ * to 256 for the cache, one of 64, 128, 256 for the attention.  Outputs do not
+ * overlap inputs unless a call says so.  Every kernel of these calls is a
+ * programmatic dependent launch that waits for the work before it.
+ * ------------------------------------------------------------------------
+ */
+#define LQ_MAX_REQUESTS 8192
+
+/*
+ * Block tables, slots and positions from the requests' lengths.  Request i
+ * holds c = cached_lens[i] tokens in ceil(c / block_size) blocks (the first
+ * entries of its table row) and brings n = new_lens[i] new ones; it gets
+ * ceil((c + n) / block_size) - ceil(c / block_size) blocks, taken in request
+ * order from the front of the free list.
+ *   cached_lens_dev, new_lens_dev  int32 [batch], >= 0;  batch <= LQ_MAX_REQUESTS
+ *   free_blocks_dev  int32 [num_free], block ids in the order they are given out
+ *   block_table_dev  int32 [batch x table_stride], table_width columns used:
+ *                    entries of held blocks are read and kept, those of new
+ *                    blocks written, -1 written to the rest
+ *   cu_new_dev       int32 [batch + 1] (written)
+ *   kv_lens_dev      int32 [batch] (written): c + n
+ *   slots_dev        int64 [max_tokens] (written): the slot of each new token;
+ *                    -1 past the last one and where there is no block
+ *   positions_dev    int32 [max_tokens] (written): its position; 0 past the last
+ *   used_dev         int32 (written): blocks asked of the free list
+ *   dev_status_dev   LQ_DEV_RANGE: a negative length (taken as 0), more blocks
+ *                    than table_width or num_free, or more tokens than max_tokens
+ * Calling it again with the same inputs gives the same outputs (the free list
+ * is not changed: drop its first used entries to go on).
+ */
+lq_status lq_kv_plan(const int32_t* cached_lens_dev, const int32_t* new_lens_dev, int batch, int block_size,
+                     const int32_t* free_blocks_dev, int64_t num_free, int32_t* block_table_dev,
+                     int64_t table_stride, int table_width, int32_t* cu_new_dev, int32_t* kv_lens_dev,
+                     int64_t* slots_dev, int32_t* positions_dev, int64_t max_tokens, int32_t* used_dev,
+                     int32_t* dev_status_dev, void* stream);
+
+/*
+ * RMS norm of every query and key head, then the rotary position rotation, in
+ * one pass: y = x * rsqrt(mean(x^2) + eps) * w over each head's head_dim
+ * values, then for the pairs (a, b) of its first rot_dim values
+ * (a cos - b sin, b cos + a sin), all in fp32, rounded once.
+ *   q_dev, k_dev    [tokens x q_heads x head_dim], [tokens x kv_heads x head_dim] of
+ *                   type dtype; token stride ldq, ldk elements, heads packed
+ *                   (for example columns of one projection's output)
+ *   head_dim        a multiple of 8 up to 256;  rot_dim a multiple of 16 up to head_dim
+ *   q_weight_dev, k_weight_dev  float32 [head_dim], or NULL: that kind is not normed
+ *   positions_dev   int32 [tokens], each in [0, max_pos)
+ *   cos_sin_dev     float32 [max_pos x rot_dim]: rot_dim / 2 cosines, then the sines
+ *   interleaved     0: pairs (i, i + rot_dim / 2); otherwise pairs (2 i, 2 i + 1)
+ *   q_out_dev, k_out_dev  outputs of type dtype, token strides ldqo, ldko; may be
+ *                   q_dev and k_dev themselves (equal strides)
+ *   dev_status_dev  LQ_DEV_RANGE: a position outside the table (its token is
+ *                   normed, not rotated)
+ * Token strides times the element size are multiples of 16 bytes.
+ */
+lq_status lq_qk_norm_rope(const void* q_dev, int64_t ldq, int q_heads, const void* k_dev, int64_t ldk, int kv_heads,
+                          int dtype, int64_t tokens, int head_dim, const float* q_weight_dev,
+                          const float* k_weight_dev, float eps, const int32_t* positions_dev,
+                          const float* cos_sin_dev, int64_t max_pos, int rot_dim, int interleaved, void* q_out_dev,
+                          int64_t ldqo, void* k_out_dev, int64_t ldko, int32_t* dev_status_dev, void* stream);
+
+/*
+ * Write new keys and values into the cache.  Rows that fall into one block
+ * share its scale with the rows already there: with s_old the stored scale (0
+ * when the first new row is the block's first token: what the block held
+ * before is forgotten) the scale becomes s = max(s_old, max |x| / 127 over the
+ * new rows), new rows are stored as rint(x / s), and where s > s_old the older
+ * rows' codes c become rint(c s_old / s) -- IEEE fp32 quotients, half to even,
+ * clipped to +-127.
+ *   k_dev, v_dev    [tokens x kv_heads x head_dim] of type dtype, token strides ldk,
+ *                   ldv (a multiple of 16 bytes)
+ *   slots_dev       int64 [tokens]; negative: the token is left out.  In one
+ *                   call the new rows of a block are consecutive tokens with
+ *                   consecutive slots (as lq_kv_plan gives them).
+ *   dev_status_dev  LQ_DEV_RANGE: a slot past the cache (nothing is written for
+ *                   it); LQ_DEV_NONFINITE: a non-finite value (stored as 0)
+ */
+lq_status lq_kv_append(const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int dtype, int64_t tokens,
+                       const int64_t* slots_dev, int8_t* k_cache_dev, float* k_scales_dev, int8_t* v_cache_dev,
+                       float* v_scales_dev, int64_t num_blocks, int block_size, int kv_heads, int head_dim,
+                       int32_t* dev_status_dev, void* stream);
+
+/*
+ * Read n slots of the cache back as the values they stand for: k_out_dev and
+ * v_out_dev [n x kv_heads x head_dim] of type out_dtype (code * scale in fp32,
+ * rounded once for LQ_BF16).  A negative slot reads as zeros, one past the
+ * cache too, with LQ_DEV_RANGE.
+ */
+lq_status lq_kv_gather(const int64_t* slots_dev, int64_t n, const int8_t* k_cache_dev, const float* k_scales_dev,
+                       const int8_t* v_cache_dev, const float* v_scales_dev, int64_t num_blocks, int block_size,
+                       int kv_heads, int head_dim, void* k_out_dev, void* v_out_dev, int out_dtype,
+                       int32_t* dev_status_dev, void* stream);
+
+/* Workspace bytes of lq_attention_paged; 0 for unsupported shapes. */
+size_t lq_attention_paged_workspace_size(int batch, int64_t total_q, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Attention of a ragged batch over the paged cache, computed from the codes.
+ * Request i's query tokens are rows cu_q[i] .. cu_q[i + 1] - 1 of q, the last
+ * of its kv_lens[i] tokens (one for a decode step, several for drafted tokens, a
+ * prompt or a chunk of one); its query token j sees the positions
+ * p <= kv_lens[i] - q_len + j:
+ *     out[t, h] = sum_p w_p v^_p,  w = softmax_p(sm_scale q[t, h] . k^_p)
+ * over the keys and values of kv head h / (q_heads / kv_heads).  A query token
+ * that sees no position, or that no request owns, gets zeros.
+ *   q_dev, out_dev  [total_q x q_heads x head_dim] of type dtype, token strides
+ *                   ldq, ldo (a multiple of 16 bytes)
+ *   cu_q_dev        int32 [batch + 1], nondecreasing from 0 to total_q
+ *   kv_lens_dev     int32 [batch]
+ *   block_table_dev int32 [batch x table_stride], table_width columns used
+ *   head_dim        64, 128 or 256;  q_heads a multiple of kv_heads, at most 1024
+ *   workspace_dev   lq_attention_paged_workspace_size(...) bytes, 16-byte aligned,
+ *                   contents unspecified before and after
+ *   dev_status_dev  LQ_DEV_RANGE: a length past the block table (cut there) or a
+ *                   block id outside the pool (its tokens are left out);
+ *                   LQ_DEV_TIMEOUT: a bounded wait expired (out unspecified)
+ * Products and sums are held in fp32 (codes are exact operands); bf16 outputs
+ * are rounded once.  The result does not depend on how the work was split
+ * beyond fp32 rounding, and equal calls give equal bits.
+ */
+lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtype, int64_t total_q, const int32_t* cu_q_dev,
+                             const int32_t* kv_lens_dev, int batch, const int32_t* block_table_dev,
+                             int64_t table_stride, int table_width, const int8_t* k_cache_dev,
+                             const float* k_scales_dev, const int8_t* v_cache_dev, const float* v_scales_dev,
+                             int64_t num_blocks, int block_size, int q_heads, int kv_heads, int head_dim,
+                             float sm_scale, void* out_dev, int64_t ldo, void* workspace_dev,
+                             size_t workspace_bytes, int32_t* dev_status_dev, void* stream);
+
+/*
+ * Verify drafted tokens against the target's probabilities with given random
+ * numbers (speculative sampling).  Request b brings n = draft_lens[b] drafted
+ * tokens x_i.  Token i is accepted while u_accept[b, i] * q_i(x_i) < p_i(x_i)
+ * (fp32), up to the first refusal; with a accepted, one more token is drawn
+ * from max(p_a - q_a, 0) (fp32) if a < n (from p_a if nothing is left of it) and from
+ * p_n otherwise: the first v whose inclusive sum of floor(2^36 weight) exceeds
+ * floor(u_sample[b] * total), whole numbers, so that the token does not depend
+ * on the order of summation.
+ *   draft_tokens_dev  int32 [batch x max_draft]
+ *   draft_lens_dev    int32 [batch], 0 .. max_draft, or NULL: max_draft for all
+ *   target_probs_dev  p, [batch x (max_draft + 1) x vocab] of type dtype, strides in
+ *                     elements; need not be normalised
+ *   draft_probs_dev   q, [batch x max_draft x vocab], or NULL: q_i is 1 at x_i
+ *   u_accept_dev, u_sample_dev  float32 [batch x max_draft], [batch], in [0, 1)
+ *   out_tokens_dev    int32 [batch x (max_draft + 1)] (written): the accepted
+ *                     tokens, the drawn one, then -1
+ *   accepted_dev      int32 [batch] (written): a
+ *   dev_status_dev    LQ_DEV_RANGE: a draft length or token out of range (the
+ *                     length clipped, the token refused) or a target row without
+ *                     weight (token -1); LQ_DEV_NONFINITE: a non-finite target
+ *                     probability in the row drawn from
+ * vocab <= 2^24, max_draft <= 1024.
+ */
+lq_status lq_verify_draft(const int32_t* draft_tokens_dev, const int32_t* draft_lens_dev, int batch, int max_draft,
+                          int64_t vocab, const void* target_probs_dev, int64_t target_req_stride,
+                          int64_t target_row_stride, const void* draft_probs_dev, int64_t draft_req_stride,
+                          int64_t draft_row_stride, int dtype, const float* u_accept_dev, const float* u_sample_dev,
+                          int32_t* out_tokens_dev, int32_t* accepted_dev, int32_t* dev_status_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

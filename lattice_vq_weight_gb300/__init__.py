@@ -67,6 +67,16 @@ SIGNATURES = {
     "lq_attention_decode": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P,
                                    ctypes.c_size_t, _P]),
     "lq_rotate_blocks": (_I32, [_P, _I32, _I32, _P, _I32, _I64, _I64, _I64, _P, _I64, _P]),
+    "lq_kv_plan": (_I32, [_P, _P, _I32, _I32, _P, _I64, _P, _I64, _I32, _P, _P, _P, _P, _I64, _P, _P, _P]),
+    "lq_qk_norm_rope": (_I32, [_P, _I64, _I32, _P, _I64, _I32, _I32, _I64, _I32, _P, _P, _F32, _P, _P, _I64, _I32,
+                               _I32, _P, _I64, _P, _I64, _P, _P]),
+    "lq_kv_append": (_I32, [_P, _I64, _P, _I64, _I32, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
+    "lq_kv_gather": (_I32, [_P, _I64, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P]),
+    "lq_attention_paged_workspace_size": (ctypes.c_size_t, [_I32, _I64, _I32, _I32, _I32]),
+    "lq_attention_paged": (_I32, [_P, _I64, _I32, _I64, _P, _P, _I32, _P, _I64, _I32, _P, _P, _P, _P, _I64, _I32,
+                                  _I32, _I32, _I32, _F32, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "lq_verify_draft": (_I32, [_P, _P, _I32, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P, _P, _P,
+                               _P]),
 }
 
 
@@ -493,6 +503,174 @@ def lq_rotate_blocks(R, X, Y, transpose: bool = False, stream=None) -> None:
     _check("lq_rotate_blocks", _get_lib().lq_rotate_blocks(
         _ptr(R), int(bool(transpose)), R.shape[0], _ptr(X), _dtype_id(X), rows, cols, X.stride(0), _ptr(Y),
         Y.stride(0), _stream(stream)))
+
+
+# ------------------------------------------------------------------ serving from a paged 8-bit KV cache
+# Largest batch of the paged calls (LQ_MAX_REQUESTS in lq.h)
+LQ_MAX_REQUESTS = 8192
+
+
+def _addr(t):
+    """Device address of a tensor (or None) as the plain number a call of every step passes quickest."""
+    return None if t is None else t.data_ptr()
+
+
+def _want(name: str, t, shape, *dtypes) -> None:
+    """Raise unless t is contiguous with this shape and one of these dtypes: the kernels trust both."""
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {tuple(shape)} tensor of {' or '.join(map(str, dtypes))}, "
+                         f"got {tuple(t.shape)} {t.dtype} with strides {tuple(t.stride())}")
+
+
+def _heads(name: str, t) -> int:
+    """Token stride of a [tokens x heads x head_dim] tensor whose heads are packed."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: want [tokens x heads x head_dim] with packed heads, got {tuple(t.shape)} with "
+                         f"strides {tuple(t.stride())}")
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+
+
+def _cache(k_cache, k_scales, v_cache, v_scales):
+    """(num_blocks, kv_heads, block_size, head_dim) of a cache's four tensors, checked."""
+    import torch
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache: want [num_blocks x kv_heads x block_size x head_dim], got {tuple(k_cache.shape)}")
+    shape = tuple(k_cache.shape)
+    _want("k_cache", k_cache, shape, torch.int8)
+    _want("v_cache", v_cache, shape, torch.int8)
+    _want("k_scales", k_scales, shape[:2], torch.float32)
+    _want("v_scales", v_scales, shape[:2], torch.float32)
+    return shape
+
+
+def paged_cache(num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device):
+    """Empty cache pool: (k_cache, k_scales, v_cache, v_scales), codes int8
+    [num_blocks x kv_heads x block_size x head_dim], scales float32 [num_blocks x kv_heads]."""
+    import torch
+    codes = [torch.empty((num_blocks, kv_heads, block_size, head_dim), dtype=torch.int8, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros((num_blocks, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return codes[0], scales[0], codes[1], scales[1]
+
+
+def lq_kv_plan(cached_lens, new_lens, block_size: int, free_blocks, block_table, cu_new, kv_lens, slots, positions,
+               used, dev_status=None, stream=None) -> None:
+    """Block table rows, slots and positions of the requests' new tokens (see lq.h); block_table is updated."""
+    import torch
+    b = cached_lens.numel()
+    for n, t, shape in (("cached_lens", cached_lens, (b,)), ("new_lens", new_lens, (b,)),
+                        ("free_blocks", free_blocks, (free_blocks.numel(),)), ("cu_new", cu_new, (b + 1,)),
+                        ("kv_lens", kv_lens, (b,)), ("positions", positions, (slots.numel(),)), ("used", used, (1,))):
+        _want(n, t, shape, torch.int32)
+    _want("slots", slots, (slots.numel(),), torch.int64)
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != b or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table: want int32 [{b} x blocks], got {tuple(block_table.shape)} {block_table.dtype}")
+    width = block_table.shape[1]
+    _check("lq_kv_plan", _get_lib().lq_kv_plan(
+        _addr(cached_lens), _addr(new_lens), b, int(block_size), _addr(free_blocks), free_blocks.numel(),
+        _addr(block_table), block_table.stride(0) if b > 1 else width, width, _addr(cu_new), _addr(kv_lens),
+        _addr(slots), _addr(positions), slots.numel(), _addr(used), _addr(dev_status), _stream(stream)))
+
+
+def lq_qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, cos_sin, q_out, k_out, interleaved: bool = False,
+                    dev_status=None, stream=None) -> None:
+    """RMS norm of every head of q and k (weights None: none), then the rotation; q_out, k_out may be q, k."""
+    import torch
+    if not q.dtype == k.dtype == q_out.dtype == k_out.dtype:
+        raise TypeError("lq_qk_norm_rope: q, k and their outputs have one dtype")
+    tokens, hq, d = q.shape
+    if k.shape[0] != tokens or k.shape[2] != d or q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("lq_qk_norm_rope: q, k and their outputs do not belong together")
+    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _want(n, w, (d,), torch.float32)
+    _want("positions", positions, (tokens,), torch.int32)
+    _want("cos_sin", cos_sin, tuple(cos_sin.shape[:1]) + (cos_sin.shape[-1],), torch.float32)
+    _check("lq_qk_norm_rope", _get_lib().lq_qk_norm_rope(
+        _addr(q), _heads("q", q), hq, _addr(k), _heads("k", k), k.shape[1], _dtype_id(q), tokens, d, _addr(q_weight),
+        _addr(k_weight), float(eps), _addr(positions), _addr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
+        int(bool(interleaved)), _addr(q_out), _heads("q_out", q_out), _addr(k_out), _heads("k_out", k_out),
+        _addr(dev_status), _stream(stream)))
+
+
+def lq_kv_append(k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status=None, stream=None) -> None:
+    """Write k, v [tokens x kv_heads x head_dim] to the cache's slots (int64 [tokens], negative: left out)."""
+    import torch
+    nb, hk, bs, d = _cache(k_cache, k_scales, v_cache, v_scales)
+    if k.shape != v.shape or k.dtype != v.dtype or tuple(k.shape[1:]) != (hk, d):
+        raise ValueError(f"lq_kv_append: k and v do not fit the cache: {tuple(k.shape)}, {tuple(v.shape)}")
+    _want("slots", slots, (k.shape[0],), torch.int64)
+    _check("lq_kv_append", _get_lib().lq_kv_append(
+        _addr(k), _heads("k", k), _addr(v), _heads("v", v), _dtype_id(k), k.shape[0], _addr(slots), _addr(k_cache),
+        _addr(k_scales), _addr(v_cache), _addr(v_scales), nb, bs, hk, d, _addr(dev_status), _stream(stream)))
+
+
+def lq_kv_gather(slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status=None, stream=None) -> None:
+    """The values that the cache's slots stand for, [n x kv_heads x head_dim] float32 or bf16."""
+    import torch
+    nb, hk, bs, d = _cache(k_cache, k_scales, v_cache, v_scales)
+    n = slots.numel()
+    _want("slots", slots, (n,), torch.int64)
+    _want("k_out", k_out, (n, hk, d), torch.float32, torch.bfloat16)
+    _want("v_out", v_out, (n, hk, d), k_out.dtype)
+    _check("lq_kv_gather", _get_lib().lq_kv_gather(
+        _addr(slots), n, _addr(k_cache), _addr(k_scales), _addr(v_cache), _addr(v_scales), nb, bs, hk, d, _addr(k_out),
+        _addr(v_out), _dtype_id(k_out), _addr(dev_status), _stream(stream)))
+
+
+def lq_attention_paged_workspace_size(batch: int, total_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_get_lib().lq_attention_paged_workspace_size(int(batch), int(total_q), int(q_heads), int(kv_heads),
+                                                            int(head_dim)))
+
+
+def lq_attention_paged(q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache, v_scales, out, workspace,
+                       sm_scale=None, dev_status=None, stream=None) -> None:
+    """out = attention of q [total_q x q_heads x head_dim] over the requests' cached tokens (see lq.h);
+    sm_scale defaults to head_dim ** -0.5."""
+    import torch
+    nb, hk, bs, d = _cache(k_cache, k_scales, v_cache, v_scales)
+    b = kv_lens.numel()
+    _want("kv_lens", kv_lens, (b,), torch.int32)
+    _want("cu_q", cu_q, (b + 1,), torch.int32)
+    if q.shape != out.shape or q.dtype != out.dtype or q.shape[2] != d:
+        raise ValueError(f"lq_attention_paged: q and out do not fit: {tuple(q.shape)}, {tuple(out.shape)}")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != b or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table: want int32 [{b} x blocks], got {tuple(block_table.shape)} {block_table.dtype}")
+    width = block_table.shape[1]
+    _check("lq_attention_paged", _get_lib().lq_attention_paged(
+        _addr(q), _heads("q", q), _dtype_id(q), q.shape[0], _addr(cu_q), _addr(kv_lens), b, _addr(block_table),
+        block_table.stride(0) if b > 1 else width, width, _addr(k_cache), _addr(k_scales), _addr(v_cache),
+        _addr(v_scales), nb, bs, q.shape[1], hk, d, d ** -0.5 if sm_scale is None else float(sm_scale), _addr(out),
+        _heads("out", out), _addr(workspace), workspace.numel() * workspace.element_size(), _addr(dev_status),
+        _stream(stream)))
+
+
+def lq_verify_draft(draft_tokens, draft_lens, target_probs, draft_probs, u_accept, u_sample, out_tokens, accepted,
+                    dev_status=None, stream=None) -> None:
+    """Accept or refuse draft_tokens [batch x n] and draw the token after the accepted ones (see lq.h)."""
+    import torch
+    b, n = draft_tokens.shape
+    vocab = target_probs.shape[2]
+    for name, t, rows in (("target_probs", target_probs, n + 1), ("draft_probs", draft_probs, n)):
+        if t is not None and (tuple(t.shape) != (b, rows, vocab) or t.dtype != target_probs.dtype or
+                              (vocab > 1 and rows > 0 and t.stride(2) != 1)):
+            raise ValueError(f"{name}: want [{b} x {rows} x {vocab}] {target_probs.dtype} with packed rows, got "
+                             f"{tuple(t.shape)} {t.dtype} with strides {tuple(t.stride())}")
+    _want("draft_tokens", draft_tokens, (b, n), torch.int32)
+    if draft_lens is not None:
+        _want("draft_lens", draft_lens, (b,), torch.int32)
+    _want("u_accept", u_accept, (b, n), torch.float32)
+    _want("u_sample", u_sample, (b,), torch.float32)
+    _want("out_tokens", out_tokens, (b, n + 1), torch.int32)
+    _want("accepted", accepted, (b,), torch.int32)
+    q = draft_probs
+    _check("lq_verify_draft", _get_lib().lq_verify_draft(
+        _addr(draft_tokens), _addr(draft_lens), b, n, vocab, _addr(target_probs), target_probs.stride(0),
+        target_probs.stride(1), _addr(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
+        _dtype_id(target_probs), _addr(u_accept), _addr(u_sample), _addr(out_tokens), _addr(accepted),
+        _addr(dev_status), _stream(stream)))
 
 
 # ------------------------------------------------------------------ allocating helpers

@@ -1,0 +1,93 @@
+// Shared by the kernels of the paged attention (lq_attn_paged.cu, the split
+// kernel for few query rows).  Internal to the library.
+#pragma once
+
+#include <cmath>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "lq_device.cuh"
+#include "lq_host.h"
+#include "lq_serve.cuh"
+#include "lq_tma.cuh"
+
+namespace lq {
+namespace attn {
+
+struct Args {
+  const void* q;
+  int64_t ldq;
+  int64_t total_q;
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  int batch;
+  const int32_t* table;
+  int64_t ldt;
+  int width;
+  const float* ks;
+  const float* vs;
+  int64_t num_blocks;
+  int log2_bs, q_heads, kv_heads, group;
+  float scale_log2;          // sm_scale * log2(e)
+  void* out;
+  int64_t ldo;
+  float* part;               // partial results of the CTAs
+  int* meta;                 // and what they belong to
+  int32_t* status;
+};
+
+constexpr long long kWaitCycles = 2000000000ll;   // about one second
+// Value scales below this count as this (a block of zeros has scale 0): their
+// logarithm stays finite, and a value of 2^-120 vanishes against any other.
+constexpr float kMinScale = 7.52316385e-37f;      // 2^-120
+// Softmax weights are held times 2^14: weights down to 2^-28 of the largest
+// are then normal fp16 numbers, and the largest, 2^14, is in range.
+constexpr float kShift = 14.f;
+constexpr float kUnshift = 6.103515625e-5f;       // 2^-14
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What pack_f16 left out, again as fp16: the two together carry 22 bits.
+__device__ __forceinline__ uint32_t rest_f16(uint32_t packed, float lo, float hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+  return pack_f16(lo - f.x, hi - f.y);
+}
+
+// Two codes, offset to unsigned bytes (code + 128) and placed by `sel`, as
+// fp16 numbers: 0x6400 + byte is 1024 + byte, exactly.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t bytes, uint32_t sel) {
+  const uint32_t h = __byte_perm(bytes, 0x64646464u, sel);
+  const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));   // 1152
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), off);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One request's share of the work: query rows (token j, head of the group)
+// numbered j * group + head for each kv head.
+struct Request {
+  int q0, q_len, len;        // len: cached tokens, cut at the block table's end
+  int shown;                 // position that query token 0 sees last
+};
+
+__device__ __forceinline__ Request load_request(const Args& a, int i) {
+  Request r;
+  const int q0 = __ldg(a.cu_q + i), q1 = __ldg(a.cu_q + i + 1), len = __ldg(a.kv_lens + i);
+  r.q0 = q0 < 0 ? 0 : q0;
+  const int64_t end = q1 < a.total_q ? q1 : a.total_q;
+  r.q_len = end > r.q0 ? (int)(end - r.q0) : 0;
+  r.shown = (len > 0 ? len : 0) - r.q_len;
+  const int64_t most = (int64_t)a.width << a.log2_bs;
+  r.len = len < 0 ? 0 : (len < most ? len : (int)most);
+  return r;
+}
+
+}  // namespace attn
+}  // namespace lq

@@ -14,7 +14,9 @@
 // (a token whose predecessor is not the slot before it in the same block
 // starts one), so no block list has to be built first.  The run is read twice,
 // for the maximum and for the codes: at most 64 KB that the first pass has
-// left in L1 or L2.
+// left in L1 or L2.  An IEEE division per value would bound the kernel, so
+// codes come from a product with 1/s wherever that is clear of a half by more
+// than its error, and from the division only in the rows that are not.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"
@@ -38,32 +40,94 @@ struct AppendArgs {
   int32_t* status;
 };
 
+// Eight values of a row as loaded: one 16-byte word of bf16, two of fp32.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+struct Raw {
+  uint4 w[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_raw(const void* p, int64_t i) {
+  Raw<BF16> r;
   if constexpr (BF16) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    r.w[0] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i));
+  } else {
+    r.w[0] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i));
+    r.w[1] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i) + 1);
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void values(const Raw<BF16>& r, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       v[2 * e] = __uint_as_float(u[e] << 16);
       v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
     }
   } else {
-    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    const float4 x = __ldg(f), y = __ldg(f + 1);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[4 * h] = __uint_as_float(r.w[h].x); v[4 * h + 1] = __uint_as_float(r.w[h].y);
+      v[4 * h + 2] = __uint_as_float(r.w[h].z); v[4 * h + 3] = __uint_as_float(r.w[h].w);
+    }
   }
+}
+
+// Running maximum of the magnitudes as bit patterns, which are ordered like
+// the numbers and put infinities and NaN on top: two bf16 side by side, or one
+// fp32.
+constexpr uint32_t kInf = 0x7F800000u;
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, const Raw<BF16>& r) {
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+    const uint32_t u[4] = {r.w[h].x, r.w[h].y, r.w[h].z, r.w[h].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = BF16 ? __vmaxu2(m, u[e] & 0x7FFF7FFFu) : max(m, u[e] & 0x7FFFFFFFu);
+  }
+  return m;
 }
 
 __device__ __forceinline__ uint32_t pack4(const int (&c)[4]) {
   return (uint32_t)(c[0] & 255) | (uint32_t)(c[1] & 255) << 8 | (uint32_t)(c[2] & 255) << 16 | (uint32_t)c[3] << 24;
 }
 
-// rint of the IEEE quotient, clipped to the code range.
+// rint of the IEEE quotient, clipped to the code range; 0 for a non-finite x.
 __device__ __forceinline__ int code_of(float x, float s) {
   const float q = rintf(__fdiv_rn(x, s));
-  return (int)fminf(fmaxf(q, -127.f), 127.f);
+  return fabsf(x) <= 3.402823466e38f ? (int)fminf(fmaxf(q, -127.f), 127.f) : 0;
+}
+
+// Codes of eight values with |x| <= 127 s (up to rounding): rint(x * inv) by
+// adding 1.5 * 2^23, whose low byte is then the code.  The quotient x / s is
+// within 127 * 2^-22 of x * inv, so rounding agrees unless x * inv is within
+// 2^-12 of a half; such values (and non-finite ones) take the division.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, float s, bool careful) {
+  constexpr float kMagic = 12582912.f;
+  float t[8], off = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    t[e] = fmaf(v[e], inv, kMagic);
+    off = fmaxf(off, fabsf(fmaf(v[e], inv, kMagic - t[e])));
+  }
+  uint32_t out[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t lo = __byte_perm(__float_as_uint(t[4 * q]), __float_as_uint(t[4 * q + 1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(t[4 * q + 2]), __float_as_uint(t[4 * q + 3]), 0x0040);
+    out[q] = __byte_perm(lo, hi, 0x5410);
+  }
+  if (careful || !(off < 0.5f - 0.000244140625f)) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      int code[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) code[e] = code_of(v[4 * q + e], s);
+      out[q] = pack4(code);
+    }
+  }
+  return make_uint2(out[0], out[1]);
 }
 
 template <bool BF16>
@@ -81,7 +145,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   int8_t* cache = which ? a.cache[1] : a.cache[0];
   float* scales = which ? a.scales[1] : a.scales[0];
   const int bs1 = (1 << a.log2_bs) - 1;
-  const int chunks = a.dim >> 3;                   // 8-element chunks per row
+  // a lane holds 8 dimensions of a row; 32 / (dim / 8) rows side by side
+  const int chunks = a.dim >> 3, step = 32 / chunks;
+  const int r0 = lane < step * chunks ? lane / chunks : 1 << 20, k0 = 8 * (lane % chunks);
 
   // which tokens of the window start a run
   const int64_t t0 = win * a.window;
@@ -110,62 +176,52 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
       len += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
       if (m != 0xffffffffu) break;
     }
-    const int n = len * chunks;
-    const int64_t src = t * ld + (int64_t)h * a.dim;
+    const int64_t src = t * ld + (int64_t)h * a.dim + k0;
     const int64_t sc = blk * a.kv_heads + h;
-    int8_t* rows = cache + (sc << a.log2_bs) * a.dim;
+    int8_t* rows = cache + (sc << a.log2_bs) * a.dim + k0;
     const float s_old = off > 0 ? scales[sc] : 0.f;
 
-    float mx = 0.f;
-    bool bad = false;
-    for (int c = lane; c < n; c += 32) {
-      const int r = c / chunks, k = c - r * chunks;
-      float v[8];
-      load8<BF16>(x, src + r * ld + 8 * k, v);
+    uint32_t mb = 0;
+#pragma unroll 8
+    for (int r = r0; r < len; r += step) mb = max_bits<BF16>(mb, load_raw<BF16>(x, src + r * ld));
+    if constexpr (BF16) mb = max(mb << 16, mb & 0xFFFF0000u);
+    for (int o = 16; o; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    const bool careful = mb >= kInf;               // something non-finite: the maximum over the rest
+    float mx = __uint_as_float(mb);
+    if (careful) {
+      mx = 0.f;
+      for (int r = r0; r < len; r += step) {
+        float v[8];
+        values<BF16>(load_raw<BF16>(x, src + r * ld), v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float m = fabsf(v[e]);
-        if (m <= 3.402823466e38f) mx = fmaxf(mx, m);
-        else bad = true;
+        for (int e = 0; e < 8; ++e)
+          if (fabsf(v[e]) <= 3.402823466e38f) mx = fmaxf(mx, fabsf(v[e]));
       }
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (lane == 0) raise_flag(a.status, LQ_DEV_NONFINITE);
     }
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (bad) raise_flag(a.status, LQ_DEV_NONFINITE);
     const float s = fmaxf(s_old, __fdiv_rn(mx, 127.f));
+    const float d = s > 0.f ? s : 1.f, inv = 1.f / d;
+    const bool tiny = !(inv <= 3.402823466e38f) || d < 1e-37f;   // 1/s out of the normal range
 
     if (s > s_old && off > 0) {
-      for (int c = lane; c < off * chunks; c += 32) {
-        uint2* p = reinterpret_cast<uint2*>(rows + 8 * c);
+      for (int r = r0; r < off; r += step) {
+        uint2* p = reinterpret_cast<uint2*>(rows + r * a.dim);
         const uint2 w = *p;
-        const uint32_t in[2] = {w.x, w.y};
-        uint32_t out[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          int code[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) code[e] = code_of((float)(int8_t)(in[q] >> (8 * e)) * s_old, s);
-          out[q] = pack4(code);
-        }
-        *p = make_uint2(out[0], out[1]);
-      }
-    }
-    const float d = s > 0.f ? s : 1.f;
-    for (int c = lane; c < n; c += 32) {
-      const int r = c / chunks, k = c - r * chunks;
-      float v[8];
-      load8<BF16>(x, src + r * ld + 8 * k, v);
-      uint32_t out[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        int code[4];
+        float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float f = v[4 * q + e];
-          code[e] = fabsf(f) <= 3.402823466e38f ? code_of(f, d) : 0;
+          v[e] = (float)(int8_t)(w.x >> (8 * e)) * s_old;
+          v[4 + e] = (float)(int8_t)(w.y >> (8 * e)) * s_old;
         }
-        out[q] = pack4(code);
+        *p = codes8(v, inv, d, tiny);
       }
-      *reinterpret_cast<uint2*>(rows + (int64_t)(off + r) * a.dim + 8 * k) = make_uint2(out[0], out[1]);
+    }
+#pragma unroll 4
+    for (int r = r0; r < len; r += step) {
+      float v[8];
+      values<BF16>(load_raw<BF16>(x, src + r * ld), v);
+      *reinterpret_cast<uint2*>(rows + (off + r) * a.dim) = codes8(v, inv, d, careful || tiny);
     }
     if (lane == 0) scales[sc] = s;
   }
@@ -176,54 +232,60 @@ struct GatherArgs {
   const int8_t* cache[2];
   const float* scales[2];
   void* out[2];
-  int64_t n, chunks, slots_in_cache;     // chunks: 8-code chunks per cache
+  int64_t n, slots_in_cache;
   int kv_heads, dim, log2_bs;
   int32_t* status;
 };
 
-// Eight codes per thread: out = code * scale, fp32 or rounded once to bf16.
+// out = code * scale, fp32 or rounded once to bf16: a warp per slot and cache,
+// 16 bytes of output per lane and step.
 template <bool BF16>
 __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
+  constexpr int E = BF16 ? 8 : 4;                  // codes per lane
   pdl_wait();
   pdl_launch();
-  const int per_row = a.kv_heads * (a.dim >> 3);
-  for (int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; c < 2 * a.chunks;
-       c += (int64_t)gridDim.x * blockDim.x) {
-    const int which = c >= a.chunks;
-    const int64_t cc = which ? c - a.chunks : c;
-    const int64_t row = cc / per_row;
-    const int rest = (int)(cc - row * per_row);
-    const int h = rest / (a.dim >> 3), k = rest - h * (a.dim >> 3);
-    const int64_t slot = __ldg(a.slots + row);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (slot >= 0 && slot < a.slots_in_cache) {
-      const int64_t sc = (slot >> a.log2_bs) * a.kv_heads + h;
-      const int64_t at = ((sc << a.log2_bs) + (slot & ((1 << a.log2_bs) - 1))) * a.dim + 8 * k;
-      const float s = __ldg((which ? a.scales[1] : a.scales[0]) + sc);
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>((which ? a.cache[1] : a.cache[0]) + at));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = (float)(int8_t)(w.x >> (8 * e)) * s;
-        v[4 + e] = (float)(int8_t)(w.y >> (8 * e)) * s;
+  const int lane = threadIdx.x & 31;
+  const int chunks = a.dim / E, per_row = a.kv_heads * chunks;
+  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < 2 * a.n; u += (int64_t)gridDim.x * 8) {
+    const int which = (int)(u & 1);
+    const int64_t row = u >> 1, slot = __ldg(a.slots + row);
+    const bool ok = slot >= 0 && slot < a.slots_in_cache;
+    if (slot >= a.slots_in_cache && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
+    const int64_t sc0 = (slot >> a.log2_bs) * a.kv_heads;
+    const int off = (int)(slot & ((1 << a.log2_bs) - 1));
+    const float* scales = (which ? a.scales[1] : a.scales[0]) + sc0;
+    const int8_t* codes = (which ? a.cache[1] : a.cache[0]) + ((sc0 << a.log2_bs) + off) * a.dim;
+    uint4* out = reinterpret_cast<uint4*>(which ? a.out[1] : a.out[0]) + row * per_row;
+#pragma unroll 4
+    for (int c = lane; c < per_row; c += 32) {
+      const int h = c / chunks, k = E * (c - h * chunks);
+      uint32_t w[E / 4] = {};
+      float s = 0.f;
+      if (ok) {
+        s = __ldg(scales + h);
+        const int8_t* p = codes + ((int64_t)h << a.log2_bs) * a.dim + k;
+        if constexpr (BF16) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+          w[0] = x.x; w[1] = x.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        }
       }
-    } else if (slot >= a.slots_in_cache) {
-      raise_flag(a.status, LQ_DEV_RANGE);
-    }
-    void* out = which ? a.out[1] : a.out[0];
-    if constexpr (BF16) {
-      uint32_t u[4];
+      float v[E];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-        u[e] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int e = 0; e < E; ++e) v[e] = (float)(int8_t)(w[e >> 2] >> (8 * (e & 3))) * s;
+      uint32_t o[4];
+      if constexpr (BF16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          o[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(v[e]);
       }
-      reinterpret_cast<uint4*>(out)[cc] = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-      float4* f = reinterpret_cast<float4*>(out) + 2 * cc;
-      f[0] = make_float4(v[0], v[1], v[2], v[3]);
-      f[1] = make_float4(v[4], v[5], v[6], v[7]);
+      out[c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -305,9 +367,9 @@ extern "C" lq_status lq_kv_gather(const int64_t* slots_dev, int64_t n, const int
   paged::GatherArgs a;
   a.slots = slots_dev; a.cache[0] = k_cache_dev; a.cache[1] = v_cache_dev;
   a.scales[0] = k_scales_dev; a.scales[1] = v_scales_dev; a.out[0] = k_out_dev; a.out[1] = v_out_dev;
-  a.n = n; a.chunks = n * kv_heads * (head_dim / 8); a.slots_in_cache = num_blocks * block_size;
+  a.n = n; a.slots_in_cache = num_blocks * block_size;
   a.kv_heads = kv_heads; a.dim = head_dim; a.log2_bs = serve::log2_of(block_size); a.status = dev_status_dev;
-  int64_t grid = (2 * a.chunks + 255) / 256;
+  int64_t grid = (2 * n + 7) / 8;
   if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
   return out_dtype == LQ_BF16 ? serve::launch(paged::gather_kernel<true>, (unsigned)grid, 256, 0, stream, a)
                               : serve::launch(paged::gather_kernel<false>, (unsigned)grid, 256, 0, stream, a);

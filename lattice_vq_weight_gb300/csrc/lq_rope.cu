@@ -7,14 +7,16 @@
 // sin); a pair is (i, i + rot/2), or (2i, 2i + 1) when interleaved.  Everything
 // between the load and the one rounding of the result is fp32.
 //
-// The pass is bound by HBM for a prompt and by latency for a decode step, so
-// the layout is chosen for wide loads and few dependent steps: eight
-// consecutive dimensions per lane (one 16-byte bf16 load), a head in the
-// smallest power-of-two group of lanes that holds it (two heads of 128 per
-// warp), the norm by shuffles within the group, and the rotation partner
-// rot/2 dimensions away by shuffles too -- no shared memory, no barrier.  A
-// warp takes IT x 32/group heads of one token with all their loads in flight
-// at once, so a lane's cos and sin values are loaded once for IT heads.
+// The pass is bound by HBM for a prompt and by latency for a decode step, and
+// at HBM speed an SM has few instructions for each value, so the layout saves
+// those: eight dimensions per lane, chosen so that rotation partners meet in
+// one lane (lane i of a head holds 4 i .. 4 i + 3 and the four dimensions
+// rot/2 further; two 8-byte bf16 loads, 128 bytes per head and load) and no
+// value is exchanged but the norm's sum.  A head takes the smallest
+// power-of-two group of lanes that holds it (two heads of 128 per warp).  A
+// warp handles IT rounds of heads of one token and one kind (query or key)
+// with all their loads in flight at once, and forms the products of cosine,
+// sine and weight once for all of them.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"
@@ -34,8 +36,8 @@ struct Args {
   void* ko;
   int64_t ldq, ldk, ldqo, ldko;
   int q_heads, kv_heads, dim, rot, interleaved;
-  int64_t tokens, units, max_pos;
-  int units_per_token;
+  int64_t tokens, max_pos;
+  int units_per_token, q_units;
   const float* qw;
   const float* kw;
   float eps, inv_dim;
@@ -45,132 +47,117 @@ struct Args {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+__device__ __forceinline__ void load4(const void* p, int64_t i, float* v) {
   if constexpr (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(u[e] << 16);
-      v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-    }
+    const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+    v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xFFFF0000u);
   } else {
-    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    const float4 x = f[0], y = f[1];
+    const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
   }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+__device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, float c, float d) {
   if constexpr (BF16) {
-    uint32_t u[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-      u[e] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   } else {
-    float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
-    f[0] = make_float4(v[0], v[1], v[2], v[3]);
-    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = make_float4(a, b, c, d);
   }
 }
 
 // G: lanes per head (a power of two, >= dim / 8); IT: rounds of 32 / G heads
-// per warp.
-template <bool BF16, int G, int IT>
+// per warp; INTER: interleaved pairs.
+template <bool BF16, int G, int IT, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
   constexpr int H = 32 / G;
   const int lane = threadIdx.x & 31, sub = lane & (G - 1);
   const bool in_head = 8 * sub < a.dim;
   const bool rotates = 8 * sub < a.rot;
   const int half = a.rot >> 1;
+  // this lane's dimensions: o0 .. o0 + 3 and o1 .. o1 + 3
+  const int o0 = (!INTER && rotates) ? 4 * sub : 8 * sub;
+  const int o1 = (!INTER && rotates) ? half + 4 * sub : 8 * sub + 4;
   pdl_wait();
   pdl_launch();
-  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= a.units) return;                       // whole warps only
-  const int64_t t = u / a.units_per_token;
-  const int h0 = (int)(u - t * a.units_per_token) * (IT * H) + lane / G;
-  const int heads = a.q_heads + a.kv_heads;
+  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const unsigned t = u / (unsigned)a.units_per_token;
+  if (t >= a.tokens) return;                      // whole warps only
+  int unit = (int)(u - t * (unsigned)a.units_per_token);
+  const bool is_q = unit < a.q_units;
+  if (!is_q) unit -= a.q_units;
+  const int heads = is_q ? a.q_heads : a.kv_heads;
+  const int h0 = unit * (IT * H) + lane / G;
+  const void* src = is_q ? a.q : a.k;
+  void* dst = is_q ? a.qo : a.ko;
+  const int64_t from = t * (is_q ? a.ldq : a.ldk) + (int64_t)h0 * a.dim;
+  const int64_t to = t * (is_q ? a.ldqo : a.ldko) + (int64_t)h0 * a.dim;
+  const int pos = __ldg(a.positions + t);
 
   float v[IT][8];
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
-    const int h = h0 + it * H;
-    if (h < heads && in_head) {
-      if (h < a.q_heads) load8<BF16>(a.q, t * a.ldq + (int64_t)h * a.dim + 8 * sub, v[it]);
-      else load8<BF16>(a.k, t * a.ldk + (int64_t)(h - a.q_heads) * a.dim + 8 * sub, v[it]);
+    if (h0 + it * H < heads && in_head) {
+      load4<BF16>(src, from + it * H * a.dim + o0, v[it]);
+      load4<BF16>(src, from + it * H * a.dim + o1, v[it] + 4);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[it][e] = 0.f;
     }
   }
 
-  // this lane's angles: element e of the lane belongs to pair i(e), as its
-  // first member (sign of sin -) or its second (+)
-  float cs[8], sn[8];
-  const int pos = __ldg(a.positions + t);
-  const bool pos_ok = pos >= 0 && pos < a.max_pos;
-  if (!pos_ok && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
-  if (rotates && pos_ok) {
-    const float* row = a.cos_sin + (int64_t)pos * a.rot;
-    if (a.interleaved) {
-      const float4 c = *reinterpret_cast<const float4*>(row + 4 * sub);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + 4 * sub);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cs[e] = cc[e >> 1];
-        sn[e] = (e & 1) ? ss[e >> 1] : -ss[e >> 1];
-      }
+  // y[e] = r (c[e] v[e] + s[e] v[partner of e]): the weights ride along
+  float c[8], s[8];
+  const float* w = is_q ? a.qw : a.kw;
+  {
+    float wv[8];
+    if (w != nullptr && in_head) {
+      load4<false>(w, o0, wv);
+      load4<false>(w, o1, wv + 4);
     } else {
-      const bool second = 8 * sub >= half;
-      const int i0 = 8 * sub - (second ? half : 0);
-      load8<false>(row, i0, cs);
-      load8<false>(row, half + i0, sn);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sn[e] = second ? sn[e] : -sn[e];
+      for (int e = 0; e < 8; ++e) wv[e] = 1.f;
     }
-  } else {
+    const bool pos_ok = pos >= 0 && pos < a.max_pos;
+    if (!pos_ok && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    if (rotates && pos_ok) {
+      load4<false>(a.cos_sin, (int64_t)pos * a.rot + 4 * sub, cs);
+      load4<false>(a.cos_sin, (int64_t)pos * a.rot + half + 4 * sub, sn);
+    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) { cs[e] = 1.f; sn[e] = 0.f; }
+    for (int i = 0; i < 4; ++i) {
+      const int p = INTER ? 2 * i : i, q = INTER ? 2 * i + 1 : i + 4;
+      c[p] = cs[i] * wv[p];
+      c[q] = cs[i] * wv[q];
+      s[p] = -sn[i] * wv[q];
+      s[q] = sn[i] * wv[p];
+    }
   }
-  // the lane holding the partner dimensions (half style)
-  int partner = lane;
-  if (!a.interleaved && rotates) partner = (8 * sub >= half) ? lane - (half >> 3) : lane + (half >> 3);
 
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
-    const int h = h0 + it * H;
-    const bool is_q = h < a.q_heads, ok = h < heads && in_head;
-    const float* w = is_q ? a.qw : a.kw;
-    // the sum in every lane, also where this kind of head is not normed: a
-    // warp may hold both kinds, and its shuffles are not to diverge
-    float s = 0.f;
+    float r = 1.f;
+    if (w != nullptr) {                           // the same in the whole warp
+      float x = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(v[it][e], v[it][e], s);
+      for (int e = 0; e < 8; ++e) x = fmaf(v[it][e], v[it][e], x);
 #pragma unroll
-    for (int o = G / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (w != nullptr && ok) {
-      const float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));
-      float wv[8];
-      load8<false>(w, 8 * sub, wv);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[it][e] = v[it][e] * r * wv[e];
+      for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      r = rsqrtf(fmaf(x, a.inv_dim, a.eps));
     }
     float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float far = __shfl_sync(0xffffffffu, v[it][e], partner);
-      const float other = a.interleaved ? v[it][e ^ 1] : far;
-      y[e] = rotates ? fmaf(other, sn[e], v[it][e] * cs[e]) : v[it][e];
+      const int p = INTER ? e ^ 1 : e ^ 4;
+      y[e] = r * fmaf(s[e], v[it][p], c[e] * v[it][e]);
     }
-    if (ok) {
-      if (is_q) store8<BF16>(a.qo, t * a.ldqo + (int64_t)h * a.dim + 8 * sub, y);
-      else store8<BF16>(a.ko, t * a.ldko + (int64_t)(h - a.q_heads) * a.dim + 8 * sub, y);
+    if (h0 + it * H < heads && in_head) {
+      store4<BF16>(dst, to + it * H * a.dim + o0, y[0], y[1], y[2], y[3]);
+      store4<BF16>(dst, to + it * H * a.dim + o1, y[4], y[5], y[6], y[7]);
     }
   }
 }
@@ -178,17 +165,21 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
 template <bool BF16, int G>
 lq_status launch_rope(Args& a, int sms, void* stream) {
   constexpr int H = 32 / G;
-  const int heads = a.q_heads + a.kv_heads;
-  // four rounds per warp keep four loads per lane in flight; a call whose
-  // warps would not fill the SMs twice takes one round per warp
-  const bool wide = a.tokens * ((heads + 4 * H - 1) / (4 * H)) >= (int64_t)sms * 2 * kWarps;
+  auto units = [&](int it) { return (a.q_heads + it * H - 1) / (it * H) + (a.kv_heads + it * H - 1) / (it * H); };
+  // four rounds per warp keep four heads' loads in flight; a call whose warps
+  // would not fill the SMs twice takes one round per warp
+  const bool wide = a.tokens * units(4) >= (int64_t)sms * 2 * kWarps;
   const int it = wide ? 4 : 1;
-  a.units_per_token = (heads + it * H - 1) / (it * H);
-  a.units = a.tokens * a.units_per_token;
-  const int64_t grid = (a.units + kWarps - 1) / kWarps;
-  if (grid > INT32_MAX) return LQ_ERR_SHAPE;
-  return wide ? serve::launch(norm_rope_kernel<BF16, G, 4>, (unsigned)grid, kThreads, 0, stream, a)
-              : serve::launch(norm_rope_kernel<BF16, G, 1>, (unsigned)grid, kThreads, 0, stream, a);
+  a.units_per_token = units(it);
+  a.q_units = (a.q_heads + it * H - 1) / (it * H);
+  const int64_t grid = (a.tokens * a.units_per_token + kWarps - 1) / kWarps;
+  if (grid > INT32_MAX / kWarps) return LQ_ERR_SHAPE;
+  const unsigned n = (unsigned)grid;
+  if (a.interleaved)
+    return wide ? serve::launch(norm_rope_kernel<BF16, G, 4, true>, n, kThreads, 0, stream, a)
+                : serve::launch(norm_rope_kernel<BF16, G, 1, true>, n, kThreads, 0, stream, a);
+  return wide ? serve::launch(norm_rope_kernel<BF16, G, 4, false>, n, kThreads, 0, stream, a)
+              : serve::launch(norm_rope_kernel<BF16, G, 1, false>, n, kThreads, 0, stream, a);
 }
 
 template <bool BF16>

@@ -15,9 +15,13 @@
 // the first v whose inclusive sum exceeds floor(u * total), u's 24 bits taken
 // as a whole number.  (A weight below 2^-36 counts as zero, 1e-11 of the mass.)
 //
-// A CTA per request: the acceptance tests in the first warp, then each warp
-// sums its share of the vocabulary, the warp in whose share the drawn token
-// lies finds it by scanning that share again.
+// A cluster of CTAs per request, up to eight by the vocabulary's size, so that
+// a small batch still reads its rows with many SMs.  Every CTA runs the
+// acceptance tests for itself (a few gathered values), sums its share of the
+// row warp by warp, and reads the other CTAs' sums from their shared memory;
+// the CTA in whose share the drawn token lies then looks again at the one
+// warp's part of it that holds the token, all its threads at once.  Bound by
+// reading the one row of p and of q that the request draws from.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"
@@ -27,13 +31,14 @@
 namespace lq {
 namespace verify {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 
 struct Args {
   const int32_t* tokens;
   const int32_t* lens;
-  int batch, max_draft;
+  int batch, max_draft, cluster;
   int64_t vocab;
   const void* p;
   int64_t p_req, p_row;
@@ -57,11 +62,75 @@ __device__ __forceinline__ unsigned long long whole(float w) {
   return w > 0.f ? __float2ull_rz(fminf(w, 4.f) * 68719476736.f) : 0ull;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+// The 64-bit word at this CTA's shared address `p`, of CTA `rank` of the cluster.
+__device__ __forceinline__ unsigned long long peer_word(const unsigned long long* p, uint32_t rank) {
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  uint32_t theirs;
+  unsigned long long v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(theirs) : "r"(mine), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(theirs) : "memory");
+  return v;
+}
+
+// A row's weights: p, or max(p - q, 0), or p without one token.
+template <bool BF16>
+struct Row {
+  const void* p;
+  const void* q;             // null: none
+  int64_t gone;              // token left out, -1: none
+  int32_t* status;
+  __device__ __forceinline__ unsigned long long one(float x, float y, int64_t v) const {
+    if (!(x <= 3.402823466e38f)) raise_flag(status, LQ_DEV_NONFINITE);
+    return whole(v == gone ? 0.f : x - y);
+  }
+  __device__ __forceinline__ unsigned long long weight(int64_t v) const {
+    return one(at<BF16>(p, v), q != nullptr ? at<BF16>(q, v) : 0.f, v);
+  }
+  // the sum over [v0, v1) of a warp's lanes; v0 a multiple of 8
+  __device__ __forceinline__ unsigned long long sum(int64_t v0, int64_t v1, int lane) const {
+    constexpr int E = BF16 ? 8 : 4;                // values per 16-byte load
+    unsigned long long n = 0;
+    int64_t v = v0;
+    const uintptr_t low = reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q);
+    if ((low & 15) == 0) {                         // rows that start at 16-byte boundaries
+#pragma unroll 4
+      for (; v + 32 * E <= v1; v += 32 * E) {
+        const int64_t c = v / E + lane;
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + c);
+        const uint4 y = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (BF16) {
+            n += one(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), c * 8 + 2 * e);
+            n += one(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), c * 8 + 2 * e + 1);
+          } else {
+            n += one(__uint_as_float(xs[e]), __uint_as_float(ys[e]), c * 4 + e);
+          }
+        }
+      }
+    }
+#pragma unroll 8
+    for (v += lane; v < v1; v += 32) n += weight(v);
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+  }
+};
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) verify_kernel(Args a) {
-  __shared__ int s_acc, s_found;
-  __shared__ unsigned long long part[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  __shared__ int s_acc;
+  __shared__ unsigned long long part[kWarps], total_here, scan[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = a.cluster, rank = ctas > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / ctas;
   pdl_wait();
   pdl_launch();
   int n = a.lens != nullptr ? __ldg(a.lens + b) : a.max_draft;
@@ -69,13 +138,14 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(Args a) {
     if (tid == 0) raise_flag(a.status, LQ_DEV_RANGE);
     n = n < 0 ? 0 : a.max_draft;
   }
+  const int32_t* drafted = a.tokens + (int64_t)b * a.max_draft;
   if (warp == 0) {
     int acc = n;
     for (int i0 = 0; i0 < n && acc == n; i0 += 32) {
       const int i = i0 + lane;
       bool ok = true;
       if (i < n) {
-        const int64_t x = __ldg(a.tokens + (int64_t)b * a.max_draft + i);
+        const int64_t x = __ldg(drafted + i);
         ok = false;
         if (x >= 0 && x < a.vocab) {
           const float p = at<BF16>(a.p, b * a.p_req + i * a.p_row + x);
@@ -88,70 +158,91 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(Args a) {
       const uint32_t no = __ballot_sync(0xffffffffu, !ok);
       if (no) acc = i0 + __ffs(no) - 1;
     }
-    if (lane == 0) {
-      s_acc = acc;
-      s_found = -1;
-    }
+    if (lane == 0) s_acc = acc;
   }
   __syncthreads();
   const int acc = s_acc;
-  bool rest = acc < n;
-  const int64_t pr = b * a.p_req + acc * a.p_row, qr = b * a.q_req + acc * a.q_row;
-  const int64_t gone = (rest && a.q == nullptr) ? __ldg(a.tokens + (int64_t)b * a.max_draft + acc) : -1;
-  const int64_t share = (a.vocab + kWarps - 1) / kWarps;
-  const int64_t v0 = min(a.vocab, warp * share), v1 = min(a.vocab, v0 + share);
-  auto weight = [&](int64_t v) {
-    float w = at<BF16>(a.p, pr + v);
-    if (!(w <= 3.402823466e38f)) raise_flag(a.status, LQ_DEV_NONFINITE);
-    if (rest) w = a.q != nullptr ? w - at<BF16>(a.q, qr + v) : (v == gone ? 0.f : w);
-    return whole(w);
-  };
-  unsigned long long total = 0, before = 0;
+  constexpr int64_t esize = BF16 ? 2 : 4;
+  Row<BF16> row;
+  row.p = reinterpret_cast<const uint8_t*>(a.p) + (b * a.p_req + acc * a.p_row) * esize;
+  row.q = acc < n && a.q != nullptr ? reinterpret_cast<const uint8_t*>(a.q) + (b * a.q_req + acc * a.q_row) * esize
+                                    : nullptr;
+  row.gone = acc < n && a.q == nullptr ? __ldg(drafted + acc) : -1;
+  row.status = a.status;
+
+  // shares of a multiple of 8 tokens: CTA by CTA, in each warp by warp
+  const int64_t share = ((a.vocab + (int64_t)ctas * kWarps - 1) / ((int64_t)ctas * kWarps) + 7) & ~(int64_t)7;
+  auto begin_of = [&](int w) { return min(a.vocab, ((int64_t)rank * kWarps + w) * share); };
+  unsigned long long total = 0, before = 0;        // all CTAs', and those before this one
   for (int pass = 0; pass < 2; ++pass) {
-    unsigned long long sum = 0;
-    for (int64_t v = v0 + lane; v < v1; v += 32) sum += weight(v);
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const unsigned long long mine = row.sum(begin_of(warp), begin_of(warp + 1), lane);
+    if (lane == 0) part[warp] = mine;
     __syncthreads();
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) before = total;
-      total += part[w];
+    unsigned long long here = 0;
+    for (int w = 0; w < kWarps; ++w) here += part[w];
+    if (ctas > 1) {
+      if (tid == 0) total_here = here;
+      cluster_sync();
+      total = 0;
+      for (int r = 0; r < ctas; ++r) {
+        if (r == rank) before = total;
+        total += peer_word(&total_here, (uint32_t)r);
+      }
+      cluster_sync();                              // read before anyone writes it again or leaves
+    } else {
+      total = here;
     }
-    if (total > 0 || !rest) break;
-    rest = false;                        // nothing left of p - q: draw from p
+    if (total > 0 || (row.q == nullptr && row.gone < 0)) break;
+    row.q = nullptr;                               // nothing left of p - q: draw from p
+    row.gone = -1;
+    __syncthreads();
   }
+
+  int32_t* out = a.out + (int64_t)b * (a.max_draft + 1);
   if (total > 0) {
     float u = __ldg(a.u_sample + b);
     u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
     const unsigned long long k = (unsigned long long)(u * 16777216.f);
     const unsigned long long goal = (__umul64hi(total, k) << 40) | ((total * k) >> 24);
-    if (goal >= before && goal < before + part[warp]) {
-      unsigned long long run = before;
-      for (int64_t c = v0; c < v1; c += 32) {
-        const unsigned long long w = c + lane < v1 ? weight(c + lane) : 0ull;
-        unsigned long long inc = w;
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
+    // the warp's part that holds the token, if it lies in this CTA
+    int w = 0;
+    unsigned long long run = before;
+    while (w < kWarps && goal >= run + part[w]) run += part[w++];
+    if (goal >= before && w < kWarps) {
+      // its tokens in runs, a run per thread; the sums before each thread's run
+      const int64_t v0 = begin_of(w), v1 = begin_of(w + 1);
+      const int64_t per = (v1 - v0 + kThreads - 1) / kThreads;
+      const int64_t c0 = min(v1, v0 + tid * per), c1 = min(v1, c0 + per);
+      unsigned long long sum = 0;
+#pragma unroll 8
+      for (int64_t v = c0; v < c1; ++v) sum += row.weight(v);
+      unsigned long long inc = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      for (int i = 0; i < warp; ++i) inc += scan[i];
+      unsigned long long at_run = run + inc - sum;
+      if (goal >= at_run && goal < at_run + sum) {
+        int64_t v = c0;
+        for (; v < c1; ++v) {
+          at_run += row.weight(v);
+          if (at_run > goal) break;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, run + inc > goal);
-        if (hit) {
-          if (lane == 0) s_found = (int)(c + __ffs(hit) - 1);
-          break;
-        }
-        run += __shfl_sync(0xffffffffu, inc, 31);
+        out[acc] = (int32_t)v;
       }
     }
-  } else if (tid == 0) {
+  } else if (rank == 0 && tid == 0) {
+    out[acc] = -1;
     raise_flag(a.status, LQ_DEV_RANGE);
   }
-  __syncthreads();
-  for (int i = tid; i <= a.max_draft; i += kThreads)
-    a.out[(int64_t)b * (a.max_draft + 1) + i] =
-        i < acc ? __ldg(a.tokens + (int64_t)b * a.max_draft + i) : (i == acc ? s_found : -1);
-  if (tid == 0) a.accepted[b] = acc;
+  if (rank == 0) {
+    for (int i = tid; i <= a.max_draft; i += kThreads)
+      if (i != acc) out[i] = i < acc ? __ldg(drafted + i) : -1;
+    if (tid == 0) a.accepted[b] = acc;
+  }
 }
 
 }  // namespace verify
@@ -190,7 +281,12 @@ extern "C" lq_status lq_verify_draft(const int32_t* draft_tokens_dev, const int3
   a.q = draft_probs_dev; a.q_req = draft_req_stride; a.q_row = draft_row_stride;
   a.u_accept = u_accept_dev; a.u_sample = u_sample_dev; a.out = out_tokens_dev; a.accepted = accepted_dev;
   a.status = dev_status_dev;
+  // a CTA for every 4096 tokens of the vocabulary: shares of 2 or more 16-byte
+  // loads per lane
+  a.cluster = 1;
+  while (a.cluster < verify::kMaxCluster && (int64_t)a.cluster * 4096 < vocab) a.cluster *= 2;
+  const unsigned grid = (unsigned)batch * (unsigned)a.cluster;
   return dtype == LQ_BF16
-             ? serve::launch(verify::verify_kernel<true>, (unsigned)batch, verify::kThreads, 0, stream, a)
-             : serve::launch(verify::verify_kernel<false>, (unsigned)batch, verify::kThreads, 0, stream, a);
+             ? serve::launch(verify::verify_kernel<true>, grid, verify::kThreads, 0, stream, a, a.cluster)
+             : serve::launch(verify::verify_kernel<false>, grid, verify::kThreads, 0, stream, a, a.cluster);
 }

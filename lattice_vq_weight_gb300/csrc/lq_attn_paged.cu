@@ -18,13 +18,15 @@
 // most 16 rows.  The batch's work is a list of 32-token tiles (request, tile of
 // rows, kv head, tokens), and every warp of one CTA per SM takes an equal,
 // contiguous part of it, whatever the lengths are: no request waits for
-// another's long tail.  A warp streams its tiles through its own ring of
-// stages by TMA (the codes' rows of 128 bytes in the 128-byte swizzle, so that
-// the fragment loads below meet no bank twice) with no barrier shared between
-// warps, keeps running maxima, sums and the output tile in registers, and
-// writes an output when it has seen all of a row's tiles.  Pieces of rows are
-// joined through shared memory within a CTA and by the merge kernel between
-// CTAs, in the order of the tiles, so that equal calls give equal bits.
+// another's long tail.  A warp streams its tiles through its own ring of half
+// tiles (K, V, K, V, ...) by TMA (the codes' rows of 128 bytes in the 128-byte
+// swizzle, so that the fragment loads below meet no bank twice) with no
+// barrier shared between warps, keeps running maxima, sums and the output tile
+// in registers, and writes an output when it has seen all of a row's tiles.
+// Pieces of rows are joined by the CTA and by the merge kernel between CTAs, in
+// the order of the tiles, so that equal calls give equal bits.  Sixteen warps
+// per SM, with half a tile's compute between refills, keep about 128 KB of
+// loads in flight and enough warps to issue from while others wait.
 //
 // Products on mma.sync m16n8k16 with the codes as the 16-row operand (fp16,
 // exact) and eight query rows as the other: scores S^T = C_k q^T, then
@@ -32,7 +34,10 @@
 // or 128 rows to earn its operand traffic through shared memory; at 8 or 16
 // rows it would still be the codes' bytes that bound the kernel.  bf16 queries
 // are exact in fp16 after a power-of-two factor per row; fp32 queries and
-// weights are split into two fp16 terms (22 bits).
+// weights are split into two fp16 terms (22 bits).  The running maximum is let
+// fall behind by up to 2^7 (weights are held times 2^8, so 2^15 is in range
+// and 2^-22 of the largest still a normal number): most tiles then only compare
+// with it and need no exchange between lanes.
 #include "lq_attn_paged.cuh"
 
 namespace lq {
@@ -40,36 +45,38 @@ namespace attn {
 
 constexpr int kTile = 32;                      // tokens per tile
 
-template <int D, int NT>
+template <int D, int NT, bool F32>
 struct Cfg {
-  static constexpr int kWarps = D == 256 ? 4 : 8;
+  // 16 warps of at most 128 registers where the output tile and the queries
+  // leave room, else 8 of at most 255
+  static constexpr int kWarps = D * NT * (F32 ? 2 : 1) <= 128 ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStageBytes = 2 * kTile * D;        // K codes, then V codes
-  // in shared memory: the rings, the warps' first pieces, scales and barriers
+  static constexpr int kHalfBytes = kTile * D;             // the K or the V codes of a tile
   static constexpr int kPiece = kRows * (D + 2);           // floats: output rows, maxima, sums
-  static constexpr int kFixed = kWarps * kPiece * 4 + 1024 + 640;   // with the alignment and the static part
-  static constexpr int kFit = (227 * 1024 - kFixed) / (kWarps * (kStageBytes + 24));
-  static constexpr int kStages = kFit < 6 ? kFit : 6;
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kRing + kWarps * kPiece * 4 + kWarps * kStages * 24 + 1024;
+  static constexpr int kPerHalf = kHalfBytes + 32;         // codes, barrier, scales, what tile it is
+  static constexpr int kEnds = 2 * kWarps;                 // pieces that the warps may leave
+  static constexpr int kFit = (227 * 1024 - 1024 - 1536 - 3 * kEnds * kRows * 4) / (kWarps * kPerHalf);
+  static constexpr int kHalves = kFit < 8 ? kFit : 8;      // of a warp's ring
+  static constexpr int kRing = kWarps * kHalves * kHalfBytes;
+  static constexpr int kSmem = kWarps * kHalves * kPerHalf + 3 * kEnds * kRows * 4 + 1024;
 };
 
 // A place in the list of tiles.
 struct Cursor {
   int i;             // request
-  int64_t rt;        // tile of rows
+  int rt, nrt;       // tile of rows, and how many the request has
   int h;             // kv head
   int t, nt;         // tile of tokens, and how many the request has
-  int64_t nrt;
-  Request r;
+  int len;
 };
 
 template <int ROWS>
 __device__ __forceinline__ void enter(const Args& a, Cursor& c) {
-  c.r = load_request(a, c.i);
-  c.nrt = ((int64_t)c.r.q_len * a.group + ROWS - 1) / ROWS;
-  c.nt = c.r.len > 0 ? (c.r.len + kTile - 1) / kTile : 1;
+  const Request r = load_request(a, c.i);
+  c.len = r.len;
+  c.nrt = (r.q_len * a.group + ROWS - 1) / ROWS;
+  c.nt = r.len > 0 ? (r.len + kTile - 1) / kTile : 1;
 }
 
 template <int ROWS>
@@ -81,6 +88,7 @@ __device__ __forceinline__ void advance(const Args& a, Cursor& c) {
   if (++c.rt < c.nrt) return;
   c.rt = 0;
   c.nrt = 0;
+#pragma unroll 1
   while (++c.i < a.batch) {
     enter<ROWS>(a, c);
     if (c.nrt > 0) break;
@@ -120,18 +128,14 @@ __device__ __forceinline__ uint32_t code_at(int t, int b) {
   return off ^ (((off >> 7) & 7u) << 4);
 }
 
-// What a piece of a row tile belongs to, in shared memory: request, row tile,
-// kv head, and whether it begins or ends the tile's tokens.
-struct Tag {
-  int64_t rt;
-  int i, h;
-  int valid, starts, ends;
-};
 __device__ __forceinline__ bool same(const Tag& x, const Tag& y) { return x.i == y.i && x.rt == y.rt && x.h == y.h; }
 
-// ints of a CTA's meta record: two tags of {valid, starts, ends, i, h, rt lo, rt hi}
-constexpr int kTagInts = 8;
-constexpr int kMetaInts = 2 * kTagInts;
+// Where a row of a row tile lies in q or out, in elements; false past the last row.
+__device__ __forceinline__ bool row_at(const Args& a, int q0, int q_len, int R, int h, int64_t ld, int dim, int64_t* at) {
+  const int j = R / a.group;
+  *at = (int64_t)(q0 + j) * ld + (h * a.group + R - j * a.group) * dim;
+  return j < q_len;
+}
 
 template <bool F32>
 __device__ __forceinline__ void store_out(const Args& a, int64_t at, float v) {
@@ -139,45 +143,62 @@ __device__ __forceinline__ void store_out(const Args& a, int64_t at, float v) {
   else reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
 }
 
-// What turns a row's accumulated values into its output: 1 / l without the
-// weights' shift, 0 for a row that sees nothing; NaN stays NaN.
-__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : kUnshift / l; }
+template <bool F32>
+__device__ __forceinline__ void store_out4(const Args& a, int64_t at, const float4& o, float inv) {
+  if constexpr (F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  } else {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+}
+
+// What turns a row's accumulated values into its output: 1 / l, or 0 for a row
+// that sees nothing; NaN stays NaN.  (The weights' shift is in both sums.)
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : kSumUnit / l; }
 
 template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, NT, F32>::kThreads, 1)
 attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const __grid_constant__ Args a) {
-  using C = Cfg<D, NT>;
-  constexpr int kWarps = C::kWarps, kRows = C::kRows, S = C::kStages;
+  using C = Cfg<D, NT, F32>;
+  constexpr int kWarps = C::kWarps, kRows = C::kRows, S = C::kHalves;
   constexpr int KS = D / 16;                   // k steps of the scores, m tiles of the output
   constexpr int Q2 = F32 ? 2 : 1;              // fp16 terms of a query or weight
   extern __shared__ uint8_t attn_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(attn_smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tid = lane & 3;
-  uint8_t* ring = smem + warp * S * C::kStageBytes;
-  float* pieces = reinterpret_cast<float*>(smem + C::kRing);          // the warps' first pieces
-  uint64_t* bars = reinterpret_cast<uint64_t*>(pieces + kWarps * C::kPiece) + warp * S;
-  float* scales = reinterpret_cast<float*>(reinterpret_cast<uint64_t*>(pieces + kWarps * C::kPiece) + kWarps * S) +
-                  warp * S * 4;
+  uint8_t* ring = smem + warp * S * C::kHalfBytes;
+  int4* infos = reinterpret_cast<int4*>(smem + C::kRing) + warp * S;               // which tile a K half is of
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing + kWarps * S * 16) + warp * S;
+  float2* scales = reinterpret_cast<float2*>(smem + C::kRing + kWarps * S * 24) + warp * S;
+  // maxima and sums of the warps' pieces, and their weights when they are joined
+  float* piece_m = reinterpret_cast<float*>(smem + kWarps * S * C::kPerHalf);
+  float* piece_l = piece_m + C::kEnds * kRows;
+  float* piece_f = piece_l + C::kEnds * kRows;
   __shared__ Tag tags[2 * kWarps];
+  __shared__ int order[2 * kWarps];            // the pieces that are there, in order
   __shared__ long long wsum[kWarps];
-  __shared__ int timeout;
-  const int bs = 1 << a.log2_bs;
+  __shared__ int2 asked[kWarps];               // the warp's current request: first query token, how many
+  __shared__ int timeout, q_end;
+  const bool paired = a.log2_bs < 5;           // a tile spans two blocks of 16
+  // where the warps' first pieces go when more follow; a last one takes the
+  // warp's ring, which is not filled again
+  float* firsts = a.part + ((int64_t)gridDim.x * 2 + (int64_t)blockIdx.x * kWarps) * C::kPiece;
 
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init1(bars + s, 5);
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) mbar_init1(bars + s, 3);
     mbar_init_fence();
     tags[2 * warp].valid = tags[2 * warp + 1].valid = 0;
   }
-  if (threadIdx.x == 0) timeout = 0;
   pdl_wait();
   pdl_launch();
-
-  // rows that no request owns
-  {
-    const int64_t end = __ldg(a.cu_q + a.batch), cols = (int64_t)a.q_heads * D;
-    for (int64_t t = (end < 0 ? 0 : end) + blockIdx.x; t < a.total_q; t += gridDim.x)
-      for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) store_out<F32>(a, t * a.ldo + c, 0.f);
+  if (threadIdx.x == 0) {
+    timeout = 0;
+    q_end = __ldg(a.cu_q + a.batch);
   }
 
   // prefix sums of the requests' tiles (in the rings, which are still empty);
@@ -185,17 +206,15 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   long long* pre = reinterpret_cast<long long*>(smem);
   const int per = (a.batch + C::kThreads - 1) / C::kThreads;
   const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
-  auto tiles_of = [&](int i) {
+  long long sum = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
     if (blockIdx.x == 0 && (int64_t)__ldg(a.kv_lens + i) > ((int64_t)a.width << a.log2_bs))
       raise_flag(a.status, LQ_DEV_RANGE);
     Cursor c;
     c.i = i;
     enter<kRows>(a, c);
-    return (long long)c.nrt * a.kv_heads * c.nt;
-  };
-  long long sum = 0;
-  for (int i = i0; i < i1; ++i) {
-    const long long n = tiles_of(i);
+    const long long n = (long long)c.nrt * a.kv_heads * c.nt;
     pre[i] = n;
     sum += n;
   }
@@ -207,11 +226,13 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   if (lane == 31) wsum[warp] = inc;
   __syncthreads();
   long long total = 0;
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w == warp) inc += total;
     total += wsum[w];
   }
   long long run = inc - sum;
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const long long n = pre[i];
     pre[i] = run;
@@ -219,359 +240,373 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   }
   __syncthreads();
   // equal parts for the CTAs, then for their warps, the first ones a tile longer
-  long long u0 = 0;
-  int64_t n = total;
-  auto part_of = [&](int parts, int i) {
-    const long long base = n / parts, more = n % parts;
-    u0 += base * i + (i < more ? i : more);
-    n = base + (i < more ? 1 : 0);
+  long long u0 = 0, part_n = total;
+  auto part_of = [&](unsigned parts, unsigned i) {
+    const long long base = part_n < INT_MAX ? (unsigned)part_n / parts : part_n / parts;
+    const unsigned more = (unsigned)(part_n - base * parts);
+    u0 += base * i + min(i, more);
+    part_n = base + (i < more ? 1 : 0);
   };
   part_of(gridDim.x, blockIdx.x);
   part_of(kWarps, warp);
-  Cursor cc, ci;
+  const int n = (int)(part_n < (1 << 29) ? part_n : (1 << 29));
+  Cursor ci;                                   // the tile whose halves are fetched next
   if (n > 0) {
     int lo = 0, hi = a.batch;                  // last request with pre[i] <= u0 (it has tiles: the next one starts later)
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= u0) lo = mid; else hi = mid;
     }
-    cc.i = lo;
-    enter<kRows>(a, cc);
-    long long rem = u0 - pre[lo];
-    cc.t = (int)(rem % cc.nt);
-    rem /= cc.nt;
-    cc.h = (int)(rem % a.kv_heads);
-    cc.rt = rem / a.kv_heads;
+    ci.i = lo;
+    enter<kRows>(a, ci);
+    const long long rem = u0 - pre[lo];
+    const long long hr = rem < INT_MAX ? (unsigned)rem / (unsigned)ci.nt : rem / ci.nt;    // row tile and head
+    ci.t = (int)(rem - hr * ci.nt);
+    ci.rt = (int)(hr < INT_MAX ? (unsigned)hr / (unsigned)a.kv_heads : hr / a.kv_heads);
+    ci.h = (int)(hr - (long long)ci.rt * a.kv_heads);
   }
   // the prefix sums have been read: the rings may fill
   fence_proxy_async_smem();
   __syncthreads();
 
   if (n > 0) {
-    ci = cc;
-    // block of part e (lanes 0 and 1) of the tile at the issue cursor
+    // lanes 0 and 1: the block of half a tile each (the same block where it
+    // holds the whole tile), and its place in the scales
+    int blk = -1, at_scale = 0;
+    bool blk_ok = false;
     auto load_block = [&]() {
-      int blk = -1;
-      const int p = ci.t * kTile + (bs < kTile ? 16 * lane : 0);
-      if (lane < 2 && p < ci.r.len) blk = __ldg(a.table + ci.i * a.ldt + (p >> a.log2_bs));
-      return blk;
+      const int p = ci.t * kTile + (paired ? 16 * lane : 0);
+      blk = -1;
+      if (lane < 2 && p < ci.len) blk = __ldg(a.table + ci.i * a.ldt + (p >> a.log2_bs));
     };
-    auto issue = [&](int s, int blk) {
-      const int e = bs < kTile ? (lane >> 1) & 1 : 0;
-      const int b = __shfl_sync(0xffffffffu, blk, e);
-      const bool ok = b >= 0 && b < a.num_blocks;
-      const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-      if (lane < 4) {
-        const int64_t sc = (int64_t)b * a.kv_heads + ci.h;
-        float* dst = scales + 4 * s + lane;    // k and v of part 0, of part 1
-        if (ok) {
-          cp_async4(smem_addr(dst), ((lane & 1) ? a.vs : a.ks) + sc);
+    const int rows_per_block = (D << a.log2_bs) >> 7;
+    int qi = 0;                                // halves issued
+    auto issue = [&](int s) {
+      const bool is_v = qi & 1;
+      if (!is_v) {
+        blk_ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+        at_scale = blk * a.kv_heads + ci.h;
+        if (lane < 2 && !blk_ok && ci.t * kTile + (paired ? 16 * lane : 0) < ci.len)
+          raise_flag(a.status, LQ_DEV_RANGE);  // a block id outside the pool
+        if (lane == 0) infos[s] = make_int4(ci.i, ci.rt, ci.h | (ci.t + 1 == ci.nt ? 1 << 16 : 0), ci.t);
+      }
+      const bool ok0 = __shfl_sync(0xffffffffu, blk_ok, 0), ok1 = __shfl_sync(0xffffffffu, blk_ok, 1);
+      if (lane < 2) {
+        float* dst = reinterpret_cast<float*>(scales + s) + lane;
+        if (blk_ok) {
+          cp_async4(smem_addr(dst), (is_v ? a.vs : a.ks) + at_scale);
           cp_async_arrive(bars + s);
         } else {
           *dst = -1.f;                         // its tokens are left out
           mbar_arrive(bars + s);
         }
-      }
-      if (lane == 0) {
-        uint8_t* dst = ring + s * C::kStageBytes;
-        if (bs < kTile) {
-          const uint32_t part = 16 * D;
-          const bool ok1 = (oks >> 2) & 1;
-          mbar_expect_tx(bars + s, 2 * part * ((ok ? 1 : 0) + (ok1 ? 1 : 0)));
-          if (ok) {
-            const int row = (int)((((int64_t)b * a.kv_heads + ci.h) << a.log2_bs) * D >> 7);
-            tma_load_2d(dst, &map_k, bars + s, 0, row);
-            tma_load_2d(dst + kTile * D, &map_v, bars + s, 0, row);
-          }
-        } else {
-          mbar_expect_tx(bars + s, ok ? C::kStageBytes : 0);
-          if (ok) {
-            const int off = (ci.t * kTile) & (bs - 1);
-            const int row = (int)(((((int64_t)b * a.kv_heads + ci.h) << a.log2_bs) + off) * D >> 7);
-            tma_load_2d(dst, &map_k, bars + s, 0, row);
-            tma_load_2d(dst + kTile * D, &map_v, bars + s, 0, row);
-          }
+        if (lane == 0)
+          mbar_expect_tx(bars + s, paired ? 16 * D * ((ok0 ? 1 : 0) + (ok1 ? 1 : 0)) : (ok0 ? C::kHalfBytes : 0));
+        if (blk_ok && (paired || lane == 0)) {
+          const int off = paired ? 0 : (ci.t * kTile) & ((1 << a.log2_bs) - 1);
+          tma_load_2d(ring + s * C::kHalfBytes + (paired ? lane * 16 * D : 0), is_v ? &map_v : &map_k, bars + s, 0,
+                      at_scale * rows_per_block + ((off * D) >> 7));
         }
-      } else if (lane == 2 && bs < kTile && ok) {
-        // the second half of a tile of two blocks; its bytes are in lane 0's count
-        uint8_t* dst = ring + s * C::kStageBytes + 16 * D;
-        const int row = (int)((((int64_t)b * a.kv_heads + ci.h) << a.log2_bs) * D >> 7);
-        tma_load_2d(dst, &map_k, bars + s, 0, row);
-        tma_load_2d(dst + kTile * D, &map_v, bars + s, 0, row);
       }
-      // a block id outside the pool, or a length past the table
-      const int p = ci.t * kTile + (bs < kTile ? 16 * e : 0);
-      if (lane < 4 && !ok && p < ci.r.len) raise_flag(a.status, LQ_DEV_RANGE);
+      if (++qi < 2 * n && is_v) {
+        advance<kRows>(a, ci);
+        load_block();
+      }
     };
 
-    int blk = load_block();
-    int64_t issued = 0;
-    for (int s = 0; s < S && issued < n; ++s) {
-      issue(s, blk);
-      if (++issued < n) {
-        advance<kRows>(a, ci);
-        blk = load_block();
-      }
-    }
+    load_block();
 
     uint32_t qf[NT][KS][2][Q2];
     float acc[KS][NT][4];
     float mx[NT][2], sum_l[NT][2], fac[NT][2];
     int lim[NT][2];                            // last position each of this thread's rows sees
     int lim_min = 0;
-    bool fresh = true, first_seg = true;
-    const bool begins = cc.t == 0;             // whether the first segment starts here
-    bool seg_starts = begins;
+    bool fresh = true, seg_starts = false, more_before = false, dead = false;
+    float sc[2][NT][4];                        // the tile's scores, then exponents
+    float2 sk2;
+    int4 info;
     int s = 0;
-    uint32_t ph = 0;
-    bool dead = false;
+    uint32_t ph = 1;
 
-    for (int64_t k = 0; k < n; ++k) {
-      if (fresh) {
-        fresh = false;
-        // this segment's query rows: lane (g, tid) holds row g's dimensions
-        // tid * D/4 ...; a power of two per row brings them into fp16's range
-        const int64_t rows = (int64_t)cc.r.q_len * a.group;
-        lim_min = INT_MAX;
+    // half tiles one after the other, K and V in turn; the first S steps only
+    // fill the ring, so that fetching stands in the code once
+#pragma unroll 1
+    for (int step = -S; step < 2 * n; ++step) {
+      const bool skip = step < 0;
+      if (fresh ? step == 2 - S || (step > 0 && !(step & 1)) : !skip && !(step & 1)) {
+        info = infos[skip ? 0 : s];            // written when the half was issued
+        if (fresh) {
+          // (the first segment's rows are fetched behind its first tile's codes)
+          fresh = false;
+          const int h = info.z & 0xFFFF;
+          seg_starts = info.w == 0;
+          // this segment's query rows: lane (g, tid) holds row g's dimensions
+          // tid * D/4 ...; a power of two per row brings them into fp16's range
+          const Request r = load_request(a, info.x);
+          if (lane == 0) asked[warp] = make_int2(r.q0, r.q_len);
+          lim_min = INT_MAX;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int64_t R = cc.rt * kRows + nt * 8 + g;
-          float v[D / 4];
-          if (R < rows) {
-            const int64_t at = (cc.r.q0 + R / a.group) * a.ldq + ((int64_t)cc.h * a.group + R % a.group) * D +
-                               tid * (D / 4);
-            if constexpr (F32) {
-              const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at);
+          for (int nt = 0; nt < NT; ++nt) {
+            float v[D / 4];
+            int64_t at;
+            if (row_at(a, r.q0, r.q_len, info.y * kRows + nt * 8 + g, h, a.ldq, D, &at)) {
+              at += tid * (D / 4);
+              if constexpr (F32) {
+                const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at);
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                const float4 x = __ldg(p + c);
-                v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
-              }
-            } else {
-              const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + at);
+                for (int c = 0; c < D / 16; ++c) {
+                  const float4 x = __ldg(p + c);
+                  v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
+                }
+              } else {
+                const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + at);
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                const uint4 x = __ldg(p + c);
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                for (int c = 0; c < D / 32; ++c) {
+                  const uint4 x = __ldg(p + c);
+                  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  v[8 * c + 2 * e] = __uint_as_float(u[e] << 16);
-                  v[8 * c + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                  for (int e = 0; e < 4; ++e) {
+                    v[8 * c + 2 * e] = __uint_as_float(u[e] << 16);
+                    v[8 * c + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                  }
                 }
               }
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 4; ++c) v[c] = 0.f;
             }
-          } else {
+            float top = 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 4; ++c) v[c] = 0.f;
-          }
-          float top = 0.f;
+            for (int c = 0; c < D / 4; ++c) top = fmaxf(top, fabsf(v[c]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^e with the row's largest value in [2^13, 2^14)
+            const int eb = (int)(__float_as_uint(top) >> 23);
+            const int ex = min(126, max(-116, 140 - eb));
+            const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+            const float down = a.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-          for (int c = 0; c < D / 4; ++c) top = fmaxf(top, fabsf(v[c]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^e with the row's largest value in [2^13, 2^14)
-          const int eb = (int)(__float_as_uint(top) >> 23);
-          const int ex = min(126, max(-116, 140 - eb));
-          const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-          const float down = a.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+            for (int c = 0; c < KS; ++c) {
 #pragma unroll
-          for (int c = 0; c < KS; ++c) {
+              for (int e = 0; e < 2; ++e) {
+                const float x = v[4 * c + 2 * e] * up, y = v[4 * c + 2 * e + 1] * up;
+                qf[nt][c][e][0] = pack_f16(x, y);
+                if constexpr (F32) qf[nt][c][e][1] = rest_f16(qf[nt][c][e][0], x, y);
+              }
+            }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float x = v[4 * c + 2 * e] * up, y = v[4 * c + 2 * e + 1] * up;
-              qf[nt][c][e][0] = pack_f16(x, y);
-              if constexpr (F32) qf[nt][c][e][1] = rest_f16(qf[nt][c][e][0], x, y);
+            for (int c = 0; c < 2; ++c) {
+              fac[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * tid + c));
+              const int j = (info.y * kRows + nt * 8 + 2 * tid + c) / a.group;
+              lim[nt][c] = j < r.q_len ? min(r.shown + j, r.len - 1) : r.len - 1;
+              lim_min = min(lim_min, lim[nt][c]);
+              mx[nt][c] = -INFINITY;
+              sum_l[nt][c] = 0.f;
             }
           }
+          lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
+          lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            fac[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * tid + c));
-            const int64_t Rc = cc.rt * kRows + nt * 8 + 2 * tid + c;
-            lim[nt][c] = Rc < rows ? cc.r.shown + (int)(Rc / a.group) : INT_MAX;
-            lim_min = min(lim_min, lim[nt][c]);
-            mx[nt][c] = -INFINITY;
-            sum_l[nt][c] = 0.f;
-          }
+          for (int c = 0; c < KS; ++c)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
         }
-        lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
-        lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
-        lim_min = min(lim_min, cc.r.len - 1);
+      }
+      if (!skip) {
+        if (!mbar_wait_bounded(bars + s, ph, kWaitCycles)) {
+          timeout = 1;
+          dead = true;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+      }
+      const bool ends = info.z >> 16;
+      if (!skip && !(step & 1)) {
+        // scores S^T [32 tokens x 8 NT rows]
+        const uint8_t* kst = ring + s * C::kHalfBytes;
 #pragma unroll
-        for (int c = 0; c < KS; ++c)
+        for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
-      }
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const int b = tid * (D / 4) + 16 * j;
+            const uint4 x = *reinterpret_cast<const uint4*>(kst + code_at<D>(16 * mt + g, b));
+            const uint4 y = *reinterpret_cast<const uint4*>(kst + code_at<D>(16 * mt + g + 8, b));
+            const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t u = xa[e] ^ 0x80808080u, v = ya[e] ^ 0x80808080u;
+              const uint32_t a0 = codes_f16(u, 0x4140), a2 = codes_f16(u, 0x4342);
+              const uint32_t a1 = codes_f16(v, 0x4140), a3 = codes_f16(v, 0x4342);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int f = 0; f < Q2; ++f)
+                  mma16816(sc[mt][nt], a0, a1, a2, a3, qf[nt][4 * j + e][0][f], qf[nt][4 * j + e][1][f]);
+            }
+          }
+        }
+        sk2 = scales[s];
+      } else if (!skip) {
+        const float2 sv2 = scales[s];
+        const int p0 = info.w * kTile;
+        const uint8_t* vst = ring + s * C::kHalfBytes;
 
-      if (!dead && !mbar_wait_bounded(bars + s, ph, kWaitCycles)) {
-        dead = true;
-        timeout = 1;
-      }
-      dead = __any_sync(0xffffffffu, dead);
-      if (dead) break;
-      const uint8_t* kst = ring + s * C::kStageBytes;
-      const uint8_t* vst = kst + kTile * D;
-      const float4 sc4 = *reinterpret_cast<const float4*>(scales + 4 * s);
-      const float sk[2] = {sc4.x, sc4.z}, sv[2] = {sc4.y, sc4.w};
-
-      // scores S^T [32 tokens x 8 NT rows]
-      float sc[2][NT][4];
+        // exponents x less the running maximum, plus the shift
+        const float sk[2] = {sk2.x, sk2.y}, sv[2] = {sv2.x, sv2.y};
+        float lv[2], iv[2];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < 2; ++mt) {
+          const float v = sv[mt] < kMinScale ? kMinScale : sv[mt];      // NaN stays NaN
+          lv[mt] = lg2(v);
+          iv[mt] = rcp(v) * kSumUnit;
+        }
+        float lead = -INFINITY;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const float b0 = kShift - (mx[nt][0] == -INFINITY ? 0.f : mx[nt][0]);
+          const float b1 = kShift - (mx[nt][1] == -INFINITY ? 0.f : mx[nt][1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+          for (int mt = 0; mt < 2; ++mt) {
+            const float c0 = fac[nt][0] * sk[mt], c1 = fac[nt][1] * sk[mt];
+            const float d0 = lv[mt] + b0, d1 = lv[mt] + b1;
+            sc[mt][nt][0] = fmaf(sc[mt][nt][0], c0, d0);
+            sc[mt][nt][1] = fmaf(sc[mt][nt][1], c1, d1);
+            sc[mt][nt][2] = fmaf(sc[mt][nt][2], c0, d0);
+            sc[mt][nt][3] = fmaf(sc[mt][nt][3], c1, d1);
+          }
+        }
+        if (p0 + kTile - 1 > lim_min || sv[0] < 0.f || sv[1] < 0.f) {
+          // tokens that some row does not see, or of a block that is not there
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const int b = tid * (D / 4) + 16 * j;
-          const uint4 x = *reinterpret_cast<const uint4*>(kst + code_at<D>(16 * mt + g, b));
-          const uint4 y = *reinterpret_cast<const uint4*>(kst + code_at<D>(16 * mt + g + 8, b));
-          const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t u = xa[e] ^ 0x80808080u, v = ya[e] ^ 0x80808080u;
-            const uint32_t a0 = codes_f16(u, 0x4140), a2 = codes_f16(u, 0x4342);
-            const uint32_t a1 = codes_f16(v, 0x4140), a3 = codes_f16(v, 0x4342);
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int f = 0; f < Q2; ++f)
-                mma16816(sc[mt][nt], a0, a1, a2, a3, qf[nt][4 * j + e][0][f], qf[nt][4 * j + e][1][f]);
-          }
+              for (int e = 0; e < 4; ++e)
+                if (p0 + 16 * mt + g + (e & 2 ? 8 : 0) > lim[nt][e & 1] || sv[mt] < 0.f) sc[mt][nt][e] = -INFINITY;
         }
-      }
-
-      // exponents x, their running maximum, weights 2^(x - max + 14)
-      const int p0 = cc.t * kTile;
-      const bool masked = p0 + kTile - 1 > lim_min || sv[0] < 0.f || sv[1] < 0.f;
-      float lv[2], iv[2];
+        bool empty = false;
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const float v = fmaxf(sv[mt], kMinScale);
-        const float vn = sv[mt] == sv[mt] ? v : sv[mt];          // NaN stays NaN
-        lv[mt] = log2f(vn);
-        iv[mt] = kUnshift / vn;
-      }
-      uint32_t pb[2][NT][2][Q2];
-      float mnew[NT][2];
-      bool grows = false;
+        for (int nt = 0; nt < NT; ++nt) {
+          empty |= mx[nt][0] == -INFINITY || mx[nt][1] == -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float m0 = -INFINITY, m1 = -INFINITY;
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const float c0 = fac[nt][0] * sk[mt], c1 = fac[nt][1] * sk[mt];
+            for (int e = 0; e < 4; ++e) lead = fmaxf(lead, sc[mt][nt][e]);
+        }
+        // a weight too large for the shift, or a row without a maximum: take the
+        // tile's maxima in
+        if (__any_sync(0xffffffffu, lead > kShift + kLead || empty)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = fmaf(sc[mt][nt][e], (e & 1) ? c1 : c0, lv[mt]);
-            if (masked) {
-              const int p = p0 + 16 * mt + g + (e & 2 ? 8 : 0);
-              if (p > lim[nt][e & 1] || p >= cc.r.len || sv[mt] < 0.f) x = -INFINITY;
+          for (int nt = 0; nt < NT; ++nt) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              m0 = fmaxf(m0, fmaxf(sc[mt][nt][0], sc[mt][nt][2]));
+              m1 = fmaxf(m1, fmaxf(sc[mt][nt][1], sc[mt][nt][3]));
             }
-            sc[mt][nt][e] = x;
-            if (e & 1) m1 = fmaxf(m1, x);
-            else m0 = fmaxf(m0, x);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+              m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // how far the maximum moves; everything so far shrinks by as much
+              float d = (c ? m1 : m0) - kShift;
+              const bool none = mx[nt][c] == -INFINITY;
+              if (!none) d = fmaxf(d, 0.f);
+              if (d == -INFINITY) d = 0.f;               // still nothing
+              else mx[nt][c] = none ? d : mx[nt][c] + d;
+              const float f = none ? 0.f : ex2(-d);
+              sum_l[nt][c] *= f;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                acc[j][nt][c] *= f;
+                acc[j][nt][c + 2] *= f;
+              }
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                sc[mt][nt][c] -= d;
+                sc[mt][nt][c + 2] -= d;
+              }
+            }
           }
         }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-        }
-        mnew[nt][0] = fmaxf(mx[nt][0], m0);
-        mnew[nt][1] = fmaxf(mx[nt][1], m1);
-        grows |= mnew[nt][0] > mx[nt][0] || mnew[nt][1] > mx[nt][1];
-      }
-      if (__any_sync(0xffffffffu, grows)) {
+        // weights and their sums; the weights transposed, as fp16
+        uint32_t pb[2][NT][2][Q2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float f = mx[nt][c] == mnew[nt][c] ? 1.f : ex2(mx[nt][c] - mnew[nt][c]);
-            mx[nt][c] = mnew[nt][c];
-            sum_l[nt][c] *= f;
+          for (int mt = 0; mt < 2; ++mt) {
+            float w[4];
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-              acc[j][nt][c] *= f;
-              acc[j][nt][c + 2] *= f;
+            for (int e = 0; e < 4; ++e) w[e] = ex2(sc[mt][nt][e]);
+            const float s0 = w[0] + w[2], s1 = w[1] + w[3];
+            // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
+            sum_l[nt][0] = fmaf(s0, s0 > 0.f ? iv[mt] : 0.f, sum_l[nt][0]);
+            sum_l[nt][1] = fmaf(s1, s1 > 0.f ? iv[mt] : 0.f, sum_l[nt][1]);
+            if (sv[mt] < kMinScale) w[0] = w[1] = w[2] = w[3] = 0.f;
+            const uint32_t x0 = pack_f16(w[0], w[1]), x1 = pack_f16(w[2], w[3]);
+            pb[mt][nt][0][0] = transpose8(x0);
+            pb[mt][nt][1][0] = transpose8(x1);
+            if constexpr (F32) {
+              pb[mt][nt][0][1] = transpose8(rest_f16(x0, w[0], w[1]));
+              pb[mt][nt][1][1] = transpose8(rest_f16(x1, w[2], w[3]));
             }
           }
         }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float b0 = (mx[nt][0] == -INFINITY ? 0.f : mx[nt][0]) - kShift;
-        const float b1 = (mx[nt][1] == -INFINITY ? 0.f : mx[nt][1]) - kShift;
+
+        // O^T [D x 8 NT rows] += C_v^T w^T; lane g holds dimensions g * D/8 ...
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          float w[4];
+          constexpr int NW = D / 32;             // words of codes per token and lane
+          uint32_t v[4][NW];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(sc[mt][nt][e] - ((e & 1) ? b1 : b0));
-          const float s0 = w[0] + w[2], s1 = w[1] + w[3];
-          // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
-          sum_l[nt][0] = fmaf(s0, s0 > 0.f ? iv[mt] : 0.f, sum_l[nt][0]);
-          sum_l[nt][1] = fmaf(s1, s1 > 0.f ? iv[mt] : 0.f, sum_l[nt][1]);
-          const uint32_t x0 = pack_f16(w[0], w[1]), x1 = pack_f16(w[2], w[3]);
-          pb[mt][nt][0][0] = transpose8(x0);
-          pb[mt][nt][1][0] = transpose8(x1);
-          if constexpr (F32) {
-            pb[mt][nt][0][1] = transpose8(rest_f16(x0, w[0], w[1]));
-            pb[mt][nt][1][1] = transpose8(rest_f16(x1, w[2], w[3]));
+          for (int r = 0; r < 4; ++r) {
+            const int t = 16 * mt + 2 * tid + (r & 1) + (r & 2 ? 8 : 0);
+            if constexpr (NW == 2) {
+              const uint2 x = *reinterpret_cast<const uint2*>(vst + code_at<D>(t, g * (D / 8)));
+              v[r][0] = x.x; v[r][1] = x.y;
+            } else {
+#pragma unroll
+              for (int c = 0; c < NW / 4; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(vst + code_at<D>(t, g * (D / 8) + 16 * c));
+                v[r][4 * c] = x.x; v[r][4 * c + 1] = x.y; v[r][4 * c + 2] = x.z; v[r][4 * c + 3] = x.w;
+              }
+            }
           }
-        }
-      }
-
-      // O^T [D x 8 NT rows] += C_v^T w^T; lane g holds dimensions g * D/8 ...
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        constexpr int NW = D / 32;             // words of codes per token and lane
-        uint32_t v[4][NW];
+          for (int c = 0; c < NW; ++c) {
+            const uint32_t p = v[0][c] ^ 0x80808080u, q = v[1][c] ^ 0x80808080u;
+            const uint32_t r = v[2][c] ^ 0x80808080u, t = v[3][c] ^ 0x80808080u;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * mt + 2 * tid + (r & 1) + (r & 2 ? 8 : 0);
-          if constexpr (NW == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(vst + code_at<D>(t, g * (D / 8)));
-            v[r][0] = x.x; v[r][1] = x.y;
-          } else {
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t x = __byte_perm(p, q, half ? 0x7362 : 0x5140);    // token pairs side by side
+              const uint32_t y = __byte_perm(r, t, half ? 0x7362 : 0x5140);
+              const uint32_t a0 = codes_f16(x, 0x4140), a1 = codes_f16(x, 0x4342);
+              const uint32_t a2 = codes_f16(y, 0x4140), a3 = codes_f16(y, 0x4342);
 #pragma unroll
-            for (int c = 0; c < NW / 4; ++c) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vst + code_at<D>(t, g * (D / 8) + 16 * c));
-              v[r][4 * c] = x.x; v[r][4 * c + 1] = x.y; v[r][4 * c + 2] = x.z; v[r][4 * c + 3] = x.w;
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int f = 0; f < Q2; ++f)
+                  mma16816(acc[2 * c + half][nt], a0, a1, a2, a3, pb[mt][nt][0][f], pb[mt][nt][1][f]);
             }
           }
         }
-#pragma unroll
-        for (int c = 0; c < NW; ++c) {
-          const uint32_t p = v[0][c] ^ 0x80808080u, q = v[1][c] ^ 0x80808080u;
-          const uint32_t r = v[2][c] ^ 0x80808080u, t = v[3][c] ^ 0x80808080u;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t x = __byte_perm(p, q, half ? 0x7362 : 0x5140);    // token pairs side by side
-            const uint32_t y = __byte_perm(r, t, half ? 0x7362 : 0x5140);
-            const uint32_t a0 = codes_f16(x, 0x4140), a1 = codes_f16(x, 0x4342);
-            const uint32_t a2 = codes_f16(y, 0x4140), a3 = codes_f16(y, 0x4342);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int f = 0; f < Q2; ++f)
-                mma16816(acc[2 * c + half][nt], a0, a1, a2, a3, pb[mt][nt][0][f], pb[mt][nt][1][f]);
-          }
-        }
       }
-      __syncwarp();                            // every lane has read the stage
-      if (issued < n) {
-        issue(s, blk);
-        if (++issued < n) {
-          advance<kRows>(a, ci);
-          blk = load_block();
-        }
-      }
+      __syncwarp();                            // every lane has read the half: refill it
+      if (qi < 2 * n) issue(s);
       if (++s == S) { s = 0; ph ^= 1; }
 
-      const bool ends = cc.t + 1 == cc.nt;
-      if (ends || k + 1 == n) {
+      if ((ends || step + 1 == 2 * n) && !skip && (step & 1)) {
         float l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -582,17 +617,17 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             l[nt][c] = x;
           }
+        const int h = info.z & 0xFFFF;
         if (ends && seg_starts) {
           // all of the rows' tokens: the outputs, D/8 dimensions per lane and row
-          const int64_t rows = (int64_t)cc.r.q_len * a.group;
+          const int2 q = asked[warp];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int64_t R = cc.rt * kRows + nt * 8 + 2 * tid + c;
-              if (R < rows) {
-                const int64_t at = (cc.r.q0 + R / a.group) * a.ldo + ((int64_t)cc.h * a.group + R % a.group) * D +
-                                   g * (D / 8);
+              int64_t at;
+              if (row_at(a, q.x, q.y, info.y * kRows + nt * 8 + 2 * tid + c, h, a.ldo, D, &at)) {
+                at += g * (D / 8);
                 const float inv = inverse(l[nt][c]);
                 if constexpr (F32) {
                   float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
@@ -604,8 +639,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                   uint32_t u[KS];
 #pragma unroll
                   for (int j = 0; j < KS; ++j) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[j][nt][c] * inv, acc[j][nt][c + 2] * inv);
-                    u[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(acc[j][nt][c] * inv, acc[j][nt][c + 2] * inv);
+                    u[j] = *reinterpret_cast<const uint32_t*>(&h2);
                   }
                   uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
 #pragma unroll
@@ -615,10 +650,8 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               }
             }
         } else {
-          // a piece: the first one of the warp has a place of its own, the last
-          // one takes the warp's ring, which is not filled again
-          const int slot = first_seg ? 0 : 1;
-          float* dst = slot == 0 ? pieces + warp * C::kPiece : reinterpret_cast<float*>(ring);
+          const int slot = more_before ? 1 : 0;
+          float* dst = step + 1 == 2 * n ? reinterpret_cast<float*>(ring) : firsts + warp * C::kPiece;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -629,156 +662,194 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 *reinterpret_cast<float2*>(dst + row * D + g * (D / 8) + 2 * j) =
                     make_float2(acc[j][nt][c], acc[j][nt][c + 2]);
               if (g == 0) {
-                dst[kRows * D + row] = mx[nt][c];
-                dst[kRows * D + kRows + row] = l[nt][c];
+                piece_m[(2 * warp + slot) * kRows + row] = mx[nt][c];
+                piece_l[(2 * warp + slot) * kRows + row] = l[nt][c];
               }
             }
           if (lane == 0) {
             Tag& t = tags[2 * warp + slot];
-            t.rt = cc.rt; t.i = cc.i; t.h = cc.h;
-            t.starts = seg_starts; t.ends = ends; t.valid = 1;
+            t.i = info.x; t.rt = info.y; t.h = h; t.q0 = asked[warp].x; t.q_len = asked[warp].y;
+            t.starts = seg_starts; t.ends = ends; t.valid = step + 1 == 2 * n ? 1 : 2;
           }
         }
         fresh = true;
-        first_seg = false;
-        seg_starts = true;
+        more_before = true;
       }
-      if (k + 1 < n) advance<kRows>(a, cc);
     }
     if (dead) {
       // let the copies in flight land before the CTA ends
+#pragma unroll 1
       for (int i = 0; i < S; ++i) mbar_wait_bounded(bars + i, ph ^ (i < s ? 1u : 0u), kWaitCycles / 8);
     }
   }
   __syncthreads();
   if (threadIdx.x == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
 
-  // join the warps' pieces: runs of consecutive pieces of the same row tile
-  int* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
-  if (threadIdx.x < 2) meta[threadIdx.x * kTagInts] = 0;
+  // rows that no request owns
+  {
+    const int64_t cols = (int64_t)a.q_heads * D;
+#pragma unroll 1
+    for (int64_t t = (int64_t)max(q_end, 0) + blockIdx.x; t < a.total_q; t += gridDim.x)
+#pragma unroll 1
+      for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) store_out<F32>(a, t * a.ldo + c, 0.f);
+  }
+
+  // join the warps' pieces.  A run is the pieces of one row tile, which follow
+  // each other; lane e of every warp looks at piece e
+  const Tag mine = tags[lane < C::kEnds ? lane : 0];
+  const bool valid = lane < C::kEnds && mine.valid;
+  const uint32_t here = __ballot_sync(0xffffffffu, valid);
+  const uint32_t below = here & ((1u << lane) - 1);
+  const bool leads = valid && (below == 0 || mine.starts || !same(tags[31 - __clz(below)], mine));
+  const uint32_t lead_mask = __ballot_sync(0xffffffffu, leads);
+  // the same by number among the pieces that are there
+  const int rank = __popc(below), pieces = __popc(here), runs = __popc(lead_mask);
+  uint32_t leaders = __reduce_or_sync(0xffffffffu, leads ? 1u << rank : 0u);
+  if (warp == 0 && valid) order[rank] = lane;
   __syncthreads();
-  int e = 0;
-  while (e < 2 * kWarps) {
-    if (!tags[e].valid) { ++e; continue; }
-    const Tag head = tags[e];
-    int f = e + 1, last = e;
-    for (; f < 2 * kWarps; ++f) {
-      if (!tags[f].valid) continue;
-      if (!same(head, tags[f]) || tags[f].starts) break;
-      last = f;
+  auto run_begin = [&](int k) { return 31 - __clz(leaders & ((2u << k) - 1)); };      // of piece k's run
+  auto run_end = [&](int k) {
+    const uint32_t after = leaders & ~((2u << k) - 1);
+    return after ? __ffs(after) - 1 : pieces;
+  };
+  // each piece's weight against the run's maximum
+  for (int x = threadIdx.x; x < pieces * kRows; x += C::kThreads) {
+    const int k = x / kRows, row = x % kRows, end = run_end(k);
+    float M = -INFINITY;
+#pragma unroll 4
+    for (int p = run_begin(k); p < end; ++p) M = fmaxf(M, piece_m[order[p] * kRows + row]);
+    const float own = piece_m[order[k] * kRows + row];
+    piece_f[x] = own == M ? 1.f : ex2(own - M);
+  }
+  if (threadIdx.x < 2) {
+    // slot 0: a run without its beginning, the CTA's first; slot 1: one without its end, its last
+    Tag t = tags[0];
+    t.valid = 0;
+    if (pieces) {
+      const int last = pieces - 1, k = threadIdx.x == 0 ? 0 : run_begin(last);
+      t = tags[order[k]];
+      t.ends = tags[order[run_end(k) - 1]].ends;
+      t.valid = threadIdx.x == 0 ? !t.starts : t.starts && !t.ends;
     }
-    const bool ends = tags[last].ends;
-    // a piece with its beginning and its end here is an output; one that lacks
-    // its beginning is the CTA's first (slot 0), one that lacks its end its last
-    const bool whole = head.starts && ends;
-    const int slot = head.starts ? 1 : 0;
-    const Request r = load_request(a, head.i);
-    const int64_t rows = (int64_t)r.q_len * a.group;
-    float* gp = a.part + ((int64_t)blockIdx.x * 2 + slot) * C::kPiece;
-    for (int x = threadIdx.x; x < kRows * D / 4; x += C::kThreads) {
-      const int row = x / (D / 4), c = x % (D / 4);
-      float M = -INFINITY;
-      for (int p = e; p <= last; ++p)
-        if (tags[p].valid) {
-          const float* src = (p & 1) ? reinterpret_cast<const float*>(smem + (p >> 1) * S * C::kStageBytes)
-                                     : pieces + (p >> 1) * C::kPiece;
-          M = fmaxf(M, src[kRows * D + row]);
-        }
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
-      for (int p = e; p <= last; ++p)
-        if (tags[p].valid) {
-          const float* src = (p & 1) ? reinterpret_cast<const float*>(smem + (p >> 1) * S * C::kStageBytes)
-                                     : pieces + (p >> 1) * C::kPiece;
-          const float m = src[kRows * D + row];
-          const float f1 = m == M ? 1.f : ex2(m - M);
-          const float4 v = *reinterpret_cast<const float4*>(src + row * D + 4 * c);
-          l = fmaf(src[kRows * D + kRows + row], f1, l);
-          o.x = fmaf(v.x, f1, o.x); o.y = fmaf(v.y, f1, o.y);
-          o.z = fmaf(v.z, f1, o.z); o.w = fmaf(v.w, f1, o.w);
-        }
-      if (whole) {
-        const int64_t R = head.rt * kRows + row;
-        if (R < rows) {
-          const int64_t at = (r.q0 + R / a.group) * a.ldo + ((int64_t)head.h * a.group + R % a.group) * D + 4 * c;
-          const float inv = inverse(l);
-          store_out<F32>(a, at, o.x * inv);
-          store_out<F32>(a, at + 1, o.y * inv);
-          store_out<F32>(a, at + 2, o.z * inv);
-          store_out<F32>(a, at + 3, o.w * inv);
-        }
-      } else {
-        *reinterpret_cast<float4*>(gp + row * D + 4 * c) = o;
-        if (c == 0) {
-          gp[kRows * D + row] = M;
-          gp[kRows * D + kRows + row] = l;
-        }
+    a.meta[2 * blockIdx.x + threadIdx.x] = t;
+  }
+  __syncthreads();
+  constexpr int kItems = kRows * D / 4;
+  for (int x = threadIdx.x; x < runs * kItems; x += C::kThreads) {
+    int k0 = 0;                                // the run's first piece
+    {
+      uint32_t m = leaders;
+      for (int r = x / kItems; r > 0; --r) m &= m - 1;
+      k0 = __ffs(m) - 1;
+    }
+    const int row = x % kItems / (D / 4), c = x % (D / 4), end = run_end(k0);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, M = -INFINITY;
+#pragma unroll 4
+    for (int k = k0; k < end; ++k) {
+      const int p = order[k];
+      const float* src = tags[p].valid == 2 ? firsts + (p >> 1) * C::kPiece
+                                            : reinterpret_cast<const float*>(smem + (p >> 1) * S * C::kHalfBytes);
+      const float f = piece_f[k * kRows + row];
+      const float4 v = *reinterpret_cast<const float4*>(src + row * D + 4 * c);
+      M = fmaxf(M, piece_m[p * kRows + row]);
+      l = fmaf(piece_l[p * kRows + row], f, l);
+      o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+    }
+    const Tag& head = tags[order[k0]];
+    if (head.starts && tags[order[end - 1]].ends) {
+      int64_t at;
+      if (row_at(a, head.q0, head.q_len, head.rt * kRows + row, head.h, a.ldo, D, &at))
+        store_out4<F32>(a, at + 4 * c, o, inverse(l));
+    } else {
+      float* gp = a.part + ((int64_t)blockIdx.x * 2 + (head.starts ? 1 : 0)) * C::kPiece;
+      *reinterpret_cast<float4*>(gp + row * D + 4 * c) = o;
+      if (c == 0) {
+        gp[kRows * D + row] = M;
+        gp[kRows * D + kRows + row] = l;
       }
     }
-    if (!whole && threadIdx.x == 0) {
-      int* t = meta + slot * kTagInts;
-      t[0] = 1; t[1] = head.starts; t[2] = ends; t[3] = head.i; t[4] = head.h;
-      t[5] = (int)(head.rt & 0xffffffff); t[6] = (int)(head.rt >> 32);
-    }
-    e = f;
   }
 }
 
 // Row tiles whose tokens fall to several CTAs: block c merges the pieces that
-// CTAs c, c + 1, ... hold of the row tile that begins in CTA c.
+// CTAs c, c + 1, ... hold of the row tile that begins in CTA c.  Thread groups
+// take every kGroups-th piece, so that a few loads in flight cover them all,
+// and are joined through shared memory in their order.
+constexpr int kMergeThreads = 1024;
+
 template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ Args a, int ctas) {
-  using C = Cfg<D, NT>;
-  constexpr int kRows = C::kRows;
+__global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_constant__ Args a, int ctas) {
+  using C = Cfg<D, NT, F32>;
+  constexpr int kRows = C::kRows, kItems = kRows * D / 4, kGroups = kMergeThreads / kItems;
+  __shared__ int first_end;
+  __shared__ float4 so[kGroups][kItems];
+  __shared__ float sm[kGroups][kItems], sl[kGroups][kItems];
+  if (threadIdx.x == 0) first_end = ctas;
   pdl_wait();
   pdl_launch();
-  const int* head = a.meta + (int64_t)blockIdx.x * kMetaInts + kTagInts;
-  if (!head[0]) return;
-  // the CTAs after this one that hold more of the same row tile
-  int n = 1;
-  while (blockIdx.x + n < ctas) {
-    const int* t = a.meta + (int64_t)(blockIdx.x + n) * kMetaInts;
-    if (!t[0]) break;
-    ++n;
-    if (t[2]) break;
+  // this CTA's open run; the CTAs after it that hold more of the same row tile:
+  // up to the first that has none or ends it
+  const Tag head = a.meta[2 * blockIdx.x + 1];
+  const int other = blockIdx.x + 1 + threadIdx.x;
+  int valid = 0, ends = 0;
+  if (other < ctas) {
+    valid = a.meta[2 * other].valid;
+    ends = a.meta[2 * other].ends;
   }
-  const Request r = load_request(a, head[3]);
-  const int h = head[4];
-  const int64_t rt = (int64_t)(uint32_t)head[5] | (int64_t)head[6] << 32;
-  const int64_t rows = (int64_t)r.q_len * a.group;
+  if (!head.valid) return;
+  __syncthreads();
+  if (!valid) atomicMin(&first_end, (int)threadIdx.x);
+  else if (ends) atomicMin(&first_end, (int)threadIdx.x + 1);
+  __syncthreads();
+  const int n = 1 + first_end;
   const float* first = a.part + ((int64_t)blockIdx.x * 2 + 1) * C::kPiece;
   const float* next = first + C::kPiece;                 // slot 0 of the CTA after, then every second piece
-  for (int x = threadIdx.x; x < kRows * D / 4; x += 256) {
-    const int row = x / (D / 4), c = x % (D / 4);
-    const int64_t R = rt * kRows + row;
-    if (R >= rows) continue;
-    float M = first[kRows * D + row];
-    for (int p = 1; p < n; ++p) M = fmaxf(M, next[(int64_t)(p - 1) * 2 * C::kPiece + kRows * D + row]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const float* src = p == 0 ? first : next + (int64_t)(p - 1) * 2 * C::kPiece;
-      const float m = src[kRows * D + row];
-      const float f = m == M ? 1.f : ex2(m - M);
-      const float4 v = *reinterpret_cast<const float4*>(src + row * D + 4 * c);
-      l = fmaf(src[kRows * D + kRows + row], f, l);
-      o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+  const int x = threadIdx.x % kItems, grp = threadIdx.x / kItems;
+  const int row = x / (D / 4), c = x % (D / 4);
+  float M = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float m, float lp, const float4& v) {
+    const float Mn = fmaxf(M, m);
+    const float f0 = M == Mn ? 1.f : ex2(M - Mn), f1 = m == Mn ? 1.f : ex2(m - Mn);
+    M = Mn;
+    l = fmaf(l, f0, lp * f1);
+    o.x = fmaf(o.x, f0, v.x * f1); o.y = fmaf(o.y, f0, v.y * f1);
+    o.z = fmaf(o.z, f0, v.z * f1); o.w = fmaf(o.w, f0, v.w * f1);
+  };
+  for (int p0 = grp; p0 < n; p0 += 4 * kGroups) {
+    float m[4], lp[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = p0 + k * kGroups;
+      if (p < n) {
+        const float* src = p == 0 ? first : next + (int64_t)(p - 1) * 2 * C::kPiece;
+        m[k] = src[kRows * D + row];
+        lp[k] = src[kRows * D + kRows + row];
+        v[k] = *reinterpret_cast<const float4*>(src + row * D + 4 * c);
+      }
     }
-    const int64_t at = (r.q0 + R / a.group) * a.ldo + ((int64_t)h * a.group + R % a.group) * D + 4 * c;
-    const float inv = inverse(l);
-    store_out<F32>(a, at, o.x * inv);
-    store_out<F32>(a, at + 1, o.y * inv);
-    store_out<F32>(a, at + 2, o.z * inv);
-    store_out<F32>(a, at + 3, o.w * inv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (p0 + k * kGroups < n) add(m[k], lp[k], v[k]);
+  }
+  so[grp][x] = o;
+  sm[grp][x] = M;
+  sl[grp][x] = l;
+  __syncthreads();
+  int64_t at;
+  if (grp == 0 && row_at(a, head.q0, head.q_len, head.rt * kRows + row, head.h, a.ldo, D, &at)) {
+    for (int k = 1; k < kGroups; ++k) add(sm[k][x], sl[k][x], so[k][x]);
+    store_out4<F32>(a, at + 4 * c, o, inverse(l));
   }
 }
 
 template <int D, int NT, bool F32>
-lq_status launch_split(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, int sms, void* stream) {
-  using C = Cfg<D, NT>;
-  static_assert(C::kStages >= 2 && C::kSmem + 640 <= 227 * 1024, "shared memory");
-  static_assert(C::kStages * C::kStageBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
+lq_status launch_split(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, int ctas, void* stream) {
+  using C = Cfg<D, NT, F32>;
+  static_assert(C::kHalves >= 3 && C::kSmem + 1536 <= 227 * 1024, "shared memory");
+  static_assert(C::kHalves * C::kHalfBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
   static_assert(C::kRing >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
   auto kern = attn_split_kernel<D, NT, F32>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
@@ -792,14 +863,14 @@ lq_status launch_split(const Args& a, const CUtensorMap& mk, const CUtensorMap& 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = (cudaStream_t)stream;
-  cfg.gridDim = dim3(sms);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mv, a);
   if (e == cudaSuccess) {
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, attn_merge_kernel<D, NT, F32>, a, sms);
+    e = cudaLaunchKernelEx(&cfg, attn_merge_kernel<D, NT, F32>, a, ctas);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -821,9 +892,10 @@ bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int rows) 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count_or_default() {
+// One CTA per SM; the merge looks at all of them with one thread each.
+int cta_count() {
   const int sms = device_sm_count();
-  return sms > 0 ? sms : 152;
+  return sms <= 0 ? 152 : sms < kMergeThreads ? sms : kMergeThreads;
 }
 
 }  // namespace attn
@@ -836,10 +908,11 @@ extern "C" size_t lq_attention_paged_workspace_size(int batch, int64_t total_q, 
   if (batch < 0 || batch > LQ_MAX_REQUESTS || total_q < 0 || kv_heads <= 0 || q_heads <= 0 ||
       q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  // two pieces of up to 16 rows per CTA, and what they belong to
-  const size_t ctas = (size_t)attn::sm_count_or_default();
-  const size_t meta = (ctas * attn::kMetaInts * sizeof(int) + 255) & ~(size_t)255;
-  return meta + ctas * 2 * 16 * (size_t)(head_dim + 2) * sizeof(float);
+  // per CTA two pieces and what they belong to, and one for each of up to 16
+  // warps, of up to 16 rows
+  const size_t ctas = (size_t)attn::cta_count();
+  const size_t meta = (ctas * 2 * sizeof(attn::Tag) + 255) & ~(size_t)255;
+  return meta + ctas * (2 + 16) * 16 * (size_t)(head_dim + 2) * sizeof(float);
 }
 
 extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtype, int64_t total_q,
@@ -863,6 +936,7 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   // rows of 128 bytes of codes are counted in 32 bits (a pool of 256 GB for K alone)
   const int64_t block_rows = (int64_t)kv_heads * block_size * head_dim / 128;
   if (num_blocks > INT32_MAX / block_rows) return LQ_ERR_SHAPE;
+  if (total_q > INT32_MAX / q_heads) return LQ_ERR_SHAPE;       // query rows are counted in 32 bits
   if (!(fabsf(sm_scale) <= 3.402823466e38f)) return LQ_ERR_ARG;
   if (total_q == 0) return LQ_OK;
   if (batch == 0) return LQ_ERR_SHAPE;
@@ -885,8 +959,9 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   a.ks = k_scales_dev; a.vs = v_scales_dev; a.num_blocks = num_blocks;
   a.log2_bs = serve::log2_of(block_size); a.q_heads = q_heads; a.kv_heads = kv_heads; a.group = q_heads / kv_heads;
   a.scale_log2 = sm_scale * 1.4426950408889634f; a.out = out_dev; a.ldo = ldo; a.status = dev_status_dev;
-  a.meta = reinterpret_cast<int*>(workspace_dev);
-  const size_t meta = ((size_t)sms * attn::kMetaInts * sizeof(int) + 255) & ~(size_t)255;
+  a.meta = reinterpret_cast<attn::Tag*>(workspace_dev);
+  const int ctas = attn::cta_count();
+  const size_t meta = ((size_t)ctas * 2 * sizeof(attn::Tag) + 255) & ~(size_t)255;
   a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + meta);
   CUtensorMap mk, mv;
   // a pool without blocks: no copy is issued, any valid map will do
@@ -898,13 +973,13 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   // eight query rows per pass over the codes, sixteen where the average request has more
   const bool few = ((total_q + batch - 1) / batch) * a.group <= 8;
   if (dtype == LQ_F32) {
-    if (head_dim == 64) return attn::launch_split<64, 1, true>(a, mk, mv, sms, stream);
-    if (head_dim == 128) return attn::launch_split<128, 1, true>(a, mk, mv, sms, stream);
-    return attn::launch_split<256, 1, true>(a, mk, mv, sms, stream);
+    if (head_dim == 64) return attn::launch_split<64, 1, true>(a, mk, mv, ctas, stream);
+    if (head_dim == 128) return attn::launch_split<128, 1, true>(a, mk, mv, ctas, stream);
+    return attn::launch_split<256, 1, true>(a, mk, mv, ctas, stream);
   }
-  if (head_dim == 256) return attn::launch_split<256, 1, false>(a, mk, mv, sms, stream);
-  if (head_dim == 64) return few ? attn::launch_split<64, 1, false>(a, mk, mv, sms, stream)
-                                 : attn::launch_split<64, 2, false>(a, mk, mv, sms, stream);
-  return few ? attn::launch_split<128, 1, false>(a, mk, mv, sms, stream)
-             : attn::launch_split<128, 2, false>(a, mk, mv, sms, stream);
+  if (head_dim == 256) return attn::launch_split<256, 1, false>(a, mk, mv, ctas, stream);
+  if (head_dim == 64) return few ? attn::launch_split<64, 1, false>(a, mk, mv, ctas, stream)
+                                 : attn::launch_split<64, 2, false>(a, mk, mv, ctas, stream);
+  return few ? attn::launch_split<128, 1, false>(a, mk, mv, ctas, stream)
+             : attn::launch_split<128, 2, false>(a, mk, mv, ctas, stream);
 }

@@ -14,6 +14,14 @@
 namespace lq {
 namespace attn {
 
+// What a piece of a row tile belongs to: request (its first query token and
+// how many it has), row tile, kv head, and whether the piece begins or ends the
+// tile's tokens.  valid: 0 no piece, 1 in its warp's ring, 2 in global memory.
+struct Tag {
+  int i, rt, h, q0, q_len;
+  int valid, starts, ends;
+};
+
 struct Args {
   const void* q;
   int64_t ldq;
@@ -32,22 +40,37 @@ struct Args {
   void* out;
   int64_t ldo;
   float* part;               // partial results of the CTAs
-  int* meta;                 // and what they belong to
+  Tag* meta;                 // and what they belong to, two for each CTA
   int32_t* status;
 };
 
 constexpr long long kWaitCycles = 2000000000ll;   // about one second
-// Value scales below this count as this (a block of zeros has scale 0): their
-// logarithm stays finite, and a value of 2^-120 vanishes against any other.
-constexpr float kMinScale = 7.52316385e-37f;      // 2^-120
-// Softmax weights are held times 2^14: weights down to 2^-28 of the largest
-// are then normal fp16 numbers, and the largest, 2^14, is in range.
-constexpr float kShift = 14.f;
-constexpr float kUnshift = 6.103515625e-5f;       // 2^-14
+// Value scales below 2^-100 count as zero (a block of zeros has scale 0): their
+// tokens take part in the sum of weights at 2^-100, so that the logarithm stays
+// finite, and not in the values' sum.  Sums of weight / scale are held times
+// 2^-20, between 2^80 per weight for such scales and normal numbers up to 2^106.
+constexpr float kMinScale = 7.88860905e-31f;      // 2^-100
+constexpr float kSumUnit = 9.5367431640625e-7f;   // 2^-20
+// Softmax weights are held times 2^8 relative to the running maximum, and the
+// maximum may be behind by up to 2^7: the largest is then 2^15, in fp16's
+// range, and weights down to 2^-22 of the maximum are normal numbers.
+constexpr float kShift = 8.f;
+constexpr float kLead = 7.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 

@@ -594,10 +594,20 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               const uint32_t a0 = codes_f16(x, 0x4140), a1 = codes_f16(x, 0x4342);
               const uint32_t a2 = codes_f16(y, 0x4140), a3 = codes_f16(y, 0x4342);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt) {
+                float (&o)[4] = acc[2 * c + half][nt];
+                if constexpr (F32) {
+                  // the matrix unit truncates its sums: over thousands of
+                  // positions that would be a bias, so they are added here
+                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(d, a0, a1, a2, a3, pb[mt][nt][0][1], pb[mt][nt][1][1]);
+                  mma16816(d, a0, a1, a2, a3, pb[mt][nt][0][0], pb[mt][nt][1][0]);
 #pragma unroll
-                for (int f = 0; f < Q2; ++f)
-                  mma16816(acc[2 * c + half][nt], a0, a1, a2, a3, pb[mt][nt][0][f], pb[mt][nt][1][f]);
+                  for (int e = 0; e < 4; ++e) o[e] += d[e];
+                } else {
+                  mma16816(o, a0, a1, a2, a3, pb[mt][nt][0][0], pb[mt][nt][1][0]);
+                }
+              }
             }
           }
         }
@@ -970,8 +980,10 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   const int64_t bytes = num_blocks > 0 ? num_blocks * block_rows * 128 : 4096;
   const int box = (block_size < attn::kTile ? block_size : attn::kTile) * head_dim / 128;
   if (!attn::encode_cache(&mk, kc, bytes, box) || !attn::encode_cache(&mv, vc, bytes, box)) return LQ_ERR_CUDA;
+  const int64_t avg_rows = ((total_q + batch - 1) / batch) * a.group;
+  if (avg_rows > 64 && dtype == LQ_BF16) return attn::launch_attn_tiles(a, k_cache_dev, v_cache_dev, head_dim, stream);
   // eight query rows per pass over the codes, sixteen where the average request has more
-  const bool few = ((total_q + batch - 1) / batch) * a.group <= 8;
+  const bool few = avg_rows <= 8;
   if (dtype == LQ_F32) {
     if (head_dim == 64) return attn::launch_split<64, 1, true>(a, mk, mv, ctas, stream);
     if (head_dim == 128) return attn::launch_split<128, 1, true>(a, mk, mv, ctas, stream);

@@ -112,5 +112,8 @@ __device__ __forceinline__ Request load_request(const Args& a, int i) {
   return r;
 }
 
+// The kernel for many query rows (lq_attn_paged_tiles.cu).
+lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int head_dim, void* stream);
+
 }  // namespace attn
 }  // namespace lq

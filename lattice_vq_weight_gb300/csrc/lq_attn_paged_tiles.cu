@@ -1,0 +1,574 @@
+// Paged attention for many query rows per kv head (prompts and chunks of
+// them), on the 5th-generation tensor cores.
+//
+// The formulas are those of lq_attn_paged.cu.  With hundreds of rows per code
+// the matrix products bound the work (4 head_dim flops per row and position),
+// so here a CTA takes 128 query rows of one kv head and walks the positions
+// they see in tiles of 128 (64 for head_dim 256):
+//     S = Q C_k^T     tcgen05.mma, both operands in shared memory, S in TMEM
+//     W = 2^(x - max) by one thread per row, straight from and back into TMEM:
+//                     the fp16 weights take the columns of the scores they
+//                     were made from
+//     O += W C_v      tcgen05.mma with W from TMEM, O in TMEM
+// Warps 0..3 fetch codes (global memory to registers, a tile ahead) and
+// write them to shared memory as fp16, exactly; warps 4..7 hold the rows'
+// maxima and sums; warp 8 issues the products.  K and V tiles have the same
+// layout, rows of 64 dimensions in the 128-byte swizzle, which the products
+// read along either axis (K-major for the scores, MN-major for the values).
+// The steps of one CTA follow each other; two CTAs share an SM (head_dim 64
+// and 128), so that one's products run under the other's exponentials,
+// with the 512 columns of TMEM and the shared memory split between them.
+//
+// As in the split kernel the running maximum may lag by 2^7, so that O is
+// rescaled (TMEM to registers and back) only when a row's maximum really
+// moves.  bf16 only: the tensor core's accumulator truncates, 6e-5 of the
+// output after 30000 positions (measured), which fp32 outputs would show; they
+// stay with the split kernel at any number of rows.  Every wait is bounded (about a second of clock cycles); on expiry
+// LQ_DEV_TIMEOUT is recorded and the CTA winds down.
+#include "lq_attn_paged.cuh"
+
+namespace lq {
+namespace attn {
+
+constexpr int kTileRows = 128;
+
+template <int D>
+struct TileCfg {
+  static constexpr int BN = D == 256 ? 64 : 128;            // tokens per tile
+  static constexpr int kSub = D / 64;                       // 64-dimension sub-tiles
+  static constexpr int kQBytes = kTileRows * D * 2;
+  static constexpr int kCodeBytes = BN * D * 2;             // a K or V tile as fp16
+  static constexpr int kSmem = kQBytes + 2 * kCodeBytes + 1024;
+  static constexpr uint32_t kCols = BN + D <= 256 ? 256 : 512;
+  static constexpr int kPerSm = kCols == 256 ? 2 : 1;
+  static constexpr int kThreads = 288;
+  // rows of codes that the 128 fetching threads take in one pass (4 lanes
+  // of 16 codes for each 64 dimensions), and passes per tile
+  static constexpr int kPassRows = 32 / kSub;
+  static constexpr int kPasses = BN / kPassRows;
+};
+
+struct TileArgs {
+  Args a;
+  const int8_t* kc;
+  const int8_t* vc;
+};
+
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+  // 128-byte swizzle, 8-row atoms of 1024 bytes one after the other
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t sub_stride) {
+  // the same atoms read along their rows: 64 columns per atom, the next 64
+  // sub_stride bytes further, the next 8 tokens 1024 bytes further
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((sub_stride >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor: D f32, A and B f16, M = 128; B along its rows when mn.
+template <int N, bool MN>
+struct Idesc {
+  static constexpr uint32_t v =
+      (1u << 4) | ((MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Bounded wait; false when the limit expired or another thread recorded that.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* timeout) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity)) {
+    if (*timeout) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *timeout = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::kThreads, TileCfg<D>::kPerSm)
+attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
+  using C = TileCfg<D>;
+  constexpr int BN = C::BN;
+  const Args& a = ta.a;
+  extern __shared__ uint8_t tiles_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tiles_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = smem;                                       // the query rows
+  uint8_t* sk = sq + C::kQBytes;
+  uint8_t* sv = sk + C::kCodeBytes;
+  __shared__ uint64_t k_full, v_full, s_full, p_full, o_done, q_full, drain;
+  __shared__ uint32_t tmem_base;
+  __shared__ int timeout_flag, found[2];
+  __shared__ int wsum[C::kThreads / 32];
+  volatile int* timeout = &timeout_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_wait();
+  pdl_launch();
+  if (threadIdx.x == 0) {
+    mbar_init1(&k_full, 4);                                 // one arrival per fetching warp
+    mbar_init1(&v_full, 4);
+    mbar_init1(&s_full, 1);                                 // scores computed: S readable, the K tile free
+    mbar_init1(&p_full, 4);                                 // one arrival per softmax warp
+    mbar_init1(&o_done, 1);                                 // values added: O readable, W and the V tile free
+    mbar_init1(&q_full, 4);
+    mbar_init1(&drain, 1);
+    mbar_init_fence();
+    timeout_flag = 0;
+    found[0] = -1;
+  }
+
+  // rows that no request owns
+  {
+    const int64_t end = max(__ldg(a.cu_q + a.batch), 0), cols = (int64_t)a.q_heads * D;
+    for (int64_t t = end + blockIdx.x; t < a.total_q; t += gridDim.x)
+      for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) {
+        reinterpret_cast<uint16_t*>(a.out)[t * a.ldo + c] = 0;
+      }
+  }
+
+  // this CTA's request and row tile, the last rows first: they see the most
+  const int h = blockIdx.x % a.kv_heads, item = blockIdx.x / a.kv_heads;
+  {
+    const int per = (a.batch + C::kThreads - 1) / C::kThreads;
+    const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
+    auto tiles_of = [&](int i) {
+      const Request r = load_request(a, i);
+      return (r.q_len * a.group + kTileRows - 1) / kTileRows;
+    };
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) {
+      if (blockIdx.x == 0 && (int64_t)__ldg(a.kv_lens + i) > ((int64_t)a.width << a.log2_bs))
+        raise_flag(a.status, LQ_DEV_RANGE);
+      sum += tiles_of(i);
+    }
+    int inc = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) inc += wsum[w];
+    int begin = inc - sum;
+    if (item >= begin && item < inc) {
+      for (int i = i0; i < i1; ++i) {
+        const int n = tiles_of(i);
+        if (item < begin + n) {
+          found[0] = i;
+          found[1] = begin + n - 1 - item;
+          break;
+        }
+        begin += n;
+      }
+    }
+    __syncthreads();
+  }
+  if (found[0] < 0) return;                                 // fewer row tiles than CTAs
+  const int req = found[0], row0 = found[1] * kTileRows;
+  const Request r = load_request(a, req);
+  const int rows = r.q_len * a.group;
+  // tokens that the last row sees, and tiles of them
+  const int last_j = min(row0 + kTileRows, rows) - 1;
+  const int seen = min(r.len, r.shown + last_j / a.group + 1);
+  const int tiles = seen > 0 ? (seen + BN - 1) / BN : 0;
+  const int32_t* table = a.table + (int64_t)req * a.ldt;
+
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_addr(&tmem_base)), "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + BN;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ codes to fp16
+    const int t = threadIdx.x, c4 = t & 3, sub = t / (4 * C::kPassRows), r0 = (t >> 2) % C::kPassRows;
+    const int col = 64 * sub + 16 * c4;
+    const int off_mask = (1 << a.log2_bs) - 1;
+    int64_t at[C::kPasses];                                 // where the thread's rows of a tile lie, -1: nowhere
+    auto locate = [&](int j) {
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int pos = j * BN + p * C::kPassRows + r0;
+        const int blk = pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
+        const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+        if (!ok && pos < seen && c4 == 0 && sub == 0) raise_flag(a.status, LQ_DEV_RANGE);
+        at[p] = ok ? (((((int64_t)blk * a.kv_heads + h) << a.log2_bs) + (pos & off_mask)) * D + col) : -1;
+      }
+    };
+    auto load = [&](const int8_t* cache, uint4 (&x)[C::kPasses]) {
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p)
+        x[p] = at[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + at[p])) : make_uint4(0, 0, 0, 0);
+    };
+    auto store = [&](uint8_t* dst, const uint4 (&x)[C::kPasses]) {
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int row = p * C::kPassRows + r0;
+        uint8_t* line = dst + sub * BN * 128 + row * 128;
+        const uint32_t w[4] = {x[p].x ^ 0x80808080u, x[p].y ^ 0x80808080u, x[p].z ^ 0x80808080u, x[p].w ^ 0x80808080u};
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          o[2 * q] = codes_f16(w[q], 0x4140);
+          o[2 * q + 1] = codes_f16(w[q], 0x4342);
+        }
+        *reinterpret_cast<uint4*>(line + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(line + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    uint4 kx[C::kPasses], vx[C::kPasses];
+    if (tiles > 0) {
+      locate(0);
+      load(ta.kc, kx);
+      load(ta.vc, vx);
+    }
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t prev = (uint32_t)(j - 1) & 1;
+      if (j > 0 && !__all_sync(0xffffffffu, wait_on(&s_full, prev, timeout))) break;
+      store(sk, kx);
+      if (lane == 0) arrive(&k_full);
+      if (j + 1 < tiles) {
+        locate(j + 1);
+        load(ta.kc, kx);
+      }
+      if (j > 0 && !__all_sync(0xffffffffu, wait_on(&o_done, prev, timeout))) break;
+      store(sv, vx);
+      if (lane == 0) arrive(&v_full);
+      if (j + 1 < tiles) load(ta.vc, vx);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t qa = smem_addr(sq), ka = smem_addr(sk), va = smem_addr(sv);
+      bool ok = tiles == 0 || wait_on(&q_full, 0, timeout);
+      for (int j = 0; j < tiles && ok; ++j) {
+        const uint32_t ph = (uint32_t)j & 1;
+        ok = wait_on(&k_full, ph, timeout);
+        if (!ok) break;
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t in = (uint32_t)((k & 3) * 32);
+          mma_ss(tmem_s, desc_k_major(qa + (k >> 2) * kTileRows * 128 + in),
+                 desc_k_major(ka + (k >> 2) * BN * 128 + in), Idesc<BN, false>::v, k > 0);
+        }
+        mma_commit(&s_full);
+        ok = wait_on(&v_full, ph, timeout) && wait_on(&p_full, ph, timeout);
+        if (!ok) break;
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_ts(tmem_o, tmem_s + (k >> 1) * 32 + (k & 1) * 8,
+                 desc_mn_major(va + k * 2048, C::kSub > 1 ? BN * 128 : 1024), Idesc<D, true>::v, j > 0 || k > 0);
+        mma_commit(&o_done);
+        // the next scores overwrite the weights' columns
+        ok = wait_on(&o_done, ph, timeout);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int R = row0 + row, j_tok = R / a.group;
+    const bool mine = R < rows;
+    const int head = h * a.group + R - j_tok * a.group;
+    const int lim = mine ? min(r.shown + j_tok, r.len - 1) : r.len - 1;     // last position the row sees
+    const int lim_min = min(r.shown + row0 / a.group, r.len - 1);           // of the tile's first row
+
+    // the query row as fp16, times a power of two that brings its largest
+    // value to [2^13, 2^14) and the sign of the scale
+    float fac;
+    {
+      const int64_t src = (int64_t)(r.q0 + j_tok) * a.ldq + (int64_t)head * D;
+      auto load8 = [&](int c, float (&v)[8]) {
+        if (!mine) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        } else {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + src + 8 * c));
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(u[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+          }
+        }
+      };
+      float top = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        float v[8];
+        load8(c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+      }
+      const int eb = (int)(__float_as_uint(top) >> 23);
+      const int ex = min(126, max(-116, 140 - eb));
+      float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+      if (a.scale_log2 < 0.f) up = -up;
+      fac = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll 2
+      for (int c = 0; c < D / 8; ++c) {
+        float v[8];
+        load8(c, v);
+        uint32_t hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[e] = pack_f16(v[2 * e] * up, v[2 * e + 1] * up);
+        uint8_t* line = sq + (c >> 3) * kTileRows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(&q_full);
+    }
+
+    // lane g < BN / 16: the scales of the tile's g-th 16 tokens, a tile ahead;
+    // value scale -1: a block that is not there
+    float nk = 0.f, nv = -1.f;
+    auto fetch_scales = [&](int j) {
+      const int pos = j * BN + 16 * lane;
+      nk = 0.f;
+      nv = -1.f;
+      if (lane < BN / 16 && pos < seen) {
+        const int blk = __ldg(table + (pos >> a.log2_bs));
+        if ((unsigned)blk < (unsigned long long)a.num_blocks) {
+          nk = __ldg(a.ks + (int64_t)blk * a.kv_heads + h);
+          nv = __ldg(a.vs + (int64_t)blk * a.kv_heads + h);
+        }
+      }
+    };
+    if (tiles > 0) fetch_scales(0);
+    float mx = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t ph = (uint32_t)j & 1;
+      // per 16 tokens: key scale, log2 and reciprocal of the value scale
+      const float ck = nk, cv = nv;
+      const float cvm = cv < kMinScale ? kMinScale : cv;    // NaN stays NaN
+      const float clv = lg2(cvm), civ = rcp(cvm) * kSumUnit;
+      const uint32_t gone = __ballot_sync(0xffffffffu, cv < 0.f), zero = __ballot_sync(0xffffffffu, cv < kMinScale);
+      if (j + 1 < tiles) fetch_scales(j + 1);
+      const int p0 = j * BN;
+      const bool masked = p0 + BN - 1 > lim_min || (gone & ((1u << (BN / 16)) - 1));
+      ok = __all_sync(0xffffffffu, wait_on(&s_full, ph, timeout));
+      if (!ok) break;
+      tc_after();
+      __syncwarp();
+
+      // the row's largest exponent in this tile
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t s[32];
+        tmem_ld32(tmem_s + lanes + 32 * c, s);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int g = 2 * c + half;
+          const float k = fac * __shfl_sync(0xffffffffu, ck, g), d = __shfl_sync(0xffffffffu, clv, g);
+          float m = -INFINITY;
+          if (!masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, __uint_as_float(s[16 * half + e]));
+          } else if (!(gone >> g & 1)) {
+            const int vis = lim - (p0 + 16 * g);            // elements 0 .. vis are seen
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e <= vis) m = fmaxf(m, __uint_as_float(s[16 * half + e]));
+          }
+          // (a group without a seen token adds nothing, whatever its scales)
+          if (m != -INFINITY) top = fmaxf(top, fmaf(m, k, d));
+        }
+      }
+      if (__any_sync(0xffffffffu, top > mx + kLead)) {
+        // the maximum moves: the sum and the output so far shrink
+        const bool moves = top > mx + kLead;
+        const float f = moves ? ex2(mx - top) : 1.f;
+        if (moves) mx = top;
+        l *= f;
+        if (j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem_o + lanes + 32 * c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(tmem_o + lanes + 32 * c, o);
+            tmem_st16(tmem_o + lanes + 32 * c + 16, o + 16);
+          }
+          tmem_wait_st();
+        }
+      }
+      const float base = kShift - (mx == -INFINITY ? 0.f : mx);
+      // weights, in place of the scores they are made from
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t s[32];
+        tmem_ld32(tmem_s + lanes + 32 * c, s);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int g = 2 * c + half;
+          const float k = fac * __shfl_sync(0xffffffffu, ck, g), d = __shfl_sync(0xffffffffu, clv, g) + base;
+          const float iv = __shfl_sync(0xffffffffu, civ, g);
+          const int vis = !masked ? 15 : (gone >> g & 1) ? -1 : lim - (p0 + 16 * g);
+          float sum = 0.f, sum2 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float w = ex2(fmaf(__uint_as_float(s[16 * half + e]), k, d));
+            if (masked) w = e <= vis ? w : 0.f;
+            if (e & 1) sum2 += w;
+            else sum += w;
+            s[16 * half + e] = __float_as_uint(w);
+          }
+          sum += sum2;
+          // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
+          l = fmaf(sum, sum > 0.f ? iv : 0.f, l);
+          if (zero >> g & 1) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[16 * half + e] = 0u;
+          }
+        }
+        uint32_t hi[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hi[e] = pack_f16(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        tmem_st16(tmem_s + lanes + 32 * c, hi);
+      }
+      tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) arrive(&p_full);
+    }
+
+    // outputs
+    if (ok && tiles > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done, (uint32_t)(tiles - 1) & 1, timeout));
+    tc_after();
+    __syncwarp();
+    if (ok) {
+      const float inv = l == 0.f ? 0.f : kSumUnit / l;
+      const int64_t dst = (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (tiles > 0) {
+          tmem_ld32(tmem_o + lanes + 32 * c, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (mine) {
+          uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + dst + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t u[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv,
+                                                             __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+              u[q] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            p[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_before();
+  __syncthreads();
+  if (warp == 8) {
+    if (timeout_flag) {
+      // products may still be in flight: all have completed once this arrives
+      if (lane == 0) {
+        mma_commit(&drain);
+        mbar_wait_bounded(&drain, 0, kWaitCycles);
+      }
+      __syncwarp();
+    }
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kCols));
+  }
+  if (threadIdx.x == 0 && timeout_flag) raise_flag(a.status, LQ_DEV_TIMEOUT);
+}
+
+template <int D>
+lq_status launch_tiles(const TileArgs& ta, int64_t ctas, void* stream) {
+  using C = TileCfg<D>;
+  static_assert(C::kSmem + 512 <= 227 * 1024 / C::kPerSm - (C::kPerSm - 1) * 1024, "shared memory");
+  auto kern = attn_tiles_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return LQ_ERR_CUDA;
+  }
+  return serve::launch(kern, (unsigned)ctas, C::kThreads, C::kSmem, stream, ta);
+}
+
+lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int head_dim, void* stream) {
+  TileArgs ta;
+  ta.a = a;
+  ta.kc = kc;
+  ta.vc = vc;
+  // as many row tiles as there can be: every request's last one may be partial
+  const int64_t rows = a.total_q * a.group;
+  const int64_t ctas = (rows / kTileRows + (a.batch < a.total_q ? a.batch : a.total_q)) * a.kv_heads;
+  if (ctas > INT32_MAX) return LQ_ERR_SHAPE;
+  switch (head_dim) {
+    case 64: return launch_tiles<64>(ta, ctas, stream);
+    case 128: return launch_tiles<128>(ta, ctas, stream);
+    default: return launch_tiles<256>(ta, ctas, stream);
+  }
+}
+
+}  // namespace attn
+}  // namespace lq

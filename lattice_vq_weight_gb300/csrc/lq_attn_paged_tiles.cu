@@ -3,27 +3,30 @@
 //
 // The formulas are those of lq_attn_paged.cu.  With hundreds of rows per code
 // the matrix products bound the work (4 head_dim flops per row and position),
-// so here a CTA takes 128 query rows of one kv head and walks the positions
-// they see in tiles of 128 (64 for head_dim 256):
+// so here a CTA takes 256 query rows of one kv head as two row tiles (one for
+// head_dim 256) and walks the positions they see in tiles of 128 (64):
 //     S = Q C_k^T     tcgen05.mma, both operands in shared memory, S in TMEM
-//     W = 2^(x - max) by one thread per row, straight from and back into TMEM:
-//                     the fp16 weights take the columns of the scores they
-//                     were made from
+//     W = 2^(x - max) by one thread per row, from TMEM and back: the fp16
+//                     weights take the columns of the scores
 //     O += W C_v      tcgen05.mma with W from TMEM, O in TMEM
 // Warps 0..3 fetch codes (global memory to registers, a tile ahead) and
-// write them to shared memory as fp16, exactly; warps 4..7 hold the rows'
-// maxima and sums; warp 8 issues the products.  K and V tiles have the same
-// layout, rows of 64 dimensions in the 128-byte swizzle, which the products
-// read along either axis (K-major for the scores, MN-major for the values).
-// The steps of one CTA follow each other; two CTAs share an SM (head_dim 64
-// and 128), so that one's products run under the other's exponentials,
-// with the 512 columns of TMEM and the shared memory split between them.
+// write them to shared memory as fp16, exactly, into two stages; four warps per
+// row tile hold its rows' maxima and sums; the last warp issues the products.
+// K and V tiles have the same layout, rows of 64 dimensions in the 128-byte
+// swizzle, which the products read along either axis (K-major for the scores,
+// MN-major for the values).  The two row tiles run half a period apart, so that
+// one's products run under the other's exponentials, and share every tile of
+// codes: shared memory (operands read at 128 bytes a clock, tiles written) and
+// the conversions would otherwise bound the kernel before the tensor core does.
+// Scores are overwritten only after the products that read the weights there
+// have completed.
 //
-// As in the split kernel the running maximum may lag by 2^7, so that O is
-// rescaled (TMEM to registers and back) only when a row's maximum really
-// moves.  bf16 only: the tensor core's accumulator truncates, 6e-5 of the
-// output after 30000 positions (measured), which fp32 outputs would show; they
-// stay with the split kernel at any number of rows.  Every wait is bounded (about a second of clock cycles); on expiry
+// As in the split kernel the running maximum may lag by 2^7, so that a row's
+// weights are made in one pass and O is rescaled (TMEM to registers and back)
+// only when the maximum really moves.  bf16 only: the tensor core's accumulator
+// truncates, 6e-5 of the output after 30000 positions (measured), which fp32
+// outputs would show; they stay with the split kernel at any number of rows.
+// Every wait is bounded (about a second of clock cycles); on expiry
 // LQ_DEV_TIMEOUT is recorded and the CTA winds down.
 #include "lq_attn_paged.cuh"
 
@@ -34,14 +37,17 @@ constexpr int kTileRows = 128;
 
 template <int D>
 struct TileCfg {
+  static constexpr int T = D == 256 ? 1 : 2;                // row tiles per CTA
+  static constexpr int kRows = T * kTileRows;
   static constexpr int BN = D == 256 ? 64 : 128;            // tokens per tile
   static constexpr int kSub = D / 64;                       // 64-dimension sub-tiles
-  static constexpr int kQBytes = kTileRows * D * 2;
+  static constexpr int kQBytes = kTileRows * D * 2;         // of a row tile
   static constexpr int kCodeBytes = BN * D * 2;             // a K or V tile as fp16
-  static constexpr int kSmem = kQBytes + 2 * kCodeBytes + 1024;
-  static constexpr uint32_t kCols = BN + D <= 256 ? 256 : 512;
-  static constexpr int kPerSm = kCols == 256 ? 2 : 1;
-  static constexpr int kThreads = 288;
+  static constexpr int kSmem = T * kQBytes + 4 * kCodeBytes + 1024;
+  static constexpr uint32_t kCols = 512;
+  static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
+  static constexpr int kMmaWarp = 4 + 4 * T;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
   // rows of codes that the 128 fetching threads take in one pass (4 lanes
   // of 16 codes for each 64 dimensions), and passes per tile
   static constexpr int kPassRows = 32 / kSub;
@@ -129,18 +135,59 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   return true;
 }
 
+// A row's weights of one tile from its scores: packed fp16 weights, the sum of
+// weight / value scale, and the largest exponent met.  MASKED: some tokens are
+// not seen.  g-th 16 tokens: exponent = score * fac * ck + clv + base in lane g.
+template <int BN, bool MASKED>
+__device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float base, float ck, float clv, float civ,
+                                             uint32_t zero, uint32_t gone, int vis0, uint32_t (&w)[BN / 2], float& l) {
+  float lead = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t s[32];
+    tmem_ld32(tmem + 32 * c, s);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int g = 2 * c + half;
+      const float k = fac * __shfl_sync(0xffffffffu, ck, g), d = __shfl_sync(0xffffffffu, clv, g) + base;
+      const float iv = __shfl_sync(0xffffffffu, civ, g);
+      const int vis = MASKED ? ((gone >> g & 1) ? -1 : vis0 - 16 * g) : 15;      // tokens 0 .. vis are seen
+      const float2 k2 = make_float2(k, k), d2 = make_float2(d, d);
+      float2 sum = make_float2(0.f, 0.f);
+      const bool none = zero >> g & 1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float2 x = fma2(make_float2(__uint_as_float(s[16 * half + 2 * e]), __uint_as_float(s[16 * half + 2 * e + 1])), k2,
+                        d2);
+        if constexpr (MASKED) {
+          if (2 * e > vis) x.x = -INFINITY;
+          if (2 * e + 1 > vis) x.y = -INFINITY;
+        }
+        lead = fmaxf(lead, fmaxf(x.x, x.y));
+        x = make_float2(ex2(x.x), ex2(x.y));
+        sum = add2(sum, x);
+        w[8 * g + e] = none ? 0u : pack_f16(x.x, x.y);
+      }
+      const float total = sum.x + sum.y;
+      // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
+      l = fmaf(total, !MASKED || total > 0.f ? iv : 0.f, l);
+    }
+  }
+  return lead;
+}
+
 template <int D>
-__global__ void __launch_bounds__(TileCfg<D>::kThreads, TileCfg<D>::kPerSm)
-attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
+__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
   using C = TileCfg<D>;
-  constexpr int BN = C::BN;
+  constexpr int BN = C::BN, T = C::T;
   const Args& a = ta.a;
   extern __shared__ uint8_t tiles_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tiles_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = smem;                                       // the query rows
-  uint8_t* sk = sq + C::kQBytes;
-  uint8_t* sv = sk + C::kCodeBytes;
-  __shared__ uint64_t k_full, v_full, s_full, p_full, o_done, q_full, drain;
+  uint8_t* sk = sq + T * C::kQBytes;                        // two stages each
+  uint8_t* sv = sk + 2 * C::kCodeBytes;
+  __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
+  __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[2];
   __shared__ int wsum[C::kThreads / 32];
@@ -150,12 +197,18 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
   pdl_wait();
   pdl_launch();
   if (threadIdx.x == 0) {
-    mbar_init1(&k_full, 4);                                 // one arrival per fetching warp
-    mbar_init1(&v_full, 4);
-    mbar_init1(&s_full, 1);                                 // scores computed: S readable, the K tile free
-    mbar_init1(&p_full, 4);                                 // one arrival per softmax warp
-    mbar_init1(&o_done, 1);                                 // values added: O readable, W and the V tile free
-    mbar_init1(&q_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init1(&k_full[i], 4);                            // one arrival per fetching warp
+      mbar_init1(&v_full[i], 4);
+      mbar_init1(&k_free[i], 1);                            // the products that read the stage are done
+      mbar_init1(&v_free[i], 1);
+    }
+    for (int t = 0; t < T; ++t) {
+      mbar_init1(&s_full[t], 1);                            // scores computed
+      mbar_init1(&p_full[t], 4);                            // one arrival per softmax warp
+      mbar_init1(&o_done[t], 1);                            // values added: O readable, the weights read
+      mbar_init1(&q_full[t], 4);
+    }
     mbar_init1(&drain, 1);
     mbar_init_fence();
     timeout_flag = 0;
@@ -178,7 +231,7 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
     const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
     auto tiles_of = [&](int i) {
       const Request r = load_request(a, i);
-      return (r.q_len * a.group + kTileRows - 1) / kTileRows;
+      return (r.q_len * a.group + C::kRows - 1) / C::kRows;
     };
     int sum = 0;
     for (int i = i0; i < i1; ++i) {
@@ -209,16 +262,21 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
     __syncthreads();
   }
   if (found[0] < 0) return;                                 // fewer row tiles than CTAs
-  const int req = found[0], row0 = found[1] * kTileRows;
+  const int req = found[0], row0 = found[1] * C::kRows;
   const Request r = load_request(a, req);
   const int rows = r.q_len * a.group;
-  // tokens that the last row sees, and tiles of them
-  const int last_j = min(row0 + kTileRows, rows) - 1;
-  const int seen = min(r.len, r.shown + last_j / a.group + 1);
-  const int tiles = seen > 0 ? (seen + BN - 1) / BN : 0;
+  // tiles of the tokens that a row tile's last row sees; none if it has no rows
+  auto tiles_seen = [&](int t) {
+    if (row0 + t * kTileRows >= rows) return 0;
+    const int last = min(row0 + (t + 1) * kTileRows, rows) - 1;
+    const int seen = min(r.len, r.shown + last / a.group + 1);
+    return seen > 0 ? (seen + BN - 1) / BN : 0;
+  };
+  const int n0 = tiles_seen(0), n1 = T > 1 ? tiles_seen(1) : 0, tiles = max(n0, n1);
+  const int seen = min(r.len, tiles * BN);                  // tokens fetched
   const int32_t* table = a.table + (int64_t)req * a.ldt;
 
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(smem_addr(&tmem_base)), "r"(C::kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -226,28 +284,35 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + BN;
+  // columns: the row tiles' scores, then their outputs
+  const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + T * BN;
 
   if (warp < 4) {
     // ------------------------------------------------------------ codes to fp16
     const int t = threadIdx.x, c4 = t & 3, sub = t / (4 * C::kPassRows), r0 = (t >> 2) % C::kPassRows;
-    const int col = 64 * sub + 16 * c4;
     const int off_mask = (1 << a.log2_bs) - 1;
-    int64_t at[C::kPasses];                                 // where the thread's rows of a tile lie, -1: nowhere
+    const int64_t own = (int64_t)(r0 & 15) * D + 64 * sub + 16 * c4;
+    int64_t at = -1;                                        // lane g: where the tile's g-th 16 tokens lie, -1: nowhere
     auto locate = [&](int j) {
-#pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) {
-        const int pos = j * BN + p * C::kPassRows + r0;
-        const int blk = pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
-        const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
-        if (!ok && pos < seen && c4 == 0 && sub == 0) raise_flag(a.status, LQ_DEV_RANGE);
-        at[p] = ok ? (((((int64_t)blk * a.kv_heads + h) << a.log2_bs) + (pos & off_mask)) * D + col) : -1;
+      const int pos = j * BN + 16 * lane;
+      at = -1;
+      if (lane < BN / 16 && pos < seen) {
+        const int blk = __ldg(table + (pos >> a.log2_bs));
+        if ((unsigned)blk < (unsigned long long)a.num_blocks)
+          at = ((((int64_t)blk * a.kv_heads + h) << a.log2_bs) + (pos & off_mask)) * D;
+        else
+          raise_flag(a.status, LQ_DEV_RANGE);
       }
     };
+    // (a last block's tokens past the length are fetched too: they are the pool's)
     auto load = [&](const int8_t* cache, uint4 (&x)[C::kPasses]) {
 #pragma unroll
-      for (int p = 0; p < C::kPasses; ++p)
-        x[p] = at[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + at[p])) : make_uint4(0, 0, 0, 0);
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int row = p * C::kPassRows + r0;
+        const int64_t from = __shfl_sync(0xffffffffu, at, row >> 4);
+        const int64_t in = own + (C::kPassRows < 16 ? (row & 15) - (r0 & 15) : 0) * D;
+        x[p] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + from + in)) : make_uint4(0, 0, 0, 0);
+      }
     };
     auto store = [&](uint8_t* dst, const uint4 (&x)[C::kPasses]) {
 #pragma unroll
@@ -274,58 +339,79 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
       load(ta.vc, vx);
     }
     for (int j = 0; j < tiles; ++j) {
-      const uint32_t prev = (uint32_t)(j - 1) & 1;
-      if (j > 0 && !__all_sync(0xffffffffu, wait_on(&s_full, prev, timeout))) break;
-      store(sk, kx);
-      if (lane == 0) arrive(&k_full);
+      const int st = j & 1;
+      const uint32_t before = (uint32_t)(j / 2 + 1) & 1;    // the stage's previous use
+      if (j >= 2 && !__all_sync(0xffffffffu, wait_on(&k_free[st], before, timeout))) break;
+      store(sk + st * C::kCodeBytes, kx);
+      if (lane == 0) arrive(&k_full[st]);
       if (j + 1 < tiles) {
         locate(j + 1);
         load(ta.kc, kx);
       }
-      if (j > 0 && !__all_sync(0xffffffffu, wait_on(&o_done, prev, timeout))) break;
-      store(sv, vx);
-      if (lane == 0) arrive(&v_full);
+      if (j >= 2 && !__all_sync(0xffffffffu, wait_on(&v_free[st], before, timeout))) break;
+      store(sv + st * C::kCodeBytes, vx);
+      if (lane == 0) arrive(&v_full[st]);
       if (j + 1 < tiles) load(ta.vc, vx);
     }
-  } else if (warp == 8) {
+  } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       const uint32_t qa = smem_addr(sq), ka = smem_addr(sk), va = smem_addr(sv);
-      bool ok = tiles == 0 || wait_on(&q_full, 0, timeout);
-      for (int j = 0; j < tiles && ok; ++j) {
-        const uint32_t ph = (uint32_t)j & 1;
-        ok = wait_on(&k_full, ph, timeout);
-        if (!ok) break;
+      auto n_of = [&](int t) { return t == 0 ? n0 : n1; };
+      // scores of row tile t and tile j, where there are any
+      auto scores = [&](int t, int j) {
+        if (j >= n_of(t)) return true;
+        const int st = j & 1;
+        if (!wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout)) return false;
+        if (j == 0 && !wait_on(&q_full[t], 0, timeout)) return false;
+        // they overwrite the weights of the tile before
+        if (j > 0 && !wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout)) return false;
         tc_after();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t in = (uint32_t)((k & 3) * 32);
-          mma_ss(tmem_s, desc_k_major(qa + (k >> 2) * kTileRows * 128 + in),
-                 desc_k_major(ka + (k >> 2) * BN * 128 + in), Idesc<BN, false>::v, k > 0);
+          mma_ss(tmem_s + t * BN, desc_k_major(qa + t * C::kQBytes + (k >> 2) * kTileRows * 128 + in),
+                 desc_k_major(ka + st * C::kCodeBytes + (k >> 2) * BN * 128 + in), Idesc<BN, false>::v, k > 0);
         }
-        mma_commit(&s_full);
-        ok = wait_on(&v_full, ph, timeout) && wait_on(&p_full, ph, timeout);
-        if (!ok) break;
+        mma_commit(&s_full[t]);
+        if (t == T - 1 || j >= n1) mma_commit(&k_free[st]);
+        return true;
+      };
+      auto add_values = [&](int t, int j) {
+        if (j >= n_of(t)) return true;
+        const int st = j & 1;
+        if (!wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout)) return false;
+        if (!wait_on(&p_full[t], (uint32_t)j & 1, timeout)) return false;
         tc_after();
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
-          mma_ts(tmem_o, tmem_s + (k >> 1) * 32 + (k & 1) * 8,
-                 desc_mn_major(va + k * 2048, C::kSub > 1 ? BN * 128 : 1024), Idesc<D, true>::v, j > 0 || k > 0);
-        mma_commit(&o_done);
-        // the next scores overwrite the weights' columns
-        ok = wait_on(&o_done, ph, timeout);
+          mma_ts(tmem_o + t * D, tmem_s + t * BN + k * 8,
+                 desc_mn_major(va + st * C::kCodeBytes + k * 2048, C::kSub > 1 ? BN * 128 : 1024), Idesc<D, true>::v,
+                 j > 0 || k > 0);
+        mma_commit(&o_done[t]);
+        if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
+        return true;
+      };
+      bool ok = scores(0, 0);
+      for (int j = 0; j < tiles && ok; ++j) {
+        if constexpr (T > 1) ok = scores(1, j);
+        ok = ok && add_values(0, j) && scores(0, j + 1);
+        if constexpr (T > 1) ok = ok && add_values(1, j);
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;                          // row tile
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int R = row0 + row, j_tok = R / a.group;
+    const uint32_t my_s = tmem_s + lanes + t * BN, my_o = tmem_o + lanes + t * D;
+    const int R0 = row0 + t * kTileRows, R = R0 + row, j_tok = R / a.group;
+    const int n = t == 0 ? n0 : n1;
     const bool mine = R < rows;
     const int head = h * a.group + R - j_tok * a.group;
     const int lim = mine ? min(r.shown + j_tok, r.len - 1) : r.len - 1;     // last position the row sees
-    const int lim_min = min(r.shown + row0 / a.group, r.len - 1);           // of the tile's first row
+    const int lim_min = min(r.shown + R0 / a.group, r.len - 1);           // of the tile's first row
 
     // the query row as fp16, times a power of two that brings its largest
     // value to [2^13, 2^14) and the sign of the scale
@@ -366,12 +452,12 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
         uint32_t hi[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) hi[e] = pack_f16(v[2 * e] * up, v[2 * e + 1] * up);
-        uint8_t* line = sq + (c >> 3) * kTileRows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        uint8_t* line = sq + t * C::kQBytes + (c >> 3) * kTileRows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
         *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive(&q_full);
+      if (lane == 0) arrive(&q_full[t]);
     }
 
     // lane g < BN / 16: the scales of the tile's g-th 16 tokens, a tile ahead;
@@ -389,109 +475,63 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
         }
       }
     };
-    if (tiles > 0) fetch_scales(0);
+    if (n > 0) fetch_scales(0);
     float mx = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
-      const uint32_t ph = (uint32_t)j & 1;
+    for (int j = 0; j < n; ++j) {
       // per 16 tokens: key scale, log2 and reciprocal of the value scale
       const float ck = nk, cv = nv;
       const float cvm = cv < kMinScale ? kMinScale : cv;    // NaN stays NaN
       const float clv = lg2(cvm), civ = rcp(cvm) * kSumUnit;
       const uint32_t gone = __ballot_sync(0xffffffffu, cv < 0.f), zero = __ballot_sync(0xffffffffu, cv < kMinScale);
-      if (j + 1 < tiles) fetch_scales(j + 1);
-      const int p0 = j * BN;
-      const bool masked = p0 + BN - 1 > lim_min || (gone & ((1u << (BN / 16)) - 1));
-      ok = __all_sync(0xffffffffu, wait_on(&s_full, ph, timeout));
+      if (j + 1 < n) fetch_scales(j + 1);
+      const int vis0 = lim - j * BN;
+      const bool masked = (j + 1) * BN - 1 > lim_min || (gone & ((1u << (BN / 16)) - 1));
+      ok = __all_sync(0xffffffffu, wait_on(&s_full[t], (uint32_t)j & 1, timeout));
       if (!ok) break;
       tc_after();
       __syncwarp();
-
-      // the row's largest exponent in this tile
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t s[32];
-        tmem_ld32(tmem_s + lanes + 32 * c, s);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int g = 2 * c + half;
-          const float k = fac * __shfl_sync(0xffffffffu, ck, g), d = __shfl_sync(0xffffffffu, clv, g);
-          float m = -INFINITY;
-          if (!masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, __uint_as_float(s[16 * half + e]));
-          } else if (!(gone >> g & 1)) {
-            const int vis = lim - (p0 + 16 * g);            // elements 0 .. vis are seen
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e <= vis) m = fmaxf(m, __uint_as_float(s[16 * half + e]));
-          }
-          // (a group without a seen token adds nothing, whatever its scales)
-          if (m != -INFINITY) top = fmaxf(top, fmaf(m, k, d));
+      uint32_t w[BN / 2];
+      float lead = INFINITY;                                // of rows without a maximum yet: to be found first
+      for (int pass = 0; pass < 2; ++pass) {
+        const float base = kShift - (mx == -INFINITY ? 0.f : mx);
+        float sum = l;
+        const float top = masked ? row_weights<BN, true>(my_s, fac, base, ck, clv, civ, zero, gone, vis0, w, sum)
+                                 : row_weights<BN, false>(my_s, fac, base, ck, clv, civ, zero, gone, vis0, w, sum);
+        lead = mx == -INFINITY && top != -INFINITY ? INFINITY : top;
+        if (!__any_sync(0xffffffffu, lead > kShift + kLead)) {
+          l = sum;
+          break;
         }
-      }
-      if (__any_sync(0xffffffffu, top > mx + kLead)) {
-        // the maximum moves: the sum and the output so far shrink
-        const bool moves = top > mx + kLead;
-        const float f = moves ? ex2(mx - top) : 1.f;
-        if (moves) mx = top;
+        // the maximum moves: the sum and the output so far shrink, and the
+        // weights are made again
+        const bool moves = lead > kShift + kLead;
+        const float m = top - base;
+        const float f = moves ? ex2(mx - m) : 1.f;
+        if (moves) mx = m;
         l *= f;
         if (j > 0) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32(tmem_o + lanes + 32 * c, o);
+            tmem_ld32(my_o + 32 * c, o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(tmem_o + lanes + 32 * c, o);
-            tmem_st16(tmem_o + lanes + 32 * c + 16, o + 16);
-          }
-          tmem_wait_st();
-        }
-      }
-      const float base = kShift - (mx == -INFINITY ? 0.f : mx);
-      // weights, in place of the scores they are made from
-#pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t s[32];
-        tmem_ld32(tmem_s + lanes + 32 * c, s);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int g = 2 * c + half;
-          const float k = fac * __shfl_sync(0xffffffffu, ck, g), d = __shfl_sync(0xffffffffu, clv, g) + base;
-          const float iv = __shfl_sync(0xffffffffu, civ, g);
-          const int vis = !masked ? 15 : (gone >> g & 1) ? -1 : lim - (p0 + 16 * g);
-          float sum = 0.f, sum2 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float w = ex2(fmaf(__uint_as_float(s[16 * half + e]), k, d));
-            if (masked) w = e <= vis ? w : 0.f;
-            if (e & 1) sum2 += w;
-            else sum += w;
-            s[16 * half + e] = __float_as_uint(w);
-          }
-          sum += sum2;
-          // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
-          l = fmaf(sum, sum > 0.f ? iv : 0.f, l);
-          if (zero >> g & 1) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[16 * half + e] = 0u;
+            tmem_st16(my_o + 32 * c, o);
+            tmem_st16(my_o + 32 * c + 16, o + 16);
           }
         }
-        uint32_t hi[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) hi[e] = pack_f16(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-        tmem_st16(tmem_s + lanes + 32 * c, hi);
       }
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_st16(my_s + 16 * c, w + 16 * c);
       tmem_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) arrive(&p_full);
+      if (lane == 0) arrive(&p_full[t]);
     }
 
     // outputs
-    if (ok && tiles > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done, (uint32_t)(tiles - 1) & 1, timeout));
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(n - 1) & 1, timeout));
     tc_after();
     __syncwarp();
     if (ok) {
@@ -500,8 +540,8 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (tiles > 0) {
-          tmem_ld32(tmem_o + lanes + 32 * c, o);
+        if (n > 0) {
+          tmem_ld32(my_o + 32 * c, o);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -527,7 +567,7 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
   // ---------------------------------------------------------------- teardown
   tc_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     if (timeout_flag) {
       // products may still be in flight: all have completed once this arrives
       if (lane == 0) {
@@ -545,7 +585,7 @@ attn_tiles_kernel(const __grid_constant__ TileArgs ta) {
 template <int D>
 lq_status launch_tiles(const TileArgs& ta, int64_t ctas, void* stream) {
   using C = TileCfg<D>;
-  static_assert(C::kSmem + 512 <= 227 * 1024 / C::kPerSm - (C::kPerSm - 1) * 1024, "shared memory");
+  static_assert(C::kSmem + 512 <= 227 * 1024, "shared memory");
   auto kern = attn_tiles_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
     cudaGetLastError();
@@ -561,7 +601,8 @@ lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, i
   ta.vc = vc;
   // as many row tiles as there can be: every request's last one may be partial
   const int64_t rows = a.total_q * a.group;
-  const int64_t ctas = (rows / kTileRows + (a.batch < a.total_q ? a.batch : a.total_q)) * a.kv_heads;
+  const int per = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;
+  const int64_t ctas = (rows / per + (a.batch < a.total_q ? a.batch : a.total_q)) * a.kv_heads;
   if (ctas > INT32_MAX) return LQ_ERR_SHAPE;
   switch (head_dim) {
     case 64: return launch_tiles<64>(ta, ctas, stream);

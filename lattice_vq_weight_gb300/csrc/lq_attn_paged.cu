@@ -889,13 +889,12 @@ lq_status launch_split(const Args& a, const CUtensorMap& mk, const CUtensorMap& 
   return check_launch();
 }
 
-// Codes of a cache as rows of 128 bytes, copied in boxes of `rows` of them.
-bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int rows) {
+bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int lines) {
   TensorMapEncodeTiledFn fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {128, (cuuint64_t)(bytes / 128)};
   const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, (cuuint32_t)rows};
+  const cuuint32_t box[2] = {128, (cuuint32_t)lines};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -973,15 +972,15 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   const int ctas = attn::cta_count();
   const size_t meta = ((size_t)ctas * 2 * sizeof(attn::Tag) + 255) & ~(size_t)255;
   a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + meta);
-  CUtensorMap mk, mv;
   // a pool without blocks: no copy is issued, any valid map will do
-  const void* kc = num_blocks > 0 ? (const void*)k_cache_dev : workspace_dev;
-  const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;
-  const int64_t bytes = num_blocks > 0 ? num_blocks * block_rows * 128 : 4096;
+  const int8_t* kc = num_blocks > 0 ? k_cache_dev : reinterpret_cast<const int8_t*>(workspace_dev);
+  const int8_t* vc = num_blocks > 0 ? v_cache_dev : reinterpret_cast<const int8_t*>(workspace_dev);
+  const int64_t bytes = num_blocks > 0 ? num_blocks * block_rows * 128 : 32768;
+  const int64_t avg_rows = ((total_q + batch - 1) / batch) * a.group;
+  if (avg_rows > 64 && dtype == LQ_BF16) return attn::launch_attn_tiles(a, kc, vc, bytes, head_dim, stream);
+  CUtensorMap mk, mv;
   const int box = (block_size < attn::kTile ? block_size : attn::kTile) * head_dim / 128;
   if (!attn::encode_cache(&mk, kc, bytes, box) || !attn::encode_cache(&mv, vc, bytes, box)) return LQ_ERR_CUDA;
-  const int64_t avg_rows = ((total_q + batch - 1) / batch) * a.group;
-  if (avg_rows > 64 && dtype == LQ_BF16) return attn::launch_attn_tiles(a, k_cache_dev, v_cache_dev, head_dim, stream);
   // eight query rows per pass over the codes, sixteen where the average request has more
   const bool few = avg_rows <= 8;
   if (dtype == LQ_F32) {

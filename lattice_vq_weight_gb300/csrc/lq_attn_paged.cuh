@@ -112,8 +112,13 @@ __device__ __forceinline__ Request load_request(const Args& a, int i) {
   return r;
 }
 
+// Tensor map of a cache's codes as lines of 128 bytes, copied in boxes of
+// `lines` of them, at most 256, in the 128-byte swizzle.
+bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int lines);
+
 // The kernel for many query rows (lq_attn_paged_tiles.cu).
-lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int head_dim, void* stream);
+lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int64_t cache_bytes, int head_dim,
+                            void* stream);
 
 }  // namespace attn
 }  // namespace lq

@@ -9,9 +9,12 @@
 //     W = 2^(x - max) by one thread per row, from TMEM and back: the fp16
 //                     weights take the columns of the scores
 //     O += W C_v      tcgen05.mma with W from TMEM, O in TMEM
-// Warps 0..3 fetch codes (global memory to registers, a tile ahead) and
-// write them to shared memory as fp16, exactly, into two stages; four warps per
-// row tile hold its rows' maxima and sums; the last warp issues the products.
+// One warp fetches the codes of a tile by TMA, up to two half tiles (K, V)
+// ahead; warps 0..3 turn them into fp16, exactly, in two stages of shared
+// memory; four warps per row tile hold its rows' maxima and sums; one warp
+// issues the products.  (Codes fetched through registers instead measured 340
+// against TMA's PROMPT us for a 2000-token chunk: the L1 that this much shared
+// memory leaves holds too few loads in flight.)
 // K and V tiles have the same layout, rows of 64 dimensions in the 128-byte
 // swizzle, which the products read along either axis (K-major for the scores,
 // MN-major for the values).  The two row tiles run half a period apart, so that
@@ -43,21 +46,22 @@ struct TileCfg {
   static constexpr int kSub = D / 64;                       // 64-dimension sub-tiles
   static constexpr int kQBytes = kTileRows * D * 2;         // of a row tile
   static constexpr int kCodeBytes = BN * D * 2;             // a K or V tile as fp16
-  static constexpr int kSmem = T * kQBytes + 4 * kCodeBytes + 1024;
+  static constexpr int kRawBytes = BN * D;                  // a K or V tile's codes
+  static constexpr int kSmem = T * kQBytes + 4 * kCodeBytes + 2 * kRawBytes + 1024;
   static constexpr uint32_t kCols = 512;
   static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
   static constexpr int kMmaWarp = 4 + 4 * T;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  // rows of codes that the 128 fetching threads take in one pass (4 lanes
+  static constexpr int kFetchWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kFetchWarp + 1);
+  // rows of codes that the 128 converting threads take in one pass (4 lanes
   // of 16 codes for each 64 dimensions), and passes per tile
   static constexpr int kPassRows = 32 / kSub;
   static constexpr int kPasses = BN / kPassRows;
 };
 
 struct TileArgs {
+  CUtensorMap map_k, map_v;      // boxes of a block's codes, or of BN tokens of it
   Args a;
-  const int8_t* kc;
-  const int8_t* vc;
 };
 
 __device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
@@ -93,6 +97,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                ::"r"(smem_addr(bar)) : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -186,7 +196,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   uint8_t* sq = smem;                                       // the query rows
   uint8_t* sk = sq + T * C::kQBytes;                        // two stages each
   uint8_t* sv = sk + 2 * C::kCodeBytes;
+  uint8_t* raw = sv + 2 * C::kCodeBytes;                    // codes as fetched, K and V
   __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
+  __shared__ uint64_t raw_full[2], raw_free[2];             // K, V
   __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[2];
@@ -198,7 +210,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   pdl_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init1(&k_full[i], 4);                            // one arrival per fetching warp
+      mbar_init1(&raw_full[i], 1);
+      mbar_init1(&raw_free[i], 4);                          // one arrival per converting warp
+      mbar_init1(&k_full[i], 4);
       mbar_init1(&v_full[i], 4);
       mbar_init1(&k_free[i], 1);                            // the products that read the stage are done
       mbar_init1(&v_free[i], 1);
@@ -289,32 +303,19 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
 
   if (warp < 4) {
     // ------------------------------------------------------------ codes to fp16
-    const int t = threadIdx.x, c4 = t & 3, sub = t / (4 * C::kPassRows), r0 = (t >> 2) % C::kPassRows;
-    const int off_mask = (1 << a.log2_bs) - 1;
-    const int64_t own = (int64_t)(r0 & 15) * D + 64 * sub + 16 * c4;
-    int64_t at = -1;                                        // lane g: where the tile's g-th 16 tokens lie, -1: nowhere
-    auto locate = [&](int j) {
-      const int pos = j * BN + 16 * lane;
-      at = -1;
-      if (lane < BN / 16 && pos < seen) {
-        const int blk = __ldg(table + (pos >> a.log2_bs));
-        if ((unsigned)blk < (unsigned long long)a.num_blocks)
-          at = ((((int64_t)blk * a.kv_heads + h) << a.log2_bs) + (pos & off_mask)) * D;
-        else
-          raise_flag(a.status, LQ_DEV_RANGE);
-      }
-    };
-    // (a last block's tokens past the length are fetched too: they are the pool's)
-    auto load = [&](const int8_t* cache, uint4 (&x)[C::kPasses]) {
+    // 16 codes per thread and pass.  The eight lanes of a shared-memory phase
+    // take four neighbouring chunks of two rows that differ in bits 0 and 2,
+    // which keeps them off each other's banks when they read codes and when
+    // they write fp16, both in the 128-byte swizzle.
+    const int t = threadIdx.x, c4 = t & 3, sub = t / (4 * C::kPassRows), q8 = (t >> 2) & 7;
+    const int r0 = ((q8 >> 1) ^ (q8 & 1 ? 5 : 0)) + ((t >> 2) % C::kPassRows & ~7);
+    auto convert = [&](const uint8_t* src, uint8_t* dst, uint64_t* src_free, uint64_t* full) {
+      uint4 x[C::kPasses];
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
-        const int row = p * C::kPassRows + r0;
-        const int64_t from = __shfl_sync(0xffffffffu, at, row >> 4);
-        const int64_t in = own + (C::kPassRows < 16 ? (row & 15) - (r0 & 15) : 0) * D;
-        x[p] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + from + in)) : make_uint4(0, 0, 0, 0);
+        const uint32_t off = (uint32_t)((p * C::kPassRows + r0) * D + 64 * sub + 16 * c4);
+        x[p] = *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 7 & 7u) << 4)));
       }
-    };
-    auto store = [&](uint8_t* dst, const uint4 (&x)[C::kPasses]) {
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
         const int row = p * C::kPassRows + r0;
@@ -331,75 +332,109 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       }
       fence_proxy_async_smem();
       __syncwarp();
+      if (lane == 0) {
+        arrive(src_free);
+        arrive(full);
+      }
     };
-    uint4 kx[C::kPasses], vx[C::kPasses];
-    if (tiles > 0) {
-      locate(0);
-      load(ta.kc, kx);
-      load(ta.vc, vx);
-    }
     for (int j = 0; j < tiles; ++j) {
       const int st = j & 1;
       const uint32_t before = (uint32_t)(j / 2 + 1) & 1;    // the stage's previous use
-      if (j >= 2 && !__all_sync(0xffffffffu, wait_on(&k_free[st], before, timeout))) break;
-      store(sk + st * C::kCodeBytes, kx);
-      if (lane == 0) arrive(&k_full[st]);
-      if (j + 1 < tiles) {
-        locate(j + 1);
-        load(ta.kc, kx);
-      }
-      if (j >= 2 && !__all_sync(0xffffffffu, wait_on(&v_free[st], before, timeout))) break;
-      store(sv + st * C::kCodeBytes, vx);
-      if (lane == 0) arrive(&v_full[st]);
-      if (j + 1 < tiles) load(ta.vc, vx);
+      bool ok = wait_on(&raw_full[0], (uint32_t)j & 1, timeout);
+      if (j >= 2) ok = ok && wait_on(&k_free[st], before, timeout);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      convert(raw, sk + st * C::kCodeBytes, &raw_free[0], &k_full[st]);
+      ok = wait_on(&raw_full[1], (uint32_t)j & 1, timeout);
+      if (j >= 2) ok = ok && wait_on(&v_free[st], before, timeout);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      convert(raw + C::kRawBytes, sv + st * C::kCodeBytes, &raw_free[1], &v_full[st]);
     }
+  } else if (warp == C::kFetchWarp) {
+    // ------------------------------------------------------------ codes from the cache
+    // lane g: the g-th part of the tile, a block or BN tokens of one
+    const int step = min(1 << a.log2_bs, BN), parts = BN / step;
+    const int block_lines = (D << a.log2_bs) >> 7;
+    auto look_up = [&](int j) {
+      const int pos = j * BN + step * lane;
+      return lane < parts && pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
+    };
+    int blk = look_up(0), issued = 0;
+    for (int j = 0; j < tiles; ++j) {
+      const int pos = j * BN + step * lane;
+      const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+      if (!ok && lane < parts && pos < seen) raise_flag(a.status, LQ_DEV_RANGE);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * step * D;
+      const int line = (blk * a.kv_heads + h) * block_lines + (((pos & ((1 << a.log2_bs) - 1)) * D) >> 7);
+      blk = look_up(j + 1);
+      bool go = true;
+      for (int v = 0; v < 2 && go; ++v) {
+        if (j > 0) go = __all_sync(0xffffffffu, wait_on(&raw_free[v], (uint32_t)(j - 1) & 1, timeout));
+        if (!go) break;
+        if (lane == 0) mbar_expect_tx(&raw_full[v], bytes);
+        __syncwarp();
+        if (ok) tma_load_2d(raw + v * C::kRawBytes + lane * step * D, v ? &ta.map_v : &ta.map_k, &raw_full[v], 0, line);
+        ++issued;
+      }
+      if (!go) break;
+    }
+    // after a timeout: let the copies in flight land before the CTA ends
+    if (*timeout)
+      for (int q = max(0, issued - 2); q < issued; ++q)
+        mbar_wait_bounded(&raw_full[q & 1], (uint32_t)(q >> 1) & 1, kWaitCycles / 8);
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t qa = smem_addr(sq), ka = smem_addr(sk), va = smem_addr(sv);
-      auto n_of = [&](int t) { return t == 0 ? n0 : n1; };
-      // scores of row tile t and tile j, where there are any
-      auto scores = [&](int t, int j) {
-        if (j >= n_of(t)) return true;
-        const int st = j & 1;
-        if (!wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout)) return false;
-        if (j == 0 && !wait_on(&q_full[t], 0, timeout)) return false;
-        // they overwrite the weights of the tile before
-        if (j > 0 && !wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout)) return false;
-        tc_after();
+    // The whole warp runs the loop, so that descriptors are uniform values; one
+    // elected lane issues.
+    const uint64_t dq = desc_k_major(smem_addr(sq)), dk = desc_k_major(smem_addr(sk));
+    const uint64_t dv = desc_mn_major(smem_addr(sv), C::kSub > 1 ? BN * 128 : 1024);
+    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+    // scores of row tile t and tile j, where there are any
+    auto scores = [&](int t, int j) {
+      if (j >= (t == 0 ? n0 : n1)) return true;
+      const int st = j & 1;
+      bool ok = wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout);
+      if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
+      // they overwrite the weights of the tile before
+      else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
+      if (!all(ok)) return false;
+      tc_after();
+      const uint64_t qd = dq + (uint64_t)(t * C::kQBytes >> 4), kd = dk + (uint64_t)(st * C::kCodeBytes >> 4);
+      const uint32_t d = tmem_s + t * BN;
+      if (elect()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t in = (uint32_t)((k & 3) * 32);
-          mma_ss(tmem_s + t * BN, desc_k_major(qa + t * C::kQBytes + (k >> 2) * kTileRows * 128 + in),
-                 desc_k_major(ka + st * C::kCodeBytes + (k >> 2) * BN * 128 + in), Idesc<BN, false>::v, k > 0);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(d, qd + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4), kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4),
+                 Idesc<BN, false>::v, k > 0);
         mma_commit(&s_full[t]);
         if (t == T - 1 || j >= n1) mma_commit(&k_free[st]);
-        return true;
-      };
-      auto add_values = [&](int t, int j) {
-        if (j >= n_of(t)) return true;
-        const int st = j & 1;
-        if (!wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout)) return false;
-        if (!wait_on(&p_full[t], (uint32_t)j & 1, timeout)) return false;
-        tc_after();
+      }
+      __syncwarp();
+      return true;
+    };
+    auto add_values = [&](int t, int j) {
+      if (j >= (t == 0 ? n0 : n1)) return true;
+      const int st = j & 1;
+      bool ok = wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout);
+      ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
+      if (!all(ok)) return false;
+      tc_after();
+      const uint64_t vd = dv + (uint64_t)(st * C::kCodeBytes >> 4);
+      const uint32_t d = tmem_o + t * D, w = tmem_s + t * BN;
+      if (elect()) {
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_ts(tmem_o + t * D, tmem_s + t * BN + k * 8,
-                 desc_mn_major(va + st * C::kCodeBytes + k * 2048, C::kSub > 1 ? BN * 128 : 1024), Idesc<D, true>::v,
-                 j > 0 || k > 0);
+        for (int k = 0; k < BN / 16; ++k) mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, true>::v, j > 0 || k > 0);
         mma_commit(&o_done[t]);
         if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
-        return true;
-      };
-      bool ok = scores(0, 0);
-      for (int j = 0; j < tiles && ok; ++j) {
-        if constexpr (T > 1) ok = scores(1, j);
-        ok = ok && add_values(0, j) && scores(0, j + 1);
-        if constexpr (T > 1) ok = ok && add_values(1, j);
       }
+      __syncwarp();
+      return true;
+    };
+    bool ok = scores(0, 0);
+    for (int j = 0; j < tiles && ok; ++j) {
+      if constexpr (T > 1) ok = scores(1, j);
+      ok = ok && add_values(0, j) && scores(0, j + 1);
+      if constexpr (T > 1) ok = ok && add_values(1, j);
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;                          // row tile
@@ -594,11 +629,13 @@ lq_status launch_tiles(const TileArgs& ta, int64_t ctas, void* stream) {
   return serve::launch(kern, (unsigned)ctas, C::kThreads, C::kSmem, stream, ta);
 }
 
-lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int head_dim, void* stream) {
+lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int64_t cache_bytes, int head_dim,
+                            void* stream) {
   TileArgs ta;
   ta.a = a;
-  ta.kc = kc;
-  ta.vc = vc;
+  const int most = head_dim == 256 ? TileCfg<256>::BN : TileCfg<128>::BN, bs = 1 << a.log2_bs;
+  const int box = (bs < most ? bs : most) * head_dim / 128;
+  if (!encode_cache(&ta.map_k, kc, cache_bytes, box) || !encode_cache(&ta.map_v, vc, cache_bytes, box)) return LQ_ERR_CUDA;
   // as many row tiles as there can be: every request's last one may be partial
   const int64_t rows = a.total_q * a.group;
   const int per = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;

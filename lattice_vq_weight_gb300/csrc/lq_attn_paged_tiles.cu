@@ -52,7 +52,12 @@ struct TileCfg {
   static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
   static constexpr int kMmaWarp = 4 + 4 * T;
   static constexpr int kFetchWarp = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (kFetchWarp + 1);
+  static constexpr int kThreads = 32 * (8 + 4 * T);         // whole groups of four warps
+  // Registers per thread: the launch gives every warp 65536 / 512 = 128 (T = 2)
+  // and the groups then divide those up, 80 + 2 x 184 + 64 = 4 x 128.
+  static constexpr bool kSplitRegs = T == 2;
+  static constexpr int kConvertRegs = 80, kSoftmaxRegs = 184, kIssueRegs = 64;
+  static_assert(!kSplitRegs || kConvertRegs + 2 * kSoftmaxRegs + kIssueRegs <= 4 * 128, "the launch's registers");
   // rows of codes that the 128 converting threads take in one pass (4 lanes
   // of 16 codes for each 64 dimensions), and passes per tile
   static constexpr int kPassRows = 32 / kSub;
@@ -119,6 +124,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr) : "memory");
 }
+// The same without waiting, and the wait for all loads issued.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
@@ -146,44 +170,60 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 }
 
 // A row's weights of one tile from its scores: packed fp16 weights, the sum of
-// weight / value scale, and the largest exponent met.  MASKED: some tokens are
-// not seen.  g-th 16 tokens: exponent = score * fac * ck + clv + base in lane g.
+// weight / value scale, and the largest exponent met.  scales[g], of the g-th
+// 16 tokens: key scale, log2 and reciprocal of the value scale; the exponent of
+// a token is score * fac * .x + .y + base.  MASKED: some tokens are not seen, or
+// some blocks are missing (gone) or count as zero.
 template <int BN, bool MASKED>
-__device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float base, float ck, float clv, float civ,
-                                             uint32_t zero, uint32_t gone, int vis0, uint32_t (&w)[BN / 2], float& l) {
-  float lead = -INFINITY;
+__device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float base, const float4* scales, uint32_t zero,
+                                             uint32_t gone, int vis0, uint32_t (&w)[BN / 2], float& l) {
+  float lead0 = -INFINITY, lead1 = -INFINITY;
+  uint32_t s[2][32];
+  float4 sc[2] = {scales[0], scales[1]};
+  tmem_ld32_async(tmem, s[0]);
 #pragma unroll
   for (int c = 0; c < BN / 32; ++c) {
-    uint32_t s[32];
-    tmem_ld32(tmem + 32 * c, s);
+    uint32_t (&x32)[32] = s[c & 1];
+    tmem_wait_ld(x32);
+    if (c + 1 < BN / 32) tmem_ld32_async(tmem + 32 * (c + 1), s[(c + 1) & 1]);
+    const float4 now[2] = {sc[0], sc[1]};
+    if (c + 1 < BN / 32) {
+      sc[0] = scales[2 * c + 2];
+      sc[1] = scales[2 * c + 3];
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int g = 2 * c + half;
-      const float k = fac * __shfl_sync(0xffffffffu, ck, g), d = __shfl_sync(0xffffffffu, clv, g) + base;
-      const float iv = __shfl_sync(0xffffffffu, civ, g);
+      const float k = fac * now[half].x, d = now[half].y + base;
       const int vis = MASKED ? ((gone >> g & 1) ? -1 : vis0 - 16 * g) : 15;      // tokens 0 .. vis are seen
       const float2 k2 = make_float2(k, k), d2 = make_float2(d, d);
-      float2 sum = make_float2(0.f, 0.f);
-      const bool none = zero >> g & 1;
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float2 x = fma2(make_float2(__uint_as_float(s[16 * half + 2 * e]), __uint_as_float(s[16 * half + 2 * e + 1])), k2,
-                        d2);
+        const uint32_t* y = x32 + 16 * half + 2 * e;
+        float2 x = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), k2, d2);
         if constexpr (MASKED) {
           if (2 * e > vis) x.x = -INFINITY;
           if (2 * e + 1 > vis) x.y = -INFINITY;
         }
-        lead = fmaxf(lead, fmaxf(x.x, x.y));
+        if (e & 1) lead1 = fmaxf(lead1, fmaxf(x.x, x.y));
+        else lead0 = fmaxf(lead0, fmaxf(x.x, x.y));
         x = make_float2(ex2(x.x), ex2(x.y));
-        sum = add2(sum, x);
-        w[8 * g + e] = none ? 0u : pack_f16(x.x, x.y);
+        if (e & 1) sum1 = add2(sum1, x);
+        else sum0 = add2(sum0, x);
+        w[8 * g + e] = pack_f16(x.x, x.y);
       }
-      const float total = sum.x + sum.y;
+      sum0 = add2(sum0, sum1);
+      const float total = sum0.x + sum0.y;
       // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
-      l = fmaf(total, !MASKED || total > 0.f ? iv : 0.f, l);
+      l = fmaf(total, !MASKED || total > 0.f ? now[half].z : 0.f, l);
+      if (MASKED && (zero >> g & 1)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[8 * g + e] = 0u;
+      }
     }
   }
-  return lead;
+  return fmaxf(lead0, lead1);
 }
 
 template <int D>
@@ -203,6 +243,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[2];
   __shared__ int wsum[C::kThreads / 32];
+  __shared__ float4 scales[4 * T][BN / 16];                 // per softmax warp
   volatile int* timeout = &timeout_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -302,6 +343,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + T * BN;
 
   if (warp < 4) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kConvertRegs));
     // ------------------------------------------------------------ codes to fp16
     // 16 codes per thread and pass.  The eight lanes of a shared-memory phase
     // take four neighbouring chunks of two rows that differ in bits 0 and 2,
@@ -349,93 +391,97 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (!__all_sync(0xffffffffu, ok)) break;
       convert(raw + C::kRawBytes, sv + st * C::kCodeBytes, &raw_free[1], &v_full[st]);
     }
-  } else if (warp == C::kFetchWarp) {
-    // ------------------------------------------------------------ codes from the cache
-    // lane g: the g-th part of the tile, a block or BN tokens of one
-    const int step = min(1 << a.log2_bs, BN), parts = BN / step;
-    const int block_lines = (D << a.log2_bs) >> 7;
-    auto look_up = [&](int j) {
-      const int pos = j * BN + step * lane;
-      return lane < parts && pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
-    };
-    int blk = look_up(0), issued = 0;
-    for (int j = 0; j < tiles; ++j) {
-      const int pos = j * BN + step * lane;
-      const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
-      if (!ok && lane < parts && pos < seen) raise_flag(a.status, LQ_DEV_RANGE);
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * step * D;
-      const int line = (blk * a.kv_heads + h) * block_lines + (((pos & ((1 << a.log2_bs) - 1)) * D) >> 7);
-      blk = look_up(j + 1);
-      bool go = true;
-      for (int v = 0; v < 2 && go; ++v) {
-        if (j > 0) go = __all_sync(0xffffffffu, wait_on(&raw_free[v], (uint32_t)(j - 1) & 1, timeout));
+  } else if (warp >= C::kMmaWarp) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+    if (warp == C::kFetchWarp) {
+      // ------------------------------------------------------------ codes from the cache
+      // lane g: the g-th part of the tile, a block or BN tokens of one
+      const int step = min(1 << a.log2_bs, BN), parts = BN / step;
+      const int block_lines = (D << a.log2_bs) >> 7;
+      auto look_up = [&](int j) {
+        const int pos = j * BN + step * lane;
+        return lane < parts && pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
+      };
+      int blk = look_up(0), issued = 0;
+      for (int j = 0; j < tiles; ++j) {
+        const int pos = j * BN + step * lane;
+        const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+        if (!ok && lane < parts && pos < seen) raise_flag(a.status, LQ_DEV_RANGE);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * step * D;
+        const int line = (blk * a.kv_heads + h) * block_lines + (((pos & ((1 << a.log2_bs) - 1)) * D) >> 7);
+        blk = look_up(j + 1);
+        bool go = true;
+        for (int v = 0; v < 2 && go; ++v) {
+          if (j > 0) go = __all_sync(0xffffffffu, wait_on(&raw_free[v], (uint32_t)(j - 1) & 1, timeout));
+          if (!go) break;
+          if (lane == 0) mbar_expect_tx(&raw_full[v], bytes);
+          __syncwarp();
+          if (ok) tma_load_2d(raw + v * C::kRawBytes + lane * step * D, v ? &ta.map_v : &ta.map_k, &raw_full[v], 0, line);
+          ++issued;
+        }
         if (!go) break;
-        if (lane == 0) mbar_expect_tx(&raw_full[v], bytes);
+      }
+      // after a timeout: let the copies in flight land before the CTA ends
+      if (*timeout)
+        for (int q = max(0, issued - 2); q < issued; ++q)
+          mbar_wait_bounded(&raw_full[q & 1], (uint32_t)(q >> 1) & 1, kWaitCycles / 8);
+    } else if (warp == C::kMmaWarp) {
+      // ------------------------------------------------------------ products
+      // The whole warp runs the loop, so that descriptors are uniform values; one
+      // elected lane issues.
+      const uint64_t dq = desc_k_major(smem_addr(sq)), dk = desc_k_major(smem_addr(sk));
+      const uint64_t dv = desc_mn_major(smem_addr(sv), C::kSub > 1 ? BN * 128 : 1024);
+      auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+      // scores of row tile t and tile j, where there are any
+      auto scores = [&](int t, int j) {
+        if (j >= (t == 0 ? n0 : n1)) return true;
+        const int st = j & 1;
+        bool ok = wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout);
+        if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
+        // they overwrite the weights of the tile before
+        else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
+        if (!all(ok)) return false;
+        tc_after();
+        const uint64_t qd = dq + (uint64_t)(t * C::kQBytes >> 4), kd = dk + (uint64_t)(st * C::kCodeBytes >> 4);
+        const uint32_t d = tmem_s + t * BN;
+        if (elect()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(d, qd + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4),
+                   kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, false>::v, k > 0);
+          mma_commit(&s_full[t]);
+          if (t == T - 1 || j >= n1) mma_commit(&k_free[st]);
+        }
         __syncwarp();
-        if (ok) tma_load_2d(raw + v * C::kRawBytes + lane * step * D, v ? &ta.map_v : &ta.map_k, &raw_full[v], 0, line);
-        ++issued;
-      }
-      if (!go) break;
-    }
-    // after a timeout: let the copies in flight land before the CTA ends
-    if (*timeout)
-      for (int q = max(0, issued - 2); q < issued; ++q)
-        mbar_wait_bounded(&raw_full[q & 1], (uint32_t)(q >> 1) & 1, kWaitCycles / 8);
-  } else if (warp == C::kMmaWarp) {
-    // ------------------------------------------------------------ products
-    // The whole warp runs the loop, so that descriptors are uniform values; one
-    // elected lane issues.
-    const uint64_t dq = desc_k_major(smem_addr(sq)), dk = desc_k_major(smem_addr(sk));
-    const uint64_t dv = desc_mn_major(smem_addr(sv), C::kSub > 1 ? BN * 128 : 1024);
-    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
-    // scores of row tile t and tile j, where there are any
-    auto scores = [&](int t, int j) {
-      if (j >= (t == 0 ? n0 : n1)) return true;
-      const int st = j & 1;
-      bool ok = wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout);
-      if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
-      // they overwrite the weights of the tile before
-      else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
-      if (!all(ok)) return false;
-      tc_after();
-      const uint64_t qd = dq + (uint64_t)(t * C::kQBytes >> 4), kd = dk + (uint64_t)(st * C::kCodeBytes >> 4);
-      const uint32_t d = tmem_s + t * BN;
-      if (elect()) {
+        return true;
+      };
+      auto add_values = [&](int t, int j) {
+        if (j >= (t == 0 ? n0 : n1)) return true;
+        const int st = j & 1;
+        bool ok = wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout);
+        ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
+        if (!all(ok)) return false;
+        tc_after();
+        const uint64_t vd = dv + (uint64_t)(st * C::kCodeBytes >> 4);
+        const uint32_t d = tmem_o + t * D, w = tmem_s + t * BN;
+        if (elect()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(d, qd + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4), kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4),
-                 Idesc<BN, false>::v, k > 0);
-        mma_commit(&s_full[t]);
-        if (t == T - 1 || j >= n1) mma_commit(&k_free[st]);
+          for (int k = 0; k < BN / 16; ++k) mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, true>::v, j > 0 || k > 0);
+          mma_commit(&o_done[t]);
+          if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = scores(0, 0);
+      for (int j = 0; j < tiles && ok; ++j) {
+        if constexpr (T > 1) ok = scores(1, j);
+        ok = ok && add_values(0, j) && scores(0, j + 1);
+        if constexpr (T > 1) ok = ok && add_values(1, j);
       }
-      __syncwarp();
-      return true;
-    };
-    auto add_values = [&](int t, int j) {
-      if (j >= (t == 0 ? n0 : n1)) return true;
-      const int st = j & 1;
-      bool ok = wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout);
-      ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
-      if (!all(ok)) return false;
-      tc_after();
-      const uint64_t vd = dv + (uint64_t)(st * C::kCodeBytes >> 4);
-      const uint32_t d = tmem_o + t * D, w = tmem_s + t * BN;
-      if (elect()) {
-#pragma unroll
-        for (int k = 0; k < BN / 16; ++k) mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, true>::v, j > 0 || k > 0);
-        mma_commit(&o_done[t]);
-        if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = scores(0, 0);
-    for (int j = 0; j < tiles && ok; ++j) {
-      if constexpr (T > 1) ok = scores(1, j);
-      ok = ok && add_values(0, j) && scores(0, j + 1);
-      if constexpr (T > 1) ok = ok && add_values(1, j);
     }
   } else {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;                          // row tile
     const int row = (warp & 3) * 32 + lane;
@@ -514,14 +560,17 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     float mx = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      // per 16 tokens: key scale, log2 and reciprocal of the value scale
-      const float ck = nk, cv = nv;
-      const float cvm = cv < kMinScale ? kMinScale : cv;    // NaN stays NaN
-      const float clv = lg2(cvm), civ = rcp(cvm) * kSumUnit;
-      const uint32_t gone = __ballot_sync(0xffffffffu, cv < 0.f), zero = __ballot_sync(0xffffffffu, cv < kMinScale);
+      const float cv = nv, cvm = cv < kMinScale ? kMinScale : cv;     // NaN stays NaN
+      const uint32_t parts = (1u << (BN / 16)) - 1;
+      const uint32_t gone = __ballot_sync(0xffffffffu, cv < 0.f) & parts;
+      const uint32_t zero = __ballot_sync(0xffffffffu, cv < kMinScale) & parts;
+      float4* sc = scales[warp - 4];
+      __syncwarp();
+      if (lane < BN / 16) sc[lane] = make_float4(nk, lg2(cvm), rcp(cvm) * kSumUnit, 0.f);
+      __syncwarp();
       if (j + 1 < n) fetch_scales(j + 1);
       const int vis0 = lim - j * BN;
-      const bool masked = (j + 1) * BN - 1 > lim_min || (gone & ((1u << (BN / 16)) - 1));
+      const bool masked = (j + 1) * BN - 1 > lim_min || zero != 0;    // (a missing block counts as zero too)
       ok = __all_sync(0xffffffffu, wait_on(&s_full[t], (uint32_t)j & 1, timeout));
       if (!ok) break;
       tc_after();
@@ -531,8 +580,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       for (int pass = 0; pass < 2; ++pass) {
         const float base = kShift - (mx == -INFINITY ? 0.f : mx);
         float sum = l;
-        const float top = masked ? row_weights<BN, true>(my_s, fac, base, ck, clv, civ, zero, gone, vis0, w, sum)
-                                 : row_weights<BN, false>(my_s, fac, base, ck, clv, civ, zero, gone, vis0, w, sum);
+        const float top = masked ? row_weights<BN, true>(my_s, fac, base, sc, zero, gone, vis0, w, sum)
+                                 : row_weights<BN, false>(my_s, fac, base, sc, zero, gone, vis0, w, sum);
         lead = mx == -INFINITY && top != -INFINITY ? INFINITY : top;
         if (!__any_sync(0xffffffffu, lead > kShift + kLead)) {
           l = sum;
@@ -620,7 +669,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
 template <int D>
 lq_status launch_tiles(const TileArgs& ta, int64_t ctas, void* stream) {
   using C = TileCfg<D>;
-  static_assert(C::kSmem + 512 <= 227 * 1024, "shared memory");
+  static_assert(C::kSmem + 1536 <= 227 * 1024, "shared memory");
   auto kern = attn_tiles_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
     cudaGetLastError();

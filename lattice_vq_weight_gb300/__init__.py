@@ -510,37 +510,69 @@ def lq_rotate_blocks(R, X, Y, transpose: bool = False, stream=None) -> None:
 LQ_MAX_REQUESTS = 8192
 
 
+# These calls run once or more per layer and step, some of them shorter on the
+# GPU than their marshalling, so the checks below are written to cost little:
+# a failed one is explained by a second look.
 def _addr(t):
-    """Device address of a tensor (or None) as the plain number a call of every step passes quickest."""
+    """Device address of a tensor (or None) as a plain number."""
     return None if t is None else t.data_ptr()
 
 
-def _want(name: str, t, shape, *dtypes) -> None:
-    """Raise unless t is contiguous with this shape and one of these dtypes: the kernels trust both."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{name}: want a contiguous {tuple(shape)} tensor of {' or '.join(map(str, dtypes))}, "
-                         f"got {tuple(t.shape)} {t.dtype} with strides {tuple(t.stride())}")
+def _stream_of(t, stream):
+    """The stream of a call on tensor t: the one given, else the current one of t's device."""
+    if stream is not None:
+        return int(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not t.is_cuda:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return raw(t.get_device())
+
+
+def _is(t, dtype, shape) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _explain(call: str, wanted) -> None:
+    """Raise for the first of (name, tensor, dtype, shape) that is not a contiguous tensor of that kind."""
+    for name, t, dtype, shape in wanted:
+        if t is not None and not _is(t, dtype, shape):
+            raise ValueError(f"{call}: {name}: want a contiguous {tuple(shape)} tensor of {dtype}, got "
+                             f"{tuple(t.shape)} {t.dtype} with strides {tuple(t.stride())}")
 
 
 def _heads(name: str, t) -> int:
     """Token stride of a [tokens x heads x head_dim] tensor whose heads are packed."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name}: want [tokens x heads x head_dim] with packed heads, got {tuple(t.shape)} with "
-                         f"strides {tuple(t.stride())}")
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+    if t.dim() == 3:
+        tokens, heads, d = t.shape
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == d or heads == 1):
+            return s0 if tokens > 1 else heads * d
+    raise ValueError(f"{name}: want [tokens x heads x head_dim] with packed heads, got {tuple(t.shape)} with "
+                     f"strides {tuple(t.stride())}")
 
 
-def _cache(k_cache, k_scales, v_cache, v_scales):
+def _cache(call, k_cache, k_scales, v_cache, v_scales):
     """(num_blocks, kv_heads, block_size, head_dim) of a cache's four tensors, checked."""
     import torch
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache: want [num_blocks x kv_heads x block_size x head_dim], got {tuple(k_cache.shape)}")
-    shape = tuple(k_cache.shape)
-    _want("k_cache", k_cache, shape, torch.int8)
-    _want("v_cache", v_cache, shape, torch.int8)
-    _want("k_scales", k_scales, shape[:2], torch.float32)
-    _want("v_scales", v_scales, shape[:2], torch.float32)
+    i8, f32, shape = torch.int8, torch.float32, k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"{call}: k_cache: want [num_blocks x kv_heads x block_size x head_dim], got {tuple(shape)}")
+    if not (_is(k_cache, i8, shape) and _is(v_cache, i8, shape) and _is(k_scales, f32, shape[:2])
+            and _is(v_scales, f32, shape[:2])):
+        _explain(call, (("k_cache", k_cache, i8, shape), ("v_cache", v_cache, i8, shape),
+                        ("k_scales", k_scales, f32, shape[:2]), ("v_scales", v_scales, f32, shape[:2])))
     return shape
+
+
+def _table(call, t, batch):
+    """(row stride, width) of a block table int32 [batch x blocks] with packed rows."""
+    import torch
+    rows, width = t.shape if t.dim() == 2 else (-1, 0)
+    if rows != batch or t.dtype is not torch.int32 or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{call}: block_table: want int32 [{batch} x blocks] with packed rows, got {tuple(t.shape)} "
+                         f"{t.dtype} with strides {tuple(t.stride())}")
+    return (t.stride(0) if rows > 1 else width), width
 
 
 def paged_cache(num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device):
@@ -557,66 +589,79 @@ def lq_kv_plan(cached_lens, new_lens, block_size: int, free_blocks, block_table,
                used, dev_status=None, stream=None) -> None:
     """Block table rows, slots and positions of the requests' new tokens (see lq.h); block_table is updated."""
     import torch
-    b = cached_lens.numel()
-    for n, t, shape in (("cached_lens", cached_lens, (b,)), ("new_lens", new_lens, (b,)),
-                        ("free_blocks", free_blocks, (free_blocks.numel(),)), ("cu_new", cu_new, (b + 1,)),
-                        ("kv_lens", kv_lens, (b,)), ("positions", positions, (slots.numel(),)), ("used", used, (1,))):
-        _want(n, t, shape, torch.int32)
-    _want("slots", slots, (slots.numel(),), torch.int64)
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != b or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table: want int32 [{b} x blocks], got {tuple(block_table.shape)} {block_table.dtype}")
-    width = block_table.shape[1]
-    _check("lq_kv_plan", _get_lib().lq_kv_plan(
-        _addr(cached_lens), _addr(new_lens), b, int(block_size), _addr(free_blocks), free_blocks.numel(),
-        _addr(block_table), block_table.stride(0) if b > 1 else width, width, _addr(cu_new), _addr(kv_lens),
-        _addr(slots), _addr(positions), slots.numel(), _addr(used), _addr(dev_status), _stream(stream)))
+    i32 = torch.int32
+    b, n, free = cached_lens.numel(), slots.numel(), free_blocks.numel()
+    if not (_is(cached_lens, i32, (b,)) and _is(new_lens, i32, (b,)) and _is(free_blocks, i32, (free,))
+            and _is(cu_new, i32, (b + 1,)) and _is(kv_lens, i32, (b,)) and _is(positions, i32, (n,))
+            and _is(used, i32, (1,)) and _is(slots, torch.int64, (n,))):
+        _explain("lq_kv_plan", (
+            ("cached_lens", cached_lens, i32, (b,)), ("new_lens", new_lens, i32, (b,)),
+            ("free_blocks", free_blocks, i32, (free,)), ("cu_new", cu_new, i32, (b + 1,)), ("kv_lens", kv_lens, i32, (b,)),
+            ("positions", positions, i32, (n,)), ("used", used, i32, (1,)), ("slots", slots, torch.int64, (n,))))
+    stride, width = _table("lq_kv_plan", block_table, b)
+    st = _get_lib().lq_kv_plan(
+        cached_lens.data_ptr(), new_lens.data_ptr(), b, block_size, free_blocks.data_ptr(), free, block_table.data_ptr(),
+        stride, width, cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), n, used.data_ptr(),
+        _addr(dev_status), _stream_of(cu_new, stream))
+    if st:
+        _check("lq_kv_plan", st)
 
 
 def lq_qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, cos_sin, q_out, k_out, interleaved: bool = False,
                     dev_status=None, stream=None) -> None:
     """RMS norm of every head of q and k (weights None: none), then the rotation; q_out, k_out may be q, k."""
     import torch
-    if not q.dtype == k.dtype == q_out.dtype == k_out.dtype:
+    f32, dt, shape, kshape = torch.float32, q.dtype, q.shape, k.shape
+    if k.dtype is not dt or q_out.dtype is not dt or k_out.dtype is not dt:
         raise TypeError("lq_qk_norm_rope: q, k and their outputs have one dtype")
-    tokens, hq, d = q.shape
-    if k.shape[0] != tokens or k.shape[2] != d or q_out.shape != q.shape or k_out.shape != k.shape:
+    ldq, ldk, ldqo, ldko = _heads("q", q), _heads("k", k), _heads("q_out", q_out), _heads("k_out", k_out)
+    tokens, hq, d = shape
+    if kshape[0] != tokens or kshape[2] != d or q_out.shape != shape or k_out.shape != kshape:
         raise ValueError("lq_qk_norm_rope: q, k and their outputs do not belong together")
-    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _want(n, w, (d,), torch.float32)
-    _want("positions", positions, (tokens,), torch.int32)
-    _want("cos_sin", cos_sin, tuple(cos_sin.shape[:1]) + (cos_sin.shape[-1],), torch.float32)
-    _check("lq_qk_norm_rope", _get_lib().lq_qk_norm_rope(
-        _addr(q), _heads("q", q), hq, _addr(k), _heads("k", k), k.shape[1], _dtype_id(q), tokens, d, _addr(q_weight),
-        _addr(k_weight), float(eps), _addr(positions), _addr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
-        int(bool(interleaved)), _addr(q_out), _heads("q_out", q_out), _addr(k_out), _heads("k_out", k_out),
-        _addr(dev_status), _stream(stream)))
+    rows, rot = cos_sin.shape
+    if not (_is(positions, torch.int32, (tokens,)) and _is(cos_sin, f32, (rows, rot))
+            and (q_weight is None or _is(q_weight, f32, (d,))) and (k_weight is None or _is(k_weight, f32, (d,)))):
+        _explain("lq_qk_norm_rope", (("positions", positions, torch.int32, (tokens,)),
+                                     ("cos_sin", cos_sin, f32, (rows, rot)), ("q_weight", q_weight, f32, (d,)),
+                                     ("k_weight", k_weight, f32, (d,))))
+    st = _get_lib().lq_qk_norm_rope(
+        q.data_ptr(), ldq, hq, k.data_ptr(), ldk, kshape[1], _dtype_id(q), tokens, d, _addr(q_weight), _addr(k_weight),
+        eps, positions.data_ptr(), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, q_out.data_ptr(), ldqo,
+        k_out.data_ptr(), ldko, _addr(dev_status), _stream_of(q, stream))
+    if st:
+        _check("lq_qk_norm_rope", st)
 
 
 def lq_kv_append(k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status=None, stream=None) -> None:
     """Write k, v [tokens x kv_heads x head_dim] to the cache's slots (int64 [tokens], negative: left out)."""
     import torch
-    nb, hk, bs, d = _cache(k_cache, k_scales, v_cache, v_scales)
-    if k.shape != v.shape or k.dtype != v.dtype or tuple(k.shape[1:]) != (hk, d):
+    nb, hk, bs, d = _cache("lq_kv_append", k_cache, k_scales, v_cache, v_scales)
+    n = k.shape[0]
+    if k.shape != v.shape or k.dtype is not v.dtype or k.shape != (n, hk, d):
         raise ValueError(f"lq_kv_append: k and v do not fit the cache: {tuple(k.shape)}, {tuple(v.shape)}")
-    _want("slots", slots, (k.shape[0],), torch.int64)
-    _check("lq_kv_append", _get_lib().lq_kv_append(
-        _addr(k), _heads("k", k), _addr(v), _heads("v", v), _dtype_id(k), k.shape[0], _addr(slots), _addr(k_cache),
-        _addr(k_scales), _addr(v_cache), _addr(v_scales), nb, bs, hk, d, _addr(dev_status), _stream(stream)))
+    if not _is(slots, torch.int64, (n,)):
+        _explain("lq_kv_append", (("slots", slots, torch.int64, (n,)),))
+    st = _get_lib().lq_kv_append(
+        k.data_ptr(), _heads("k", k), v.data_ptr(), _heads("v", v), _dtype_id(k), n, slots.data_ptr(),
+        k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk, d,
+        _addr(dev_status), _stream_of(k, stream))
+    if st:
+        _check("lq_kv_append", st)
 
 
 def lq_kv_gather(slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status=None, stream=None) -> None:
     """The values that the cache's slots stand for, [n x kv_heads x head_dim] float32 or bf16."""
     import torch
-    nb, hk, bs, d = _cache(k_cache, k_scales, v_cache, v_scales)
-    n = slots.numel()
-    _want("slots", slots, (n,), torch.int64)
-    _want("k_out", k_out, (n, hk, d), torch.float32, torch.bfloat16)
-    _want("v_out", v_out, (n, hk, d), k_out.dtype)
-    _check("lq_kv_gather", _get_lib().lq_kv_gather(
-        _addr(slots), n, _addr(k_cache), _addr(k_scales), _addr(v_cache), _addr(v_scales), nb, bs, hk, d, _addr(k_out),
-        _addr(v_out), _dtype_id(k_out), _addr(dev_status), _stream(stream)))
+    nb, hk, bs, d = _cache("lq_kv_gather", k_cache, k_scales, v_cache, v_scales)
+    n, dt, shape = slots.numel(), k_out.dtype, (slots.numel(), hk, d)
+    if not (_is(slots, torch.int64, (n,)) and _is(k_out, dt, shape) and _is(v_out, dt, shape)):
+        _explain("lq_kv_gather", (("slots", slots, torch.int64, (n,)), ("k_out", k_out, dt, shape),
+                                  ("v_out", v_out, dt, shape)))
+    st = _get_lib().lq_kv_gather(
+        slots.data_ptr(), n, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk,
+        d, k_out.data_ptr(), v_out.data_ptr(), _dtype_id(k_out), _addr(dev_status), _stream_of(slots, stream))
+    if st:
+        _check("lq_kv_gather", st)
 
 
 def lq_attention_paged_workspace_size(batch: int, total_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -629,48 +674,54 @@ def lq_attention_paged(q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache
     """out = attention of q [total_q x q_heads x head_dim] over the requests' cached tokens (see lq.h);
     sm_scale defaults to head_dim ** -0.5."""
     import torch
-    nb, hk, bs, d = _cache(k_cache, k_scales, v_cache, v_scales)
-    b = kv_lens.numel()
-    _want("kv_lens", kv_lens, (b,), torch.int32)
-    _want("cu_q", cu_q, (b + 1,), torch.int32)
-    if q.shape != out.shape or q.dtype != out.dtype or q.shape[2] != d:
+    nb, hk, bs, d = _cache("lq_attention_paged", k_cache, k_scales, v_cache, v_scales)
+    b, i32 = kv_lens.numel(), torch.int32
+    ldq, ldo = _heads("q", q), _heads("out", out)
+    total, hq, dq = q.shape
+    if out.shape != q.shape or q.dtype is not out.dtype or dq != d:
         raise ValueError(f"lq_attention_paged: q and out do not fit: {tuple(q.shape)}, {tuple(out.shape)}")
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != b or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table: want int32 [{b} x blocks], got {tuple(block_table.shape)} {block_table.dtype}")
-    width = block_table.shape[1]
-    _check("lq_attention_paged", _get_lib().lq_attention_paged(
-        _addr(q), _heads("q", q), _dtype_id(q), q.shape[0], _addr(cu_q), _addr(kv_lens), b, _addr(block_table),
-        block_table.stride(0) if b > 1 else width, width, _addr(k_cache), _addr(k_scales), _addr(v_cache),
-        _addr(v_scales), nb, bs, q.shape[1], hk, d, d ** -0.5 if sm_scale is None else float(sm_scale), _addr(out),
-        _heads("out", out), _addr(workspace), workspace.numel() * workspace.element_size(), _addr(dev_status),
-        _stream(stream)))
+    if not (_is(kv_lens, i32, (b,)) and _is(cu_q, i32, (b + 1,))):
+        _explain("lq_attention_paged", (("kv_lens", kv_lens, i32, (b,)), ("cu_q", cu_q, i32, (b + 1,))))
+    stride, width = _table("lq_attention_paged", block_table, b)
+    st = _get_lib().lq_attention_paged(
+        q.data_ptr(), ldq, _dtype_id(q), total, cu_q.data_ptr(), kv_lens.data_ptr(), b, block_table.data_ptr(), stride,
+        width, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hq, hk, d,
+        d ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), ldo, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _addr(dev_status), _stream_of(q, stream))
+    if st:
+        _check("lq_attention_paged", st)
 
 
 def lq_verify_draft(draft_tokens, draft_lens, target_probs, draft_probs, u_accept, u_sample, out_tokens, accepted,
                     dev_status=None, stream=None) -> None:
     """Accept or refuse draft_tokens [batch x n] and draw the token after the accepted ones (see lq.h)."""
     import torch
+    i32, f32, dt = torch.int32, torch.float32, target_probs.dtype
     b, n = draft_tokens.shape
     vocab = target_probs.shape[2]
-    for name, t, rows in (("target_probs", target_probs, n + 1), ("draft_probs", draft_probs, n)):
-        if t is not None and (tuple(t.shape) != (b, rows, vocab) or t.dtype != target_probs.dtype or
-                              (vocab > 1 and rows > 0 and t.stride(2) != 1)):
-            raise ValueError(f"{name}: want [{b} x {rows} x {vocab}] {target_probs.dtype} with packed rows, got "
-                             f"{tuple(t.shape)} {t.dtype} with strides {tuple(t.stride())}")
-    _want("draft_tokens", draft_tokens, (b, n), torch.int32)
-    if draft_lens is not None:
-        _want("draft_lens", draft_lens, (b,), torch.int32)
-    _want("u_accept", u_accept, (b, n), torch.float32)
-    _want("u_sample", u_sample, (b,), torch.float32)
-    _want("out_tokens", out_tokens, (b, n + 1), torch.int32)
-    _want("accepted", accepted, (b,), torch.int32)
-    q = draft_probs
-    _check("lq_verify_draft", _get_lib().lq_verify_draft(
-        _addr(draft_tokens), _addr(draft_lens), b, n, vocab, _addr(target_probs), target_probs.stride(0),
-        target_probs.stride(1), _addr(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
-        _dtype_id(target_probs), _addr(u_accept), _addr(u_sample), _addr(out_tokens), _addr(accepted),
-        _addr(dev_status), _stream(stream)))
+
+    def rows_of(name, t, rows):
+        s0, s1, s2 = t.stride()
+        if t.shape != (b, rows, vocab) or t.dtype is not dt or (s2 != 1 and vocab > 1 and rows > 0):
+            raise ValueError(f"lq_verify_draft: {name}: want [{b} x {rows} x {vocab}] {dt} with packed rows, got "
+                             f"{tuple(t.shape)} {t.dtype} with strides {(s0, s1, s2)}")
+        return s0, s1
+
+    t0, t1 = rows_of("target_probs", target_probs, n + 1)
+    q0, q1 = (0, 0) if draft_probs is None else rows_of("draft_probs", draft_probs, n)
+    if not (_is(draft_tokens, i32, (b, n)) and _is(u_accept, f32, (b, n)) and _is(u_sample, f32, (b,))
+            and _is(out_tokens, i32, (b, n + 1)) and _is(accepted, i32, (b,))
+            and (draft_lens is None or _is(draft_lens, i32, (b,)))):
+        _explain("lq_verify_draft", (
+            ("draft_tokens", draft_tokens, i32, (b, n)), ("u_accept", u_accept, f32, (b, n)),
+            ("u_sample", u_sample, f32, (b,)), ("out_tokens", out_tokens, i32, (b, n + 1)),
+            ("accepted", accepted, i32, (b,)), ("draft_lens", draft_lens, i32, (b,))))
+    st = _get_lib().lq_verify_draft(
+        draft_tokens.data_ptr(), _addr(draft_lens), b, n, vocab, target_probs.data_ptr(), t0, t1, _addr(draft_probs), q0,
+        q1, _dtype_id(target_probs), u_accept.data_ptr(), u_sample.data_ptr(), out_tokens.data_ptr(), accepted.data_ptr(),
+        _addr(dev_status), _stream_of(target_probs, stream))
+    if st:
+        _check("lq_verify_draft", st)
 
 
 # ------------------------------------------------------------------ allocating helpers

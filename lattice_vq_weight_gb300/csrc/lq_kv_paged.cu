@@ -10,13 +10,15 @@
 // with IEEE fp32 quotients, so the codes depend on nothing but the order in
 // which tokens arrive.
 //
-// Append: a warp per (run, head, K or V).  Runs are found from the slots alone
-// (a token whose predecessor is not the slot before it in the same block
-// starts one), so no block list has to be built first.  The run is read twice,
-// for the maximum and for the codes: at most 64 KB that the first pass has
-// left in L1 or L2.  An IEEE division per value would bound the kernel, so
-// codes come from a product with 1/s wherever that is clear of a half by more
-// than its error, and from the division only in the rows that are not.
+// Append: runs are found from the slots alone (a token whose predecessor is not
+// the slot before it in the same block starts one), so no block list has to be
+// built first.  A CTA looks through a window of tokens for one head, four warps
+// for K and four for V.  Long runs (prompts) are shared by the four, which hold
+// the run in registers between the maximum and the codes, so that it is read
+// once and in one round of loads; where a window holds many runs (decode steps)
+// each warp takes runs of its own.  An IEEE division per value would bound the
+// kernel, so codes come from a product with 1/s wherever that is clear of a
+// half by more than its error, and from the division where it is not.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"
@@ -26,8 +28,8 @@
 namespace lq {
 namespace paged {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;                          // for each of K and V
+constexpr int kThreads = 2 * kWarps * 32;
 
 struct AppendArgs {
   const void* x[2];          // k, v
@@ -35,7 +37,7 @@ struct AppendArgs {
   int8_t* cache[2];
   float* scales[2];
   const int64_t* slots;
-  int64_t tokens, units, slots_in_cache;
+  int64_t tokens, slots_in_cache;
   int kv_heads, dim, log2_bs, window;
   int32_t* status;
 };
@@ -101,8 +103,21 @@ __device__ __forceinline__ int code_of(float x, float s) {
 
 // Codes of eight values with |x| <= 127 s (up to rounding): rint(x * inv) by
 // adding 1.5 * 2^23, whose low byte is then the code.  The quotient x / s is
-// within 127 * 2^-22 of x * inv, so rounding agrees unless x * inv is within
-// 2^-12 of a half; such values (and non-finite ones) take the division.
+// within 127 * 2^-23 of x * inv (two roundings), so rounding agrees unless
+// x * inv is within 2^-15 of a half: then, and when told to be careful, the
+// eight take the division.
+__noinline__ __device__ uint2 codes8_exact(float4 a, float4 b, float s) {
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t out[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    int code[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) code[e] = code_of(v[4 * q + e], s);
+    out[q] = pack4(code);
+  }
+  return make_uint2(out[0], out[1]);
+}
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, float s, bool careful) {
   constexpr float kMagic = 12582912.f;
   float t[8], off = 0.f;
@@ -118,78 +133,102 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, float s,
     const uint32_t hi = __byte_perm(__float_as_uint(t[4 * q + 2]), __float_as_uint(t[4 * q + 3]), 0x0040);
     out[q] = __byte_perm(lo, hi, 0x5410);
   }
-  if (careful || !(off < 0.5f - 0.000244140625f)) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      int code[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) code[e] = code_of(v[4 * q + e], s);
-      out[q] = pack4(code);
-    }
-  }
+  if (careful || !(off < 0.5f - 0.000030517578125f))
+    return codes8_exact(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), s);
   return make_uint2(out[0], out[1]);
 }
 
+// Eight codes of a block times the scale they were made with.
+__device__ __forceinline__ void old_values(const uint2& w, float s_old, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = (float)(int8_t)(w.x >> (8 * e)) * s_old;
+    v[4 + e] = (float)(int8_t)(w.y >> (8 * e)) * s_old;
+  }
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) append_kernel(AppendArgs a) {
+  constexpr int kHold = 8;                         // rows that a lane of a shared run keeps
+  __shared__ uint32_t s_max[2][kWarps];
+  __shared__ float s_fin[2][kWarps];
+  const int lane = threadIdx.x & 31, which = threadIdx.x >> 7, warp = (threadIdx.x >> 5) & (kWarps - 1);
   pdl_wait();
   pdl_launch();
-  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= a.units) return;
-  const int per = 2 * a.kv_heads;
-  const int64_t win = u / per;
-  const int which = (int)(u - win * per) & 1, h = (int)(u - win * per) >> 1;
+  const unsigned win = blockIdx.x / (unsigned)a.kv_heads;
+  const int h = (int)(blockIdx.x - win * (unsigned)a.kv_heads);
+  const int bs1 = (1 << a.log2_bs) - 1;
+
+  // the slots of the window, and of the up to 127 tokens after it that a run
+  // may carry on to: lane l has slots l, l + 32, ...
+  const int64_t t0 = (int64_t)win * a.window;
+  int64_t ahead[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    ahead[i] = (i == 0 || 32 * i < a.window + bs1) && t0 + 32 * i + lane < a.tokens ? __ldg(a.slots + t0 + 32 * i + lane)
+                                                                                  : -1;
+  const int64_t prev = lane < a.window && t0 + lane > 0 && t0 + lane < a.tokens ? __ldg(a.slots + t0 + lane - 1) : -1;
+  const int64_t mine = ahead[0];
+  const bool starts = lane < a.window && mine >= 0 && !(prev >= 0 && prev + 1 == mine && (mine & bs1) != 0);
+  if (starts && mine >= a.slots_in_cache) raise_flag(a.status, LQ_DEV_RANGE);
+  uint32_t todo = __ballot_sync(0xffffffffu, starts && mine < a.slots_in_cache);
+  if (todo == 0) return;                           // the same in every warp
+  const bool shared = __popc(todo) < kWarps;
+
   const void* x = which ? a.x[1] : a.x[0];
   const int64_t ld = which ? a.ld[1] : a.ld[0];
   int8_t* cache = which ? a.cache[1] : a.cache[0];
   float* scales = which ? a.scales[1] : a.scales[0];
-  const int bs1 = (1 << a.log2_bs) - 1;
   // a lane holds 8 dimensions of a row; 32 / (dim / 8) rows side by side
-  const int chunks = a.dim >> 3, step = 32 / chunks;
-  const int r0 = lane < step * chunks ? lane / chunks : 1 << 20, k0 = 8 * (lane % chunks);
+  const int chunks = a.dim >> 3, rows_step = 32 / chunks;
+  const int k0 = 8 * (lane % chunks);
+  const int r0 = lane < rows_step * chunks ? lane / chunks + (shared ? warp * rows_step : 0) : 1 << 20;
+  const int step = shared ? kWarps * rows_step : rows_step;
 
-  // which tokens of the window start a run
-  const int64_t t0 = win * a.window;
-  int64_t mine = -1;
-  bool starts = false;
-  if (lane < a.window && t0 + lane < a.tokens) {
-    mine = __ldg(a.slots + t0 + lane);
-    const int64_t prev = t0 + lane > 0 ? __ldg(a.slots + t0 + lane - 1) : -1;
-    starts = mine >= 0 && !(prev >= 0 && prev + 1 == mine && (mine & bs1) != 0);
-    if (mine >= a.slots_in_cache) raise_flag(a.status, LQ_DEV_RANGE);
-  }
-  uint32_t todo = __ballot_sync(0xffffffffu, starts);
-  while (todo) {
+  for (int n = 0; todo; ++n) {
     const int first = __ffs(todo) - 1;
     todo &= todo - 1;
+    if (!shared && n % kWarps != warp) continue;
     const int64_t slot = __shfl_sync(0xffffffffu, mine, first), t = t0 + first;
-    const int64_t blk = slot >> a.log2_bs;
-    const int off = (int)(slot & bs1);
-    if (slot >= a.slots_in_cache) continue;
+    const int off = (int)(slot & bs1), most = bs1 + 1 - off;
+    const int64_t sc = (slot >> a.log2_bs) * a.kv_heads + h;
+    const float s_old = off > 0 ? scales[sc] : 0.f;
     // the run's length: tokens that carry on with consecutive slots of the block
     int len = 0;
-    for (int c = 0; c <= bs1 - off; c += 32) {
-      const int64_t i = t + c + lane;
-      const bool in = c + lane <= bs1 - off && i < a.tokens && __ldg(a.slots + i) == slot + c + lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      len += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-      if (m != 0xffffffffu) break;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int p = 32 * i + lane - first;         // token of the run
+      const uint32_t stop = __ballot_sync(0xffffffffu, p >= 0 && !(p < most && ahead[i] == slot + p));
+      if (len == 32 * i - (i ? first : 0)) len = stop ? 32 * i + __ffs(stop) - 1 - first : 32 * (i + 1) - first;
     }
     const int64_t src = t * ld + (int64_t)h * a.dim + k0;
-    const int64_t sc = blk * a.kv_heads + h;
     int8_t* rows = cache + (sc << a.log2_bs) * a.dim + k0;
-    const float s_old = off > 0 ? scales[sc] : 0.f;
 
+    Raw<BF16> held[kHold];
     uint32_t mb = 0;
-#pragma unroll 8
-    for (int r = r0; r < len; r += step) mb = max_bits<BF16>(mb, load_raw<BF16>(x, src + r * ld));
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * step < len) held[i] = load_raw<BF16>(x, src + (r0 + i * step) * ld);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * step < len) mb = max_bits<BF16>(mb, held[i]);
+#pragma unroll 4
+    for (int r = r0 + kHold * step; r < len; r += step) mb = max_bits<BF16>(mb, load_raw<BF16>(x, src + r * ld));
     if constexpr (BF16) mb = max(mb << 16, mb & 0xFFFF0000u);
-    for (int o = 16; o; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    const bool careful = mb >= kInf;               // something non-finite: the maximum over the rest
+    mb = __reduce_max_sync(0xffffffffu, mb);
+    if (shared) {
+      __syncthreads();                             // the run before has been read
+      if (lane == 0) s_max[which][warp] = mb;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) mb = max(mb, s_max[which][i]);
+    }
     float mx = __uint_as_float(mb);
-    if (careful) {
+    // something non-finite, in K or V where the run is shared: the maximum over the rest
+    const bool odd = mb >= kInf;
+    if (shared ? __syncthreads_or(odd) : odd) {
       mx = 0.f;
+#pragma unroll 1
       for (int r = r0; r < len; r += step) {
         float v[8];
         values<BF16>(load_raw<BF16>(x, src + r * ld), v);
@@ -197,33 +236,45 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
         for (int e = 0; e < 8; ++e)
           if (fabsf(v[e]) <= 3.402823466e38f) mx = fmaxf(mx, fabsf(v[e]));
       }
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) raise_flag(a.status, LQ_DEV_NONFINITE);
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      if (shared) {
+        if (lane == 0) s_fin[which][warp] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, s_fin[which][i]);
+      }
+      if (odd && lane == 0) raise_flag(a.status, LQ_DEV_NONFINITE);
     }
     const float s = fmaxf(s_old, __fdiv_rn(mx, 127.f));
     const float d = s > 0.f ? s : 1.f, inv = 1.f / d;
-    const bool tiny = !(inv <= 3.402823466e38f) || d < 1e-37f;   // 1/s out of the normal range
-
+    // non-finite values, or 1/s out of the normal range
+    const bool slow = odd || !(inv <= 3.402823466e38f) || d < 1e-37f;
     if (s > s_old && off > 0) {
+#pragma unroll 1
       for (int r = r0; r < off; r += step) {
         uint2* p = reinterpret_cast<uint2*>(rows + r * a.dim);
-        const uint2 w = *p;
         float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = (float)(int8_t)(w.x >> (8 * e)) * s_old;
-          v[4 + e] = (float)(int8_t)(w.y >> (8 * e)) * s_old;
-        }
-        *p = codes8(v, inv, d, tiny);
+        old_values(*p, s_old, v);
+        *p = codes8(v, inv, d, slow);
       }
     }
-#pragma unroll 4
-    for (int r = r0; r < len; r += step) {
+    int8_t* to = rows + off * a.dim;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int r = r0 + i * step;
+      if (r < len) {
+        float v[8];
+        values<BF16>(held[i], v);
+        *reinterpret_cast<uint2*>(to + r * a.dim) = codes8(v, inv, d, slow);
+      }
+    }
+#pragma unroll 2
+    for (int r = r0 + kHold * step; r < len; r += step) {
       float v[8];
       values<BF16>(load_raw<BF16>(x, src + r * ld), v);
-      *reinterpret_cast<uint2*>(rows + (off + r) * a.dim) = codes8(v, inv, d, careful || tiny);
+      *reinterpret_cast<uint2*>(to + r * a.dim) = codes8(v, inv, d, slow);
     }
-    if (lane == 0) scales[sc] = s;
+    if (lane == 0 && (!shared || warp == 0)) scales[sc] = s;
   }
 }
 
@@ -238,55 +289,68 @@ struct GatherArgs {
 };
 
 // out = code * scale, fp32 or rounded once to bf16: a warp per slot and cache,
-// 16 bytes of output per lane and step.
+// 16 bytes of output per lane and step, the loads of eight steps and the next
+// slot in flight at once.
 template <bool BF16>
 __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
-  constexpr int E = BF16 ? 8 : 4;                  // codes per lane
+  constexpr int E = BF16 ? 8 : 4;                  // codes per lane and step
+  constexpr int U = 8;
   pdl_wait();
   pdl_launch();
   const int lane = threadIdx.x & 31;
-  const int chunks = a.dim / E, per_row = a.kv_heads * chunks;
-  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < 2 * a.n; u += (int64_t)gridDim.x * 8) {
+  const unsigned chunks = (unsigned)(a.dim / E), per_row = (unsigned)a.kv_heads * chunks;
+  // c / chunks for c < 2^16, chunks <= 64: the high word of c * ceil(2^32 / chunks)
+  const unsigned magic = 0xffffffffu / chunks + 1u;
+  const int64_t warps = (int64_t)gridDim.x * 8;
+  int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int64_t slot = u < 2 * a.n ? __ldg(a.slots + (u >> 1)) : -1;
+  for (; u < 2 * a.n; u += warps) {
     const int which = (int)(u & 1);
-    const int64_t row = u >> 1, slot = __ldg(a.slots + row);
+    const int64_t next = u + warps < 2 * a.n ? __ldg(a.slots + ((u + warps) >> 1)) : -1;
     const bool ok = slot >= 0 && slot < a.slots_in_cache;
     if (slot >= a.slots_in_cache && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
     const int64_t sc0 = (slot >> a.log2_bs) * a.kv_heads;
     const int off = (int)(slot & ((1 << a.log2_bs) - 1));
     const float* scales = (which ? a.scales[1] : a.scales[0]) + sc0;
     const int8_t* codes = (which ? a.cache[1] : a.cache[0]) + ((sc0 << a.log2_bs) + off) * a.dim;
-    uint4* out = reinterpret_cast<uint4*>(which ? a.out[1] : a.out[0]) + row * per_row;
-#pragma unroll 4
-    for (int c = lane; c < per_row; c += 32) {
-      const int h = c / chunks, k = E * (c - h * chunks);
-      uint32_t w[E / 4] = {};
-      float s = 0.f;
-      if (ok) {
-        s = __ldg(scales + h);
-        const int8_t* p = codes + ((int64_t)h << a.log2_bs) * a.dim + k;
-        if constexpr (BF16) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-          w[0] = x.x; w[1] = x.y;
-        } else {
-          w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    uint4* out = reinterpret_cast<uint4*>(which ? a.out[1] : a.out[0]) + (u >> 1) * per_row;
+    for (unsigned c0 = 0; c0 < per_row; c0 += 32 * U) {
+      uint2 w[U];
+      float s[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const unsigned c = c0 + 32 * i + lane;
+        w[i] = make_uint2(0u, 0u);
+        s[i] = 0.f;
+        if (ok && c < per_row) {
+          const unsigned h = __umulhi(c, magic), k = E * (c - h * chunks);
+          const int8_t* p = codes + ((int64_t)h << a.log2_bs) * a.dim + k;
+          s[i] = __ldg(scales + h);
+          if constexpr (BF16) w[i] = __ldg(reinterpret_cast<const uint2*>(p));
+          else w[i].x = __ldg(reinterpret_cast<const uint32_t*>(p));
         }
       }
-      float v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = (float)(int8_t)(w[e >> 2] >> (8 * (e & 3))) * s;
-      uint32_t o[4];
-      if constexpr (BF16) {
+      for (int i = 0; i < U; ++i) {
+        const unsigned c = c0 + 32 * i + lane;
+        if (c >= per_row) break;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = (float)(int8_t)((e < 4 ? w[i].x : w[i].y) >> (8 * (e & 3))) * s[i];
+        uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-          o[e] = *reinterpret_cast<const uint32_t*>(&b);
+          if constexpr (BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            o[e] = *reinterpret_cast<const uint32_t*>(&b);
+          } else {
+            o[e] = __float_as_uint(v[e]);
+          }
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(v[e]);
+        out[c] = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      out[c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
+    slot = next;
   }
 }
 
@@ -335,14 +399,13 @@ extern "C" lq_status lq_kv_append(const void* k_dev, int64_t ldk, const void* v_
   a.cache[0] = k_cache_dev; a.cache[1] = v_cache_dev; a.scales[0] = k_scales_dev; a.scales[1] = v_scales_dev;
   a.slots = slots_dev; a.tokens = tokens; a.slots_in_cache = num_blocks * block_size;
   a.kv_heads = kv_heads; a.dim = head_dim; a.log2_bs = serve::log2_of(block_size); a.status = dev_status_dev;
-  // tokens that one warp looks through for runs: one while that fits one wave
-  // of resident warps (decode steps: every token is a run), up to 32 for long
+  // tokens that one CTA looks through for runs: one while that fits one wave of
+  // resident CTAs (decode steps: every token is a run), up to 32 for long
   // prompts, where most tokens start none
-  const int64_t warps = tokens * 2 * kv_heads, wave = (int64_t)sms * 64;
-  int64_t window = (warps + wave - 1) / wave;
+  const int64_t ctas = tokens * kv_heads, wave = (int64_t)sms * 8;
+  int64_t window = (ctas + wave - 1) / wave;
   a.window = (int)(window > 32 ? 32 : window);
-  a.units = (tokens + a.window - 1) / a.window * 2 * kv_heads;
-  const int64_t grid = (a.units + paged::kWarps - 1) / paged::kWarps;
+  const int64_t grid = (tokens + a.window - 1) / a.window * kv_heads;
   if (grid > INT32_MAX) return LQ_ERR_SHAPE;
   return dtype == LQ_BF16 ? serve::launch(paged::append_kernel<true>, (unsigned)grid, paged::kThreads, 0, stream, a)
                           : serve::launch(paged::append_kernel<false>, (unsigned)grid, paged::kThreads, 0, stream, a);

@@ -13,13 +13,18 @@
 // one lane (lane i of a head holds 4 i .. 4 i + 3 and the four dimensions
 // rot/2 further; two 8-byte bf16 loads, 128 bytes per head and load) and no
 // value is exchanged but the norm's sum.  A head takes the smallest
-// power-of-two group of lanes that holds it (two heads of 128 per warp).  A
-// warp handles IT rounds of heads of one token and one kind (query or key)
-// with all their loads in flight at once, and forms the products of cosine,
-// sine and weight once for all of them.
+// power-of-two group of lanes that holds it (two heads of 128 per warp).  A unit is IT
+// rounds of heads of one token and one kind (query or key), whose loads are in
+// flight at once and which share the products of cosine, sine and weight.  A
+// warp goes from unit to unit with the next one's values, the angles of the
+// next one's position and the position after that under way: one unit per warp
+// measured 81 us for a prompt of 8191 tokens and 72 heads of 128, most of it
+// the latency of position, angles and values one after the other.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"
+
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -36,7 +41,7 @@ struct Args {
   void* ko;
   int64_t ldq, ldk, ldqo, ldko;
   int q_heads, kv_heads, dim, rot, interleaved;
-  int64_t tokens, max_pos;
+  int64_t tokens, units, max_pos;
   int units_per_token, q_units;
   const float* qw;
   const float* kw;
@@ -69,10 +74,41 @@ __device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, flo
   }
 }
 
+// Four values as loaded.
+template <bool BF16>
+struct Four {
+  uint32_t w[BF16 ? 2 : 4];
+};
+template <bool BF16>
+__device__ __forceinline__ Four<BF16> fetch4(const void* p, int64_t i) {
+  Four<BF16> f;
+  if constexpr (BF16) {
+    const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+    f.w[0] = x.x; f.w[1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i);
+    f.w[0] = x.x; f.w[1] = x.y; f.w[2] = x.z; f.w[3] = x.w;
+  }
+  return f;
+}
+// Values 2 i and 2 i + 1 of it.
+template <bool BF16>
+__device__ __forceinline__ float2 pair_of(const Four<BF16>& f, int i) {
+  if constexpr (BF16) return make_float2(__uint_as_float(f.w[i] << 16), __uint_as_float(f.w[i] & 0xFFFF0000u));
+  else return make_float2(__uint_as_float(f.w[2 * i]), __uint_as_float(f.w[2 * i + 1]));
+}
+
+// A unit of work: token, kind, first head of this lane's group.
+struct Unit {
+  unsigned t;
+  int h0, heads;
+  bool is_q;
+};
+
 // G: lanes per head (a power of two, >= dim / 8); IT: rounds of 32 / G heads
-// per warp; INTER: interleaved pairs.
+// per unit; INTER: interleaved pairs.
 template <bool BF16, int G, int IT, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
   constexpr int H = 32 / G;
   const int lane = threadIdx.x & 31, sub = lane & (G - 1);
   const bool in_head = 8 * sub < a.dim;
@@ -81,84 +117,127 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
   // this lane's dimensions: o0 .. o0 + 3 and o1 .. o1 + 3
   const int o0 = (!INTER && rotates) ? 4 * sub : 8 * sub;
   const int o1 = (!INTER && rotates) ? half + 4 * sub : 8 * sub + 4;
-  pdl_wait();
-  pdl_launch();
-  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const unsigned t = u / (unsigned)a.units_per_token;
-  if (t >= a.tokens) return;                      // whole warps only
-  int unit = (int)(u - t * (unsigned)a.units_per_token);
-  const bool is_q = unit < a.q_units;
-  if (!is_q) unit -= a.q_units;
-  const int heads = is_q ? a.q_heads : a.kv_heads;
-  const int h0 = unit * (IT * H) + lane / G;
-  const void* src = is_q ? a.q : a.k;
-  void* dst = is_q ? a.qo : a.ko;
-  const int64_t from = t * (is_q ? a.ldq : a.ldk) + (int64_t)h0 * a.dim;
-  const int64_t to = t * (is_q ? a.ldqo : a.ldko) + (int64_t)h0 * a.dim;
-  const int pos = __ldg(a.positions + t);
-
-  float v[IT][8];
+  const unsigned units = (unsigned)a.units, warps = gridDim.x * kWarps;
+  auto unit_of = [&](unsigned u) {
+    Unit x;
+    x.t = u / (unsigned)a.units_per_token;
+    int i = (int)(u - x.t * (unsigned)a.units_per_token);
+    x.is_q = i < a.q_units;
+    if (!x.is_q) i -= a.q_units;
+    x.heads = x.is_q ? a.q_heads : a.kv_heads;
+    x.h0 = i * (IT * H) + lane / G;
+    return x;
+  };
+  auto fetch = [&](const Unit& x, Four<BF16> (&v)[IT][2]) {
+    const void* src = x.is_q ? a.q : a.k;
+    const int64_t from = x.t * (x.is_q ? a.ldq : a.ldk) + (int64_t)x.h0 * a.dim;
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    if (h0 + it * H < heads && in_head) {
-      load4<BF16>(src, from + it * H * a.dim + o0, v[it]);
-      load4<BF16>(src, from + it * H * a.dim + o1, v[it] + 4);
-    } else {
+    for (int it = 0; it < IT; ++it)
+      if (x.h0 + it * H < x.heads && in_head) {
+        v[it][0] = fetch4<BF16>(src, from + it * H * a.dim + o0);
+        v[it][1] = fetch4<BF16>(src, from + it * H * a.dim + o1);
+      }
+  };
+  auto angles = [&](int pos, float (&cs)[4], float (&sn)[4]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[it][e] = 0.f;
-    }
-  }
-
-  // y[e] = r (c[e] v[e] + s[e] v[partner of e]): the weights ride along
-  float c[8], s[8];
-  const float* w = is_q ? a.qw : a.kw;
-  {
-    float wv[8];
-    if (w != nullptr && in_head) {
-      load4<false>(w, o0, wv);
-      load4<false>(w, o1, wv + 4);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wv[e] = 1.f;
-    }
-    const bool pos_ok = pos >= 0 && pos < a.max_pos;
-    if (!pos_ok && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
-    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-    if (rotates && pos_ok) {
+    for (int i = 0; i < 4; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
+    if (rotates && pos >= 0 && pos < a.max_pos) {
       load4<false>(a.cos_sin, (int64_t)pos * a.rot + 4 * sub, cs);
       load4<false>(a.cos_sin, (int64_t)pos * a.rot + half + 4 * sub, sn);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = INTER ? 2 * i : i, q = INTER ? 2 * i + 1 : i + 4;
-      c[p] = cs[i] * wv[p];
-      c[q] = cs[i] * wv[q];
-      s[p] = -sn[i] * wv[q];
-      s[q] = sn[i] * wv[p];
-    }
-  }
+  };
+  pdl_wait();
+  pdl_launch();
 
-#pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    float r = 1.f;
-    if (w != nullptr) {                           // the same in the whole warp
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x = fmaf(v[it][e], v[it][e], x);
-#pragma unroll
-      for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      r = rsqrtf(fmaf(x, a.inv_dim, a.eps));
+  unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= units) return;                         // whole warps only
+  Unit now = unit_of(u), next = unit_of(min(u + warps, units - 1));
+  Four<BF16> v[IT][2], vn[IT][2];
+  float cs[4], sn[4], csn[4], snn[4];
+  int pos = __ldg(a.positions + now.t), pos_next = __ldg(a.positions + next.t);
+  fetch(now, v);
+  angles(pos, cs, sn);
+  for (;;) {
+    const bool more = u + warps < units;
+    Unit after = next;
+    int pos_after = pos_next;
+    if (more) {
+      fetch(next, vn);
+      angles(pos_next, csn, snn);
+      after = unit_of(min(u + 2 * warps, units - 1));
+      pos_after = __ldg(a.positions + after.t);
     }
-    float y[8];
+
+    // y[e] = r (c[e] v[e] + s[e] v[partner of e]): the weights ride along
+    float2 c[4], s[4];
+    const float* w = now.is_q ? a.qw : a.kw;
+    {
+      float wv[8];
+      if (w != nullptr && in_head) {
+        load4<false>(w, o0, wv);
+        load4<false>(w, o1, wv + 4);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int p = INTER ? e ^ 1 : e ^ 4;
-      y[e] = r * fmaf(s[e], v[it][p], c[e] * v[it][e]);
+        for (int e = 0; e < 8; ++e) wv[e] = 1.f;
+      }
+      float cc[8], ss[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = INTER ? 2 * i : i, q = INTER ? 2 * i + 1 : i + 4;
+        cc[p] = cs[i] * wv[p];
+        cc[q] = cs[i] * wv[q];
+        ss[p] = -sn[i] * wv[q];
+        ss[q] = sn[i] * wv[p];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = make_float2(cc[2 * e], cc[2 * e + 1]);
+        s[e] = make_float2(ss[2 * e], ss[2 * e + 1]);
+      }
     }
-    if (h0 + it * H < heads && in_head) {
-      store4<BF16>(dst, to + it * H * a.dim + o0, y[0], y[1], y[2], y[3]);
-      store4<BF16>(dst, to + it * H * a.dim + o1, y[4], y[5], y[6], y[7]);
+    if (!(pos >= 0 && pos < a.max_pos) && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
+    void* dst = now.is_q ? a.qo : a.ko;
+    const int64_t to = now.t * (now.is_q ? a.ldqo : a.ldko) + (int64_t)now.h0 * a.dim;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const bool here = now.h0 + it * H < now.heads && in_head;
+      float2 x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = here ? pair_of<BF16>(v[it][e >> 1], e & 1) : make_float2(0.f, 0.f);
+      float r = 1.f;
+      if (w != nullptr) {                         // the same in the whole warp
+        float2 q = mul2(x[0], x[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) q = fma2(x[e], x[e], q);
+        float z = q.x + q.y;
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        r = rsqrtf(fmaf(z, a.inv_dim, a.eps));
+      }
+      const float2 r2 = make_float2(r, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = INTER ? make_float2(x[e].y, x[e].x) : x[e ^ 2];
+        y[e] = mul2(r2, fma2(s[e], p, mul2(c[e], x[e])));
+      }
+      if (here) {
+        store4<BF16>(dst, to + it * H * a.dim + o0, y[0].x, y[0].y, y[1].x, y[1].y);
+        store4<BF16>(dst, to + it * H * a.dim + o1, y[2].x, y[2].y, y[3].x, y[3].y);
+      }
     }
+    if (!more) break;
+    u += warps;
+    now = next;
+    next = after;
+    pos = pos_next;
+    pos_next = pos_after;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      v[it][0] = vn[it][0];
+      v[it][1] = vn[it][1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { cs[i] = csn[i]; sn[i] = snn[i]; }
   }
 }
 
@@ -166,20 +245,23 @@ template <bool BF16, int G>
 lq_status launch_rope(Args& a, int sms, void* stream) {
   constexpr int H = 32 / G;
   auto units = [&](int it) { return (a.q_heads + it * H - 1) / (it * H) + (a.kv_heads + it * H - 1) / (it * H); };
-  // four rounds per warp keep four heads' loads in flight; a call whose warps
-  // would not fill the SMs twice takes one round per warp
-  const bool wide = a.tokens * units(4) >= (int64_t)sms * 2 * kWarps;
-  const int it = wide ? 4 : 1;
+  // four rounds per unit (two for fp32, whose values take twice the registers);
+  // one where that would leave SMs without a unit per warp
+  constexpr int kMost = BF16 ? 4 : 2;
+  const int it = a.tokens * units(kMost) >= (int64_t)sms * kWarps ? kMost : 1;
   a.units_per_token = units(it);
   a.q_units = (a.q_heads + it * H - 1) / (it * H);
-  const int64_t grid = (a.tokens * a.units_per_token + kWarps - 1) / kWarps;
-  if (grid > INT32_MAX / kWarps) return LQ_ERR_SHAPE;
+  a.units = a.tokens * a.units_per_token;
+  if (a.units > INT32_MAX / 2) return LQ_ERR_SHAPE;
+  int64_t grid = (a.units + kWarps - 1) / kWarps;
+  if (grid > (int64_t)sms * 3) grid = (int64_t)sms * 3;
   const unsigned n = (unsigned)grid;
-  if (a.interleaved)
-    return wide ? serve::launch(norm_rope_kernel<BF16, G, 4, true>, n, kThreads, 0, stream, a)
-                : serve::launch(norm_rope_kernel<BF16, G, 1, true>, n, kThreads, 0, stream, a);
-  return wide ? serve::launch(norm_rope_kernel<BF16, G, 4, false>, n, kThreads, 0, stream, a)
-              : serve::launch(norm_rope_kernel<BF16, G, 1, false>, n, kThreads, 0, stream, a);
+  auto go = [&](auto inter) {
+    constexpr bool I = decltype(inter)::value;
+    if (it == 1) return serve::launch(norm_rope_kernel<BF16, G, 1, I>, n, kThreads, 0, stream, a);
+    return serve::launch(norm_rope_kernel<BF16, G, kMost, I>, n, kThreads, 0, stream, a);
+  };
+  return a.interleaved ? go(std::true_type{}) : go(std::false_type{});
 }
 
 template <bool BF16>

@@ -58,8 +58,13 @@ __device__ __forceinline__ float at(const void* p, int64_t i) {
 }
 
 // floor(2^36 w) of a weight in [0, 4]; NaN and negative weights count as zero.
+// From the bits, mantissa shifted by exponent: the conversion instruction to 64
+// bits would bound the kernel.
 __device__ __forceinline__ unsigned long long whole(float w) {
-  return w > 0.f ? __float2ull_rz(fminf(w, 4.f) * 68719476736.f) : 0ull;
+  const uint32_t bits = __float_as_uint(fminf(fmaxf(w, 0.f), 4.f));       // (fmaxf of NaN and 0 is 0)
+  const int e = (int)(bits >> 23);                                        // w = 1.m 2^(e - 127)
+  const uint32_t top = bits << 8 | 0x80000000u;
+  return e < 91 ? 0ull : ((unsigned long long)top << 32) >> (154 - e);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

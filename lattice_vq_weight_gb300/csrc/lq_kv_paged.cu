@@ -18,7 +18,7 @@
 // once and in one round of loads; where a window holds many runs (decode steps)
 // each warp takes runs of its own.  An IEEE division per value would bound the
 // kernel, so codes come from a product with 1/s wherever that is clear of a
-// half by more than its error, and from the division where it is not.
+// half by more than its error, and from the exact remainder where it is not.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"
@@ -101,11 +101,8 @@ __device__ __forceinline__ int code_of(float x, float s) {
   return fabsf(x) <= 3.402823466e38f ? (int)fminf(fmaxf(q, -127.f), 127.f) : 0;
 }
 
-// Codes of eight values with |x| <= 127 s (up to rounding): rint(x * inv) by
-// adding 1.5 * 2^23, whose low byte is then the code.  The quotient x / s is
-// within 127 * 2^-23 of x * inv (two roundings), so rounding agrees unless
-// x * inv is within 2^-15 of a half: then, and when told to be careful, the
-// eight take the division.
+// Eight codes by division: for values that are not finite and for 1/s out of
+// the normal range.
 __noinline__ __device__ uint2 codes8_exact(float4 a, float4 b, float s) {
   const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t out[2];
@@ -118,13 +115,38 @@ __noinline__ __device__ uint2 codes8_exact(float4 a, float4 b, float s) {
   }
   return make_uint2(out[0], out[1]);
 }
+// rint of the IEEE quotient x / s by its remainder, given the sign-carrying
+// nearest half h = n +- 1/2 of x * inv: the quotient is h itself (and goes to the
+// even neighbour) when |x - h s| is at most half a unit in h's last place times
+// s, else on the side of h that the exact remainder tells.  (Below 1/2 units are
+// half as large.)
+__device__ __forceinline__ float by_remainder(float x, float h, float s) {
+  const float e = fmaf(-h, s, x);                  // exact where it is small
+  float unit = __uint_as_float(__float_as_uint(h) & 0x7F800000u) * 5.9604644775390625e-8f;      // 2^-24
+  const bool away = (__float_as_uint(e) ^ __float_as_uint(h)) >> 31 == 0;       // |x / s| > |h|
+  if (fabsf(h) == 0.5f && !away) unit *= 0.5f;
+  return fabsf(e) <= unit * s ? rintf(h) : h + copysignf(0.5f, e);
+}
+
+// Codes of eight values with |x| <= 127 s (up to rounding): rint(x * inv) by
+// adding 1.5 * 2^23, whose low byte is then the code.  The quotient x / s is
+// within 127 * 2^-23 of x * inv (two roundings), so rounding agrees unless
+// x * inv is within 2^-15 of a half; bf16 values are often exactly there (half of
+// the block's largest is), so that case is settled by remainders, not divisions.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, float s, bool careful) {
   constexpr float kMagic = 12582912.f;
-  float t[8], off = 0.f;
+  float t[8], f[8], off = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     t[e] = fmaf(v[e], inv, kMagic);
-    off = fmaxf(off, fabsf(fmaf(v[e], inv, kMagic - t[e])));
+    f[e] = fmaf(v[e], inv, kMagic - t[e]);
+    off = fmaxf(off, fabsf(f[e]));
+  }
+  if (careful) return codes8_exact(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), s);
+  if (off > 0.5f - 0.000030517578125f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      t[e] = kMagic + by_remainder(v[e], (t[e] - kMagic) + copysignf(0.5f, f[e]), s);
   }
   uint32_t out[2];
 #pragma unroll
@@ -133,8 +155,6 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, float s,
     const uint32_t hi = __byte_perm(__float_as_uint(t[4 * q + 2]), __float_as_uint(t[4 * q + 3]), 0x0040);
     out[q] = __byte_perm(lo, hi, 0x5410);
   }
-  if (careful || !(off < 0.5f - 0.000030517578125f))
-    return codes8_exact(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), s);
   return make_uint2(out[0], out[1]);
 }
 

@@ -136,11 +136,13 @@ __device__ __forceinline__ float by_remainder(float x, float h, float s) {
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, float s, bool careful) {
   constexpr float kMagic = 12582912.f;
   float t[8], f[8], off = 0.f;
+  const float2 inv2 = make_float2(inv, inv), magic2 = make_float2(kMagic, kMagic);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    t[e] = fmaf(v[e], inv, kMagic);
-    f[e] = fmaf(v[e], inv, kMagic - t[e]);
-    off = fmaxf(off, fabsf(f[e]));
+  for (int e = 0; e < 8; e += 2) {
+    const float2 x = make_float2(v[e], v[e + 1]), t2 = fma2(x, inv2, magic2), f2 = fma2(x, inv2, sub2(magic2, t2));
+    t[e] = t2.x; t[e + 1] = t2.y;
+    f[e] = f2.x; f[e + 1] = f2.y;
+    off = fmaxf(off, fmaxf(fabsf(f2.x), fabsf(f2.y)));
   }
   if (careful) return codes8_exact(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), s);
   if (off > 0.5f - 0.000030517578125f) {

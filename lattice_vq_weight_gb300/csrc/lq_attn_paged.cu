@@ -131,7 +131,8 @@ __device__ __forceinline__ uint32_t code_at(int t, int b) {
 __device__ __forceinline__ bool same(const Tag& x, const Tag& y) { return x.i == y.i && x.rt == y.rt && x.h == y.h; }
 
 // Where a row of a row tile lies in q or out, in elements; false past the last row.
-__device__ __forceinline__ bool row_at(const Args& a, int q0, int q_len, int R, int h, int64_t ld, int dim, int64_t* at) {
+__device__ __forceinline__ bool row_at(const Args& a, int q0, int q_len, int R, int h, int64_t ld, int dim,
+                                       int64_t* at) {
   const int j = R / a.group;
   *at = (int64_t)(q0 + j) * ld + (h * a.group + R - j * a.group) * dim;
   return j < q_len;
@@ -149,7 +150,8 @@ __device__ __forceinline__ void store_out4(const Args& a, int64_t at, const floa
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) =
         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   } else {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
@@ -252,7 +254,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int n = (int)(part_n < (1 << 29) ? part_n : (1 << 29));
   Cursor ci;                                   // the tile whose halves are fetched next
   if (n > 0) {
-    int lo = 0, hi = a.batch;                  // last request with pre[i] <= u0 (it has tiles: the next one starts later)
+    int lo = 0, hi = a.batch;                  // last request with pre[i] <= u0: it has tiles
 #pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -907,6 +909,18 @@ int cta_count() {
   return sms <= 0 ? 152 : sms < kMergeThreads ? sms : kMergeThreads;
 }
 
+// Whether the tensor-core kernel takes a bf16 call: by the query rows that an
+// average request has for each kv head.  Its time hardly depends on them up to
+// 256, the split kernel's grows with every 16.  Measured at 8 kv heads of 128,
+// 16 / 24 / 32 / 64 rows: 16 requests of 4000 tokens 64 us against 52 / 85 / 85 /
+// 153; one of 32000 tokens 46 to 54 us against 34 / 50 / 50 / 83; one of 4000
+// tokens 27 us against 18 / 21 / 21 / 25.  (head_dim 64 and 256 cross there too.)
+bool many_rows(int batch, int64_t total_q, int group) {
+  return batch > 0 && (total_q + batch - 1) / batch * group > 16;
+}
+
+size_t meta_bytes(int ctas) { return (ctas * 2 * sizeof(Tag) + 255) & ~(size_t)255; }
+
 }  // namespace attn
 }  // namespace lq
 
@@ -918,10 +932,14 @@ extern "C" size_t lq_attention_paged_workspace_size(int batch, int64_t total_q, 
       q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   // per CTA two pieces and what they belong to, and one for each of up to 16
-  // warps, of up to 16 rows
-  const size_t ctas = (size_t)attn::cta_count();
-  const size_t meta = (ctas * 2 * sizeof(attn::Tag) + 255) & ~(size_t)255;
-  return meta + ctas * (2 + 16) * 16 * (size_t)(head_dim + 2) * sizeof(float);
+  // warps, of up to 16 rows; or what the tensor-core kernel leaves
+  const int ctas = attn::cta_count(), group = q_heads / kv_heads;
+  size_t floats = (size_t)ctas * (2 + 16) * 16 * (size_t)(head_dim + 2);
+  if (attn::many_rows(batch, total_q, group)) {
+    const attn::TilePlan p = attn::plan_tiles(batch, total_q, group, kv_heads, head_dim, INT64_MAX, ctas);
+    if (p.part_floats > floats) floats = p.part_floats;
+  }
+  return attn::meta_bytes(ctas) + floats * sizeof(float);
 }
 
 extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtype, int64_t total_q,
@@ -970,19 +988,21 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   a.scale_log2 = sm_scale * 1.4426950408889634f; a.out = out_dev; a.ldo = ldo; a.status = dev_status_dev;
   a.meta = reinterpret_cast<attn::Tag*>(workspace_dev);
   const int ctas = attn::cta_count();
-  const size_t meta = ((size_t)ctas * 2 * sizeof(attn::Tag) + 255) & ~(size_t)255;
-  a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + meta);
+  a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + attn::meta_bytes(ctas));
   // a pool without blocks: no copy is issued, any valid map will do
   const int8_t* kc = num_blocks > 0 ? k_cache_dev : reinterpret_cast<const int8_t*>(workspace_dev);
   const int8_t* vc = num_blocks > 0 ? v_cache_dev : reinterpret_cast<const int8_t*>(workspace_dev);
   const int64_t bytes = num_blocks > 0 ? num_blocks * block_rows * 128 : 32768;
-  const int64_t avg_rows = ((total_q + batch - 1) / batch) * a.group;
-  if (avg_rows > 64 && dtype == LQ_BF16) return attn::launch_attn_tiles(a, kc, vc, bytes, head_dim, stream);
+  if (dtype == LQ_BF16 && attn::many_rows(batch, total_q, a.group))
+    return attn::launch_attn_tiles(a, kc, vc, bytes, head_dim,
+                                   attn::plan_tiles(batch, total_q, a.group, kv_heads, head_dim,
+                                                    (int64_t)table_width * block_size, ctas),
+                                   stream);
   CUtensorMap mk, mv;
   const int box = (block_size < attn::kTile ? block_size : attn::kTile) * head_dim / 128;
   if (!attn::encode_cache(&mk, kc, bytes, box) || !attn::encode_cache(&mv, vc, bytes, box)) return LQ_ERR_CUDA;
   // eight query rows per pass over the codes, sixteen where the average request has more
-  const bool few = avg_rows <= 8;
+  const bool few = ((total_q + batch - 1) / batch) * a.group <= 8;
   if (dtype == LQ_F32) {
     if (head_dim == 64) return attn::launch_split<64, 1, true>(a, mk, mv, ctas, stream);
     if (head_dim == 128) return attn::launch_split<128, 1, true>(a, mk, mv, ctas, stream);

@@ -116,9 +116,18 @@ __device__ __forceinline__ Request load_request(const Args& a, int i) {
 // `lines` of them, at most 256, in the 128-byte swizzle.
 bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int lines);
 
-// The kernel for many query rows (lq_attn_paged_tiles.cu).
+// The kernel for many query rows (lq_attn_paged_tiles.cu): its units of work
+// (pairs of row tiles of a kv head, at most so many), the CTAs that share one,
+// and what they leave in the workspace.
+struct TilePlan {
+  int64_t units;
+  int splits;
+  size_t part_floats;
+};
+// most_tokens: positions that any request can have.
+TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms);
 lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int64_t cache_bytes, int head_dim,
-                            void* stream);
+                            const TilePlan& plan, void* stream);
 
 }  // namespace attn
 }  // namespace lq

@@ -12,8 +12,8 @@
 // One warp fetches the codes of a tile by TMA, up to two half tiles (K, V)
 // ahead; warps 0..3 turn them into fp16, exactly, in two stages of shared
 // memory; four warps per row tile hold its rows' maxima and sums; one warp
-// issues the products.  (Codes fetched through registers instead measured 340
-// against TMA's PROMPT us for a 2000-token chunk: the L1 that this much shared
+// issues the products.  (Codes fetched through registers instead made the
+// converting warps the slowest part: the L1 that this much shared
 // memory leaves holds too few loads in flight.)
 // K and V tiles have the same layout, rows of 64 dimensions in the 128-byte
 // swizzle, which the products read along either axis (K-major for the scores,
@@ -29,6 +29,10 @@
 // only when the maximum really moves.  bf16 only: the tensor core's accumulator
 // truncates, 6e-5 of the output after 30000 positions (measured), which fp32
 // outputs would show; they stay with the split kernel at any number of rows.
+// Few row tiles (a short chunk over a long cache) would leave SMs idle: then
+// several CTAs share one, a range of the positions each, and a second kernel
+// joins their outputs, in the order of the positions.
+//
 // Every wait is bounded (about a second of clock cycles); on expiry
 // LQ_DEV_TIMEOUT is recorded and the CTA winds down.
 #include "lq_attn_paged.cuh"
@@ -67,6 +71,7 @@ struct TileCfg {
 struct TileArgs {
   CUtensorMap map_k, map_v;      // boxes of a block's codes, or of BN tokens of it
   Args a;
+  int splits;                    // CTAs per pair of row tiles and kv head
 };
 
 __device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
@@ -280,7 +285,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   }
 
   // this CTA's request and row tile, the last rows first: they see the most
-  const int h = blockIdx.x % a.kv_heads, item = blockIdx.x / a.kv_heads;
+  const int split = blockIdx.x % ta.splits, unit = blockIdx.x / ta.splits;
+  const int h = unit % a.kv_heads, item = unit / a.kv_heads;
   {
     const int per = (a.batch + C::kThreads - 1) / C::kThreads;
     const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
@@ -316,7 +322,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     }
     __syncthreads();
   }
-  if (found[0] < 0) return;                                 // fewer row tiles than CTAs
+  if (found[0] < 0) {                                       // fewer row tiles than CTAs
+    if (ta.splits > 1 && split == 0 && threadIdx.x == 0) a.meta[unit].valid = 0;
+    return;
+  }
   const int req = found[0], row0 = found[1] * C::kRows;
   const Request r = load_request(a, req);
   const int rows = r.q_len * a.group;
@@ -327,8 +336,16 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     const int seen = min(r.len, r.shown + last / a.group + 1);
     return seen > 0 ? (seen + BN - 1) / BN : 0;
   };
-  const int n0 = tiles_seen(0), n1 = T > 1 ? tiles_seen(1) : 0, tiles = max(n0, n1);
-  const int seen = min(r.len, tiles * BN);                  // tokens fetched
+  const int all0 = tiles_seen(0), all1 = T > 1 ? tiles_seen(1) : 0, all = max(all0, all1);
+  // this CTA's tiles: `first` and the ones after it
+  const int first = (int)((int64_t)all * split / ta.splits), past = (int)((int64_t)all * (split + 1) / ta.splits);
+  const int n0 = max(0, min(all0, past) - first), n1 = max(0, min(all1, past) - first), tiles = max(n0, n1);
+  const int seen = min(r.len, past * BN);                   // tokens fetched end here
+  if (ta.splits > 1 && split == 0 && threadIdx.x == 0) {
+    Tag tag = {};
+    tag.i = req; tag.h = h; tag.rt = found[1]; tag.q0 = r.q0; tag.q_len = r.q_len; tag.valid = 1;
+    a.meta[unit] = tag;
+  }
   const int32_t* table = a.table + (int64_t)req * a.ldt;
 
   if (warp == C::kMmaWarp) {
@@ -399,12 +416,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       const int step = min(1 << a.log2_bs, BN), parts = BN / step;
       const int block_lines = (D << a.log2_bs) >> 7;
       auto look_up = [&](int j) {
-        const int pos = j * BN + step * lane;
+        const int pos = (first + j) * BN + step * lane;
         return lane < parts && pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
       };
       int blk = look_up(0), issued = 0;
       for (int j = 0; j < tiles; ++j) {
-        const int pos = j * BN + step * lane;
+        const int pos = (first + j) * BN + step * lane;
         const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
         if (!ok && lane < parts && pos < seen) raise_flag(a.status, LQ_DEV_RANGE);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * step * D;
@@ -416,7 +433,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
           if (!go) break;
           if (lane == 0) mbar_expect_tx(&raw_full[v], bytes);
           __syncwarp();
-          if (ok) tma_load_2d(raw + v * C::kRawBytes + lane * step * D, v ? &ta.map_v : &ta.map_k, &raw_full[v], 0, line);
+          if (ok)
+            tma_load_2d(raw + v * C::kRawBytes + lane * step * D, v ? &ta.map_v : &ta.map_k, &raw_full[v], 0, line);
           ++issued;
         }
         if (!go) break;
@@ -466,7 +484,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
         const uint32_t d = tmem_o + t * D, w = tmem_s + t * BN;
         if (elect()) {
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k) mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, true>::v, j > 0 || k > 0);
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, true>::v, j > 0 || k > 0);
           mma_commit(&o_done[t]);
           if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
         }
@@ -545,7 +564,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     // value scale -1: a block that is not there
     float nk = 0.f, nv = -1.f;
     auto fetch_scales = [&](int j) {
-      const int pos = j * BN + 16 * lane;
+      const int pos = (first + j) * BN + 16 * lane;
       nk = 0.f;
       nv = -1.f;
       if (lane < BN / 16 && pos < seen) {
@@ -569,8 +588,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (lane < BN / 16) sc[lane] = make_float4(nk, lg2(cvm), rcp(cvm) * kSumUnit, 0.f);
       __syncwarp();
       if (j + 1 < n) fetch_scales(j + 1);
-      const int vis0 = lim - j * BN;
-      const bool masked = (j + 1) * BN - 1 > lim_min || zero != 0;    // (a missing block counts as zero too)
+      const int vis0 = lim - (first + j) * BN;
+      const bool masked = (first + j + 1) * BN - 1 > lim_min || zero != 0;    // (a missing block counts as zero too)
       ok = __all_sync(0xffffffffu, wait_on(&s_full[t], (uint32_t)j & 1, timeout));
       if (!ok) break;
       tc_after();
@@ -621,6 +640,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     if (ok) {
       const float inv = l == 0.f ? 0.f : kSumUnit / l;
       const int64_t dst = (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D;
+      // with the positions split: the row's sums as they are
+      float* piece = a.part + ((int64_t)blockIdx.x * C::kRows + t * kTileRows + row) * (D + 4);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -630,7 +651,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (mine) {
+        if (ta.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(piece + 32 * c)[e] =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else if (mine) {
           uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + dst + 32 * c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -644,6 +670,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
             p[e] = make_uint4(u[0], u[1], u[2], u[3]);
           }
         }
+      }
+      if (ta.splits > 1) {
+        piece[D] = mx;
+        piece[D + 1] = l;
       }
     }
   }
@@ -666,8 +696,48 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   if (threadIdx.x == 0 && timeout_flag) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 
+// Joins the pieces of rows whose positions were split: a warp per row, D / 32
+// neighbouring dimensions per lane.
 template <int D>
-lq_status launch_tiles(const TileArgs& ta, int64_t ctas, void* stream) {
+__global__ void __launch_bounds__(256) attn_tiles_merge_kernel(const __grid_constant__ TileArgs ta) {
+  using C = TileCfg<D>;
+  constexpr int E = D / 32;
+  const Args& a = ta.a;
+  pdl_wait();
+  pdl_launch();
+  const int unit = blockIdx.x / (C::kRows / 8), row = (blockIdx.x % (C::kRows / 8)) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const Tag tag = a.meta[unit];
+  const int R = tag.rt * C::kRows + row, j = R / a.group;
+  if (!tag.valid || j >= tag.q_len) return;
+  const float* piece = a.part + ((int64_t)unit * ta.splits * C::kRows + row) * (D + 4);
+  constexpr int64_t next = (int64_t)C::kRows * (D + 4);
+  float M = -INFINITY;
+  for (int p = 0; p < ta.splits; ++p) M = fmaxf(M, piece[p * next + D]);
+  float o[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < ta.splits; ++p) {
+    const float m = piece[p * next + D], f = m == M ? 1.f : ex2(m - M);
+    l = fmaf(piece[p * next + D + 1], f, l);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(piece + p * next + E * lane + e);
+      o[e] = fmaf(v.x, f, o[e]);
+      o[e + 1] = fmaf(v.y, f, o[e + 1]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : kSumUnit / l;
+  const int64_t dst = (int64_t)(tag.q0 + j) * a.ldo + (int64_t)(tag.h * a.group + R - j * a.group) * D + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + dst + e) =
+        __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+}
+
+template <int D>
+lq_status launch_tiles(const TileArgs& ta, const TilePlan& plan, void* stream) {
   using C = TileCfg<D>;
   static_assert(C::kSmem + 1536 <= 227 * 1024, "shared memory");
   auto kern = attn_tiles_kernel<D>;
@@ -675,25 +745,42 @@ lq_status launch_tiles(const TileArgs& ta, int64_t ctas, void* stream) {
     cudaGetLastError();
     return LQ_ERR_CUDA;
   }
-  return serve::launch(kern, (unsigned)ctas, C::kThreads, C::kSmem, stream, ta);
+  const lq_status st =
+      serve::launch(kern, (unsigned)(plan.units * plan.splits), C::kThreads, C::kSmem, stream, ta);
+  if (st != LQ_OK || plan.splits == 1) return st;
+  return serve::launch(attn_tiles_merge_kernel<D>, (unsigned)(plan.units * (C::kRows / 8)), 256, 0, stream, ta);
+}
+
+TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms) {
+  TilePlan p;
+  const int rows = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;
+  const int bn = head_dim == 256 ? TileCfg<256>::BN : TileCfg<128>::BN;
+  // as many row tiles as there can be: every request's last one may be partial
+  p.units = (total_q * group / rows + (batch < total_q ? batch : total_q)) * kv_heads;
+  // split the positions where half the SMs or more would have no CTA, into parts
+  // of at least four tiles
+  int64_t splits = p.units > 0 ? sms / p.units : 1;
+  const int64_t most = most_tokens / (4 * bn);
+  if (splits > most) splits = most;
+  p.splits = splits > 1 ? (int)splits : 1;
+  p.part_floats = p.splits > 1 ? (size_t)p.units * p.splits * rows * (head_dim + 4) : 0;
+  return p;
 }
 
 lq_status launch_attn_tiles(const Args& a, const int8_t* kc, const int8_t* vc, int64_t cache_bytes, int head_dim,
-                            void* stream) {
+                            const TilePlan& plan, void* stream) {
+  if (plan.units * plan.splits > INT32_MAX) return LQ_ERR_SHAPE;
   TileArgs ta;
   ta.a = a;
+  ta.splits = plan.splits;
   const int most = head_dim == 256 ? TileCfg<256>::BN : TileCfg<128>::BN, bs = 1 << a.log2_bs;
   const int box = (bs < most ? bs : most) * head_dim / 128;
-  if (!encode_cache(&ta.map_k, kc, cache_bytes, box) || !encode_cache(&ta.map_v, vc, cache_bytes, box)) return LQ_ERR_CUDA;
-  // as many row tiles as there can be: every request's last one may be partial
-  const int64_t rows = a.total_q * a.group;
-  const int per = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;
-  const int64_t ctas = (rows / per + (a.batch < a.total_q ? a.batch : a.total_q)) * a.kv_heads;
-  if (ctas > INT32_MAX) return LQ_ERR_SHAPE;
+  if (!encode_cache(&ta.map_k, kc, cache_bytes, box) || !encode_cache(&ta.map_v, vc, cache_bytes, box))
+    return LQ_ERR_CUDA;
   switch (head_dim) {
-    case 64: return launch_tiles<64>(ta, ctas, stream);
-    case 128: return launch_tiles<128>(ta, ctas, stream);
-    default: return launch_tiles<256>(ta, ctas, stream);
+    case 64: return launch_tiles<64>(ta, plan, stream);
+    case 128: return launch_tiles<128>(ta, plan, stream);
+    default: return launch_tiles<256>(ta, plan, stream);
   }
 }
 

@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) append_kernel(AppendAr
   int64_t ahead[5];
 #pragma unroll
   for (int i = 0; i < 5; ++i)
-    ahead[i] = (i == 0 || 32 * i < a.window + bs1) && t0 + 32 * i + lane < a.tokens ? __ldg(a.slots + t0 + 32 * i + lane)
-                                                                                  : -1;
+    ahead[i] = (i == 0 || 32 * i < a.window + bs1) && t0 + 32 * i + lane < a.tokens
+                   ? __ldg(a.slots + t0 + 32 * i + lane) : -1;
   const int64_t prev = lane < a.window && t0 + lane > 0 && t0 + lane < a.tokens ? __ldg(a.slots + t0 + lane - 1) : -1;
   const int64_t mine = ahead[0];
   const bool starts = lane < a.window && mine >= 0 && !(prev >= 0 && prev + 1 == mine && (mine & bs1) != 0);

@@ -293,7 +293,8 @@ extern "C" lq_status lq_qk_norm_rope(const void* q_dev, int64_t ldq, int q_heads
   if (!(eps >= 0.f)) return LQ_ERR_ARG;
   const int64_t esize = dtype == LQ_BF16 ? 2 : 4;
   const int64_t qc = (int64_t)q_heads * head_dim, kc = (int64_t)kv_heads * head_dim;
-  if (q_heads > 0 && (ldq < qc || ldqo < qc || (ldq * esize) % 16 != 0 || (ldqo * esize) % 16 != 0)) return LQ_ERR_SHAPE;
+  if (q_heads > 0 && (ldq < qc || ldqo < qc || (ldq * esize) % 16 != 0 || (ldqo * esize) % 16 != 0))
+    return LQ_ERR_SHAPE;
   if (kv_heads > 0 && (ldk < kc || ldko < kc || (ldk * esize) % 16 != 0 || (ldko * esize) % 16 != 0))
     return LQ_ERR_SHAPE;
   if (tokens == 0 || q_heads + kv_heads == 0) return LQ_OK;

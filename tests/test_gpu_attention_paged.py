@@ -83,6 +83,11 @@ CASES = [
     ([(150, 70)], 16, 1, 16, 64),
     ([(900, 300)], 4, 4, 32, 128),
     ([(i * 7 % 90 + 1, 1) for i in range(150)], 2, 1, 16, 128),
+    # many rows for few heads over long caches: the positions are split
+    ([(5000, 40)], 4, 2, 16, 128),
+    ([(3000, 70), (100, 66)], 4, 1, 64, 256),
+    ([(2600, 300), (700, 5)], 2, 1, 32, 64),
+    ([(3, 200), (4000, 90)], 2, 2, 128, 128),
 ]
 
 

@@ -13,7 +13,7 @@
 // they need just the 8 bytes of lengths per request, so every CTA computes
 // them for itself in shared memory instead of waiting for another launch, and
 // then writes its share of the table rows (a warp per row) and of the tokens
-// (a thread per token; its request by binary search in cu).  A block that
+// (four to a thread; their requests by search in cu).  A block that
 // another CTA writes in this launch is never read back from the table: it is
 // taken from the free list.
 #include "lq_host.h"
@@ -118,31 +118,41 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
     }
   }
 
-  // tokens
+  // tokens, 128 neighbouring ones per warp and turn: the first of a lane's four
+  // finds its request by binary search, the others go on from there
   const int64_t total = min((long long)cu[a.batch], (long long)a.max_tokens);
-  for (int64_t t = (int64_t)blockIdx.x * kThreads + tid; t < a.max_tokens; t += (int64_t)gridDim.x * kThreads) {
-    long long slot = -1;
-    int pos = 0;
-    if (t < total) {
-      int lo = 0, hi = a.batch;                // last i with cu[i] <= t: empty requests are skipped
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * 128; t0 < a.max_tokens;
+       t0 += (int64_t)gridDim.x * kWarps * 128) {
+    int lo = 0, hi = a.batch;                  // last i with cu[i] <= t: empty requests are skipped
+    if (t0 + lane < total) {
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid; else hi = mid;
+        if (cu[mid] <= t0 + lane) lo = mid; else hi = mid;
       }
-      const long long c = clip_len(__ldg(a.cached + lo));
-      const long long p = c + t - cu[lo];
-      const long long have = (c + bs1) >> a.log2_bs, j = p >> a.log2_bs;
-      int32_t blk = -1;
-      if (j < a.width) {
-        const long long f = (long long)fs[lo] + j - have;
-        if (j < have) blk = __ldg(a.table + (int64_t)lo * a.ldt + j);
-        else if (f < a.num_free) blk = __ldg(a.free_blocks + f);
-      }
-      if (blk >= 0) slot = ((long long)blk << a.log2_bs) + (p & bs1);
-      pos = (int)(p < INT32_MAX ? p : INT32_MAX);
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 32 * i + lane;
+      if (t >= a.max_tokens) break;
+      long long slot = -1;
+      int pos = 0;
+      if (t < total) {
+        while (cu[lo + 1] <= t) ++lo;          // (cu[batch] > t)
+        const long long c = clip_len(__ldg(a.cached + lo));
+        const long long p = c + t - cu[lo];
+        const long long have = (c + bs1) >> a.log2_bs, j = p >> a.log2_bs;
+        int32_t blk = -1;
+        if (j < a.width) {
+          const long long f = (long long)fs[lo] + j - have;
+          if (j < have) blk = __ldg(a.table + (int64_t)lo * a.ldt + j);
+          else if (f < a.num_free) blk = __ldg(a.free_blocks + f);
+        }
+        if (blk >= 0) slot = ((long long)blk << a.log2_bs) + (p & bs1);
+        pos = (int)(p < INT32_MAX ? p : INT32_MAX);
+      }
+      a.slots[t] = slot;
+      a.positions[t] = pos;
+    }
   }
 }
 
@@ -188,9 +198,9 @@ extern "C" lq_status lq_kv_plan(const int32_t* cached_lens_dev, const int32_t* n
       return LQ_ERR_CUDA;
     }
   }
-  // a CTA per kWarps table rows or 2 x kThreads tokens, at most two per SM
+  // a CTA per kWarps table rows or kWarps x 128 tokens, at most two per SM
   int64_t grid = (batch + plan::kWarps - 1) / plan::kWarps;
-  const int64_t by_tokens = (max_tokens + 2 * plan::kThreads - 1) / (2 * plan::kThreads);
+  const int64_t by_tokens = (max_tokens + plan::kWarps * 128 - 1) / (plan::kWarps * 128);
   if (by_tokens > grid) grid = by_tokens;
   if (grid > 2 * (int64_t)sms) grid = 2 * (int64_t)sms;
   if (grid < 1) grid = 1;

@@ -85,6 +85,34 @@ __device__ __forceinline__ unsigned long long peer_word(const unsigned long long
   return v;
 }
 
+// Shifts whose amount past 31, also a negative one, gives 0 (as PTX defines them).
+__device__ __forceinline__ uint32_t shr0(uint32_t x, int by) {
+  uint32_t y;
+  asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(by));
+  return y;
+}
+__device__ __forceinline__ uint32_t shl0(uint32_t x, int by) {
+  uint32_t y;
+  asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(by));
+  return y;
+}
+
+// Sum of the weights of x - y: whole() without a branch or a 64-bit shift, the
+// two words of the weight by shifts that leave 0 where there is nothing.
+// `most` grows to the largest magnitude of x, as bits.
+struct Sum {
+  unsigned long long n = 0;
+  uint32_t most = 0;
+  __device__ __forceinline__ void add(float x, float y) {
+    most = max(most, __float_as_uint(x) & 0x7FFFFFFFu);
+    const uint32_t bits = __float_as_uint(fminf(fmaxf(x - y, 0.f), 4.f));
+    const uint32_t top = bits << 8 | 0x80000000u;
+    const int e = 122 - (int)(bits >> 23);
+    const uint32_t hi = shr0(top, e + 32), lo = shr0(top, e) | shl0(top, -e);
+    n += (unsigned long long)hi << 32 | lo;
+  }
+};
+
 // A row's weights: p, or max(p - q, 0), or p without one token.
 template <bool BF16>
 struct Row {
@@ -92,41 +120,42 @@ struct Row {
   const void* q;             // null: none
   int64_t gone;              // token left out, -1: none
   int32_t* status;
-  __device__ __forceinline__ unsigned long long one(float x, float y, int64_t v) const {
-    if (!(x <= 3.402823466e38f)) raise_flag(status, LQ_DEV_NONFINITE);
-    return whole(v == gone ? 0.f : x - y);
-  }
   __device__ __forceinline__ unsigned long long weight(int64_t v) const {
-    return one(at<BF16>(p, v), q != nullptr ? at<BF16>(q, v) : 0.f, v);
+    return whole(v == gone ? 0.f : at<BF16>(p, v) - (q != nullptr ? at<BF16>(q, v) : 0.f));
   }
   // the sum over [v0, v1) of a warp's lanes; v0 a multiple of 8
   __device__ __forceinline__ unsigned long long sum(int64_t v0, int64_t v1, int lane) const {
     constexpr int E = BF16 ? 8 : 4;                // values per 16-byte load
-    unsigned long long n = 0;
+    Sum n;
     int64_t v = v0;
     const uintptr_t low = reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q);
     if ((low & 15) == 0) {                         // rows that start at 16-byte boundaries
+      const uint4* pv = reinterpret_cast<const uint4*>(p) + v0 / E + lane;
+      const uint4* qv = reinterpret_cast<const uint4*>(q) + v0 / E + lane;
+      const int steps = (int)(v1 > v0 ? (v1 - v0) / (32 * E) : 0);
 #pragma unroll 4
-      for (; v + 32 * E <= v1; v += 32 * E) {
-        const int64_t c = v / E + lane;
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + c);
-        const uint4 y = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < steps; ++i) {
+        const uint4 x = __ldg(pv + 32 * i);
+        const uint4 y = q != nullptr ? __ldg(qv + 32 * i) : make_uint4(0, 0, 0, 0);
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (BF16) {
-            n += one(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), c * 8 + 2 * e);
-            n += one(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), c * 8 + 2 * e + 1);
+            n.add(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16));
+            n.add(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u));
           } else {
-            n += one(__uint_as_float(xs[e]), __uint_as_float(ys[e]), c * 4 + e);
+            n.add(__uint_as_float(xs[e]), __uint_as_float(ys[e]));
           }
         }
       }
+      v += (int64_t)steps * (32 * E);
     }
 #pragma unroll 8
-    for (v += lane; v < v1; v += 32) n += weight(v);
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    for (v += lane; v < v1; v += 32) n.add(at<BF16>(p, v), q != nullptr ? at<BF16>(q, v) : 0.f);
+    if (lane == 0 && gone >= v0 && gone < v1) n.n -= whole(at<BF16>(p, gone));
+    for (int o = 16; o; o >>= 1) n.n += __shfl_xor_sync(0xffffffffu, n.n, o);
+    if (n.most >= 0x7F800000u) raise_flag(status, LQ_DEV_NONFINITE);
+    return n.n;
   }
 };
 

@@ -203,74 +203,97 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     q_end = __ldg(a.cu_q + a.batch);
   }
 
-  // prefix sums of the requests' tiles (in the rings, which are still empty);
-  // the list's length, and this warp's part of it
-  long long* pre = reinterpret_cast<long long*>(smem);
-  const int per = (a.batch + C::kThreads - 1) / C::kThreads;
-  const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
-  long long sum = 0;
-#pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
+  // prefix sums of the requests' tiles, the list's length, and this warp's part
+  // of it: u0 and part_n
+  auto tiles_of = [&](int i) {
     if (blockIdx.x == 0 && (int64_t)__ldg(a.kv_lens + i) > ((int64_t)a.width << a.log2_bs))
       raise_flag(a.status, LQ_DEV_RANGE);
     Cursor c;
     c.i = i;
     enter<kRows>(a, c);
-    const long long n = (long long)c.nrt * a.kv_heads * c.nt;
-    pre[i] = n;
-    sum += n;
-  }
-  long long inc = sum;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) wsum[warp] = inc;
-  __syncthreads();
-  long long total = 0;
+    return (long long)c.nrt * a.kv_heads * c.nt;
+  };
+  auto scan = [&](long long x) {               // inclusive, over the warp
 #pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) inc += total;
-    total += wsum[w];
-  }
-  long long run = inc - sum;
-#pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
-    const long long n = pre[i];
-    pre[i] = run;
-    run += n;
-  }
-  __syncthreads();
-  // equal parts for the CTAs, then for their warps, the first ones a tile longer
-  long long u0 = 0, part_n = total;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  long long u0 = 0, part_n = 0, before = 0;
   auto part_of = [&](unsigned parts, unsigned i) {
     const long long base = part_n < INT_MAX ? (unsigned)part_n / parts : part_n / parts;
     const unsigned more = (unsigned)(part_n - base * parts);
     u0 += base * i + min(i, more);
     part_n = base + (i < more ? 1 : 0);
   };
-  part_of(gridDim.x, blockIdx.x);
-  part_of(kWarps, warp);
-  const int n = (int)(part_n < (1 << 29) ? part_n : (1 << 29));
+  // equal parts for the CTAs, then for their warps, the first ones a tile longer
+  auto parts = [&](long long total) {
+    part_n = total;
+    part_of(gridDim.x, blockIdx.x);
+    part_of(kWarps, warp);
+  };
   Cursor ci;                                   // the tile whose halves are fetched next
-  if (n > 0) {
-    int lo = 0, hi = a.batch;                  // last request with pre[i] <= u0: it has tiles
+  if (a.batch <= 32) {
+    // every warp for itself, a request per lane
+    const long long mine = lane < a.batch ? tiles_of(lane) : 0, inc = scan(mine);
+    parts(__shfl_sync(0xffffffffu, inc, 31));
+    const uint32_t here = __ballot_sync(0xffffffffu, lane < a.batch && inc - mine <= u0);
+    ci.i = 31 - __clz(here);                   // last request that starts at or before u0: it has tiles
+    before = __shfl_sync(0xffffffffu, inc - mine, ci.i);
+    __syncwarp();                              // the barriers are there
+  } else {
+    // a run of requests per thread (in the rings, which are still empty)
+    long long* pre = reinterpret_cast<long long*>(smem);
+    const int per = (a.batch + C::kThreads - 1) / C::kThreads;
+    const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
+    long long sum = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const long long n = tiles_of(i);
+      pre[i] = n;
+      sum += n;
+    }
+    long long inc = scan(sum);
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) inc += total;
+      total += wsum[w];
+    }
+    long long run = inc - sum;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const long long n = pre[i];
+      pre[i] = run;
+      run += n;
+    }
+    __syncthreads();
+    parts(total);
+    int lo = 0, hi = a.batch;
 #pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= u0) lo = mid; else hi = mid;
     }
     ci.i = lo;
+    before = pre[lo];
+    // the prefix sums have been read: the rings may fill
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+  const int n = (int)(part_n < (1 << 29) ? part_n : (1 << 29));
+  if (n > 0) {
     enter<kRows>(a, ci);
-    const long long rem = u0 - pre[lo];
+    const long long rem = u0 - before;
     const long long hr = rem < INT_MAX ? (unsigned)rem / (unsigned)ci.nt : rem / ci.nt;    // row tile and head
     ci.t = (int)(rem - hr * ci.nt);
     ci.rt = (int)(hr < INT_MAX ? (unsigned)hr / (unsigned)a.kv_heads : hr / a.kv_heads);
     ci.h = (int)(hr - (long long)ci.rt * a.kv_heads);
   }
-  // the prefix sums have been read: the rings may fill
-  fence_proxy_async_smem();
-  __syncthreads();
 
   if (n > 0) {
     // lanes 0 and 1: the block of half a tile each (the same block where it
@@ -282,6 +305,9 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       blk = -1;
       if (lane < 2 && p < ci.len) blk = __ldg(a.table + ci.i * a.ldt + (p >> a.log2_bs));
     };
+    auto info_of = [](const Cursor& c) {
+      return make_int4(c.i, c.rt, c.h | (c.t + 1 == c.nt ? 1 << 16 : 0), c.t);
+    };
     const int rows_per_block = (D << a.log2_bs) >> 7;
     int qi = 0;                                // halves issued
     auto issue = [&](int s) {
@@ -291,7 +317,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         at_scale = blk * a.kv_heads + ci.h;
         if (lane < 2 && !blk_ok && ci.t * kTile + (paired ? 16 * lane : 0) < ci.len)
           raise_flag(a.status, LQ_DEV_RANGE);  // a block id outside the pool
-        if (lane == 0) infos[s] = make_int4(ci.i, ci.rt, ci.h | (ci.t + 1 == ci.nt ? 1 << 16 : 0), ci.t);
+        if (lane == 0) infos[s] = info_of(ci);
       }
       const bool ok0 = __shfl_sync(0xffffffffu, blk_ok, 0), ok1 = __shfl_sync(0xffffffffu, blk_ok, 1);
       if (lane < 2) {
@@ -336,10 +362,10 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll 1
     for (int step = -S; step < 2 * n; ++step) {
       const bool skip = step < 0;
-      if (fresh ? step == 2 - S || (step > 0 && !(step & 1)) : !skip && !(step & 1)) {
-        info = infos[skip ? 0 : s];            // written when the half was issued
+      if (step == -S || (!skip && !(step & 1))) {
+        // (the first segment's rows are fetched beside its first block id)
+        info = skip ? info_of(ci) : infos[s];  // written when the half was issued
         if (fresh) {
-          // (the first segment's rows are fetched behind its first tile's codes)
           fresh = false;
           const int h = info.z & 0xFFFF;
           seg_starts = info.w == 0;

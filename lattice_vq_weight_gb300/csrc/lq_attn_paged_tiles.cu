@@ -5,13 +5,14 @@
 // the matrix products bound the work (4 head_dim flops per row and position),
 // so here a CTA takes 256 query rows of one kv head as two row tiles (one for
 // head_dim 256) and walks the positions they see in tiles of 128 (64):
-//     S = Q C_k^T     tcgen05.mma, both operands in shared memory, S in TMEM
+//     S = Q C_k^T     tcgen05.mma in bf16, both operands in shared memory, S in
+//                     TMEM (queries as they are; codes are whole numbers)
 //     W = 2^(x - max) by one thread per row, from TMEM and back: the fp16
 //                     weights take the columns of the scores
-//     O += W C_v      tcgen05.mma with W from TMEM, O in TMEM
+//     O += W C_v      tcgen05.mma in fp16 with W from TMEM, O in TMEM
 // One warp fetches the codes of a tile by TMA, up to two half tiles (K, V)
-// ahead; warps 0..3 turn them into fp16, exactly, in two stages of shared
-// memory; four warps per row tile hold its rows' maxima and sums; one warp
+// ahead; warps 0..3 turn them into bf16 and fp16, exactly, in two stages of
+// shared memory; four warps per row tile hold its rows' maxima and sums; one warp
 // issues the products.  (Codes fetched through registers instead made the
 // converting warps the slowest part: the L1 that this much shared
 // memory leaves holds too few loads in flight.)
@@ -22,7 +23,13 @@
 // codes: shared memory (operands read at 128 bytes a clock, tiles written) and
 // the conversions would otherwise bound the kernel before the tensor core does.
 // Scores are overwritten only after the products that read the weights there
-// have completed.
+// have completed.  A step of 128 tokens takes 2.07 us for the 256 rows (the
+// products alone would 1.07), and a CTA's start, first and last tiles and
+// outputs about 9 us: what happens once per CTA is serial, so queries are
+// copied without a pass over them in registers, masked tiles go through short
+// loops, and outputs leave by whole lines.  (CTAs that go on from one group of
+// rows to the next, an equal part of all positions each, took longer: 285 us
+// to 257 for chunks of 1900 tokens over 2300 to 5400.)
 //
 // As in the split kernel the running maximum may lag by 2^7, so that a row's
 // weights are made in one pass and O is rescaled (TMEM to registers and back)
@@ -85,11 +92,12 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t sub_st
   return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((sub_stride >> 4) & 0x3FFFu) << 16 |
          (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// Instruction descriptor: D f32, A and B f16, M = 128; B along its rows when mn.
-template <int N, bool MN>
+// Instruction descriptor: D f32, M = 128; A and B bf16 or f16; B along its rows when mn.
+template <int N, bool BF16, bool MN>
 struct Idesc {
-  static constexpr uint32_t v =
-      (1u << 4) | ((MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+  static constexpr uint32_t v = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) |
+                                ((MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+                                ((uint32_t)(kTileRows >> 4) << 24);
 };
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -174,14 +182,27 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   return true;
 }
 
+// Two codes, offset to unsigned bytes and placed by `sel`, as bf16 numbers.
+// 0x4300 + (the low seven bits) is 128 + those, and 0x4300 or 0x4380 is 128 or
+// 256, as bit 7 is set or not: their difference is byte - 128, exactly.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t bytes, uint32_t sel) {
+  const uint32_t p = __byte_perm(bytes, 0x43434343u, sel), x = p & 0xFF7FFF7Fu, y = (p & 0xFF80FF80u) ^ 0x00800080u;
+  const __nv_bfloat162 v =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
 // A row's weights of one tile from its scores: packed fp16 weights, the sum of
 // weight / value scale, and the largest exponent met.  scales[g], of the g-th
 // 16 tokens: key scale, log2 and reciprocal of the value scale; the exponent of
-// a token is score * fac * .x + .y + base.  MASKED: some tokens are not seen, or
-// some blocks are missing (gone) or count as zero.
-template <int BN, bool MASKED>
-__device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float base, const float4* scales, uint32_t zero,
-                                             uint32_t gone, int vis0, uint32_t (&w)[BN / 2], float& l) {
+// a token is score * fac * .x + .y + base.
+template <int BN>
+__device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float base, const float4* scales,
+                                             uint32_t (&w)[BN / 2], float& l) {
   float lead0 = -INFINITY, lead1 = -INFINITY;
   uint32_t s[2][32];
   float4 sc[2] = {scales[0], scales[1]};
@@ -198,37 +219,78 @@ __device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float bas
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int g = 2 * c + half;
       const float k = fac * now[half].x, d = now[half].y + base;
-      const int vis = MASKED ? ((gone >> g & 1) ? -1 : vis0 - 16 * g) : 15;      // tokens 0 .. vis are seen
       const float2 k2 = make_float2(k, k), d2 = make_float2(d, d);
       float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t* y = x32 + 16 * half + 2 * e;
         float2 x = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), k2, d2);
-        if constexpr (MASKED) {
-          if (2 * e > vis) x.x = -INFINITY;
-          if (2 * e + 1 > vis) x.y = -INFINITY;
-        }
         if (e & 1) lead1 = fmaxf(lead1, fmaxf(x.x, x.y));
         else lead0 = fmaxf(lead0, fmaxf(x.x, x.y));
         x = make_float2(ex2(x.x), ex2(x.y));
         if (e & 1) sum1 = add2(sum1, x);
         else sum0 = add2(sum0, x);
-        w[8 * g + e] = pack_f16(x.x, x.y);
+        w[16 * c + 8 * half + e] = pack_f16(x.x, x.y);
       }
       sum0 = add2(sum0, sum1);
-      const float total = sum0.x + sum0.y;
-      // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
-      l = fmaf(total, !MASKED || total > 0.f ? now[half].z : 0.f, l);
-      if (MASKED && (zero >> g & 1)) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[8 * g + e] = 0u;
-      }
+      l = fmaf(sum0.x + sum0.y, now[half].z, l);
     }
   }
   return fmaxf(lead0, lead1);
+}
+
+// The tiles that the above does not serve, few of a unit: tokens that a row does
+// not see (beyond vis0, or in a block that is gone), blocks that count as zero,
+// rows whose maximum moves.  Two short loops, the largest exponent and then the
+// weights: code that runs so seldom comes from far away, and unrolled twice
+// over it took three times as long as the common tiles' (3.5 us a tile to 1.1).
+template <int BN>
+__device__ __forceinline__ float row_top(uint32_t tmem, float fac, const float4* scales, uint32_t gone, int vis0) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x32[32];
+    tmem_ld32(tmem + 32 * c, x32);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int g = 2 * c + half, vis = (gone >> g & 1) ? -1 : vis0 - 16 * g;      // tokens 0 .. vis are seen
+      const float4 sc = scales[g];
+      const float k = fac * sc.x;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        top = fmaxf(top, e > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + e]), k, sc.y));
+    }
+  }
+  return top;
+}
+template <int BN>
+__device__ __forceinline__ void store_weights(uint32_t tmem, float fac, float base, const float4* scales, uint32_t zero,
+                                              uint32_t gone, int vis0, float& l) {
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x32[32], w[16];
+    tmem_ld32(tmem + 32 * c, x32);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int g = 2 * c + half, vis = (gone >> g & 1) ? -1 : vis0 - 16 * g;
+      const float4 sc = scales[g];
+      const float k = fac * sc.x, d = sc.y + base;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x0 = ex2(2 * e > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + 2 * e]), k, d));
+        const float x1 = ex2(2 * e + 1 > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + 2 * e + 1]), k, d));
+        sum0 += x0;
+        sum1 += x1;
+        w[8 * half + e] = (zero >> g & 1) ? 0u : pack_f16(x0, x1);
+      }
+      const float total = sum0 + sum1;
+      // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
+      l = fmaf(total, total > 0.f ? sc.z : 0.f, l);
+    }
+    tmem_st16(tmem + 16 * c, w);                            // over scores read before
+  }
 }
 
 template <int D>
@@ -368,7 +430,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     // they write fp16, both in the 128-byte swizzle.
     const int t = threadIdx.x, c4 = t & 3, sub = t / (4 * C::kPassRows), q8 = (t >> 2) & 7;
     const int r0 = ((q8 >> 1) ^ (q8 & 1 ? 5 : 0)) + ((t >> 2) % C::kPassRows & ~7);
-    auto convert = [&](const uint8_t* src, uint8_t* dst, uint64_t* src_free, uint64_t* full) {
+    auto convert = [&](auto one, const uint8_t* src, uint8_t* dst, uint64_t* src_free, uint64_t* full) {
       uint4 x[C::kPasses];
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
@@ -383,8 +445,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
         uint32_t o[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          o[2 * q] = codes_f16(w[q], 0x4140);
-          o[2 * q + 1] = codes_f16(w[q], 0x4342);
+          o[2 * q] = one(w[q], 0);
+          o[2 * q + 1] = one(w[q], 1);
         }
         *reinterpret_cast<uint4*>(line + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(line + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -396,17 +458,19 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
         arrive(full);
       }
     };
+    const auto as_bf16 = [](uint32_t bytes, int half) { return codes_bf16(bytes, half ? 0x4342 : 0x4140); };
+    const auto as_f16 = [](uint32_t bytes, int half) { return codes_f16(bytes, half ? 0x4342 : 0x4140); };
     for (int j = 0; j < tiles; ++j) {
       const int st = j & 1;
       const uint32_t before = (uint32_t)(j / 2 + 1) & 1;    // the stage's previous use
       bool ok = wait_on(&raw_full[0], (uint32_t)j & 1, timeout);
       if (j >= 2) ok = ok && wait_on(&k_free[st], before, timeout);
       if (!__all_sync(0xffffffffu, ok)) break;
-      convert(raw, sk + st * C::kCodeBytes, &raw_free[0], &k_full[st]);
+      convert(as_bf16, raw, sk + st * C::kCodeBytes, &raw_free[0], &k_full[st]);
       ok = wait_on(&raw_full[1], (uint32_t)j & 1, timeout);
       if (j >= 2) ok = ok && wait_on(&v_free[st], before, timeout);
       if (!__all_sync(0xffffffffu, ok)) break;
-      convert(raw + C::kRawBytes, sv + st * C::kCodeBytes, &raw_free[1], &v_full[st]);
+      convert(as_f16, raw + C::kRawBytes, sv + st * C::kCodeBytes, &raw_free[1], &v_full[st]);
     }
   } else if (warp >= C::kMmaWarp) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
@@ -466,7 +530,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ss(d, qd + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4),
-                   kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, false>::v, k > 0);
+                   kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, true, false>::v, k > 0);
           mma_commit(&s_full[t]);
           if (t == T - 1 || j >= n1) mma_commit(&k_free[st]);
         }
@@ -485,7 +549,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
         if (elect()) {
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
-            mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, true>::v, j > 0 || k > 0);
+            mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
           mma_commit(&o_done[t]);
           if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
         }
@@ -513,51 +577,26 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     const int lim = mine ? min(r.shown + j_tok, r.len - 1) : r.len - 1;     // last position the row sees
     const int lim_min = min(r.shown + R0 / a.group, r.len - 1);           // of the tile's first row
 
-    // the query row as fp16, times a power of two that brings its largest
-    // value to [2^13, 2^14) and the sign of the scale
-    float fac;
+    // The warp's query rows go to shared memory as they are, D / 8 lanes to a
+    // row; rows past the request's are zeros.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+    uint8_t* my_line = sq + t * C::kQBytes + row * 128;
+    auto line_of = [&](int r32, int c) {                    // 16-byte part c of the warp's row
+      const int rr = (warp & 3) * 32 + r32;
+      return sq + t * C::kQBytes + (c >> 3) * kTileRows * 128 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+    };
     {
-      const int64_t src = (int64_t)(r.q0 + j_tok) * a.ldq + (int64_t)head * D;
-      auto load8 = [&](int c, float (&v)[8]) {
-        if (!mine) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        } else {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + src + 8 * c));
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(u[e] << 16);
-            v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-          }
-        }
-      };
-      float top = 0.f;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q);
+      if (mine) src += (int64_t)(r.q0 + j_tok) * a.ldq + (int64_t)head * D;
+      const uint32_t have = __ballot_sync(0xffffffffu, mine);
+      const int c = lane & (kLanes - 1);
 #pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        float v[8];
-        load8(c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+      for (int pass = 0; pass < kLanes; ++pass) {
+        const int from = pass * kAtOnce + lane / kLanes;
+        const uint16_t* p =
+            reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+        copy16(line_of(from, c), p + 8 * c, have >> from & 1 ? 16 : 0);
       }
-      const int eb = (int)(__float_as_uint(top) >> 23);
-      const int ex = min(126, max(-116, 140 - eb));
-      float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-      if (a.scale_log2 < 0.f) up = -up;
-      fac = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll 2
-      for (int c = 0; c < D / 8; ++c) {
-        float v[8];
-        load8(c, v);
-        uint32_t hi[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) hi[e] = pack_f16(v[2 * e] * up, v[2 * e + 1] * up);
-        uint8_t* line = sq + t * C::kQBytes + (c >> 3) * kTileRows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive(&q_full[t]);
     }
 
     // lane g < BN / 16: the scales of the tile's g-th 16 tokens, a tile ahead;
@@ -576,6 +615,43 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       }
     };
     if (n > 0) fetch_scales(0);
+
+    // The factor of the row's scores.  Rows so large (or small) that the sums of
+    // products could leave fp32's range are brought nearer to 1 by a power of two.
+    float fac = a.scale_log2;
+    {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      uint32_t top = 0;                                     // of the two halves' magnitudes
+#pragma unroll 8
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x =
+            *reinterpret_cast<const uint4*>(my_line + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4));
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+      }
+      top = max(top >> 16, top & 0xFFFFu);
+      const int up = top >= 0x7080u ? -64 : top < 0x2000u && top != 0 ? 64 : 0;      // 2^98, 2^-63
+      if (__any_sync(0xffffffffu, up != 0)) {
+        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+        fac *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+          uint4* x = reinterpret_cast<uint4*>(my_line + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4));
+          uint32_t v[4] = {x->x, x->y, x->z, x->w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[e] << 16) * f,
+                                                           __uint_as_float(v[e] & 0xFFFF0000u) * f);
+            v[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *x = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(&q_full[t]);
+    }
     float mx = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -594,26 +670,26 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (!ok) break;
       tc_after();
       __syncwarp();
-      uint32_t w[BN / 2];
-      float lead = INFINITY;                                // of rows without a maximum yet: to be found first
-      for (int pass = 0; pass < 2; ++pass) {
-        const float base = kShift - (mx == -INFINITY ? 0.f : mx);
+      bool common = !masked && !__any_sync(0xffffffffu, mx == -INFINITY);
+      if (common) {
+        uint32_t w[BN / 2];
         float sum = l;
-        const float top = masked ? row_weights<BN, true>(my_s, fac, base, sc, zero, gone, vis0, w, sum)
-                                 : row_weights<BN, false>(my_s, fac, base, sc, zero, gone, vis0, w, sum);
-        lead = mx == -INFINITY && top != -INFINITY ? INFINITY : top;
-        if (!__any_sync(0xffffffffu, lead > kShift + kLead)) {
+        const float lead = row_weights<BN>(my_s, fac, kShift - mx, sc, w, sum);
+        common = !__any_sync(0xffffffffu, lead > kShift + kLead);
+        if (common) {
           l = sum;
-          break;
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) tmem_st16(my_s + 16 * c, w + 16 * c);
         }
-        // the maximum moves: the sum and the output so far shrink, and the
-        // weights are made again
-        const bool moves = lead > kShift + kLead;
-        const float m = top - base;
-        const float f = moves ? ex2(mx - m) : 1.f;
-        if (moves) mx = m;
+      }
+      if (!common) {
+        // where the maximum moves, the sum and the output so far shrink
+        const float top = row_top<BN>(my_s, fac, sc, gone, vis0);
+        const bool moves = mx == -INFINITY ? top != -INFINITY : top > mx + kLead;
+        const float f = moves ? ex2(mx - top) : 1.f;
+        if (moves) mx = top;
         l *= f;
-        if (j > 0) {
+        if (j > 0 && __any_sync(0xffffffffu, moves)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -624,54 +700,72 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
             tmem_st16(my_o + 32 * c + 16, o + 16);
           }
         }
+        store_weights<BN>(my_s, fac, kShift - (mx == -INFINITY ? 0.f : mx), sc, zero, gone, vis0, l);
       }
-#pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_st16(my_s + 16 * c, w + 16 * c);
       tmem_wait_st();
       tc_before();
       __syncwarp();
       if (lane == 0) arrive(&p_full[t]);
     }
 
-    // outputs
+    // Outputs, by way of the rows of shared memory where the queries were (the
+    // products with them are done): a warp's stores then cover whole lines.
     if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(n - 1) & 1, timeout));
     tc_after();
     __syncwarp();
     if (ok) {
-      const float inv = l == 0.f ? 0.f : kSumUnit / l;
-      const int64_t dst = (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D;
+      const bool whole = ta.splits == 1;
+      const uint32_t rows_out = whole ? __ballot_sync(0xffffffffu, mine) : 0xffffffffu;
       // with the positions split: the row's sums as they are
       float* piece = a.part + ((int64_t)blockIdx.x * C::kRows + t * kTileRows + row) * (D + 4);
+      uint8_t* dst = reinterpret_cast<uint8_t*>(
+          whole ? reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D
+                : reinterpret_cast<uint16_t*>(piece));
+      const float inv = l == 0.f ? 0.f : kSumUnit / l;
+      auto put = [&](int c, uint4 v) {
+        *reinterpret_cast<uint4*>(my_line + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+      };
+      // 2 D bytes of each row: all of it as bf16, or half of it
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(my_o + 32 * c, o);
-        } else {
+      for (int part = 0; part < (whole ? 1 : 2); ++part) {
+#pragma unroll 1
+        for (int c = 0; c < (whole ? D / 32 : D / 64); ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(my_o + part * (D / 2) + 32 * c, o);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (ta.splits > 1) {
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(piece + 32 * c)[e] =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else if (mine) {
-          uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + dst + 32 * c);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t u[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv,
-                                                             __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
-              u[q] = *reinterpret_cast<const uint32_t*>(&b);
+              for (int q = 0; q < 4; ++q) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv,
+                                                               __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+                u[q] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              put(4 * c + e, make_uint4(u[0], u[1], u[2], u[3]));
             }
-            p[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) put(8 * c + e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
           }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int pass = 0; pass < kLanes; ++pass) {
+          const int from = pass * kAtOnce + lane / kLanes, c = lane & (kLanes - 1);
+          uint8_t* p = reinterpret_cast<uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
+          if (rows_out >> from & 1)
+            *reinterpret_cast<uint4*>(p + part * 2 * D + 16 * c) = *reinterpret_cast<const uint4*>(line_of(from, c));
+        }
+        __syncwarp();
       }
-      if (ta.splits > 1) {
+      if (!whole) {
         piece[D] = mx;
         piece[D + 1] = l;
       }

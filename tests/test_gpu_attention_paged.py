@@ -116,6 +116,20 @@ def test_rows_that_see_nothing_and_requests_without_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_len", [2, 70])
+@pytest.mark.parametrize("exponent", [-105, -40, 105])
+def test_queries_near_the_ends_of_their_range(dtype, q_len, exponent):
+    """Queries times a power of two and the scale, here below 0, times its inverse: the result does not move."""
+    torch, L = cuda()
+    s = build(torch, np.random.default_rng(16), [(300, q_len), (90, 3)], 8, 2, 32, 128, dtype, q_size=2.0 ** exponent)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    scale = -0.088 * 2.0 ** -exponent
+    got = run(torch, L, s, st, sm_scale=scale)
+    assert int(st) == 0
+    check(got, reference(s, scale), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("q_len", [1, 5, 200])
 def test_strides_scale_and_peaked_scores(dtype, q_len):
     """Queries and outputs as columns of wider rows, a table wider than its columns, sm_scale given, scores in

@@ -48,6 +48,8 @@ namespace lq {
 namespace attn {
 
 constexpr int kTileRows = 128;
+constexpr uint32_t kTopWeight = (15u + 15u) << 10;        // 2^(kShift + kLead) as fp16
+static_assert(kShift + kLead == 15.f, "the largest weight");
 
 template <int D>
 struct TileCfg {
@@ -182,11 +184,11 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   return true;
 }
 
-// Two codes, offset to unsigned bytes and placed by `sel`, as bf16 numbers.
-// 0x4300 + (the low seven bits) is 128 + those, and 0x4300 or 0x4380 is 128 or
-// 256, as bit 7 is set or not: their difference is byte - 128, exactly.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t bytes, uint32_t sel) {
-  const uint32_t p = __byte_perm(bytes, 0x43434343u, sel), x = p & 0xFF7FFF7Fu, y = (p & 0xFF80FF80u) ^ 0x00800080u;
+// Two codes, placed by `sel`, as bf16 numbers.  0x4300 + (the low seven bits) is
+// 128 + those, and 0x4300 or 0x4380 is 128 or 256, as the sign bit is clear or
+// set: their difference is the code, exactly.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t codes, uint32_t sel) {
+  const uint32_t p = __byte_perm(codes, 0x43434343u, sel), x = p & 0xFF7FFF7Fu, y = p & 0xFF80FF80u;
   const __nv_bfloat162 v =
       __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -197,13 +199,15 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
 }
 
 // A row's weights of one tile from its scores: packed fp16 weights, the sum of
-// weight / value scale, and the largest exponent met.  scales[g], of the g-th
-// 16 tokens: key scale, log2 and reciprocal of the value scale; the exponent of
-// a token is score * fac * .x + .y + base.
+// weight / value scale; returns the largest weight's bits, or more (positive
+// fp16 numbers are in the order of their bits, with infinity and NaN above, and
+// take three-way integer maxima two at a time).  scales[g], of the g-th 16
+// tokens: key scale, log2 and reciprocal of the value scale; the exponent of a
+// token is score * fac * .x + .y + base.
 template <int BN>
-__device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float base, const float4* scales,
+__device__ __forceinline__ uint32_t row_weights(uint32_t tmem, float fac, float base, const float4* scales,
                                              uint32_t (&w)[BN / 2], float& l) {
-  float lead0 = -INFINITY, lead1 = -INFINITY;
+  uint32_t top = 0;
   uint32_t s[2][32];
   float4 sc[2] = {scales[0], scales[1]};
   tmem_ld32_async(tmem, s[0]);
@@ -226,18 +230,17 @@ __device__ __forceinline__ float row_weights(uint32_t tmem, float fac, float bas
       for (int e = 0; e < 8; ++e) {
         const uint32_t* y = x32 + 16 * half + 2 * e;
         float2 x = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), k2, d2);
-        if (e & 1) lead1 = fmaxf(lead1, fmaxf(x.x, x.y));
-        else lead0 = fmaxf(lead0, fmaxf(x.x, x.y));
         x = make_float2(ex2(x.x), ex2(x.y));
         if (e & 1) sum1 = add2(sum1, x);
         else sum0 = add2(sum0, x);
         w[16 * c + 8 * half + e] = pack_f16(x.x, x.y);
+        if (e & 1) top = __vimax3_u16x2(top, w[16 * c + 8 * half + e - 1], w[16 * c + 8 * half + e]);
       }
       sum0 = add2(sum0, sum1);
       l = fmaf(sum0.x + sum0.y, now[half].z, l);
     }
   }
-  return fmaxf(lead0, lead1);
+  return max(top >> 16, top & 0xFFFFu);
 }
 
 // The tiles that the above does not serve, few of a unit: tokens that a row does
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       for (int p = 0; p < C::kPasses; ++p) {
         const int row = p * C::kPassRows + r0;
         uint8_t* line = dst + sub * BN * 128 + row * 128;
-        const uint32_t w[4] = {x[p].x ^ 0x80808080u, x[p].y ^ 0x80808080u, x[p].z ^ 0x80808080u, x[p].w ^ 0x80808080u};
+        const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
         uint32_t o[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       }
     };
     const auto as_bf16 = [](uint32_t bytes, int half) { return codes_bf16(bytes, half ? 0x4342 : 0x4140); };
-    const auto as_f16 = [](uint32_t bytes, int half) { return codes_f16(bytes, half ? 0x4342 : 0x4140); };
+    const auto as_f16 = [](uint32_t bytes, int half) { return codes_f16(bytes ^ 0x80808080u, half ? 0x4342 : 0x4140); };
     for (int j = 0; j < tiles; ++j) {
       const int st = j & 1;
       const uint32_t before = (uint32_t)(j / 2 + 1) & 1;    // the stage's previous use
@@ -674,8 +677,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (common) {
         uint32_t w[BN / 2];
         float sum = l;
-        const float lead = row_weights<BN>(my_s, fac, kShift - mx, sc, w, sum);
-        common = !__any_sync(0xffffffffu, lead > kShift + kLead);
+        const uint32_t top = row_weights<BN>(my_s, fac, kShift - mx, sc, w, sum);
+        common = !__any_sync(0xffffffffu, top > kTopWeight);
         if (common) {
           l = sum;
 #pragma unroll

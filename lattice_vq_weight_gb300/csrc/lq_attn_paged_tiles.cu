@@ -12,8 +12,8 @@
 //     O += W C_v      tcgen05.mma in fp16 with W from TMEM, O in TMEM
 // One warp fetches the codes of a tile by TMA, up to two half tiles (K, V)
 // ahead; warps 0..3 turn them into bf16 and fp16, exactly, in two stages of
-// shared memory; four warps per row tile hold its rows' maxima and sums; one warp
-// issues the products.  (Codes fetched through registers instead made the
+// shared memory; four warps per row tile hold its rows' maxima and sums, and one
+// issues its products.  (Codes fetched through registers instead made the
 // converting warps the slowest part: the L1 that this much shared
 // memory leaves holds too few loads in flight.)
 // K and V tiles have the same layout, rows of 64 dimensions in the 128-byte
@@ -63,8 +63,8 @@ struct TileCfg {
   static constexpr int kSmem = T * kQBytes + 4 * kCodeBytes + 2 * kRawBytes + 1024;
   static constexpr uint32_t kCols = 512;
   static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
-  static constexpr int kMmaWarp = 4 + 4 * T;
-  static constexpr int kFetchWarp = kMmaWarp + 1;
+  static constexpr int kMmaWarp = 4 + 4 * T;                // and the next, one per row tile
+  static constexpr int kFetchWarp = kMmaWarp + T;
   static constexpr int kThreads = 32 * (8 + 4 * T);         // whole groups of four warps
   // Registers per thread: the launch gives every warp 65536 / 512 = 128 (T = 2)
   // and the groups then divide those up, 80 + 2 x 184 + 64 = 4 x 128.
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   uint8_t* raw = sv + 2 * C::kCodeBytes;                    // codes as fetched, K and V
   __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
   __shared__ uint64_t raw_full[2], raw_free[2];             // K, V
-  __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], drain;
+  __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], turn[T][2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[2];
   __shared__ int wsum[C::kThreads / 32];
@@ -325,16 +325,18 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       mbar_init1(&raw_free[i], 4);                          // one arrival per converting warp
       mbar_init1(&k_full[i], 4);
       mbar_init1(&v_full[i], 4);
-      mbar_init1(&k_free[i], 1);                            // the products that read the stage are done
-      mbar_init1(&v_free[i], 1);
+      mbar_init1(&k_free[i], T);                            // the row tiles' products that read the stage are done
+      mbar_init1(&v_free[i], T);
     }
     for (int t = 0; t < T; ++t) {
       mbar_init1(&s_full[t], 1);                            // scores computed
       mbar_init1(&p_full[t], 4);                            // one arrival per softmax warp
       mbar_init1(&o_done[t], 1);                            // values added: O readable, the weights read
       mbar_init1(&q_full[t], 4);
+      mbar_init1(&turn[t][0], 1);                           // scores issued
+      mbar_init1(&turn[t][1], 1);
     }
-    mbar_init1(&drain, 1);
+    mbar_init1(&drain, T);
     mbar_init_fence();
     timeout_flag = 0;
     found[0] = -1;
@@ -510,61 +512,75 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (*timeout)
         for (int q = max(0, issued - 2); q < issued; ++q)
           mbar_wait_bounded(&raw_full[q & 1], (uint32_t)(q >> 1) & 1, kWaitCycles / 8);
-    } else if (warp == C::kMmaWarp) {
+    } else if (warp < C::kFetchWarp) {
       // ------------------------------------------------------------ products
-      // The whole warp runs the loop, so that descriptors are uniform values; one
-      // elected lane issues.
-      const uint64_t dq = desc_k_major(smem_addr(sq)), dk = desc_k_major(smem_addr(sk));
+      // A warp per row tile: the products of one then run while the other's warp
+      // waits (one warp for both, in line: 3950 clocks a step, 2050 of them
+      // products).  The whole warp runs the loop, so that descriptors are uniform
+      // values; one elected lane issues.
+      const int t = warp - C::kMmaWarp, n = t == 0 ? n0 : n1;
+      const uint64_t dq = desc_k_major(smem_addr(sq + t * C::kQBytes)), dk = desc_k_major(smem_addr(sk));
       const uint64_t dv = desc_mn_major(smem_addr(sv), C::kSub > 1 ? BN * 128 : 1024);
+      const uint32_t my_s = tmem_s + t * BN, my_o = tmem_o + t * D;
       auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
-      // scores of row tile t and tile j, where there are any
-      auto scores = [&](int t, int j) {
-        if (j >= (t == 0 ? n0 : n1)) return true;
+      // scores of tile j; past this row tile's last, the other's codes are let go
+      auto scores = [&](int j) {
+        if (j >= tiles) return true;
         const int st = j & 1;
         bool ok = wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout);
-        if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
-        // they overwrite the weights of the tile before
-        else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
+        if (j < n) {
+          if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
+          // they overwrite the weights of the tile before
+          else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
+        }
         if (!all(ok)) return false;
         tc_after();
-        const uint64_t qd = dq + (uint64_t)(t * C::kQBytes >> 4), kd = dk + (uint64_t)(st * C::kCodeBytes >> 4);
-        const uint32_t d = tmem_s + t * BN;
         if (elect()) {
+          if (j < n) {
+            const uint64_t kd = dk + (uint64_t)(st * C::kCodeBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(d, qd + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4),
-                   kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, true, false>::v, k > 0);
-          mma_commit(&s_full[t]);
-          if (t == T - 1 || j >= n1) mma_commit(&k_free[st]);
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(my_s, dq + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4),
+                     kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, true, false>::v, k > 0);
+            mma_commit(&s_full[t]);
+            mma_commit(&k_free[st]);
+            arrive(&turn[t][st]);
+          } else {
+            arrive(&k_free[st]);
+          }
         }
         __syncwarp();
         return true;
       };
-      auto add_values = [&](int t, int j) {
-        if (j >= (t == 0 ? n0 : n1)) return true;
+      auto add_values = [&](int j) {
         const int st = j & 1;
         bool ok = wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout);
-        ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
+        if (j < n) ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
+        // In turn, values and next scores of one row tile, then of the other: when
+        // both had weights ready together, they would stay in step and neither's
+        // exponentials run under the other's products.  (Neither can be two tiles
+        // ahead here: a parity tells.)
+        if (T > 1 && t == 0 && j < n1) ok = ok && wait_on(&turn[T - 1][st], (uint32_t)(j >> 1) & 1, timeout);
+        if (T > 1 && t == 1 && j + 1 < n0) ok = ok && wait_on(&turn[0][st ^ 1], (uint32_t)((j + 1) >> 1) & 1, timeout);
         if (!all(ok)) return false;
         tc_after();
-        const uint64_t vd = dv + (uint64_t)(st * C::kCodeBytes >> 4);
-        const uint32_t d = tmem_o + t * D, w = tmem_s + t * BN;
         if (elect()) {
+          if (j < n) {
+            const uint64_t vd = dv + (uint64_t)(st * C::kCodeBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_ts(d, w + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
-          mma_commit(&o_done[t]);
-          if (t == T - 1 || j >= n1) mma_commit(&v_free[st]);
+            for (int k = 0; k < BN / 16; ++k)
+              mma_ts(my_o, my_s + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
+            mma_commit(&o_done[t]);
+            mma_commit(&v_free[st]);
+          } else {
+            arrive(&v_free[st]);
+          }
         }
         __syncwarp();
         return true;
       };
-      bool ok = scores(0, 0);
-      for (int j = 0; j < tiles && ok; ++j) {
-        if constexpr (T > 1) ok = scores(1, j);
-        ok = ok && add_values(0, j) && scores(0, j + 1);
-        if constexpr (T > 1) ok = ok && add_values(1, j);
-      }
+      bool ok = scores(0);
+      for (int j = 0; j < tiles && ok; ++j) ok = add_values(j) && scores(j + 1);
     }
   } else {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
@@ -778,15 +794,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   // ---------------------------------------------------------------- teardown
   tc_before();
   __syncthreads();
+  if (timeout_flag && warp >= C::kMmaWarp && warp < C::kFetchWarp) {
+    // products may still be in flight: all have completed once this arrives
+    if (elect()) mma_commit(&drain);
+    __syncwarp();
+  }
   if (warp == C::kMmaWarp) {
-    if (timeout_flag) {
-      // products may still be in flight: all have completed once this arrives
-      if (lane == 0) {
-        mma_commit(&drain);
-        mbar_wait_bounded(&drain, 0, kWaitCycles);
-      }
-      __syncwarp();
-    }
+    if (timeout_flag) mbar_wait_bounded(&drain, 0, kWaitCycles);
+    __syncwarp();
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kCols));
   }

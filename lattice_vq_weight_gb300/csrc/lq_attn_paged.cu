@@ -938,9 +938,9 @@ int cta_count() {
 // Whether the tensor-core kernel takes a bf16 call: by the query rows that an
 // average request has for each kv head.  Its time hardly depends on them up to
 // 256, the split kernel's grows with every 16.  Measured at 8 kv heads of 128,
-// 16 / 24 / 32 / 64 rows: 16 requests of 4000 tokens 64 us against 50 / 84 / 84 /
-// 152; one of 32000 tokens 43 to 49 us against 33 / 48 / 48 / 81; one of 4000
-// tokens 23 us against 17 / 20 / 20 / 24.  (head_dim 64 and 256 cross there too.)
+// 16 / 24 / 32 / 64 rows: 16 requests of 4000 tokens 66 us against 50 / 84 / 84 /
+// 152; one of 32000 tokens 44 to 50 us against 33 / 48 / 48 / 81; one of 4000
+// tokens 24 us against 17 / 20 / 20 / 24.  (head_dim 64 and 256 cross there too.)
 bool many_rows(int batch, int64_t total_q, int group) {
   return batch > 0 && (total_q + batch - 1) / batch * group > 16;
 }

@@ -23,13 +23,13 @@
 // codes: shared memory (operands read at 128 bytes a clock, tiles written) and
 // the conversions would otherwise bound the kernel before the tensor core does.
 // Scores are overwritten only after the products that read the weights there
-// have completed.  A step of 128 tokens takes 2.07 us for the 256 rows (the
+// have completed.  A step of 128 tokens takes 1.99 us for the 256 rows (the
 // products alone would 1.07), and a CTA's start, first and last tiles and
 // outputs about 9 us: what happens once per CTA is serial, so queries are
 // copied without a pass over them in registers, masked tiles go through short
 // loops, and outputs leave by whole lines.  (CTAs that go on from one group of
 // rows to the next, an equal part of all positions each, took longer: 285 us
-// to 257 for chunks of 1900 tokens over 2300 to 5400.)
+// to 257 for chunks of 1900 tokens over 2300 to 5400, now 242.)
 //
 // As in the split kernel the running maximum may lag by 2^7, so that a row's
 // weights are made in one pass and O is rescaled (TMEM to registers and back)
@@ -559,9 +559,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
         // In turn, values and next scores of one row tile, then of the other: when
         // both had weights ready together, they would stay in step and neither's
         // exponentials run under the other's products.  (Neither can be two tiles
-        // ahead here: a parity tells.)
-        if (T > 1 && t == 0 && j < n1) ok = ok && wait_on(&turn[T - 1][st], (uint32_t)(j >> 1) & 1, timeout);
-        if (T > 1 && t == 1 && j + 1 < n0) ok = ok && wait_on(&turn[0][st ^ 1], (uint32_t)((j + 1) >> 1) & 1, timeout);
+        // ahead here: a parity tells.  The turn passes when the scores have been
+        // issued: passed before, the two warps' products interleave and the row
+        // tile that is ahead loses its lead, 252 us to 242.)
+        if (T > 1 && t == 0 && j < min(n, n1)) ok = ok && wait_on(&turn[T - 1][st], (uint32_t)(j >> 1) & 1, timeout);
+        if (T > 1 && t == 1 && j < n && j + 1 < n0) ok = ok && wait_on(&turn[0][st ^ 1], (uint32_t)((j + 1) >> 1) & 1, timeout);
         if (!all(ok)) return false;
         tc_after();
         if (elect()) {

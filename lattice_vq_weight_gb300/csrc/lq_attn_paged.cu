@@ -200,13 +200,13 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   pdl_launch();
   if (threadIdx.x == 0) {
     timeout = 0;
-    q_end = __ldg(a.cu_q + a.batch);
+    q_end = a.cu_q[a.batch];
   }
 
   // prefix sums of the requests' tiles, the list's length, and this warp's part
   // of it: u0 and part_n
   auto tiles_of = [&](int i) {
-    if (blockIdx.x == 0 && (int64_t)__ldg(a.kv_lens + i) > ((int64_t)a.width << a.log2_bs))
+    if (blockIdx.x == 0 && (int64_t)a.kv_lens[i] > ((int64_t)a.width << a.log2_bs))
       raise_flag(a.status, LQ_DEV_RANGE);
     Cursor c;
     c.i = i;
@@ -303,7 +303,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     auto load_block = [&]() {
       const int p = ci.t * kTile + (paired ? 16 * lane : 0);
       blk = -1;
-      if (lane < 2 && p < ci.len) blk = __ldg(a.table + ci.i * a.ldt + (p >> a.log2_bs));
+      if (lane < 2 && p < ci.len) blk = a.table[ci.i * a.ldt + (p >> a.log2_bs)];
     };
     auto info_of = [](const Cursor& c) {
       return make_int4(c.i, c.rt, c.h | (c.t + 1 == c.nt ? 1 << 16 : 0), c.t);
@@ -384,14 +384,14 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at);
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                  const float4 x = __ldg(p + c);
+                  const float4 x = p[c];
                   v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
                 }
               } else {
                 const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + at);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                  const uint4 x = __ldg(p + c);
+                  const uint4 x = p[c];
                   const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {

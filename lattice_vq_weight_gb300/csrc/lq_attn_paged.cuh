@@ -102,7 +102,7 @@ struct Request {
 
 __device__ __forceinline__ Request load_request(const Args& a, int i) {
   Request r;
-  const int q0 = __ldg(a.cu_q + i), q1 = __ldg(a.cu_q + i + 1), len = __ldg(a.kv_lens + i);
+  const int q0 = a.cu_q[i], q1 = a.cu_q[i + 1], len = a.kv_lens[i];
   r.q0 = q0 < 0 ? 0 : q0;
   const int64_t end = q1 < a.total_q ? q1 : a.total_q;
   r.q_len = end > r.q0 ? (int)(end - r.q0) : 0;

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
 
   // rows that no request owns
   {
-    const int64_t end = max(__ldg(a.cu_q + a.batch), 0), cols = (int64_t)a.q_heads * D;
+    const int64_t end = max(a.cu_q[a.batch], 0), cols = (int64_t)a.q_heads * D;
     for (int64_t t = end + blockIdx.x; t < a.total_q; t += gridDim.x)
       for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) {
         reinterpret_cast<uint16_t*>(a.out)[t * a.ldo + c] = 0;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
     };
     int sum = 0;
     for (int i = i0; i < i1; ++i) {
-      if (blockIdx.x == 0 && (int64_t)__ldg(a.kv_lens + i) > ((int64_t)a.width << a.log2_bs))
+      if (blockIdx.x == 0 && (int64_t)a.kv_lens[i] > ((int64_t)a.width << a.log2_bs))
         raise_flag(a.status, LQ_DEV_RANGE);
       sum += tiles_of(i);
     }
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       const int block_lines = (D << a.log2_bs) >> 7;
       auto look_up = [&](int j) {
         const int pos = (first + j) * BN + step * lane;
-        return lane < parts && pos < seen ? __ldg(table + (pos >> a.log2_bs)) : -1;
+        return lane < parts && pos < seen ? table[pos >> a.log2_bs] : -1;
       };
       int blk = look_up(0), issued = 0;
       for (int j = 0; j < tiles; ++j) {
@@ -628,10 +628,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       nk = 0.f;
       nv = -1.f;
       if (lane < BN / 16 && pos < seen) {
-        const int blk = __ldg(table + (pos >> a.log2_bs));
+        const int blk = table[pos >> a.log2_bs];
         if ((unsigned)blk < (unsigned long long)a.num_blocks) {
-          nk = __ldg(a.ks + (int64_t)blk * a.kv_heads + h);
-          nv = __ldg(a.vs + (int64_t)blk * a.kv_heads + h);
+          nk = a.ks[(int64_t)blk * a.kv_heads + h];
+          nv = a.vs[(int64_t)blk * a.kv_heads + h];
         }
       }
     };

@@ -51,10 +51,10 @@ template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_raw(const void* p, int64_t i) {
   Raw<BF16> r;
   if constexpr (BF16) {
-    r.w[0] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i));
+    r.w[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
   } else {
-    r.w[0] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i));
-    r.w[1] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i) + 1);
+    r.w[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i);
+    r.w[1] = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i)[1];
   }
   return r;
 }
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) append_kernel(AppendAr
 #pragma unroll
   for (int i = 0; i < 5; ++i)
     ahead[i] = (i == 0 || 32 * i < a.window + bs1) && t0 + 32 * i + lane < a.tokens
-                   ? __ldg(a.slots + t0 + 32 * i + lane) : -1;
-  const int64_t prev = lane < a.window && t0 + lane > 0 && t0 + lane < a.tokens ? __ldg(a.slots + t0 + lane - 1) : -1;
+                   ? a.slots[t0 + 32 * i + lane] : -1;
+  const int64_t prev = lane < a.window && t0 + lane > 0 && t0 + lane < a.tokens ? a.slots[t0 + lane - 1] : -1;
   const int64_t mine = ahead[0];
   const bool starts = lane < a.window && mine >= 0 && !(prev >= 0 && prev + 1 == mine && (mine & bs1) != 0);
   if (starts && mine >= a.slots_in_cache) raise_flag(a.status, LQ_DEV_RANGE);
@@ -325,10 +325,10 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
   const unsigned magic = 0xffffffffu / chunks + 1u;
   const int64_t warps = (int64_t)gridDim.x * 8;
   int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  int64_t slot = u < 2 * a.n ? __ldg(a.slots + (u >> 1)) : -1;
+  int64_t slot = u < 2 * a.n ? a.slots[u >> 1] : -1;
   for (; u < 2 * a.n; u += warps) {
     const int which = (int)(u & 1);
-    const int64_t next = u + warps < 2 * a.n ? __ldg(a.slots + ((u + warps) >> 1)) : -1;
+    const int64_t next = u + warps < 2 * a.n ? a.slots[(u + warps) >> 1] : -1;
     const bool ok = slot >= 0 && slot < a.slots_in_cache;
     if (slot >= a.slots_in_cache && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
     const int64_t sc0 = (slot >> a.log2_bs) * a.kv_heads;
@@ -347,9 +347,9 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
         if (ok && c < per_row) {
           const unsigned h = __umulhi(c, magic), k = E * (c - h * chunks);
           const int8_t* p = codes + ((int64_t)h << a.log2_bs) * a.dim + k;
-          s[i] = __ldg(scales + h);
-          if constexpr (BF16) w[i] = __ldg(reinterpret_cast<const uint2*>(p));
-          else w[i].x = __ldg(reinterpret_cast<const uint32_t*>(p));
+          s[i] = scales[h];
+          if constexpr (BF16) w[i] = *reinterpret_cast<const uint2*>(p);
+          else w[i].x = *reinterpret_cast<const uint32_t*>(p);
         }
       }
 #pragma unroll

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
   long long sn = 0, sb = 0;
   bool bad = false;
   for (int i = i0; i < i1; ++i) {
-    const int32_t rc = __ldg(a.cached + i), rn = __ldg(a.fresh + i);
+    const int32_t rc = a.cached[i], rn = a.fresh[i];
     const long long c = clip_len(rc), n = clip_len(rn);
     const long long need = (c + n + bs1) >> a.log2_bs;
     bad |= rc < 0 || rn < 0 || c + n > INT32_MAX || need > a.width;
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
   eb -= sb;
   auto clip = [](long long v) { return (int32_t)(v < INT32_MAX ? v : INT32_MAX); };
   for (int i = i0; i < i1; ++i) {
-    const long long c = clip_len(__ldg(a.cached + i)), n = clip_len(__ldg(a.fresh + i));
+    const long long c = clip_len(a.cached[i]), n = clip_len(a.fresh[i]);
     cu[i] = clip(en);
     fs[i] = clip(eb);
     if (blockIdx.x == 0) {
@@ -109,12 +109,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
 
   // table rows: blocks held stay, new ones come from the free list, -1 after
   for (int64_t i = (int64_t)blockIdx.x * kWarps + warp; i < a.batch; i += (int64_t)gridDim.x * kWarps) {
-    const long long c = clip_len(__ldg(a.cached + i)), n = clip_len(__ldg(a.fresh + i));
+    const long long c = clip_len(a.cached[i]), n = clip_len(a.fresh[i]);
     const long long have = (c + bs1) >> a.log2_bs, need = (c + n + bs1) >> a.log2_bs;
     int32_t* row = a.table + i * a.ldt;
     for (long long j = have + lane; j < a.width; j += 32) {
       const long long f = (long long)fs[i] + j - have;
-      row[j] = (j < need && f < a.num_free) ? __ldg(a.free_blocks + f) : -1;
+      row[j] = (j < need && f < a.num_free) ? a.free_blocks[f] : -1;
     }
   }
 
@@ -130,28 +130,35 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
         if (cu[mid] <= t0 + lane) lo = mid; else hi = mid;
       }
     }
+    long long slot[4];
+    int pos[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t t = t0 + 32 * i + lane;
-      if (t >= a.max_tokens) break;
-      long long slot = -1;
-      int pos = 0;
+      slot[i] = -1;
+      pos[i] = 0;
       if (t < total) {
         while (cu[lo + 1] <= t) ++lo;          // (cu[batch] > t)
-        const long long c = clip_len(__ldg(a.cached + lo));
+        const long long c = clip_len(a.cached[lo]);
         const long long p = c + t - cu[lo];
         const long long have = (c + bs1) >> a.log2_bs, j = p >> a.log2_bs;
         int32_t blk = -1;
         if (j < a.width) {
           const long long f = (long long)fs[lo] + j - have;
-          if (j < have) blk = __ldg(a.table + (int64_t)lo * a.ldt + j);
-          else if (f < a.num_free) blk = __ldg(a.free_blocks + f);
+          if (j < have) blk = a.table[(int64_t)lo * a.ldt + j];
+          else if (f < a.num_free) blk = a.free_blocks[f];
         }
-        if (blk >= 0) slot = ((long long)blk << a.log2_bs) + (p & bs1);
-        pos = (int)(p < INT32_MAX ? p : INT32_MAX);
+        if (blk >= 0) slot[i] = ((long long)blk << a.log2_bs) + (p & bs1);
+        pos[i] = (int)(p < INT32_MAX ? p : INT32_MAX);
       }
-      a.slots[t] = slot;
-      a.positions[t] = pos;
+    }
+    // (stored last: the four tokens' loads need not wait for each other's stores)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 32 * i + lane;
+      if (t >= a.max_tokens) break;
+      a.slots[t] = slot[i];
+      a.positions[t] = pos[i];
     }
   }
 }

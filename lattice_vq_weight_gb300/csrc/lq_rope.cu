@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
   Unit now = unit_of(u), next = unit_of(min(u + warps, units - 1));
   Four<BF16> v[IT][2], vn[IT][2];
   float cs[4], sn[4], csn[4], snn[4];
-  int pos = __ldg(a.positions + now.t), pos_next = __ldg(a.positions + next.t);
+  int pos = a.positions[now.t], pos_next = a.positions[next.t];
   fetch(now, v);
   angles(pos, cs, sn);
   for (;;) {
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
       fetch(next, vn);
       angles(pos_next, csn, snn);
       after = unit_of(min(u + 2 * warps, units - 1));
-      pos_after = __ldg(a.positions + after.t);
+      pos_after = a.positions[after.t];
     }
 
     // y[e] = r (c[e] v[e] + s[e] v[partner of e]): the weights ride along

@@ -14,7 +14,11 @@ namespace lq {
 
 // Every kernel of these operators is a programmatic dependent launch: it may
 // be scheduled while the kernel before it ends, waits for that grid before its
-// first access to global memory, and lets the next kernel be scheduled.
+// first access to global memory, and lets the next kernel be scheduled.  What
+// an earlier call may have written (any input of these calls) is read with
+// ordinary loads: the read-only path (ld.global.nc) is for data that nothing
+// writes while the kernel runs, and here the producer may still be at it when
+// the kernel starts; nor does the wait keep such loads behind it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 

@@ -9,9 +9,13 @@
 // With x_p = sm_scale log2(e) s_k (q . c_k) + log2(s_v) the output is
 //     (sum_p 2^x_p c_v) / (sum_p 2^x_p / s_v):
 // the value scale rides in the exponent, so one weight per position serves
-// both sums, codes enter the matrix products as they are, and value scales of
-// any size cannot push a weight out of fp16's range (the running maximum is
-// that of x, not of the score).
+// both sums, codes enter the matrix products as they are, and a large value
+// scale cannot push a weight out of fp16's range (the running maximum is that
+// of x, not of the score).  Scales too far apart for one exponent to serve both
+// sums are looked after separately (the tcgen05 kernel in place, this one by
+// rows_apart).  Running maxima are whole numbers: moving one shifts exponents and
+// rounds nothing, so how the positions were split shows in fp32 roundings, and
+// in an fp16 weight only where it lies that near to the middle of two.
 //
 // The split kernel, for few query rows per kv head (decode steps, drafted
 // tokens), is bound by reading the codes from HBM: every code is used for at
@@ -53,13 +57,14 @@ struct Cfg {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kHalfBytes = kTile * D;             // the K or the V codes of a tile
-  static constexpr int kPiece = kRows * (D + 2);           // floats: output rows, maxima, sums
+  static constexpr int kPiece = kRows * (D + 3);           // floats: output rows, maxima, sums, their units
   static constexpr int kPerHalf = kHalfBytes + 32;         // codes, barrier, scales, what tile it is
   static constexpr int kEnds = 2 * kWarps;                 // pieces that the warps may leave
-  static constexpr int kFit = (227 * 1024 - 1024 - 1536 - 3 * kEnds * kRows * 4) / (kWarps * kPerHalf);
+  static constexpr int kRowBytes = 5 * kEnds * kRows * 4;                // the pieces' rows
+  static constexpr int kFit = (227 * 1024 - 1024 - 2048 - kRowBytes) / (kWarps * kPerHalf);
   static constexpr int kHalves = kFit < 8 ? kFit : 8;      // of a warp's ring
   static constexpr int kRing = kWarps * kHalves * kHalfBytes;
-  static constexpr int kSmem = kWarps * kHalves * kPerHalf + 3 * kEnds * kRows * 4 + 1024;
+  static constexpr int kSmem = kWarps * kHalves * kPerHalf + kRowBytes + 1024;
 };
 
 // A place in the list of tiles.
@@ -145,21 +150,137 @@ __device__ __forceinline__ void store_out(const Args& a, int64_t at, float v) {
 }
 
 template <bool F32>
-__device__ __forceinline__ void store_out4(const Args& a, int64_t at, const float4& o, float inv) {
+__device__ __forceinline__ void store_out4(const Args& a, int64_t at, const float4& o, float inv, float unit) {
   if constexpr (F32) {
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) =
-        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        make_float4(o.x * inv * unit, o.y * inv * unit, o.z * inv * unit, o.w * inv * unit);
   } else {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv * unit, o.y * inv * unit);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv * unit, o.w * inv * unit);
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
 }
 
-// What turns a row's accumulated values into its output: 1 / l, or 0 for a row
-// that sees nothing; NaN stays NaN.  (The weights' shift is in both sums.)
-__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : kSumUnit / l; }
+// What turns a row's accumulated values into its output, with its unit_of: 1 / l,
+// or 0 for a row that sees nothing; NaN stays NaN.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// The loop below puts the value scale into the weights.  With scales that differ
+// by up to 2^60 (zeros count as 2^-60) every weight that matters in the sum of
+// weights is a normal number: x more than 134 below the maximum is a score more
+// than 43 below the largest.  What meets any other scale, or zeros that were a
+// row's maximum, is done again by rows_apart where there are such scales beside
+// others.
+constexpr float kScaleBits = 30.f;
+constexpr float kLeastScale = 9.31322575e-10f, kMostScale = 1073741824.f;       // 2^-30, 2^30
+constexpr float kZeroScale = 8.67361738e-19f;                                   // 2^-60
+// Sums of weight / value scale are held times 2^-20: at most 2^55 for a weight.
+constexpr float kSumUnit = 9.5367431640625e-7f, kSumUnitBits = 20.f;
+__device__ __forceinline__ bool far_scale(float v) { return v > kMostScale || (v < kLeastScale && v > 0.f); }
+
+// Whether tokens [p0, p1) of a request and kv head have value scales that the loop
+// does not serve: one out of its range, or zeros beside others.
+__device__ __noinline__ bool scales_apart(const Args& a, int req, int h, int p0, int p1) {
+  bool far = false, zeros = false, values = false;
+  for (int p = (p0 >> a.log2_bs) + (threadIdx.x & 31); p << a.log2_bs < p1; p += 32) {
+    const int blk = a.table[req * a.ldt + p];
+    if ((unsigned)blk < (unsigned long long)a.num_blocks) {
+      const float v = a.vs[(int64_t)blk * a.kv_heads + h];
+      far |= far_scale(v);
+      zeros |= v == 0.f;
+      values |= v >= kLeastScale;
+    }
+  }
+  return __any_sync(0xffffffffu, far) ||
+         (__any_sync(0xffffffffu, zeros) && __any_sync(0xffffffffu, values));
+}
+
+// Query rows row0 .. row0 + rows - 1 of a request and kv head over the tokens
+// [p0, p1), for value scales of any size: one row after the other, 32 tokens at a
+// time in fp32, with the two exponents of every row apart.  The outputs where dst is
+// null, else the values' sums to dst and maxima, sums and units to the rows' lists.
+template <int D, bool F32>
+__device__ __noinline__ void rows_apart(const Args& a, int req, int row0, int rows, int h, int p0, int p1, float* dst,
+                                        float* rows_m, float* rows_l, float* rows_u) {
+  constexpr int E = D / 32;                    // dimensions per lane
+  const int lane = threadIdx.x & 31, bs1 = (1 << a.log2_bs) - 1;
+  const Request r = load_request(a, req);
+  const int32_t* table = a.table + req * a.ldt;
+#pragma unroll 1
+  for (int row = 0; row < rows; ++row) {
+    int64_t at_q, at_out;
+    const bool here = row_at(a, r.q0, r.q_len, row0 + row, h, a.ldq, D, &at_q);
+    row_at(a, r.q0, r.q_len, row0 + row, h, a.ldo, D, &at_out);
+    const int past = here ? min(min(r.shown + (row0 + row) / a.group, r.len - 1) + 1, p1) : p0;
+    float mx = -INFINITY, un = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 1
+    for (int t0 = p0; t0 < past; t0 += 32) {
+      const int p = t0 + lane, blk = p < past ? table[p >> a.log2_bs] : -1;
+      const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+      const int64_t head = (int64_t)blk * a.kv_heads + h, line = ((head << a.log2_bs) + (p & bs1)) * D;
+      float s = -INFINITY, x = -INFINITY;
+      if (ok) {
+        float sum = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          const uint4 k = *reinterpret_cast<const uint4*>(a.kc + line + c);
+          const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float q;
+            if constexpr (F32) q = reinterpret_cast<const float*>(a.q)[at_q + c + e];
+            else q = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.q)[at_q + c + e] << 16);
+            sum = fmaf(q * a.scale_log2, (float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), sum);
+          }
+        }
+        s = sum * a.ks[head];
+        x = s + log2_scale(a.vs[head]);
+      }
+      float most = s, top = x;
+#pragma unroll
+      for (int i = 16; i; i >>= 1) {
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, i));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      }
+      const float un_to = fmaxf(un, ceilf(most)), mx_to = fmaxf(mx, ceilf(top)), f = pow2(mx - mx_to);
+      float w = ok ? ex2(s - un_to) : 0.f;
+      const float v = ok && x != -INFINITY ? ex2(x - mx_to + kShift) : 0.f;
+#pragma unroll
+      for (int i = 16; i; i >>= 1) w += __shfl_xor_sync(0xffffffffu, w, i);
+      l = fmaf(l, pow2(un - un_to), w);        // (NaN before any score: 0 of 0)
+      un = un_to;
+      mx = mx_to;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      const uint32_t there = __ballot_sync(0xffffffffu, ok);
+#pragma unroll 4
+      for (int t = 0; t < 32; ++t) {
+        const int64_t from = __shfl_sync(0xffffffffu, line, t);
+        const float vt = __shfl_sync(0xffffffffu, v, t);
+        if (there >> t & 1)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(vt, (float)a.vc[from + lane * E + e], o[e]);
+      }
+    }
+    if (dst != nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) dst[row * D + lane * E + e] = o[e];
+      if (lane == 0) {
+        rows_m[row] = mx;
+        rows_l[row] = l;
+        rows_u[row] = un;
+      }
+    } else if (here) {
+      const float inv = inverse(l), unit = unit_of(mx, un);
+#pragma unroll
+      for (int e = 0; e < E; ++e) store_out<F32>(a, at_out + lane * E + e, o[e] * inv * unit);
+    }
+  }
+  __syncwarp();
+}
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(Cfg<D, NT, F32>::kThreads, 1)
@@ -176,13 +297,17 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   int4* infos = reinterpret_cast<int4*>(smem + C::kRing) + warp * S;               // which tile a K half is of
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing + kWarps * S * 16) + warp * S;
   float2* scales = reinterpret_cast<float2*>(smem + C::kRing + kWarps * S * 24) + warp * S;
-  // maxima and sums of the warps' pieces, and their weights when they are joined
+  // maxima, sums and units of the warps' pieces, and their weights when they are joined
   float* piece_m = reinterpret_cast<float*>(smem + kWarps * S * C::kPerHalf);
   float* piece_l = piece_m + C::kEnds * kRows;
-  float* piece_f = piece_l + C::kEnds * kRows;
+  float* piece_u = piece_l + C::kEnds * kRows;
+  float* piece_f = piece_u + C::kEnds * kRows;
+  float* piece_w = piece_f + C::kEnds * kRows;
   __shared__ Tag tags[2 * kWarps];
   __shared__ int order[2 * kWarps];            // the pieces that are there, in order
   __shared__ long long wsum[kWarps];
+  __shared__ int again[kWarps];                // value scales far apart, or zeros that were a maximum
+  __shared__ int4 part_at[kWarps];             // the first tile of the warp's part
   __shared__ int2 asked[kWarps];               // the warp's current request: first query token, how many
   __shared__ int timeout, q_end;
   const bool paired = a.log2_bs < 5;           // a tile spans two blocks of 16
@@ -195,6 +320,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     for (int s = 0; s < S; ++s) mbar_init1(bars + s, 3);
     mbar_init_fence();
     tags[2 * warp].valid = tags[2 * warp + 1].valid = 0;
+    again[warp] = 0;
   }
   pdl_wait();
   pdl_launch();
@@ -344,6 +470,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     };
 
     load_block();
+    if (lane == 0) part_at[warp] = make_int4(ci.i, ci.rt, ci.h, ci.t);
 
     uint32_t qf[NT][KS][2][Q2];
     float acc[KS][NT][4];
@@ -491,10 +618,12 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         float lv[2], iv[2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const float v = sv[mt] < kMinScale ? kMinScale : sv[mt];      // NaN stays NaN
+          const float v = sv[mt] < kLeastScale ? kZeroScale : sv[mt];   // NaN stays NaN
           lv[mt] = lg2(v);
           iv[mt] = rcp(v) * kSumUnit;
         }
+        if (fmaxf(fabsf(lv[0]), fabsf(lv[1])) > kScaleBits)         // seldom
+          if (far_scale(sv[0]) || far_scale(sv[1])) again[warp] = 1;
         float lead = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -548,9 +677,14 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               // how far the maximum moves; everything so far shrinks by as much
-              float d = (c ? m1 : m0) - kShift;
+              float d = ceilf((c ? m1 : m0) - kShift);   // by whole powers of two
               const bool none = mx[nt][c] == -INFINITY;
               if (!none) d = fmaxf(d, 0.f);
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)             // moved by a token of a block of zeros?
+                if (sv[mt] == 0.f && (none || d > 0.f) && d > -INFINITY &&
+                    fmaxf(sc[mt][nt][c], sc[mt][nt][c + 2]) == (c ? m1 : m0))
+                  again[warp] = 1;
               if (d == -INFINITY) d = 0.f;               // still nothing
               else mx[nt][c] = none ? d : mx[nt][c] + d;
               const float f = none ? 0.f : ex2(-d);
@@ -581,7 +715,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
             sum_l[nt][0] = fmaf(s0, s0 > 0.f ? iv[mt] : 0.f, sum_l[nt][0]);
             sum_l[nt][1] = fmaf(s1, s1 > 0.f ? iv[mt] : 0.f, sum_l[nt][1]);
-            if (sv[mt] < kMinScale) w[0] = w[1] = w[2] = w[3] = 0.f;
+            if (sv[mt] < kLeastScale) w[0] = w[1] = w[2] = w[3] = 0.f;
             const uint32_t x0 = pack_f16(w[0], w[1]), x1 = pack_f16(w[2], w[3]);
             pb[mt][nt][0][0] = transpose8(x0);
             pb[mt][nt][1][0] = transpose8(x1);
@@ -666,7 +800,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               int64_t at;
               if (row_at(a, q.x, q.y, info.y * kRows + nt * 8 + 2 * tid + c, h, a.ldo, D, &at)) {
                 at += g * (D / 8);
-                const float inv = inverse(l[nt][c]);
+                const float inv = inverse(l[nt][c]) * kSumUnit;
                 if constexpr (F32) {
                   float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
 #pragma unroll
@@ -674,16 +808,16 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     p[j] = make_float4(acc[2 * j][nt][c] * inv, acc[2 * j][nt][c + 2] * inv,
                                        acc[2 * j + 1][nt][c] * inv, acc[2 * j + 1][nt][c + 2] * inv);
                 } else {
-                  uint32_t u[KS];
+                  uint32_t w[KS];
 #pragma unroll
                   for (int j = 0; j < KS; ++j) {
                     const __nv_bfloat162 h2 = __floats2bfloat162_rn(acc[j][nt][c] * inv, acc[j][nt][c + 2] * inv);
-                    u[j] = *reinterpret_cast<const uint32_t*>(&h2);
+                    w[j] = *reinterpret_cast<const uint32_t*>(&h2);
                   }
                   uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
 #pragma unroll
                   for (int j = 0; j < KS / 4; ++j)
-                    p[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+                    p[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                 }
               }
             }
@@ -700,8 +834,12 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 *reinterpret_cast<float2*>(dst + row * D + g * (D / 8) + 2 * j) =
                     make_float2(acc[j][nt][c], acc[j][nt][c + 2]);
               if (g == 0) {
-                piece_m[(2 * warp + slot) * kRows + row] = mx[nt][c];
-                piece_l[(2 * warp + slot) * kRows + row] = l[nt][c];
+                // the sum as a number from 1 to 2 and its unit
+                const float e = (float)((int)(__float_as_uint(l[nt][c]) >> 23 & 255u) - 127);
+                const int at = (2 * warp + slot) * kRows + row;
+                piece_m[at] = mx[nt][c];
+                piece_l[at] = l[nt][c] * pow2(-e);
+                piece_u[at] = l[nt][c] == 0.f ? -INFINITY : mx[nt][c] - kShift + kSumUnitBits + e;
               }
             }
           if (lane == 0) {
@@ -712,6 +850,29 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
         fresh = true;
         more_before = true;
+      }
+    }
+    __syncwarp();
+    if (again[warp] && !dead) {
+      // value scales far apart in the part, perhaps: the pieces of which that is so, again
+      const int4 at = part_at[warp];
+      Cursor c;
+      c.i = at.x;
+      enter<kRows>(a, c);
+      c.rt = at.y; c.h = at.z; c.t = at.w;
+      int slot = 0;
+#pragma unroll 1
+      for (int left = n; left > 0;) {
+        const int tiles = min(left, c.nt - c.t), rows = (2 * warp + slot) * kRows;
+        const bool whole = c.t == 0 && tiles == c.nt;
+        left -= tiles;
+        if (scales_apart(a, c.i, c.h, c.t * kTile, min((c.t + tiles) * kTile, c.len)))
+          rows_apart<D, F32>(a, c.i, c.rt * kRows, kRows, c.h, c.t * kTile, (c.t + tiles) * kTile,
+                             whole ? nullptr : left == 0 ? reinterpret_cast<float*>(ring) : firsts + warp * C::kPiece,
+                             piece_m + rows, piece_l + rows, piece_u + rows);
+        c.t += tiles - 1;
+        advance<kRows>(a, c);
+        slot = 1;
       }
     }
     if (dead) {
@@ -750,14 +911,18 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const uint32_t after = leaders & ~((2u << k) - 1);
     return after ? __ffs(after) - 1 : pieces;
   };
-  // each piece's weight against the run's maximum
+  // each piece's weight against the run's maximum, its sum in the run's unit
   for (int x = threadIdx.x; x < pieces * kRows; x += C::kThreads) {
     const int k = x / kRows, row = x % kRows, end = run_end(k);
-    float M = -INFINITY;
+    float M = -INFINITY, U = -INFINITY;
 #pragma unroll 4
-    for (int p = run_begin(k); p < end; ++p) M = fmaxf(M, piece_m[order[p] * kRows + row]);
-    const float own = piece_m[order[k] * kRows + row];
-    piece_f[x] = own == M ? 1.f : ex2(own - M);
+    for (int p = run_begin(k); p < end; ++p) {
+      M = fmaxf(M, piece_m[order[p] * kRows + row]);
+      U = fmaxf(U, piece_u[order[p] * kRows + row]);
+    }
+    const int own = order[k] * kRows + row;
+    piece_f[x] = piece_m[own] == M ? 1.f : ex2(piece_m[own] - M);
+    piece_w[x] = piece_l[own] * (piece_u[own] == U ? 1.f : ex2(piece_u[own] - U));
   }
   if (threadIdx.x < 2) {
     // slot 0: a run without its beginning, the CTA's first; slot 1: one without its end, its last
@@ -782,7 +947,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
     const int row = x % kItems / (D / 4), c = x % (D / 4), end = run_end(k0);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f, M = -INFINITY;
+    float l = 0.f, M = -INFINITY, U = -INFINITY;
 #pragma unroll 4
     for (int k = k0; k < end; ++k) {
       const int p = order[k];
@@ -791,20 +956,22 @@ attn_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       const float f = piece_f[k * kRows + row];
       const float4 v = *reinterpret_cast<const float4*>(src + row * D + 4 * c);
       M = fmaxf(M, piece_m[p * kRows + row]);
-      l = fmaf(piece_l[p * kRows + row], f, l);
+      U = fmaxf(U, piece_u[p * kRows + row]);
+      l += piece_w[k * kRows + row];
       o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
     }
     const Tag& head = tags[order[k0]];
     if (head.starts && tags[order[end - 1]].ends) {
       int64_t at;
       if (row_at(a, head.q0, head.q_len, head.rt * kRows + row, head.h, a.ldo, D, &at))
-        store_out4<F32>(a, at + 4 * c, o, inverse(l));
+        store_out4<F32>(a, at + 4 * c, o, inverse(l), unit_of(M, U));
     } else {
       float* gp = a.part + ((int64_t)blockIdx.x * 2 + (head.starts ? 1 : 0)) * C::kPiece;
       *reinterpret_cast<float4*>(gp + row * D + 4 * c) = o;
       if (c == 0) {
         gp[kRows * D + row] = M;
         gp[kRows * D + kRows + row] = l;
+        gp[kRows * D + 2 * kRows + row] = U;
       }
     }
   }
@@ -822,7 +989,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_
   constexpr int kRows = C::kRows, kItems = kRows * D / 4, kGroups = kMergeThreads / kItems;
   __shared__ int first_end;
   __shared__ float4 so[kGroups][kItems];
-  __shared__ float sm[kGroups][kItems], sl[kGroups][kItems];
+  __shared__ float sm[kGroups][kItems], sl[kGroups][kItems], su[kGroups][kItems];
   if (threadIdx.x == 0) first_end = ctas;
   pdl_wait();
   pdl_launch();
@@ -845,18 +1012,19 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_
   const float* next = first + C::kPiece;                 // slot 0 of the CTA after, then every second piece
   const int x = threadIdx.x % kItems, grp = threadIdx.x / kItems;
   const int row = x / (D / 4), c = x % (D / 4);
-  float M = -INFINITY, l = 0.f;
+  float M = -INFINITY, U = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float m, float lp, const float4& v) {
-    const float Mn = fmaxf(M, m);
+  auto add = [&](float m, float u, float lp, const float4& v) {
+    const float Mn = fmaxf(M, m), Un = fmaxf(U, u);
     const float f0 = M == Mn ? 1.f : ex2(M - Mn), f1 = m == Mn ? 1.f : ex2(m - Mn);
+    l = fmaf(l, U == Un ? 1.f : ex2(U - Un), lp * (u == Un ? 1.f : ex2(u - Un)));
     M = Mn;
-    l = fmaf(l, f0, lp * f1);
+    U = Un;
     o.x = fmaf(o.x, f0, v.x * f1); o.y = fmaf(o.y, f0, v.y * f1);
     o.z = fmaf(o.z, f0, v.z * f1); o.w = fmaf(o.w, f0, v.w * f1);
   };
   for (int p0 = grp; p0 < n; p0 += 4 * kGroups) {
-    float m[4], lp[4];
+    float m[4], lp[4], up[4];
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -865,28 +1033,30 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_
         const float* src = p == 0 ? first : next + (int64_t)(p - 1) * 2 * C::kPiece;
         m[k] = src[kRows * D + row];
         lp[k] = src[kRows * D + kRows + row];
+        up[k] = src[kRows * D + 2 * kRows + row];
         v[k] = *reinterpret_cast<const float4*>(src + row * D + 4 * c);
       }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (p0 + k * kGroups < n) add(m[k], lp[k], v[k]);
+      if (p0 + k * kGroups < n) add(m[k], up[k], lp[k], v[k]);
   }
   so[grp][x] = o;
   sm[grp][x] = M;
   sl[grp][x] = l;
+  su[grp][x] = U;
   __syncthreads();
   int64_t at;
   if (grp == 0 && row_at(a, head.q0, head.q_len, head.rt * kRows + row, head.h, a.ldo, D, &at)) {
-    for (int k = 1; k < kGroups; ++k) add(sm[k][x], sl[k][x], so[k][x]);
-    store_out4<F32>(a, at + 4 * c, o, inverse(l));
+    for (int k = 1; k < kGroups; ++k) add(sm[k][x], su[k][x], sl[k][x], so[k][x]);
+    store_out4<F32>(a, at + 4 * c, o, inverse(l), unit_of(M, U));
   }
 }
 
 template <int D, int NT, bool F32>
 lq_status launch_split(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, int ctas, void* stream) {
   using C = Cfg<D, NT, F32>;
-  static_assert(C::kHalves >= 3 && C::kSmem + 1536 <= 227 * 1024, "shared memory");
+  static_assert(C::kHalves >= 3 && C::kSmem + 2048 <= 227 * 1024, "shared memory");
   static_assert(C::kHalves * C::kHalfBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
   static_assert(C::kRing >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
   auto kern = attn_split_kernel<D, NT, F32>;
@@ -960,7 +1130,7 @@ extern "C" size_t lq_attention_paged_workspace_size(int batch, int64_t total_q, 
   // per CTA two pieces and what they belong to, and one for each of up to 16
   // warps, of up to 16 rows; or what the tensor-core kernel leaves
   const int ctas = attn::cta_count(), group = q_heads / kv_heads;
-  size_t floats = (size_t)ctas * (2 + 16) * 16 * (size_t)(head_dim + 2);
+  size_t floats = (size_t)ctas * (2 + 16) * 16 * (size_t)(head_dim + 3);
   if (attn::many_rows(batch, total_q, group)) {
     const attn::TilePlan p = attn::plan_tiles(batch, total_q, group, kv_heads, head_dim, INT64_MAX, ctas);
     if (p.part_floats > floats) floats = p.part_floats;
@@ -1007,6 +1177,7 @@ extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtyp
   const int sms = device_sm_count();
   if (sms <= 0) return LQ_ERR_CUDA;
   attn::Args a;
+  a.kc = k_cache_dev; a.vc = v_cache_dev;
   a.q = q_dev; a.ldq = ldq; a.total_q = total_q; a.cu_q = cu_q_dev; a.kv_lens = kv_lens_dev; a.batch = batch;
   a.table = block_table_dev; a.ldt = table_stride; a.width = table_width;
   a.ks = k_scales_dev; a.vs = v_scales_dev; a.num_blocks = num_blocks;

@@ -32,6 +32,8 @@ struct Args {
   const int32_t* table;
   int64_t ldt;
   int width;
+  const int8_t* kc;
+  const int8_t* vc;
   const float* ks;
   const float* vs;
   int64_t num_blocks;
@@ -45,12 +47,20 @@ struct Args {
 };
 
 constexpr long long kWaitCycles = 2000000000ll;   // about one second
-// Value scales below 2^-100 count as zero (a block of zeros has scale 0): their
-// tokens take part in the sum of weights at 2^-100, so that the logarithm stays
-// finite, and not in the values' sum.  Sums of weight / scale are held times
-// 2^-20, between 2^80 per weight for such scales and normal numbers up to 2^106.
-constexpr float kMinScale = 7.88860905e-31f;      // 2^-100
-constexpr float kSumUnit = 9.5367431640625e-7f;   // 2^-20
+// Where value scales may be far apart (the kernel for many rows; rows_apart of the
+// split kernel) a row carries two exponents, both whole numbers: `mx`, the values'
+// (its weights are 2^(x - mx + kShift), x the exponent that holds the value scale),
+// and `un`, the unit of its sum of weights 2^un, near the largest score.  Their
+// difference is about the log2 of the value scales that matter, whatever those
+// are, so neither sum can leave fp32's range.  A weight goes into the sum as
+// weight / value scale times one factor per row, 2^(mx - kShift - un) (`unit_of`).
+
+// 2^k of a whole number, subnormal ones too; 0 where that is too small and for NaN.
+__device__ __forceinline__ float pow2(float k) {
+  const int e = (int)fminf(fmaxf(k, -150.f), 127.f);
+  return __int_as_float(e >= -126 ? (e + 127) << 23 : (1 << 23) >> (-126 - e));
+}
+
 // Softmax weights are held times 2^8 relative to the running maximum, and the
 // maximum may be behind by up to 2^7: the largest is then 2^15, in fp16's
 // range, and weights down to 2^-22 of the maximum are normal numbers.
@@ -73,6 +83,14 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// log2 of a value scale: -inf of 0, subnormal scales too.
+__device__ __forceinline__ float log2_scale(float v) {
+  return v < 7.88860905e-31f ? lg2(v * 18446744073709551616.f) - 64.f : lg2(v);       // 2^-100, 2^64
+}
+
+// The factor of a row's weights over value scales in its sum.
+__device__ __forceinline__ float unit_of(float mx, float un) { return pow2(mx - kShift - un); }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);

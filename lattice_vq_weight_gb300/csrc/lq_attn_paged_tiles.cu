@@ -51,6 +51,31 @@ constexpr int kTileRows = 128;
 constexpr uint32_t kTopWeight = (15u + 15u) << 10;        // 2^(kShift + kLead) as fp16
 static_assert(kShift + kLead == 15.f, "the largest weight");
 
+// Which weights may go into a row's sum as weight / value scale: those of blocks
+// whose value scale is at least a floor.  With lv its log2 and lv >= mx - un - 60,
+// the score of a weight that is flushed (x < mx - 134) is below un - 74, and no
+// score is above un + 67.  Blocks below the floor (zeros above all) go into the sum
+// by their scores, 2^(score - un), at the cost of an exponential of their own; so
+// does everything where mx - un is so low that a row's factor would leave fp32's
+// range.
+constexpr float kFloorGap = 60.f, kFloorLeast = -100.f, kUnitLeast = -100.f;
+
+// The warp's floor under value scales for the rows of its lanes (mx of -inf: a row
+// without a weight yet); infinite where a row's factor is out of range: no block is above it.
+struct Floor {
+  int most = -300, least = 300;
+  __device__ __forceinline__ void add(float mx, float un) {
+    if (mx == -INFINITY) return;
+    const int d = (int)fminf(fmaxf(mx - un, -300.f), 300.f);
+    most = max(most, d);
+    least = min(least, d);
+  }
+  __device__ __forceinline__ float over_warp() const {
+    const int hi = __reduce_max_sync(0xffffffffu, most), lo = __reduce_min_sync(0xffffffffu, least);
+    return lo < (int)kUnitLeast ? INFINITY : pow2(fmaxf((float)hi - kFloorGap, kFloorLeast));
+  }
+};
+
 template <int D>
 struct TileCfg {
   static constexpr int T = D == 256 ? 1 : 2;                // row tiles per CTA
@@ -199,13 +224,13 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
 }
 
 // A row's weights of one tile from its scores: packed fp16 weights, the sum of
-// weight / value scale; returns the largest weight's bits, or more (positive
+// weight / value scale in the row's unit; returns the largest weight's bits, or more (positive
 // fp16 numbers are in the order of their bits, with infinity and NaN above, and
 // take three-way integer maxima two at a time).  scales[g], of the g-th 16
 // tokens: key scale, log2 and reciprocal of the value scale; the exponent of a
 // token is score * fac * .x + .y + base.
 template <int BN>
-__device__ __forceinline__ uint32_t row_weights(uint32_t tmem, float fac, float base, const float4* scales,
+__device__ __forceinline__ uint32_t row_weights(uint32_t tmem, float fac, float base, float unit, const float4* scales,
                                              uint32_t (&w)[BN / 2], float& l) {
   uint32_t top = 0;
   uint32_t s[2][32];
@@ -237,20 +262,21 @@ __device__ __forceinline__ uint32_t row_weights(uint32_t tmem, float fac, float 
         if (e & 1) top = __vimax3_u16x2(top, w[16 * c + 8 * half + e - 1], w[16 * c + 8 * half + e]);
       }
       sum0 = add2(sum0, sum1);
-      l = fmaf(sum0.x + sum0.y, now[half].z, l);
+      l = fmaf(sum0.x + sum0.y, now[half].z * unit, l);
     }
   }
   return max(top >> 16, top & 0xFFFFu);
 }
 
 // The tiles that the above does not serve, few of a unit: tokens that a row does
-// not see (beyond vis0, or in a block that is gone), blocks that count as zero,
-// rows whose maximum moves.  Two short loops, the largest exponent and then the
-// weights: code that runs so seldom comes from far away, and unrolled twice
-// over it took three times as long as the common tiles' (3.5 us a tile to 1.1).
+// not see (beyond vis0, or in a block that is gone), blocks below the floor of
+// value scales, rows whose maximum moves.  Two short loops, the largest exponent
+// (.x) and score (.y) and then the weights: code that runs so seldom comes from
+// far away, and unrolled twice over it took three times as long as the common
+// tiles' (3.5 us a tile to 1.1).
 template <int BN>
-__device__ __forceinline__ float row_top(uint32_t tmem, float fac, const float4* scales, uint32_t gone, int vis0) {
-  float top = -INFINITY;
+__device__ __forceinline__ float2 row_top(uint32_t tmem, float fac, const float4* scales, uint32_t gone, int vis0) {
+  float2 top = make_float2(-INFINITY, -INFINITY);
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     uint32_t x32[32];
@@ -260,16 +286,18 @@ __device__ __forceinline__ float row_top(uint32_t tmem, float fac, const float4*
       const int g = 2 * c + half, vis = (gone >> g & 1) ? -1 : vis0 - 16 * g;      // tokens 0 .. vis are seen
       const float4 sc = scales[g];
       const float k = fac * sc.x;
+      float most = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        top = fmaxf(top, e > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + e]), k, sc.y));
+      for (int e = 0; e < 16; ++e) most = fmaxf(most, e > vis ? -INFINITY : __uint_as_float(x32[16 * half + e]) * k);
+      // (fmaxf passes over the NaN of a block of infinite scale that the row does not see)
+      top = make_float2(fmaxf(top.x, most + sc.y), fmaxf(top.y, most));
     }
   }
   return top;
 }
 template <int BN>
-__device__ __forceinline__ void store_weights(uint32_t tmem, float fac, float base, const float4* scales, uint32_t zero,
-                                              uint32_t gone, int vis0, float& l) {
+__device__ __forceinline__ void store_weights(uint32_t tmem, float fac, float base, float unit, float un,
+                                              const float4* scales, uint32_t low, uint32_t gone, int vis0, float& l) {
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     uint32_t x32[32], w[16];
@@ -286,11 +314,19 @@ __device__ __forceinline__ void store_weights(uint32_t tmem, float fac, float ba
         const float x1 = ex2(2 * e + 1 > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + 2 * e + 1]), k, d));
         sum0 += x0;
         sum1 += x1;
-        w[8 * half + e] = (zero >> g & 1) ? 0u : pack_f16(x0, x1);
+        w[8 * half + e] = pack_f16(x0, x1);
       }
-      const float total = sum0 + sum1;
-      // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
-      l = fmaf(total, total > 0.f ? sc.z : 0.f, l);
+      if (low >> g & 1) {                                   // below the floor: by the scores
+        sum0 = sum1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          sum0 += e > vis ? 0.f : ex2(fmaf(__uint_as_float(x32[16 * half + e]), k, -un));
+        l += sum0;
+      } else {
+        const float total = sum0 + sum1;
+        // a block the row does not see may have any scale: its sum is 0, not 0 * NaN
+        l = fmaf(total, total > 0.f ? sc.z * unit : 0.f, l);
+      }
     }
     tmem_st16(tmem + 16 * c, w);                            // over scores read before
   }
@@ -673,20 +709,20 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       __syncwarp();
       if (lane == 0) arrive(&q_full[t]);
     }
-    float mx = -INFINITY, l = 0.f;
+    float mx = -INFINITY, un = -INFINITY, l = 0.f, unit = 0.f, floor = pow2(kFloorLeast);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const float cv = nv, cvm = cv < kMinScale ? kMinScale : cv;     // NaN stays NaN
+      const float cv = nv;
       const uint32_t parts = (1u << (BN / 16)) - 1;
       const uint32_t gone = __ballot_sync(0xffffffffu, cv < 0.f) & parts;
-      const uint32_t zero = __ballot_sync(0xffffffffu, cv < kMinScale) & parts;
+      uint32_t low = __ballot_sync(0xffffffffu, cv < floor) & parts;          // a missing block too; NaN is not
       float4* sc = scales[warp - 4];
       __syncwarp();
-      if (lane < BN / 16) sc[lane] = make_float4(nk, lg2(cvm), rcp(cvm) * kSumUnit, 0.f);
+      if (lane < BN / 16) sc[lane] = make_float4(nk, log2_scale(cv), rcp(cv), 0.f);
       __syncwarp();
       if (j + 1 < n) fetch_scales(j + 1);
       const int vis0 = lim - (first + j) * BN;
-      const bool masked = (first + j + 1) * BN - 1 > lim_min || zero != 0;    // (a missing block counts as zero too)
+      const bool masked = (first + j + 1) * BN - 1 > lim_min || low != 0;
       ok = __all_sync(0xffffffffu, wait_on(&s_full[t], (uint32_t)j & 1, timeout));
       if (!ok) break;
       tc_after();
@@ -695,7 +731,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (common) {
         uint32_t w[BN / 2];
         float sum = l;
-        const uint32_t top = row_weights<BN>(my_s, fac, kShift - mx, sc, w, sum);
+        const uint32_t top = row_weights<BN>(my_s, fac, kShift - mx, unit, sc, w, sum);
         common = !__any_sync(0xffffffffu, top > kTopWeight);
         if (common) {
           l = sum;
@@ -704,12 +740,19 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
         }
       }
       if (!common) {
-        // where the maximum moves, the sum and the output so far shrink
-        const float top = row_top<BN>(my_s, fac, sc, gone, vis0);
-        const bool moves = mx == -INFINITY ? top != -INFINITY : top > mx + kLead;
-        const float f = moves ? ex2(mx - top) : 1.f;
-        if (moves) mx = top;
-        l *= f;
+        // where the maximum moves, the output so far shrinks; where the unit does, the sum
+        const float2 top = row_top<BN>(my_s, fac, sc, gone, vis0);
+        const bool moves = mx == -INFINITY ? top.x != -INFINITY : top.x > mx + kLead;
+        const float to = moves ? ceilf(top.x) : mx, f = moves ? pow2(mx - to) : 1.f;
+        const float un_to = fmaxf(un, ceilf(top.y));
+        l *= pow2(un - un_to);                              // (NaN before any score: 0 of 0)
+        mx = to;
+        un = un_to;
+        unit = unit_of(mx, un);
+        Floor fl;
+        fl.add(mx, un);
+        floor = fl.over_warp();
+        low = __ballot_sync(0xffffffffu, cv < floor || floor == INFINITY) & parts;
         if (j > 0 && __any_sync(0xffffffffu, moves)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -721,7 +764,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
             tmem_st16(my_o + 32 * c + 16, o + 16);
           }
         }
-        store_weights<BN>(my_s, fac, kShift - (mx == -INFINITY ? 0.f : mx), sc, zero, gone, vis0, l);
+        store_weights<BN>(my_s, fac, kShift - (mx == -INFINITY ? 0.f : mx), unit, un, sc, low, gone, vis0, l);
       }
       tmem_wait_st();
       tc_before();
@@ -742,7 +785,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       uint8_t* dst = reinterpret_cast<uint8_t*>(
           whole ? reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D
                 : reinterpret_cast<uint16_t*>(piece));
-      const float inv = l == 0.f ? 0.f : kSumUnit / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       auto put = [&](int c, uint4 v) {
         *reinterpret_cast<uint4*>(my_line + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
       };
@@ -764,8 +807,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
               uint32_t u[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv,
-                                                               __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv * unit,
+                                                               __uint_as_float(o[8 * e + 2 * q + 1]) * inv * unit);
                 u[q] = *reinterpret_cast<const uint32_t*>(&b);
               }
               put(4 * c + e, make_uint4(u[0], u[1], u[2], u[3]));
@@ -789,6 +832,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
       if (!whole) {
         piece[D] = mx;
         piece[D + 1] = l;
+        piece[D + 2] = un;
       }
     }
   }
@@ -826,15 +870,18 @@ __global__ void __launch_bounds__(256) attn_tiles_merge_kernel(const __grid_cons
   if (!tag.valid || j >= tag.q_len) return;
   const float* piece = a.part + ((int64_t)unit * ta.splits * C::kRows + row) * (D + 4);
   constexpr int64_t next = (int64_t)C::kRows * (D + 4);
-  float M = -INFINITY;
-  for (int p = 0; p < ta.splits; ++p) M = fmaxf(M, piece[p * next + D]);
+  float M = -INFINITY, U = -INFINITY;
+  for (int p = 0; p < ta.splits; ++p) {
+    M = fmaxf(M, piece[p * next + D]);
+    U = fmaxf(U, piece[p * next + D + 2]);
+  }
   float o[E], l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
   for (int p = 0; p < ta.splits; ++p) {
-    const float m = piece[p * next + D], f = m == M ? 1.f : ex2(m - M);
-    l = fmaf(piece[p * next + D + 1], f, l);
+    const float f = pow2(piece[p * next + D] - M);
+    l = fmaf(piece[p * next + D + 1], pow2(piece[p * next + D + 2] - U), l);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float2 v = *reinterpret_cast<const float2*>(piece + p * next + E * lane + e);
@@ -842,12 +889,12 @@ __global__ void __launch_bounds__(256) attn_tiles_merge_kernel(const __grid_cons
       o[e + 1] = fmaf(v.y, f, o[e + 1]);
     }
   }
-  const float inv = l == 0.f ? 0.f : kSumUnit / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l, back = unit_of(M, U);
   const int64_t dst = (int64_t)(tag.q0 + j) * a.ldo + (int64_t)(tag.h * a.group + R - j * a.group) * D + E * lane;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + dst + e) =
-        __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+        __floats2bfloat162_rn(o[e] * inv * back, o[e + 1] * inv * back);
 }
 
 template <int D>

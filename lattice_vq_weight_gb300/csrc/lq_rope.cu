@@ -105,14 +105,50 @@ struct Unit {
   bool is_q;
 };
 
+// The heads of a unit whose position is outside the table: normed, not turned.
+// (On its own and after the others, so that the usual units pay nothing for it.)
+template <bool BF16, int G, int IT>
+__device__ __noinline__ void norm_only(const Args& a, const Unit& u) {
+  constexpr int H = 32 / G;
+  const int sub = threadIdx.x & (G - 1);
+  const float* w = u.is_q ? a.qw : a.kw;
+  const void* src = u.is_q ? a.q : a.k;
+  void* dst = u.is_q ? a.qo : a.ko;
+  const int64_t from = u.t * (u.is_q ? a.ldq : a.ldk) + (int64_t)u.h0 * a.dim + 8 * sub;
+  const int64_t to = u.t * (u.is_q ? a.ldqo : a.ldko) + (int64_t)u.h0 * a.dim + 8 * sub;
+#pragma unroll 1
+  for (int it = 0; it < IT; ++it) {
+    const bool here = u.h0 + it * H < u.heads && 8 * sub < a.dim;
+    float x[8] = {}, wv[8], q = 0.f;
+    if (here) {
+      load4<BF16>(src, from + it * H * a.dim, x);
+      load4<BF16>(src, from + it * H * a.dim + 4, x + 4);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      q = fmaf(x[e], x[e], q);
+      wv[e] = w != nullptr && here ? w[8 * sub + e] : 1.f;
+    }
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+    const float r = w != nullptr ? rsqrtf(fmaf(q, a.inv_dim, a.eps)) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = r * (wv[e] * x[e]);
+    if (here) {
+      store4<BF16>(dst, to + it * H * a.dim, x[0], x[1], x[2], x[3]);
+      store4<BF16>(dst, to + it * H * a.dim + 4, x[4], x[5], x[6], x[7]);
+    }
+  }
+}
+
 // G: lanes per head (a power of two, >= dim / 8); IT: rounds of 32 / G heads
-// per unit; INTER: interleaved pairs.
-template <bool BF16, int G, int IT, bool INTER>
+// per unit; INTER: interleaved pairs; PART: only the first dimensions are turned.
+template <bool BF16, int G, int IT, bool INTER, bool PART>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
   constexpr int H = 32 / G;
   const int lane = threadIdx.x & 31, sub = lane & (G - 1);
   const bool in_head = 8 * sub < a.dim;
-  const bool rotates = 8 * sub < a.rot;
+  const bool rotates = PART ? 8 * sub < a.rot : in_head;
   const int half = a.rot >> 1;
   // this lane's dimensions: o0 .. o0 + 3 and o1 .. o1 + 3
   const int o0 = (!INTER && rotates) ? 4 * sub : 8 * sub;
@@ -154,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
   Unit now = unit_of(u), next = unit_of(min(u + warps, units - 1));
   Four<BF16> v[IT][2], vn[IT][2];
   float cs[4], sn[4], csn[4], snn[4];
+  bool outside = false;                           // a position was
   int pos = a.positions[now.t], pos_next = a.positions[next.t];
   fetch(now, v);
   angles(pos, cs, sn);
@@ -195,7 +232,10 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
         s[e] = make_float2(ss[2 * e], ss[2 * e + 1]);
       }
     }
-    if (!(pos >= 0 && pos < a.max_pos) && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
+    if (!(pos >= 0 && pos < a.max_pos)) {           // left to the pass below
+      now.heads = 0;
+      outside = true;
+    }
     void* dst = now.is_q ? a.qo : a.ko;
     const int64_t to = now.t * (now.is_q ? a.ldqo : a.ldko) + (int64_t)now.h0 * a.dim;
 #pragma unroll
@@ -217,8 +257,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
       const float2 r2 = make_float2(r, r);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 p = INTER ? make_float2(x[e].y, x[e].x) : x[e ^ 2];
-        y[e] = mul2(r2, fma2(s[e], p, mul2(c[e], x[e])));
+        const float2 p = INTER ? make_float2(x[e].y, x[e].x) : x[e ^ 2], cx = mul2(c[e], x[e]);
+        // (a value that is not turned has no partner: 0 times an infinite one would be NaN)
+        y[e] = mul2(r2, !PART || rotates ? fma2(s[e], p, cx) : cx);
       }
       if (here) {
         store4<BF16>(dst, to + it * H * a.dim + o0, y[0].x, y[0].y, y[1].x, y[1].y);
@@ -239,6 +280,15 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) { cs[i] = csn[i]; sn[i] = snn[i]; }
   }
+  if (outside) {
+    if (lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
+#pragma unroll 1
+    for (u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += warps) {
+      const Unit x = unit_of(u);
+      const int p = a.positions[x.t];
+      if (!(p >= 0 && p < a.max_pos)) norm_only<BF16, G, IT>(a, x);
+    }
+  }
 }
 
 template <bool BF16, int G>
@@ -256,12 +306,15 @@ lq_status launch_rope(Args& a, int sms, void* stream) {
   int64_t grid = (a.units + kWarps - 1) / kWarps;
   if (grid > (int64_t)sms * 3) grid = (int64_t)sms * 3;
   const unsigned n = (unsigned)grid;
-  auto go = [&](auto inter) {
-    constexpr bool I = decltype(inter)::value;
-    if (it == 1) return serve::launch(norm_rope_kernel<BF16, G, 1, I>, n, kThreads, 0, stream, a);
-    return serve::launch(norm_rope_kernel<BF16, G, kMost, I>, n, kThreads, 0, stream, a);
+  auto go = [&](auto inter, auto part) {
+    constexpr bool I = decltype(inter)::value, P = decltype(part)::value;
+    if (it == 1) return serve::launch(norm_rope_kernel<BF16, G, 1, I, P>, n, kThreads, 0, stream, a);
+    return serve::launch(norm_rope_kernel<BF16, G, kMost, I, P>, n, kThreads, 0, stream, a);
   };
-  return a.interleaved ? go(std::true_type{}) : go(std::false_type{});
+  const std::true_type yes;
+  const std::false_type no;
+  if (a.rot < a.dim) return a.interleaved ? go(yes, yes) : go(no, yes);
+  return a.interleaved ? go(yes, no) : go(no, no);
 }
 
 template <bool BF16>

@@ -707,21 +707,22 @@ lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtype, int64_t 
  * (fp32), up to the first refusal; with a accepted, one more token is drawn
  * from max(p_a - q_a, 0) (fp32) if a < n (from p_a if nothing is left of it) and from
  * p_n otherwise: the first v whose inclusive sum of floor(2^36 weight) exceeds
- * floor(u_sample[b] * total), whole numbers, so that the token does not depend
- * on the order of summation.
+ * floor(floor(2^24 u_sample[b]) * total / 2^24), whole numbers, so that the token
+ * does not depend on the order of summation.
  *   draft_tokens_dev  int32 [batch x max_draft]
  *   draft_lens_dev    int32 [batch], 0 .. max_draft, or NULL: max_draft for all
  *   target_probs_dev  p, [batch x (max_draft + 1) x vocab] of type dtype, strides in
- *                     elements; need not be normalised
+ *                     elements; need not be normalised, but a value above 4
+ *                     counts as 4 in the draw
  *   draft_probs_dev   q, [batch x max_draft x vocab], or NULL: q_i is 1 at x_i
  *   u_accept_dev, u_sample_dev  float32 [batch x max_draft], [batch], in [0, 1)
  *   out_tokens_dev    int32 [batch x (max_draft + 1)] (written): the accepted
  *                     tokens, the drawn one, then -1
  *   accepted_dev      int32 [batch] (written): a
  *   dev_status_dev    LQ_DEV_RANGE: a draft length or token out of range (the
- *                     length clipped, the token refused) or a target row without
- *                     weight (token -1); LQ_DEV_NONFINITE: a non-finite target
- *                     probability in the row drawn from
+ *                     length clipped, the token refused), a target row without
+ *                     weight (token -1) or a value above 4 in the target row drawn
+ *                     from; LQ_DEV_NONFINITE: a non-finite one there
  * vocab <= 2^24, max_draft <= 1024.
  */
 lq_status lq_verify_draft(const int32_t* draft_tokens_dev, const int32_t* draft_lens_dev, int batch, int max_draft,

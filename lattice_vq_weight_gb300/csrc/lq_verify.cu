@@ -13,7 +13,8 @@
 // whole numbers, floor(2^36 w), so their sums do not depend on the order or the
 // split of the summation and the drawn token is a function of the inputs alone:
 // the first v whose inclusive sum exceeds floor(u * total), u's 24 bits taken
-// as a whole number.  (A weight below 2^-36 counts as zero, 1e-11 of the mass.)
+// as a whole number.  (A weight below 2^-36 counts as zero, 1e-11 of the mass, and
+// one above 4, which no probability is, as 4: 2^24 of them then fit 64 bits.)
 //
 // A cluster of CTAs per request, up to eight by the vocabulary's size, so that
 // a small batch still reads its rows with many SMs.  Every CTA runs the
@@ -155,6 +156,7 @@ struct Row {
     if (lane == 0 && gone >= v0 && gone < v1) n.n -= whole(at<BF16>(p, gone));
     for (int o = 16; o; o >>= 1) n.n += __shfl_xor_sync(0xffffffffu, n.n, o);
     if (n.most >= 0x7F800000u) raise_flag(status, LQ_DEV_NONFINITE);
+    else if (n.most > 0x40800000u) raise_flag(status, LQ_DEV_RANGE);      // above 4
     return n.n;
   }
 };

@@ -1059,6 +1059,7 @@ lq_status launch_split(const Args& a, const CUtensorMap& mk, const CUtensorMap& 
   static_assert(C::kHalves >= 3 && C::kSmem + 2048 <= 227 * 1024, "shared memory");
   static_assert(C::kHalves * C::kHalfBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
   static_assert(C::kRing >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
+  static_assert((2 + C::kWarps) * C::kPiece <= work_floats(D), "the pieces fit the workspace");
   auto kern = attn_split_kernel<D, NT, F32>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
     cudaGetLastError();
@@ -1127,15 +1128,8 @@ extern "C" size_t lq_attention_paged_workspace_size(int batch, int64_t total_q, 
   if (batch < 0 || batch > LQ_MAX_REQUESTS || total_q < 0 || kv_heads <= 0 || q_heads <= 0 ||
       q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  // per CTA two pieces and what they belong to, and one for each of up to 16
-  // warps, of up to 16 rows; or what the tensor-core kernel leaves
-  const int ctas = attn::cta_count(), group = q_heads / kv_heads;
-  size_t floats = (size_t)ctas * (2 + 16) * 16 * (size_t)(head_dim + 3);
-  if (attn::many_rows(batch, total_q, group)) {
-    const attn::TilePlan p = attn::plan_tiles(batch, total_q, group, kv_heads, head_dim, INT64_MAX, ctas);
-    if (p.part_floats > floats) floats = p.part_floats;
-  }
-  return attn::meta_bytes(ctas) + floats * sizeof(float);
+  const int ctas = attn::cta_count();
+  return attn::meta_bytes(ctas) + (size_t)ctas * attn::work_floats(head_dim) * sizeof(float);
 }
 
 extern "C" lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtype, int64_t total_q,

@@ -1,5 +1,6 @@
-// Shared by the kernels of the paged attention (lq_attn_paged.cu, the split
-// kernel for few query rows).  Internal to the library.
+// Shared by the kernels of the paged attention: the split kernel for few query
+// rows (lq_attn_paged.cu) and the one for many (lq_attn_paged_tiles.cu).  Internal
+// to the library.
 #pragma once
 
 #include <cmath>
@@ -111,6 +112,12 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t bytes, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Floats of the workspace per SM: of the split kernel's CTA two pieces and one for
+// each of up to 16 warps, of up to 16 rows with their maxima, sums and units.  What
+// the kernel for many rows leaves is less (one piece per CTA, at most a CTA per SM
+// when there are any).
+constexpr int work_floats(int head_dim) { return (2 + 16) * 16 * (head_dim + 3); }
+
 // One request's share of the work: query rows (token j, head of the group)
 // numbered j * group + head for each kv head.
 struct Request {
@@ -135,12 +142,10 @@ __device__ __forceinline__ Request load_request(const Args& a, int i) {
 bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int lines);
 
 // The kernel for many query rows (lq_attn_paged_tiles.cu): its units of work
-// (pairs of row tiles of a kv head, at most so many), the CTAs that share one,
-// and what they leave in the workspace.
+// (pairs of row tiles of a kv head, at most so many) and the CTAs that share one.
 struct TilePlan {
   int64_t units;
   int splits;
-  size_t part_floats;
 };
 // most_tokens: positions that any request can have.
 TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms);

@@ -901,6 +901,7 @@ template <int D>
 lq_status launch_tiles(const TileArgs& ta, const TilePlan& plan, void* stream) {
   using C = TileCfg<D>;
   static_assert(C::kSmem + 1536 <= 227 * 1024, "shared memory");
+  static_assert(C::kRows * (D + 4) <= work_floats(D), "a CTA's piece fits its SM's share of the workspace");
   auto kern = attn_tiles_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
     cudaGetLastError();
@@ -924,7 +925,6 @@ TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int hea
   const int64_t most = most_tokens / (4 * bn);
   if (splits > most) splits = most;
   p.splits = splits > 1 ? (int)splits : 1;
-  p.part_floats = p.splits > 1 ? (size_t)p.units * p.splits * rows * (head_dim + 4) : 0;
   return p;
 }
 

@@ -518,15 +518,19 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(t, stream):
-    """The stream of a call on tensor t: the one given, else the current one of t's device."""
+_raw_stream = None
+
+
+def _stream_of(device: int, stream):
+    """The stream of a call on tensors of a device: the one given, else the device's current one."""
+    global _raw_stream
     if stream is not None:
         return int(stream)
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None or not t.is_cuda:
-        return torch.cuda.current_stream(t.device).cuda_stream
-    return raw(t.get_device())
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 def _is(t, dtype, shape) -> bool:
@@ -541,13 +545,14 @@ def _explain(call: str, wanted) -> None:
                              f"{tuple(t.shape)} {t.dtype} with strides {tuple(t.stride())}")
 
 
-def _one_device(call: str, *tensors) -> None:
-    """Refuse tensors that are not all (None aside) in the memory of one CUDA device."""
+def _one_device(call: str, *tensors) -> int:
+    """The CUDA device that all tensors (None aside) are on; tensors in host memory or on several are refused."""
     d = tensors[0].get_device()
     for t in tensors:
         if t is not None and (t.get_device() != d or d < 0):
             raise ValueError(f"{call}: want tensors on one CUDA device, got "
                              f"{sorted({str(x.device) for x in tensors if x is not None})}")
+    return d
 
 
 def _heads(name: str, t) -> int:
@@ -608,12 +613,12 @@ def lq_kv_plan(cached_lens, new_lens, block_size: int, free_blocks, block_table,
             ("free_blocks", free_blocks, i32, (free,)), ("cu_new", cu_new, i32, (b + 1,)), ("kv_lens", kv_lens, i32, (b,)),
             ("positions", positions, i32, (n,)), ("used", used, i32, (1,)), ("slots", slots, torch.int64, (n,))))
     stride, width = _table("lq_kv_plan", block_table, b)
-    _one_device("lq_kv_plan", cached_lens, new_lens, free_blocks, block_table, cu_new, kv_lens, slots, positions, used,
-                dev_status)
+    dev = _one_device("lq_kv_plan", cached_lens, new_lens, free_blocks, block_table, cu_new, kv_lens, slots, positions,
+                      used, dev_status)
     st = _get_lib().lq_kv_plan(
         cached_lens.data_ptr(), new_lens.data_ptr(), b, block_size, free_blocks.data_ptr(), free, block_table.data_ptr(),
         stride, width, cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), n, used.data_ptr(),
-        _addr(dev_status), _stream_of(cu_new, stream))
+        _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_kv_plan", st)
 
@@ -635,11 +640,11 @@ def lq_qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, cos_sin, q_
         _explain("lq_qk_norm_rope", (("positions", positions, torch.int32, (tokens,)),
                                      ("cos_sin", cos_sin, f32, (rows, rot)), ("q_weight", q_weight, f32, (d,)),
                                      ("k_weight", k_weight, f32, (d,))))
-    _one_device("lq_qk_norm_rope", q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, dev_status)
+    dev = _one_device("lq_qk_norm_rope", q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, dev_status)
     st = _get_lib().lq_qk_norm_rope(
         q.data_ptr(), ldq, hq, k.data_ptr(), ldk, kshape[1], _dtype_id(q), tokens, d, _addr(q_weight), _addr(k_weight),
         eps, positions.data_ptr(), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, q_out.data_ptr(), ldqo,
-        k_out.data_ptr(), ldko, _addr(dev_status), _stream_of(q, stream))
+        k_out.data_ptr(), ldko, _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_qk_norm_rope", st)
 
@@ -653,11 +658,11 @@ def lq_kv_append(k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status=N
         raise ValueError(f"lq_kv_append: k and v do not fit the cache: {tuple(k.shape)}, {tuple(v.shape)}")
     if not _is(slots, torch.int64, (n,)):
         _explain("lq_kv_append", (("slots", slots, torch.int64, (n,)),))
-    _one_device("lq_kv_append", k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status)
+    dev = _one_device("lq_kv_append", k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status)
     st = _get_lib().lq_kv_append(
         k.data_ptr(), _heads("k", k), v.data_ptr(), _heads("v", v), _dtype_id(k), n, slots.data_ptr(),
         k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk, d,
-        _addr(dev_status), _stream_of(k, stream))
+        _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_kv_append", st)
 
@@ -670,10 +675,10 @@ def lq_kv_gather(slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_
     if not (_is(slots, torch.int64, (n,)) and _is(k_out, dt, shape) and _is(v_out, dt, shape)):
         _explain("lq_kv_gather", (("slots", slots, torch.int64, (n,)), ("k_out", k_out, dt, shape),
                                   ("v_out", v_out, dt, shape)))
-    _one_device("lq_kv_gather", slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status)
+    dev = _one_device("lq_kv_gather", slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status)
     st = _get_lib().lq_kv_gather(
         slots.data_ptr(), n, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk,
-        d, k_out.data_ptr(), v_out.data_ptr(), _dtype_id(k_out), _addr(dev_status), _stream_of(slots, stream))
+        d, k_out.data_ptr(), v_out.data_ptr(), _dtype_id(k_out), _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_kv_gather", st)
 
@@ -697,13 +702,13 @@ def lq_attention_paged(q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache
     if not (_is(kv_lens, i32, (b,)) and _is(cu_q, i32, (b + 1,))):
         _explain("lq_attention_paged", (("kv_lens", kv_lens, i32, (b,)), ("cu_q", cu_q, i32, (b + 1,))))
     stride, width = _table("lq_attention_paged", block_table, b)
-    _one_device("lq_attention_paged", q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache, v_scales, out, workspace,
-                dev_status)
+    dev = _one_device("lq_attention_paged", q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache, v_scales, out,
+                      workspace, dev_status)
     st = _get_lib().lq_attention_paged(
         q.data_ptr(), ldq, _dtype_id(q), total, cu_q.data_ptr(), kv_lens.data_ptr(), b, block_table.data_ptr(), stride,
         width, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hq, hk, d,
         d ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), ldo, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _addr(dev_status), _stream_of(q, stream))
+        workspace.numel() * workspace.element_size(), _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_attention_paged", st)
 
@@ -732,12 +737,12 @@ def lq_verify_draft(draft_tokens, draft_lens, target_probs, draft_probs, u_accep
             ("draft_tokens", draft_tokens, i32, (b, n)), ("u_accept", u_accept, f32, (b, n)),
             ("u_sample", u_sample, f32, (b,)), ("out_tokens", out_tokens, i32, (b, n + 1)),
             ("accepted", accepted, i32, (b,)), ("draft_lens", draft_lens, i32, (b,))))
-    _one_device("lq_verify_draft", draft_tokens, draft_lens, target_probs, draft_probs, u_accept, u_sample, out_tokens,
-                accepted, dev_status)
+    dev = _one_device("lq_verify_draft", draft_tokens, draft_lens, target_probs, draft_probs, u_accept, u_sample,
+                      out_tokens, accepted, dev_status)
     st = _get_lib().lq_verify_draft(
         draft_tokens.data_ptr(), _addr(draft_lens), b, n, vocab, target_probs.data_ptr(), t0, t1, _addr(draft_probs), q0,
         q1, _dtype_id(target_probs), u_accept.data_ptr(), u_sample.data_ptr(), out_tokens.data_ptr(), accepted.data_ptr(),
-        _addr(dev_status), _stream_of(target_probs, stream))
+        _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_verify_draft", st)
 

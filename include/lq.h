@@ -688,9 +688,14 @@ size_t lq_attention_paged_workspace_size(int batch, int64_t total_q, int q_heads
  *   dev_status_dev  LQ_DEV_RANGE: a length past the block table (cut there) or a
  *                   block id outside the pool (its tokens are left out);
  *                   LQ_DEV_TIMEOUT: a bounded wait expired (out unspecified)
- * Products and sums are held in fp32 (codes are exact operands); bf16 outputs
- * are rounded once.  The result does not depend on how the work was split
- * beyond fp32 rounding, and equal calls give equal bits.
+ * Codes are exact operands, scores and sums are fp32, outputs are rounded once,
+ * and value scales may be of any size.  The softmax weights of a bf16 call are
+ * rounded to fp16: 11 bits, fewer below 2^-22 of the row's largest; its sum of
+ * weights uses them unrounded, and its sums of values stay in the matrix unit,
+ * whose additions truncate.  Those of an fp32 call carry 22 bits and are added in
+ * fp32.  Equal calls give equal bits.  In another batch, where a request's
+ * positions are split elsewhere, its result may differ by fp32 rounding and, for
+ * bf16, by the fp16 rounding (2^-12) of some of its weights.
  */
 lq_status lq_attention_paged(const void* q_dev, int64_t ldq, int dtype, int64_t total_q, const int32_t* cu_q_dev,
                              const int32_t* kv_lens_dev, int batch, const int32_t* block_table_dev,

@@ -1108,10 +1108,14 @@ int cta_count() {
 
 // Whether the tensor-core kernel takes a bf16 call: by the query rows that an
 // average request has for each kv head.  Its time hardly depends on them up to
-// 256, the split kernel's grows with every 16.  Measured at 8 kv heads of 128,
-// 16 / 24 / 32 / 64 rows: 16 requests of 4000 tokens 66 us against 50 / 84 / 84 /
-// 152; one of 32000 tokens 44 to 50 us against 33 / 48 / 48 / 81; one of 4000
-// tokens 24 us against 17 / 20 / 20 / 24.  (head_dim 64 and 256 cross there too.)
+// 256, the split kernel's grows with every 16.  Measured at 8 kv heads, this
+// kernel's time against the split kernel's at 16 / 24 / 32 / 64 rows, in us:
+//   head_dim                      64                     128                       256
+//   16 requests of 4000  55: 45/74/74/134    66: 51/85/85/153    106: 103/146/185/351
+//   one of 32000 tokens  37: 31/44/44/73  43-49: 34/49/50/82      65: 61/79/100/178
+//   one of 4000 tokens   20: 16/18/18/24     24: 18/21/21/25      32: 24/27/30/39
+// (All rows alike: a batch that mixes prompts and single tokens gets one kernel by
+// its average.)
 bool many_rows(int batch, int64_t total_q, int group) {
   return batch > 0 && (total_q + batch - 1) / batch * group > 16;
 }

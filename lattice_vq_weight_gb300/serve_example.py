@@ -14,7 +14,10 @@ pass of the model over them, and the drafts that survive kept.  A step runs
     lq_attention_paged  attention over it
     lq_verify_draft     accepted drafts and the next token
 
-with every buffer the calls need allocated once.
+The weights, cache pools, block tables and lengths are allocated once; what
+depends on the number of new tokens (slots, positions, workspace, outputs) comes
+from torch's caching allocator step by step, and the free list is made with the
+host waiting (`nonzero`), which a server that keeps one would not do.
 """
 from __future__ import annotations
 

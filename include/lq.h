@@ -736,6 +736,100 @@ lq_status lq_verify_draft(const int32_t* draft_tokens_dev, const int32_t* draft_
                           int64_t draft_row_stride, int dtype, const float* u_accept_dev, const float* u_sample_dev,
                           int32_t* out_tokens_dev, int32_t* accepted_dev, int32_t* dev_status_dev, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The paged cache in 4 bits: the pool, block tables and slots of the calls above
+ * (lq_kv_plan serves both), with
+ *   codes  uint8   [num_blocks x kv_heads x block_size x head_dim / 2]: byte j of a
+ *          vector holds the codes (0 .. 15) of dimensions 2 j (low bits) and 2 j + 1
+ *   scales float16 [num_blocks x kv_heads x block_size x head_dim / group_size x 2]
+ *          (raw 16-bit patterns): a scale s and a base b for every group_size
+ *          neighbouring dimensions of a vector
+ * for K and for V; a cached value is fp16(fma(16 + code, s, b)), rounded once.
+ * head_dim is 64, 128 or 256, group_size 32, 64 or 128 and at most head_dim;
+ * codes and scales are 16-byte aligned.  A vector takes head_dim / 2 + 4 head_dim /
+ * group_size bytes.
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * Write new keys and values into the 4-bit cache.  In IEEE fp32 steps a group x
+ * of a vector becomes
+ *     s = fp16((max x - min x) / 15),  b = fp16(min x - 16 s),
+ *     code = rint((x - b) (1 / s)) - 16, cut to 0 .. 15;  0 where s is 0,
+ * so codes and scales depend on the group alone.  A value is off by at most half a
+ * step s / 2, a little more where fp16 rounds s, b or the value itself: groups
+ * whose values differ by less than 2^-24 become one value.
+ *   k_dev, v_dev    [tokens x kv_heads x head_dim] of type dtype, token strides ldk,
+ *                   ldv (a multiple of 16 bytes)
+ *   slots_dev       int64 [tokens]; negative: the token is left out.  No slot
+ *                   twice in one call.
+ *   dev_status_dev  LQ_DEV_RANGE: a slot past the cache (nothing is written for
+ *                   it), or a value beyond +-16384 (cut there);
+ *                   LQ_DEV_NONFINITE: a non-finite value (stored as 0)
+ */
+lq_status lq_kv_append_q4(const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int dtype, int64_t tokens,
+                          const int64_t* slots_dev, uint8_t* k_cache_dev, uint16_t* k_scales_dev,
+                          uint8_t* v_cache_dev, uint16_t* v_scales_dev, int64_t num_blocks, int block_size,
+                          int kv_heads, int head_dim, int group_size, int32_t* dev_status_dev, void* stream);
+
+/* lq_kv_gather of the 4-bit cache: the values of n slots, exactly for LQ_F32,
+ * rounded once more for LQ_BF16. */
+lq_status lq_kv_gather_q4(const int64_t* slots_dev, int64_t n, const uint8_t* k_cache_dev,
+                          const uint16_t* k_scales_dev, const uint8_t* v_cache_dev, const uint16_t* v_scales_dev,
+                          int64_t num_blocks, int block_size, int kv_heads, int head_dim, int group_size,
+                          void* k_out_dev, void* v_out_dev, int out_dtype, int32_t* dev_status_dev, void* stream);
+
+/* Workspace bytes of lq_attention_paged_q4; 0 for unsupported shapes. */
+size_t lq_attention_paged_q4_workspace_size(int batch, int64_t total_q, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * lq_attention_paged over the 4-bit cache: the same arguments but for the cache and
+ * its group_size, the same masks, zeros and status bits.  The values, exact fp16
+ * numbers, are the operands of the products; scores and sums are fp32, outputs are
+ * rounded once.  The softmax weights of a bf16 call are rounded to fp16 (11 bits,
+ * fewer below 2^-22 of the row's largest), its sum of weights uses them unrounded;
+ * those of an fp32 call carry 22 bits and are added in fp32.  Equal calls give equal
+ * bits.  Slots that hold no token of a request may hold anything; the scales and
+ * bases of its tokens are finite (as lq_kv_append_q4 writes them).
+ */
+lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int dtype, int64_t total_q, const int32_t* cu_q_dev,
+                                const int32_t* kv_lens_dev, int batch, const int32_t* block_table_dev,
+                                int64_t table_stride, int table_width, const uint8_t* k_cache_dev,
+                                const uint16_t* k_scales_dev, const uint8_t* v_cache_dev,
+                                const uint16_t* v_scales_dev, int64_t num_blocks, int block_size, int q_heads,
+                                int kv_heads, int head_dim, int group_size, float sm_scale, void* out_dev,
+                                int64_t ldo, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status_dev,
+                                void* stream);
+
+/*
+ * Log probabilities of given tokens from the logits x, fp32 throughout: with
+ * lse = log sum_v e^(x_v) of a row,
+ *     logprob = x_token - lse,   entropy = -sum_v p_v log p_v,  p_v = e^(x_v - lse),
+ *     rank = the number of tokens before it in the order (logit descending, token
+ *     ascending), and the first `top` tokens of that order with their logprobs.
+ * Logits of -inf (masked tokens) have probability 0 and come last.
+ *   logits_dev      [rows x vocab] of type dtype, row stride ld elements (rows may
+ *                   start at any element)
+ *   tokens_dev      int32 [rows]; negative: none is given, logprob 0 and rank -1
+ *   logprobs_dev    float32 [rows] (written)
+ *   entropy_dev     float32 [rows] (written), or NULL
+ *   ranks_dev       int32 [rows] (written), or NULL
+ *   top             0 .. LQ_MAX_ALTERNATIVES, at most vocab
+ *   top_tokens_dev, top_logprobs_dev  int32, float32 [rows x top] (written); unused
+ *                   for top 0
+ *   dev_status_dev  LQ_DEV_NONFINITE: NaN or +inf in a row (its floats NaN, its
+ *                   tokens and rank -1); LQ_DEV_RANGE: a token past the vocabulary
+ *                   (as if none were given), or a row of -inf alone (logprobs -inf,
+ *                   entropy 0)
+ * vocab <= 2^24, rows <= 2^24.
+ */
+#define LQ_MAX_ALTERNATIVES 32
+lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int dtype, int64_t rows, int64_t vocab,
+                            const int32_t* tokens_dev, float* logprobs_dev, float* entropy_dev, int32_t* ranks_dev,
+                            int top, int32_t* top_tokens_dev, float* top_logprobs_dev, int32_t* dev_status_dev,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -77,6 +77,13 @@ SIGNATURES = {
                                   _I32, _I32, _I32, _F32, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
     "lq_verify_draft": (_I32, [_P, _P, _I32, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P, _P, _P,
                                _P]),
+    "lq_kv_append_q4": (_I32, [_P, _I64, _P, _I64, _I32, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P,
+                               _P]),
+    "lq_kv_gather_q4": (_I32, [_P, _I64, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _P]),
+    "lq_attention_paged_q4_workspace_size": (ctypes.c_size_t, [_I32, _I64, _I32, _I32, _I32]),
+    "lq_attention_paged_q4": (_I32, [_P, _I64, _I32, _I64, _P, _P, _I32, _P, _I64, _I32, _P, _P, _P, _P, _I64, _I32,
+                                     _I32, _I32, _I32, _I32, _F32, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "lq_token_logprobs": (_I32, [_P, _I64, _I32, _I64, _I64, _P, _P, _P, _P, _I32, _P, _P, _P, _P]),
 }
 
 
@@ -745,6 +752,140 @@ def lq_verify_draft(draft_tokens, draft_lens, target_probs, draft_probs, u_accep
         _addr(dev_status), _stream_of(dev, stream))
     if st:
         _check("lq_verify_draft", st)
+
+
+# ------------------------------------------------------------------ the paged cache in 4 bits, and scores of tokens
+# Most alternatives that lq_token_logprobs gives (LQ_MAX_ALTERNATIVES in lq.h)
+LQ_MAX_ALTERNATIVES = 32
+
+
+def _run(call: str, device: int, *args) -> None:
+    """The library's call with `device` as the current one: kernels are launched there."""
+    import torch
+    fn = getattr(_get_lib(), call)
+    if device == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        _check(call, st)
+
+
+def _cache_q4(call, k_cache, k_scales, v_cache, v_scales):
+    """(num_blocks, kv_heads, block_size, head_dim, group_size) of a 4-bit cache's four tensors, checked."""
+    import torch
+    u8, f16, shape = torch.uint8, torch.float16, k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"{call}: k_cache: want [num_blocks x kv_heads x block_size x head_dim / 2], got {tuple(shape)}")
+    groups = k_scales.shape[3] if k_scales.dim() == 5 else 0
+    if groups <= 0 or 2 * shape[3] % groups:
+        raise ValueError(f"{call}: k_scales: want [num_blocks x kv_heads x block_size x groups x 2] with groups that "
+                         f"divide head_dim {2 * shape[3]}, got {tuple(k_scales.shape)}")
+    per_group = (*shape[:3], groups, 2)
+    if not (_is(k_cache, u8, shape) and _is(v_cache, u8, shape) and _is(k_scales, f16, per_group)
+            and _is(v_scales, f16, per_group)):
+        _explain(call, (("k_cache", k_cache, u8, shape), ("v_cache", v_cache, u8, shape),
+                        ("k_scales", k_scales, f16, per_group), ("v_scales", v_scales, f16, per_group)))
+    d = 2 * shape[3]
+    return (*shape[:3], d, d // groups)
+
+
+def paged_cache_q4(num_blocks: int, kv_heads: int, block_size: int, head_dim: int, group_size: int, device):
+    """Empty 4-bit cache pool: (k_cache, k_scales, v_cache, v_scales), codes uint8 [num_blocks x kv_heads x block_size x
+    head_dim / 2], scales and bases float16 [num_blocks x kv_heads x block_size x head_dim / group_size x 2]."""
+    import torch
+    if group_size <= 0 or head_dim % group_size:
+        raise ValueError(f"paged_cache_q4: group_size {group_size} does not divide head_dim {head_dim}")
+    codes = [torch.empty((num_blocks, kv_heads, block_size, head_dim // 2), dtype=torch.uint8, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros((num_blocks, kv_heads, block_size, head_dim // group_size, 2), dtype=torch.float16,
+                          device=device) for _ in range(2)]
+    return codes[0], scales[0], codes[1], scales[1]
+
+
+def lq_kv_append_q4(k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status=None, stream=None) -> None:
+    """Write k, v [tokens x kv_heads x head_dim] to the 4-bit cache's slots (int64 [tokens], negative: left out)."""
+    import torch
+    nb, hk, bs, d, group = _cache_q4("lq_kv_append_q4", k_cache, k_scales, v_cache, v_scales)
+    n = k.shape[0]
+    if k.shape != v.shape or k.dtype is not v.dtype or k.shape != (n, hk, d):
+        raise ValueError(f"lq_kv_append_q4: k and v do not fit the cache: {tuple(k.shape)}, {tuple(v.shape)}")
+    if not _is(slots, torch.int64, (n,)):
+        _explain("lq_kv_append_q4", (("slots", slots, torch.int64, (n,)),))
+    dev = _one_device("lq_kv_append_q4", k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status)
+    _run("lq_kv_append_q4", dev, k.data_ptr(), _heads("k", k), v.data_ptr(), _heads("v", v), _dtype_id(k), n,
+         slots.data_ptr(), k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk,
+         d, group, _addr(dev_status), _stream_of(dev, stream))
+
+
+def lq_kv_gather_q4(slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status=None, stream=None) -> None:
+    """The values that the 4-bit cache's slots stand for, [n x kv_heads x head_dim] float32 or bf16."""
+    import torch
+    nb, hk, bs, d, group = _cache_q4("lq_kv_gather_q4", k_cache, k_scales, v_cache, v_scales)
+    n, dt, shape = slots.numel(), k_out.dtype, (slots.numel(), hk, d)
+    if not (_is(slots, torch.int64, (n,)) and _is(k_out, dt, shape) and _is(v_out, dt, shape)):
+        _explain("lq_kv_gather_q4", (("slots", slots, torch.int64, (n,)), ("k_out", k_out, dt, shape),
+                                     ("v_out", v_out, dt, shape)))
+    dev = _one_device("lq_kv_gather_q4", slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status)
+    _run("lq_kv_gather_q4", dev, slots.data_ptr(), n, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
+         v_scales.data_ptr(), nb, bs, hk, d, group, k_out.data_ptr(), v_out.data_ptr(), _dtype_id(k_out),
+         _addr(dev_status), _stream_of(dev, stream))
+
+
+def lq_attention_paged_q4_workspace_size(batch: int, total_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_get_lib().lq_attention_paged_q4_workspace_size(int(batch), int(total_q), int(q_heads), int(kv_heads),
+                                                               int(head_dim)))
+
+
+def lq_attention_paged_q4(q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache, v_scales, out, workspace,
+                          sm_scale=None, dev_status=None, stream=None) -> None:
+    """lq_attention_paged over a 4-bit cache (see lq.h); sm_scale defaults to head_dim ** -0.5."""
+    import torch
+    nb, hk, bs, d, group = _cache_q4("lq_attention_paged_q4", k_cache, k_scales, v_cache, v_scales)
+    b, i32 = kv_lens.numel(), torch.int32
+    ldq, ldo = _heads("q", q), _heads("out", out)
+    total, hq, dq = q.shape
+    if out.shape != q.shape or q.dtype is not out.dtype or dq != d:
+        raise ValueError(f"lq_attention_paged_q4: q and out do not fit: {tuple(q.shape)}, {tuple(out.shape)}")
+    if not (_is(kv_lens, i32, (b,)) and _is(cu_q, i32, (b + 1,))):
+        _explain("lq_attention_paged_q4", (("kv_lens", kv_lens, i32, (b,)), ("cu_q", cu_q, i32, (b + 1,))))
+    if not workspace.is_contiguous():
+        raise ValueError("lq_attention_paged_q4: workspace: want a contiguous tensor")
+    stride, width = _table("lq_attention_paged_q4", block_table, b)
+    dev = _one_device("lq_attention_paged_q4", q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache, v_scales, out,
+                      workspace, dev_status)
+    _run("lq_attention_paged_q4", dev, q.data_ptr(), ldq, _dtype_id(q), total, cu_q.data_ptr(), kv_lens.data_ptr(), b,
+         block_table.data_ptr(), stride, width, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
+         v_scales.data_ptr(), nb, bs, hq, hk, d, group, d ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), ldo,
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(dev_status), _stream_of(dev, stream))
+
+
+def lq_token_logprobs(logits, tokens, logprobs, entropy=None, ranks=None, top_tokens=None, top_logprobs=None,
+                      dev_status=None, stream=None) -> None:
+    """Log probabilities of tokens [rows] from logits [rows x vocab], and what of entropy, ranks and alternatives
+    [rows x top] is asked for (see lq.h)."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    rows, vocab = logits.shape if logits.dim() == 2 else (-1, 0)
+    if rows < 0 or (vocab > 1 and rows > 0 and logits.stride(1) != 1):
+        raise ValueError(f"lq_token_logprobs: logits: want [rows x vocab] with packed rows, got {tuple(logits.shape)} "
+                         f"with strides {tuple(logits.stride())}")
+    top = 0 if top_tokens is None else top_tokens.shape[-1]
+    if (top_tokens is None) != (top_logprobs is None):
+        raise ValueError("lq_token_logprobs: top_tokens and top_logprobs belong together")
+    if not (_is(tokens, i32, (rows,)) and _is(logprobs, f32, (rows,))
+            and (entropy is None or _is(entropy, f32, (rows,))) and (ranks is None or _is(ranks, i32, (rows,)))
+            and (top_tokens is None or (_is(top_tokens, i32, (rows, top)) and _is(top_logprobs, f32, (rows, top))))):
+        _explain("lq_token_logprobs", (
+            ("tokens", tokens, i32, (rows,)), ("logprobs", logprobs, f32, (rows,)), ("entropy", entropy, f32, (rows,)),
+            ("ranks", ranks, i32, (rows,)), ("top_tokens", top_tokens, i32, (rows, top)),
+            ("top_logprobs", top_logprobs, f32, (rows, top))))
+    dev = _one_device("lq_token_logprobs", logits, tokens, logprobs, entropy, ranks, top_tokens, top_logprobs,
+                      dev_status)
+    _run("lq_token_logprobs", dev, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _dtype_id(logits), rows,
+         vocab, tokens.data_ptr(), logprobs.data_ptr(), _addr(entropy), _addr(ranks), top, _addr(top_tokens),
+         _addr(top_logprobs), _addr(dev_status), _stream_of(dev, stream))
 
 
 # ------------------------------------------------------------------ allocating helpers

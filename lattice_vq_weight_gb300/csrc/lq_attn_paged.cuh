@@ -141,6 +141,11 @@ __device__ __forceinline__ Request load_request(const Args& a, int i) {
 // `lines` of them, at most 256, in the 128-byte swizzle.
 bool encode_cache(CUtensorMap* map, const void* codes, int64_t bytes, int lines);
 
+// One CTA per SM; the merge looks at all of them with one thread each.
+int cta_count();
+// Bytes of the workspace that hold the CTAs' Tags, in front of their pieces.
+size_t meta_bytes(int ctas);
+
 // The kernel for many query rows (lq_attn_paged_tiles.cu): its units of work
 // (pairs of row tiles of a kv head, at most so many) and the CTAs that share one.
 struct TilePlan {

@@ -7,115 +7,604 @@
 // k_p and v_p of kv head h / (q_heads / kv_heads).  A query token that sees
 // nothing gets zeros.
 //
-// One warp per query token and head: 32 tokens at a time, a score per lane in
-// fp32, running maximum and sum, then the values token by token, D / 32
-// dimensions per lane.
+// The split kernel: every warp of one CTA per SM takes an equal, contiguous part
+// of the batch's list of 32-token tiles (lq_attn_split.cuh) and streams it through
+// its own ring of half tiles (K, V, K, V, ...): codes by TMA in rows of 128 bytes
+// with the 128-byte swizzle, scales and bases by untiled bulk copies, one barrier
+// per half.  Codes become fp16 values in registers (one shift, one logic and one
+// fma instruction for two) and are the 16-row operand of mma.sync m16n8k16, eight
+// query rows the other: scores S^T = K q^T, then O^T += V^T w^T with the weights
+// transposed in registers.  Values being exact operands, the softmax knows nothing
+// of scales.  bf16 queries are exact in fp16 after a power-of-two factor per row;
+// fp32 queries and weights are split into two fp16 terms (22 bits).  The running
+// maximum, a whole number, may fall behind by up to 2^7: most tiles only compare
+// with it.
+//
+// Token order inside a half tile: row i of a 16-token product is token
+// 4 (i / 2) + i % 2 for i < 8, two further for i + 8, so that the pairs of tokens
+// a lane holds for the second product are neighbours (2 tid, 2 tid + 1, ... in the
+// operand's order, 4 tid .. 4 tid + 3 in the tile's) and the lanes' reads of V
+// spread over the banks.
 #include "lq_attn_paged.cuh"
+#include "lq_attn_split.cuh"
 #include "lq_q4.cuh"
 
 namespace lq {
 namespace q4 {
 
-struct AttnArgs {
-  attn::Args a;
-  const uint32_t* kc;
-  const uint32_t* vc;
-  const uint32_t* ks;
+using namespace attn;
+
+struct SplitArgs {
+  Args a;
+  const uint32_t* ks;        // (scale, base) pairs
   const uint32_t* vs;
-  int log2_group, dim;
+  int log2_group;
+  int halves;                // of a warp's ring
 };
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const __grid_constant__ AttnArgs qa) {
-  using namespace attn;
-  constexpr int E = D / 32;
-  const Args& a = qa.a;
-  pdl_wait();
-  pdl_launch();
-  const int lane = threadIdx.x & 31, bs1 = (1 << a.log2_bs) - 1, groups = D >> qa.log2_group;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.batch; i += blockDim.x)
-      if ((int64_t)a.kv_lens[i] > ((int64_t)a.width << a.log2_bs)) raise_flag(a.status, LQ_DEV_RANGE);
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= a.total_q * a.q_heads) return;
-  const int t = (int)(item / a.q_heads), head = (int)(item % a.q_heads), h = head / a.group;
-  // the request that owns the token
-  int lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
+template <int D, int NT, bool F32>
+struct Cfg {
+  // 16 warps of at most 128 registers where the output tile and the queries
+  // leave room, else 8 of at most 255
+  static constexpr int kWarps = D * NT * (F32 ? 2 : 1) <= 128 ? 16 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kHalfBytes = kTile * D / 2;         // the K or the V codes of a tile
+  static constexpr int kPiece = piece_floats(kRows, D);
+  static constexpr int kEnds = 2 * kWarps;                 // pieces that the warps may leave
+  static constexpr int kRowBytes = 5 * kEnds * kRows * 4;                // the pieces' rows
+  static constexpr int kMostHalves = 8;
+  // a half: codes, scales (128 bytes per group of the vector), what tile it is, its barrier
+  static constexpr int per_half(int groups) { return kHalfBytes + 4 * kTile * groups + 24; }
+  static constexpr int halves(int groups) {
+    const int fit = (227 * 1024 - 1024 - 2048 - kRowBytes) / (kWarps * per_half(groups));
+    return fit < kMostHalves ? fit : kMostHalves;
   }
-  while (lo + 1 < a.batch && a.cu_q[lo + 1] <= t) ++lo;
-  const Request r = load_request(a, lo);
-  int past = 0;
-  if (t >= r.q0 && t < r.q0 + r.q_len) past = min(r.shown + (t - r.q0) + 1, r.len);
-  const int32_t* table = a.table + lo * a.ldt;
-  const int64_t at_q = (int64_t)t * a.ldq + (int64_t)head * D, at_out = (int64_t)t * a.ldo + (int64_t)head * D;
-  float mx = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int t0 = 0; t0 < past; t0 += 32) {
-    const int p = t0 + lane, blk = p < past ? table[p >> a.log2_bs] : -1;
-    const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
-    if (p < past && !ok) raise_flag(a.status, LQ_DEV_RANGE);
-    const int64_t row = ((((int64_t)blk * a.kv_heads + h) << a.log2_bs) + (p & bs1));
-    float x = -INFINITY;
-    if (ok) {
-      float sum = 0.f;
-      for (int c = 0; c < D; c += 8) {
-        float v[8];
-        values8(qa.kc[row * (D / 8) + c / 8], qa.ks[row * groups + (c >> qa.log2_group)], v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float q;
-          if constexpr (F32) q = reinterpret_cast<const float*>(a.q)[at_q + c + e];
-          else q = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.q)[at_q + c + e] << 16);
-          sum = fmaf(q, v[e], sum);
-        }
-      }
-      x = sum * a.scale_log2;
-    }
-    float top = x;
-    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    const float to = fmaxf(mx, top), f = mx == -INFINITY ? 0.f : ex2(mx - to);
-    const float w = ok ? ex2(x - to) : 0.f;
-    mx = to;
-    float sum = w;
-    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    l = fmaf(l, f, sum);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= f;
-    const uint32_t there = __ballot_sync(0xffffffffu, ok);
-    for (int i = 0; i < 32; ++i) {
-      const int64_t from = __shfl_sync(0xffffffffu, row, i);
-      const float wt = __shfl_sync(0xffffffffu, w, i);
-      if (there >> i & 1) {
-        float v[8];
-        const int c = lane * E;
-        values8(qa.vc[from * (D / 8) + c / 8], qa.vs[from * groups + (c >> qa.log2_group)], v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float x8 = v[0];
-#pragma unroll
-          for (int k = 1; k < 8; ++k) x8 = (c & 7) + e == k ? v[k] : x8;
-          o[e] = fmaf(wt, x8, o[e]);
-        }
-      }
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (F32) reinterpret_cast<float*>(a.out)[at_out + lane * E + e] = o[e] * inv;
-    else reinterpret_cast<__nv_bfloat16*>(a.out)[at_out + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
+  static constexpr int smem(int groups) { return kWarps * halves(groups) * per_half(groups) + kRowBytes + 1024; }
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
+}
+
+// Byte `b` of token `t`'s codes in a half, after the swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(int t, int b) {
+  const uint32_t off = (uint32_t)(t * (D / 2) + b);
+  return off ^ (((off >> 7) & 7u) << 4);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x; w[1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
   }
 }
 
-template <int D>
-lq_status launch_rows(const AttnArgs& qa, bool f32, void* stream) {
-  const int64_t grid = (qa.a.total_q * qa.a.q_heads + 3) / 4;
-  return f32 ? serve::launch(attn_rows_kernel<D, true>, (unsigned)grid, 128, 0, stream, qa)
-             : serve::launch(attn_rows_kernel<D, false>, (unsigned)grid, 128, 0, stream, qa);
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(Cfg<D, NT, F32>::kThreads, 1)
+split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+             const __grid_constant__ SplitArgs sa) {
+  using C = Cfg<D, NT, F32>;
+  const Args& a = sa.a;
+  constexpr int kWarps = C::kWarps, kRows = C::kRows;
+  constexpr int KS = D / 16;                   // k steps of the scores, m tiles of the output
+  constexpr int Q2 = F32 ? 2 : 1;              // fp16 terms of a query or weight
+  extern __shared__ uint8_t q4_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q4_smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tid = lane & 3;
+  const int S = sa.halves, groups = D >> sa.log2_group;
+  uint8_t* ring = smem + warp * S * C::kHalfBytes;
+  uint8_t* after = smem + kWarps * S * C::kHalfBytes;
+  uint32_t* scales = reinterpret_cast<uint32_t*>(after) + warp * S * kTile * groups;
+  after += kWarps * S * kTile * groups * 4;
+  int4* infos = reinterpret_cast<int4*>(after) + warp * S;                         // which tile a K half is of
+  after += kWarps * S * 16;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * S;
+  after += kWarps * S * 8;
+  // maxima, sums and units of the warps' pieces, and their weights when they are joined
+  float* piece_m = reinterpret_cast<float*>(after);
+  float* piece_l = piece_m + C::kEnds * kRows;
+  float* piece_u = piece_l + C::kEnds * kRows;
+  float* piece_f = piece_u + C::kEnds * kRows;
+  float* piece_w = piece_f + C::kEnds * kRows;
+  __shared__ Tag tags[2 * kWarps];
+  __shared__ int order[2 * kWarps];            // the pieces that are there, in order
+  __shared__ long long wsum[kWarps];
+  __shared__ int2 asked[kWarps];               // the warp's current request: first query token, how many
+  __shared__ int timeout, q_end;
+  const bool paired = a.log2_bs < 5;           // a tile spans two blocks of 16
+  // where the warps' first pieces go when more follow; a last one takes the
+  // warp's ring, which is not filled again
+  float* firsts = a.part + ((int64_t)gridDim.x * 2 + (int64_t)blockIdx.x * kWarps) * C::kPiece;
+
+  if (lane == 0) {
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) mbar_init1(bars + s, 1);
+    mbar_init_fence();
+    tags[2 * warp].valid = tags[2 * warp + 1].valid = 0;
+  }
+  pdl_wait();
+  pdl_launch();
+  if (threadIdx.x == 0) {
+    timeout = 0;
+    q_end = a.cu_q[a.batch];
+  }
+  Cursor ci;                                   // the tile whose halves are fetched next
+  const int n = part_of_warp<kRows, kWarps>(a, reinterpret_cast<long long*>(smem), wsum, ci);
+
+  if (n > 0) {
+    // lanes 0 and 1: the block of half a tile each (the same block where it
+    // holds the whole tile), and its head's place in the pool
+    const int step = paired ? 16 : kTile;      // tokens that a copy brings
+    int blk = -1, at_head = 0;
+    bool blk_ok = false;
+    auto load_block = [&]() {
+      const int p = ci.t * kTile + (paired ? 16 * lane : 0);
+      blk = -1;
+      if (lane < 2 && p < ci.len) blk = a.table[ci.i * a.ldt + (p >> a.log2_bs)];
+    };
+    const int rows_per_block = (D / 2 << a.log2_bs) >> 7;
+    int qi = 0;                                // halves issued
+    auto issue = [&](int s) {
+      const bool is_v = qi & 1;
+      if (!is_v) {
+        blk_ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+        at_head = blk * a.kv_heads + ci.h;
+        if (lane < 2 && !blk_ok && ci.t * kTile + (paired ? 16 * lane : 0) < ci.len)
+          raise_flag(a.status, LQ_DEV_RANGE);  // a block id outside the pool
+        const uint32_t ok = __ballot_sync(0xffffffffu, blk_ok);
+        // bit 16: the rows' last tile; 17, 18: the half of the tile that is not there
+        if (lane == 0)
+          infos[s] = make_int4(ci.i, ci.rt, ci.h | (ci.t + 1 == ci.nt ? 1 << 16 : 0) | (int)(~ok & 3u) << 17, ci.t);
+      }
+      const uint32_t there = __popc(__ballot_sync(0xffffffffu, blk_ok && lane < (paired ? 2 : 1)));
+      if (lane == 0) mbar_expect_tx(bars + s, there * step * (D / 2 + 4 * groups));
+      __syncwarp();
+      if (lane < (paired ? 2 : 1) && blk_ok) {
+        const int off = paired ? 0 : (ci.t * kTile) & ((1 << a.log2_bs) - 1);
+        tma_load_2d(ring + s * C::kHalfBytes + lane * 16 * (D / 2), is_v ? &map_v : &map_k, bars + s, 0,
+                    at_head * rows_per_block + ((off * (D / 2)) >> 7));
+        bulk_load(scales + (s * kTile + lane * 16) * groups,
+                  (is_v ? sa.vs : sa.ks) + (((int64_t)at_head << a.log2_bs) + off) * groups, step * groups * 4, bars + s);
+      }
+      if (++qi < 2 * n && is_v) {
+        advance<kRows>(a, ci);
+        load_block();
+      }
+    };
+
+    load_block();
+    int4 info = make_int4(ci.i, ci.rt, ci.h, ci.t);
+    uint32_t qf[NT][KS][2][Q2];
+    float acc[KS][NT][4];
+    float mx[NT][2], sum_l[NT][2], fac[NT][2];
+    int lim[NT][2];                            // last position each of this thread's rows sees
+    int lim_min = 0, len = 0;
+    bool fresh = true, seg_starts = false, more_before = false, dead = false;
+    float sc[2][NT][4];                        // the tile's scores, then exponents
+    const int tg = (g >> 1) * 4 + (g & 1);     // the token of row g of a product
+    int s = 0;
+    uint32_t ph = 1;
+
+    // half tiles one after the other, K and V in turn; the first S steps only
+    // fill the ring, so that fetching stands in the code once
+#pragma unroll 1
+    for (int st = -S; st < 2 * n; ++st) {
+      const bool skip = st < 0;
+      if (st == -S || (!skip && !(st & 1))) {
+        // (the first segment's rows are fetched beside its first block id)
+        if (!skip) info = infos[s];            // written when the half was issued
+        if (fresh) {
+          fresh = false;
+          const int h = info.z & 0xFFFF;
+          seg_starts = info.w == 0;
+          // this segment's query rows: lane (g, tid) holds row g's dimensions
+          // tid * D/4 ...; a power of two per row brings them into fp16's range
+          const Request r = load_request(a, info.x);
+          len = r.len;
+          if (lane == 0) asked[warp] = make_int2(r.q0, r.q_len);
+          lim_min = INT_MAX;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float v[D / 4];
+            int64_t at;
+            if (row_at(a, r.q0, r.q_len, info.y * kRows + nt * 8 + g, h, a.ldq, D, &at)) {
+              at += tid * (D / 4);
+              if constexpr (F32) {
+                const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  const float4 x = p[c];
+                  v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
+                }
+              } else {
+                const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + at);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                  const uint4 x = p[c];
+                  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    v[8 * c + 2 * e] = __uint_as_float(u[e] << 16);
+                    v[8 * c + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 4; ++c) v[c] = 0.f;
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 4; ++c) top = fmaxf(top, fabsf(v[c]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^e with the row's largest value in [2^13, 2^14)
+            const int eb = (int)(__float_as_uint(top) >> 23);
+            const int ex = min(126, max(-116, 140 - eb));
+            const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+            const float down = a.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+            // step (word w of codes, half e): codes 2 e and 2 e + 4, then 2 e + 1 and 2 e + 5
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int at8 = 8 * (c >> 1) + 2 * (c & 1) + e;
+                const float x = v[at8] * up, y = v[at8 + 4] * up;
+                qf[nt][c][e][0] = pack_f16(x, y);
+                if constexpr (F32) qf[nt][c][e][1] = rest_f16(qf[nt][c][e][0], x, y);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              fac[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * tid + c));
+              const int j = (info.y * kRows + nt * 8 + 2 * tid + c) / a.group;
+              lim[nt][c] = j < r.q_len ? min(r.shown + j, r.len - 1) : r.len - 1;
+              lim_min = min(lim_min, lim[nt][c]);
+              mx[nt][c] = -INFINITY;
+              sum_l[nt][c] = 0.f;
+            }
+          }
+          lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
+          lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
+#pragma unroll
+          for (int c = 0; c < KS; ++c)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
+        }
+      }
+      if (!skip) {
+        if (!mbar_wait_bounded(bars + s, ph, kWaitCycles)) {
+          timeout = 1;
+          dead = true;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+      }
+      const bool ends = info.z >> 16 & 1;
+      const uint8_t* codes = ring + s * C::kHalfBytes;
+      uint32_t* params = scales + s * kTile * groups;
+      if (!skip && !(st & 1)) {
+        // scores S^T [32 tokens x 8 NT rows]
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+          constexpr int NW = D == 64 ? 2 : 4;          // words of codes per load, of one group
+#pragma unroll
+          for (int j = 0; j < D / 32 / NW; ++j) {
+            const int b = tid * (D / 8) + 16 * j, t = 16 * mt + tg, grp = (2 * b) >> sa.log2_group;
+            uint32_t x[NW], y[NW];
+            load_words(codes + code_at<D>(t, b), x);
+            load_words(codes + code_at<D>(t + 2, b), y);
+            const uint32_t px = params[t * groups + grp], py = params[(t + 2) * groups + grp];
+            const uint32_t sx = twice_low(px), bx = twice_high(px), sy = twice_low(py), by = twice_high(py);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              const uint32_t vx[4] = {fma_h2(pair<0>(x[w]), sx, bx), fma_h2(pair<1>(x[w]), sx, bx),
+                                      fma_h2(pair<2>(x[w]), sx, bx), fma_h2(pair<3>(x[w]), sx, bx)};
+              const uint32_t vy[4] = {fma_h2(pair<0>(y[w]), sy, by), fma_h2(pair<1>(y[w]), sy, by),
+                                      fma_h2(pair<2>(y[w]), sy, by), fma_h2(pair<3>(y[w]), sy, by)};
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int f = 0; f < Q2; ++f) {
+                    const int c = 2 * (NW * j + w) + e;
+                    mma16816(sc[mt][nt], vx[2 * e], vy[2 * e], vx[2 * e + 1], vy[2 * e + 1], qf[nt][c][0][f],
+                             qf[nt][c][1][f]);
+                  }
+            }
+          }
+        }
+      } else if (!skip) {
+        const int p0 = info.w * kTile;
+        // exponents less the running maximum, plus the shift
+        float lead = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float b0 = kShift - (mx[nt][0] == -INFINITY ? 0.f : mx[nt][0]);
+          const float b1 = kShift - (mx[nt][1] == -INFINITY ? 0.f : mx[nt][1]);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            sc[mt][nt][0] = fmaf(sc[mt][nt][0], fac[nt][0], b0);
+            sc[mt][nt][1] = fmaf(sc[mt][nt][1], fac[nt][1], b1);
+            sc[mt][nt][2] = fmaf(sc[mt][nt][2], fac[nt][0], b0);
+            sc[mt][nt][3] = fmaf(sc[mt][nt][3], fac[nt][1], b1);
+          }
+        }
+        const int gone = info.z >> 17;
+        if (p0 + kTile - 1 > lim_min || gone) {
+          // tokens that some row does not see, or of a block that is not there
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (p0 + 16 * mt + tg + (e & 2) > lim[nt][e & 1] || (gone >> (paired ? mt : 0) & 1))
+                  sc[mt][nt][e] = -INFINITY;
+          // what the slots without a token hold must not meet the weights, 0 though they are
+          if (p0 + lane >= len || (gone >> (paired ? lane >> 4 : 0) & 1)) {
+            for (int k = 0; k < groups; ++k) params[lane * groups + k] = 0u;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+        bool empty = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          empty |= mx[nt][0] == -INFINITY || mx[nt][1] == -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) lead = fmaxf(lead, sc[mt][nt][e]);
+        }
+        // a weight too large for the shift, or a row without a maximum: take the
+        // tile's maxima in
+        if (__any_sync(0xffffffffu, lead > kShift + kLead || empty)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              m0 = fmaxf(m0, fmaxf(sc[mt][nt][0], sc[mt][nt][2]));
+              m1 = fmaxf(m1, fmaxf(sc[mt][nt][1], sc[mt][nt][3]));
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+              m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // how far the maximum moves; everything so far shrinks by as much
+              float d = ceilf((c ? m1 : m0) - kShift);   // by whole powers of two
+              const bool none = mx[nt][c] == -INFINITY;
+              if (!none) d = fmaxf(d, 0.f);
+              if (d == -INFINITY) d = 0.f;               // still nothing
+              else mx[nt][c] = none ? d : mx[nt][c] + d;
+              const float f = none ? 0.f : ex2(-d);
+              sum_l[nt][c] *= f;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                acc[j][nt][c] *= f;
+                acc[j][nt][c + 2] *= f;
+              }
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                sc[mt][nt][c] -= d;
+                sc[mt][nt][c + 2] -= d;
+              }
+            }
+          }
+        }
+        // weights and their sums; the weights transposed, as fp16
+        uint32_t pb[2][NT][2][Q2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ex2(sc[mt][nt][e]);
+            sum_l[nt][0] += w[0] + w[2];
+            sum_l[nt][1] += w[1] + w[3];
+            const uint32_t x0 = pack_f16(w[0], w[1]), x1 = pack_f16(w[2], w[3]);
+            pb[mt][nt][0][0] = transpose8(x0);
+            pb[mt][nt][1][0] = transpose8(x1);
+            if constexpr (F32) {
+              pb[mt][nt][0][1] = transpose8(rest_f16(x0, w[0], w[1]));
+              pb[mt][nt][1][1] = transpose8(rest_f16(x1, w[2], w[3]));
+            }
+          }
+        }
+
+        // O^T [D x 8 NT rows] += V^T w^T; lane g holds dimensions g * D/8 ...
+        const int grp = (g * (D / 8)) >> sa.log2_group;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          constexpr int NW = D / 64;             // words of codes per token and lane
+          uint32_t v[4][NW], pr[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 16 * mt + 4 * tid + r;
+            load_words(codes + code_at<D>(t, g * (D / 16)), v[r]);
+            pr[r] = params[t * groups + grp];
+          }
+          const uint32_t s01 = __byte_perm(pr[0], pr[1], 0x5410), b01 = __byte_perm(pr[0], pr[1], 0x7632);
+          const uint32_t s23 = __byte_perm(pr[2], pr[3], 0x5410), b23 = __byte_perm(pr[2], pr[3], 0x7632);
+#pragma unroll
+          for (int c = 0; c < 2 * NW; ++c) {
+            // four dimensions of two tokens side by side
+            const uint32_t sel = c & 1 ? 0x7632 : 0x5410;
+            const uint32_t x = __byte_perm(v[0][c >> 1], v[1][c >> 1], sel), y = __byte_perm(v[2][c >> 1], v[3][c >> 1], sel);
+            const uint32_t vx[4] = {fma_h2(pair<0>(x), s01, b01), fma_h2(pair<1>(x), s01, b01),
+                                    fma_h2(pair<2>(x), s01, b01), fma_h2(pair<3>(x), s01, b01)};
+            const uint32_t vy[4] = {fma_h2(pair<0>(y), s23, b23), fma_h2(pair<1>(y), s23, b23),
+                                    fma_h2(pair<2>(y), s23, b23), fma_h2(pair<3>(y), s23, b23)};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float (&o)[4] = acc[2 * c + half][nt];
+                const uint32_t a0 = vx[2 * half], a1 = vx[2 * half + 1], a2 = vy[2 * half], a3 = vy[2 * half + 1];
+                if constexpr (F32) {
+                  // the matrix unit truncates its sums: over thousands of
+                  // positions that would be a bias, so they are added here
+                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(d, a0, a1, a2, a3, pb[mt][nt][0][1], pb[mt][nt][1][1]);
+                  mma16816(d, a0, a1, a2, a3, pb[mt][nt][0][0], pb[mt][nt][1][0]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[e] += d[e];
+                } else {
+                  mma16816(o, a0, a1, a2, a3, pb[mt][nt][0][0], pb[mt][nt][1][0]);
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();                            // every lane has read the half: refill it
+      if (qi < 2 * n) issue(s);
+      if (++s == S) { s = 0; ph ^= 1; }
+
+      if ((ends || st + 1 == 2 * n) && !skip && (st & 1)) {
+        float l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = sum_l[nt][c];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            l[nt][c] = x;
+          }
+        const int h = info.z & 0xFFFF;
+        if (ends && seg_starts) {
+          // all of the rows' tokens: the outputs, D/8 dimensions per lane and row
+          const int2 q = asked[warp];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              int64_t at;
+              if (row_at(a, q.x, q.y, info.y * kRows + nt * 8 + 2 * tid + c, h, a.ldo, D, &at)) {
+                at += g * (D / 8);
+                const float inv = inverse(l[nt][c]);
+                if constexpr (F32) {
+                  float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
+#pragma unroll
+                  for (int j = 0; j < KS / 2; ++j)
+                    p[j] = make_float4(acc[2 * j][nt][c] * inv, acc[2 * j][nt][c + 2] * inv,
+                                       acc[2 * j + 1][nt][c] * inv, acc[2 * j + 1][nt][c + 2] * inv);
+                } else {
+                  uint32_t w[KS];
+#pragma unroll
+                  for (int j = 0; j < KS; ++j) {
+                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(acc[j][nt][c] * inv, acc[j][nt][c + 2] * inv);
+                    w[j] = *reinterpret_cast<const uint32_t*>(&h2);
+                  }
+                  uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
+#pragma unroll
+                  for (int j = 0; j < KS / 4; ++j)
+                    p[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                }
+              }
+            }
+        } else {
+          const int slot = more_before ? 1 : 0;
+          float* dst = st + 1 == 2 * n ? reinterpret_cast<float*>(ring) : firsts + warp * C::kPiece;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int row = nt * 8 + 2 * tid + c;
+#pragma unroll
+              for (int j = 0; j < KS; ++j)
+                *reinterpret_cast<float2*>(dst + row * D + g * (D / 8) + 2 * j) =
+                    make_float2(acc[j][nt][c], acc[j][nt][c + 2]);
+              if (g == 0) {
+                const int at = (2 * warp + slot) * kRows + row;
+                piece_m[at] = mx[nt][c];
+                piece_l[at] = l[nt][c];
+                piece_u[at] = mx[nt][c] - kShift;      // the unit of the sum: 2^that
+              }
+            }
+          if (lane == 0) {
+            Tag& t = tags[2 * warp + slot];
+            t.i = info.x; t.rt = info.y; t.h = h; t.q0 = asked[warp].x; t.q_len = asked[warp].y;
+            t.starts = seg_starts; t.ends = ends; t.valid = st + 1 == 2 * n ? 1 : 2;
+          }
+        }
+        fresh = true;
+        more_before = true;
+      }
+    }
+    if (dead) {
+      // let the copies in flight land before the CTA ends
+#pragma unroll 1
+      for (int i = 0; i < S; ++i) mbar_wait_bounded(bars + i, ph ^ (i < s ? 1u : 0u), kWaitCycles / 8);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
+  zero_unowned<D, C::kThreads, F32>(a, q_end);
+  join_pieces<D, kRows, kWarps, F32>(a, tags, order, piece_m, piece_l, piece_u, piece_f, piece_w, [&](int w, int valid) {
+    return valid == 2 ? firsts + w * C::kPiece : reinterpret_cast<const float*>(smem + w * S * C::kHalfBytes);
+  });
+}
+
+template <int D, int NT, bool F32>
+lq_status launch_split(const SplitArgs& sa, const CUtensorMap& mk, const CUtensorMap& mv, int ctas, void* stream) {
+  using C = Cfg<D, NT, F32>;
+  static_assert(C::halves(D / 32) >= 3 && C::smem(1) + 2048 <= 227 * 1024 && C::smem(D / 32) + 2048 <= 227 * 1024,
+                "shared memory");
+  static_assert(C::halves(D / 32) * C::kHalfBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
+  static_assert(C::kWarps * C::halves(D / 32) * C::kHalfBytes >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
+  static_assert((2 + C::kWarps) * C::kPiece <= work_floats(D), "the pieces fit the workspace");
+  auto kern = split_kernel<D, NT, F32>;
+  const int groups = D >> sa.log2_group, smem = C::smem(groups);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return LQ_ERR_CUDA;
+  }
+  SplitArgs args = sa;
+  args.halves = C::halves(groups);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mv, args);
+  if (e == cudaSuccess) {
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, attn_merge_kernel<D, NT, F32>, sa.a, ctas);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return LQ_ERR_CUDA;
+  }
+  return check_launch();
 }
 
 }  // namespace q4
@@ -164,20 +653,37 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
     return LQ_ERR_ARG;
   if (workspace_bytes < lq_attention_paged_q4_workspace_size(batch, total_q, q_heads, kv_heads, head_dim))
     return LQ_ERR_SHAPE;
-  q4::AttnArgs qa;
-  attn::Args& a = qa.a;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LQ_ERR_CUDA;
+  q4::SplitArgs sa;
+  attn::Args& a = sa.a;
   a = attn::Args{};
   a.q = q_dev; a.ldq = ldq; a.total_q = total_q; a.cu_q = cu_q_dev; a.kv_lens = kv_lens_dev; a.batch = batch;
   a.table = block_table_dev; a.ldt = table_stride; a.width = table_width; a.num_blocks = num_blocks;
   a.log2_bs = serve::log2_of(block_size); a.q_heads = q_heads; a.kv_heads = kv_heads; a.group = q_heads / kv_heads;
   a.scale_log2 = sm_scale * 1.4426950408889634f; a.out = out_dev; a.ldo = ldo; a.status = dev_status_dev;
-  qa.kc = reinterpret_cast<const uint32_t*>(k_cache_dev); qa.vc = reinterpret_cast<const uint32_t*>(v_cache_dev);
-  qa.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); qa.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
-  qa.log2_group = serve::log2_of(group_size); qa.dim = head_dim;
-  const bool f32 = dtype == LQ_F32;
-  switch (head_dim) {
-    case 64: return q4::launch_rows<64>(qa, f32, stream);
-    case 128: return q4::launch_rows<128>(qa, f32, stream);
-    default: return q4::launch_rows<256>(qa, f32, stream);
+  a.meta = reinterpret_cast<attn::Tag*>(workspace_dev);
+  const int ctas = attn::cta_count();
+  a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + attn::meta_bytes(ctas));
+  sa.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); sa.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
+  sa.log2_group = serve::log2_of(group_size);
+  // a pool without blocks: no copy is issued, any valid map will do
+  const void* kc = num_blocks > 0 ? (const void*)k_cache_dev : workspace_dev;
+  const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;
+  const int64_t bytes = num_blocks > 0 ? num_blocks * block_rows * 128 : 32768;
+  CUtensorMap mk, mv;
+  const int box = (block_size < attn::kTile ? block_size : attn::kTile) * head_dim / 256;
+  if (!attn::encode_cache(&mk, kc, bytes, box) || !attn::encode_cache(&mv, vc, bytes, box)) return LQ_ERR_CUDA;
+  // eight query rows per pass over the codes, sixteen where the average request has more
+  const bool few = ((total_q + batch - 1) / batch) * a.group <= 8;
+  if (dtype == LQ_F32) {
+    if (head_dim == 64) return q4::launch_split<64, 1, true>(sa, mk, mv, ctas, stream);
+    if (head_dim == 128) return q4::launch_split<128, 1, true>(sa, mk, mv, ctas, stream);
+    return q4::launch_split<256, 1, true>(sa, mk, mv, ctas, stream);
   }
+  if (head_dim == 256) return q4::launch_split<256, 1, false>(sa, mk, mv, ctas, stream);
+  if (head_dim == 64) return few ? q4::launch_split<64, 1, false>(sa, mk, mv, ctas, stream)
+                                 : q4::launch_split<64, 2, false>(sa, mk, mv, ctas, stream);
+  return few ? q4::launch_split<128, 1, false>(sa, mk, mv, ctas, stream)
+             : q4::launch_split<128, 2, false>(sa, mk, mv, ctas, stream);
 }

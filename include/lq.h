@@ -804,9 +804,9 @@ lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int dtype, int64
 
 /*
  * Log probabilities of given tokens from the logits x, fp32 throughout: with
- * lse = log sum_v e^(x_v) of a row,
- *     logprob = x_token - lse,   entropy = -sum_v p_v log p_v,  p_v = e^(x_v - lse),
- *     rank = the number of tokens before it in the order (logit descending, token
+ * d_v = x_v - max x (rounded to fp32) and l = sum_v e^(d_v) of a row,
+ *     logprob = d_token - log l,   entropy = -sum_v p_v log p_v,  p_v = e^(d_v) / l,
+ *     rank = the number of tokens before it in the order (d descending, token
  *     ascending), and the first `top` tokens of that order with their logprobs.
  * Logits of -inf (masked tokens) have probability 0 and come last.
  *   logits_dev      [rows x vocab] of type dtype, row stride ld elements (rows may

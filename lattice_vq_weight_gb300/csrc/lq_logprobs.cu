@@ -1,11 +1,13 @@
 // Log probabilities of given tokens from the logits, with the entropy of the
 // distribution, the token's rank and the most likely alternatives.
 //
-// With m = max x, l = sum e^(x - m), S = sum e^(x - m) (x - m) over a row x:
-//     log p(v) = x_v - m - log l,    entropy = -sum p log p = log l - S / l,
-//     rank(t) = the number of v with x_v > x_t, or x_v = x_t and v < t.
+// With m = max x, d = x - m rounded to fp32, l = sum e^d and S = sum e^d d over a
+// row x:
+//     log p(v) = d_v - log l,    entropy = -sum p log p = log l - S / l,
+//     rank(t) = the number of v with d_v > d_t, or d_v = d_t and v < t.
 // S is negative, so the entropy's two terms do not cancel.  Alternatives are in
-// the order of (logit descending, token ascending).
+// the order of (d descending, token ascending): that of the log probabilities as
+// they are given, in which logits that differ by less than d's last place are equal.
 //
 // One CTA per row, several passes over it.
 #include "lq_device.cuh"
@@ -40,13 +42,13 @@ __device__ __forceinline__ float at(const void* p, int64_t i) {
   else return reinterpret_cast<const float*>(p)[i];
 }
 
-// A logit and its token as one number, larger for the ones that come first.
+// A value and its token as one number, larger for the ones that come first.
 __device__ __forceinline__ unsigned long long key_of(float x, uint32_t v) {
   uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);                 // -0 is 0
   b = b & 0x80000000u ? ~b : b | 0x80000000u;
   return (unsigned long long)b << 32 | (0xFFFFFFFFu - v);
 }
-__device__ __forceinline__ float logit_of(unsigned long long key) {
+__device__ __forceinline__ float value_of(unsigned long long key) {
   const uint32_t b = (uint32_t)(key >> 32);
   return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
 }
@@ -89,21 +91,21 @@ __global__ void __launch_bounds__(kThreads) score_kernel(Args a) {
     if (token >= a.vocab) raise_flag(a.status, LQ_DEV_RANGE);
   }
   const float base = m == -INFINITY ? 0.f : m;
-  const unsigned long long own = given ? key_of(at<BF16>(x, token), token) : ~0ull;
+  const unsigned long long own = given ? key_of(at<BF16>(x, token) - base, token) : ~0ull;
   float l = 0.f, s = 0.f;
   int before = 0;
   for (int64_t v = threadIdx.x; v < a.vocab; v += kThreads) {
     const float y = at<BF16>(x, v), d = y - base, e = expf(d);
     l += e;
     if (e > 0.f) s = fmaf(e, d, s);
-    before += key_of(y, (uint32_t)v) > own;
+    before += key_of(d, (uint32_t)v) > own;
   }
   l = over_cta(l, shf, add);
   s = over_cta(s, shf, add);
   before = over_cta(before, shi, [](int p, int q) { return p + q; });
   const float log_l = l > 0.f ? logf(l) : 0.f;
   if (threadIdx.x == 0) {
-    a.logprobs[row] = bad ? NAN : given ? logit_of(own) - base - log_l : 0.f;
+    a.logprobs[row] = bad ? NAN : given ? value_of(own) - log_l : 0.f;
     if (a.entropy != nullptr) a.entropy[row] = bad ? NAN : l > 0.f ? log_l - s / l : 0.f;
     if (a.ranks != nullptr) a.ranks[row] = bad || !given ? -1 : before;
   }
@@ -112,14 +114,14 @@ __global__ void __launch_bounds__(kThreads) score_kernel(Args a) {
     unsigned long long best = 0;
     if (!bad)
       for (int64_t v = threadIdx.x; v < a.vocab; v += kThreads) {
-        const unsigned long long key = key_of(at<BF16>(x, v), (uint32_t)v);
+        const unsigned long long key = key_of(at<BF16>(x, v) - base, (uint32_t)v);
         if (key < last && key > best) best = key;
       }
     best = over_cta(best, shk, [](unsigned long long p, unsigned long long q) { return p > q ? p : q; });
     last = best;
     if (threadIdx.x == 0) {
       a.top_tokens[row * a.top + k] = bad ? -1 : (int32_t)(0xFFFFFFFFu - (uint32_t)best);
-      a.top_logprobs[row * a.top + k] = bad ? NAN : logit_of(best) - base - log_l;
+      a.top_logprobs[row * a.top + k] = bad ? NAN : value_of(best) - log_l;
     }
   }
 }

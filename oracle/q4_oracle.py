@@ -82,7 +82,8 @@ def attention(q, cu_q, kv_lens, table, k_codes, k_scales, v_codes, v_scales, sm_
 
 
 def token_logprobs(logits, tokens, top):
-    """(logprobs, entropy, ranks, top_tokens, top_logprobs) of rows of finite or -inf logits."""
+    """(logprobs, entropy, ranks, top_tokens, top_logprobs) of rows of finite or -inf logits; the order is that of
+    the float32 differences from the row's largest, then of the tokens."""
     n, vocab = logits.shape
     logprobs, entropy = np.zeros(n), np.zeros(n)
     ranks, top_tokens = np.full(n, -1, np.int64), np.zeros((n, top), np.int64)
@@ -93,7 +94,9 @@ def token_logprobs(logits, tokens, top):
         lse = m + math.log(np.exp(x - m).sum()) if m > -math.inf else 0.0
         p = np.exp(x - lse)
         entropy[i] = -sum(float(a) * float(b - lse) for a, b in zip(p, x) if a > 0)
-        order = sorted(range(vocab), key=lambda v: (-x[v], v))
+        with np.errstate(over="ignore"):
+            d = x.astype(np.float32) - np.float32(m if m > -math.inf else 0.0)
+        order = sorted(range(vocab), key=lambda v: (-d[v], v))
         top_tokens[i] = order[:top]
         top_logprobs[i] = x[order[:top]] - lse
         t = int(tokens[i])

@@ -8,7 +8,7 @@
 // nothing gets zeros.
 //
 // The split kernel: every warp of one CTA per SM takes an equal, contiguous part
-// of the batch's list of 32-token tiles (lq_attn_split.cuh) and streams it through
+// of the batch's list of 64-token tiles (lq_attn_split.cuh) and streams it through
 // its own ring of half tiles (K, V, K, V, ...): codes by TMA in rows of 128 bytes
 // with the 128-byte swizzle, scales and bases by untiled bulk copies, one barrier
 // per half.  Codes become fp16 values in registers (one shift, one logic and one
@@ -34,6 +34,9 @@ namespace q4 {
 
 using namespace attn;
 
+constexpr int kTokens = 64;                    // tokens per tile
+constexpr int kMTiles = kTokens / 16;
+
 struct SplitArgs {
   Args a;
   const uint32_t* ks;        // (scale, base) pairs
@@ -44,18 +47,18 @@ struct SplitArgs {
 
 template <int D, int NT, bool F32>
 struct Cfg {
-  // 16 warps of at most 128 registers where the output tile and the queries
+  // 12 warps of at most 168 registers where the output tile and the queries
   // leave room, else 8 of at most 255
-  static constexpr int kWarps = D * NT * (F32 ? 2 : 1) <= 128 ? 16 : 8;
+  static constexpr int kWarps = D * NT * (F32 ? 2 : 1) <= 128 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kHalfBytes = kTile * D / 2;         // the K or the V codes of a tile
+  static constexpr int kHalfBytes = kTokens * D / 2;         // the K or the V codes of a tile
   static constexpr int kPiece = piece_floats(kRows, D);
   static constexpr int kEnds = 2 * kWarps;                 // pieces that the warps may leave
   static constexpr int kRowBytes = 5 * kEnds * kRows * 4;                // the pieces' rows
   static constexpr int kMostHalves = 8;
-  // a half: codes, scales (128 bytes per group of the vector), what tile it is, its barrier
-  static constexpr int per_half(int groups) { return kHalfBytes + 4 * kTile * groups + 24; }
+  // a half: codes, scales, what tile it is, its barrier
+  static constexpr int per_half(int groups) { return kHalfBytes + 4 * kTokens * groups + 24; }
   static constexpr int halves(int groups) {
     const int fit = (227 * 1024 - 1024 - 2048 - kRowBytes) / (kWarps * per_half(groups));
     return fit < kMostHalves ? fit : kMostHalves;
@@ -68,12 +71,29 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
-// Byte `b` of token `t`'s codes in a half, after the swizzle.
+// Codes of a half lie in lines of 128 bytes whose 16-byte chunks are swizzled by the
+// line's number.  A lane reads at one offset (k_at, v_at) and others that differ from
+// it by constants alone: some bits flipped, then a distance.
 template <int D>
-__device__ __forceinline__ uint32_t code_at(int t, int b) {
-  const uint32_t off = (uint32_t)(t * (D / 2) + b);
-  return off ^ (((off >> 7) & 7u) << 4);
-}
+struct At {
+  static constexpr int row = D / 2;            // bytes of a token
+  static __device__ __forceinline__ uint32_t swizzled(uint32_t off) { return off ^ ((off >> 7 & 7u) << 4); }
+  // scores: token tg of the first product, bytes tid * D / 8 ...; of product m, `two`
+  // tokens further, chunk j
+  static __device__ __forceinline__ uint32_t k_at(int tg, int tid) { return swizzled(tg * row + tid * (D / 8)); }
+  static __device__ __forceinline__ uint32_t k_at(uint32_t at, int m, int two, int j) {
+    const uint32_t flip = (D == 64 ? (m & 1) * 64u ^ two * 64u : D == 128 ? two * 16u : two * 32u) ^ j * 16u;
+    return (at ^ flip) + m * 16 * row + (D == 64 ? 0 : two * 2 * row);
+  }
+  // values: token 4 tid of the first product, bytes g * D / 16 ...; of product m, r
+  // tokens further
+  static __device__ __forceinline__ uint32_t v_at(int g, int tid) { return swizzled(4 * tid * row + g * (D / 16)); }
+  static __device__ __forceinline__ uint32_t v_at(uint32_t at, int m, int r) {
+    const uint32_t flip =
+        D == 64 ? (m & 1) * 64u ^ r * 32u : D == 128 ? (r & 1) * 64u ^ (r >> 1) * 16u : (uint32_t)r * 16u;
+    return (at ^ flip) + m * 16 * row + (D == 64 ? 0 : D == 128 ? (r >> 1) * 128 : r * 128);
+  }
+};
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -98,13 +118,15 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
   constexpr int KS = D / 16;                   // k steps of the scores, m tiles of the output
   constexpr int Q2 = F32 ? 2 : 1;              // fp16 terms of a query or weight
   extern __shared__ uint8_t q4_smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q4_smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a cast to and from a number, lets the compiler see shared memory)
+  uint8_t* smem = q4_smem_raw + ((0u - smem_addr(q4_smem_raw)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tid = lane & 3;
   const int S = sa.halves, groups = D >> sa.log2_group;
+  const Masks masks;
   uint8_t* ring = smem + warp * S * C::kHalfBytes;
   uint8_t* after = smem + kWarps * S * C::kHalfBytes;
-  uint32_t* scales = reinterpret_cast<uint32_t*>(after) + warp * S * kTile * groups;
-  after += kWarps * S * kTile * groups * 4;
+  uint32_t* scales = reinterpret_cast<uint32_t*>(after) + warp * S * kTokens * groups;
+  after += kWarps * S * kTokens * groups * 4;
   int4* infos = reinterpret_cast<int4*>(after) + warp * S;                         // which tile a K half is of
   after += kWarps * S * 16;
   uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * S;
@@ -120,7 +142,8 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
   __shared__ long long wsum[kWarps];
   __shared__ int2 asked[kWarps];               // the warp's current request: first query token, how many
   __shared__ int timeout, q_end;
-  const bool paired = a.log2_bs < 5;           // a tile spans two blocks of 16
+  // a tile is one block, or part of one, or up to four
+  const int log2_step = min(a.log2_bs, 6), step = 1 << log2_step, parts = kTokens >> log2_step;
   // where the warps' first pieces go when more follow; a last one takes the
   // warp's ring, which is not filled again
   float* firsts = a.part + ((int64_t)gridDim.x * 2 + (int64_t)blockIdx.x * kWarps) * C::kPiece;
@@ -138,18 +161,17 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     q_end = a.cu_q[a.batch];
   }
   Cursor ci;                                   // the tile whose halves are fetched next
-  const int n = part_of_warp<kRows, kWarps>(a, reinterpret_cast<long long*>(smem), wsum, ci);
+  const int n = part_of_warp<kRows, kWarps, kTokens>(a, reinterpret_cast<long long*>(smem), wsum, ci);
 
   if (n > 0) {
-    // lanes 0 and 1: the block of half a tile each (the same block where it
-    // holds the whole tile), and its head's place in the pool
-    const int step = paired ? 16 : kTile;      // tokens that a copy brings
+    // lane i < parts: the block of the tile's i-th part, and its head's place in the pool
     int blk = -1, at_head = 0;
     bool blk_ok = false;
+    uint32_t there = 0;                        // the parts whose block is in the pool
     auto load_block = [&]() {
-      const int p = ci.t * kTile + (paired ? 16 * lane : 0);
+      const int p = ci.t * kTokens + step * lane;
       blk = -1;
-      if (lane < 2 && p < ci.len) blk = a.table[ci.i * a.ldt + (p >> a.log2_bs)];
+      if (lane < parts && p < ci.len) blk = a.table[ci.i * a.ldt + (p >> a.log2_bs)];
     };
     const int rows_per_block = (D / 2 << a.log2_bs) >> 7;
     int qi = 0;                                // halves issued
@@ -158,25 +180,25 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
       if (!is_v) {
         blk_ok = (unsigned)blk < (unsigned long long)a.num_blocks;
         at_head = blk * a.kv_heads + ci.h;
-        if (lane < 2 && !blk_ok && ci.t * kTile + (paired ? 16 * lane : 0) < ci.len)
+        if (lane < parts && !blk_ok && ci.t * kTokens + step * lane < ci.len)
           raise_flag(a.status, LQ_DEV_RANGE);  // a block id outside the pool
-        const uint32_t ok = __ballot_sync(0xffffffffu, blk_ok);
-        // bit 16: the rows' last tile; 17, 18: the half of the tile that is not there
+        there = __ballot_sync(0xffffffffu, blk_ok);
+        // bit 16: the rows' last tile; from 17 on, the parts that are not there
         if (lane == 0)
-          infos[s] = make_int4(ci.i, ci.rt, ci.h | (ci.t + 1 == ci.nt ? 1 << 16 : 0) | (int)(~ok & 3u) << 17, ci.t);
+          infos[s] = make_int4(ci.i, ci.rt, ci.h | (ci.t + 1 == ci.nt ? 1 << 16 : 0) |
+                                                (int)(~there & ((1u << parts) - 1)) << 17, ci.t);
       }
-      const uint32_t there = __popc(__ballot_sync(0xffffffffu, blk_ok && lane < (paired ? 2 : 1)));
-      if (lane == 0) mbar_expect_tx(bars + s, there * step * (D / 2 + 4 * groups));
+      if (lane == 0) mbar_expect_tx(bars + s, __popc(there) * step * (D / 2 + 4 * groups));
       __syncwarp();
-      if (lane < (paired ? 2 : 1) && blk_ok) {
-        const int off = paired ? 0 : (ci.t * kTile) & ((1 << a.log2_bs) - 1);
-        tma_load_2d(ring + s * C::kHalfBytes + lane * 16 * (D / 2), is_v ? &map_v : &map_k, bars + s, 0,
+      if (blk_ok) {
+        const int off = (ci.t * kTokens) & ((1 << a.log2_bs) - 1);
+        tma_load_2d(ring + s * C::kHalfBytes + lane * step * (D / 2), is_v ? &map_v : &map_k, bars + s, 0,
                     at_head * rows_per_block + ((off * (D / 2)) >> 7));
-        bulk_load(scales + (s * kTile + lane * 16) * groups,
+        bulk_load(scales + (s * kTokens + lane * step) * groups,
                   (is_v ? sa.vs : sa.ks) + (((int64_t)at_head << a.log2_bs) + off) * groups, step * groups * 4, bars + s);
       }
       if (++qi < 2 * n && is_v) {
-        advance<kRows>(a, ci);
+        advance<kRows, kTokens>(a, ci);
         load_block();
       }
     };
@@ -189,8 +211,10 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     int lim[NT][2];                            // last position each of this thread's rows sees
     int lim_min = 0, len = 0;
     bool fresh = true, seg_starts = false, more_before = false, dead = false;
-    float sc[2][NT][4];                        // the tile's scores, then exponents
+    float sc[kMTiles][NT][4];                  // the tile's scores, then exponents
     const int tg = (g >> 1) * 4 + (g & 1);     // the token of row g of a product
+    const uint32_t k_at = At<D>::k_at(tg, tid), v_at = At<D>::v_at(g, tid);
+    const int v_grp = (g * (D / 8)) >> sa.log2_group;
     int s = 0;
     uint32_t ph = 1;
 
@@ -293,11 +317,11 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
       }
       const bool ends = info.z >> 16 & 1;
       const uint8_t* codes = ring + s * C::kHalfBytes;
-      uint32_t* params = scales + s * kTile * groups;
+      uint32_t* params = scales + s * kTokens * groups;
       if (!skip && !(st & 1)) {
-        // scores S^T [32 tokens x 8 NT rows]
+        // scores S^T [64 tokens x 8 NT rows]
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < kMTiles; ++mt) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -305,18 +329,18 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           constexpr int NW = D == 64 ? 2 : 4;          // words of codes per load, of one group
 #pragma unroll
           for (int j = 0; j < D / 32 / NW; ++j) {
-            const int b = tid * (D / 8) + 16 * j, t = 16 * mt + tg, grp = (2 * b) >> sa.log2_group;
+            const int grp = (tid * (D / 4) + 32 * j) >> sa.log2_group;
             uint32_t x[NW], y[NW];
-            load_words(codes + code_at<D>(t, b), x);
-            load_words(codes + code_at<D>(t + 2, b), y);
-            const uint32_t px = params[t * groups + grp], py = params[(t + 2) * groups + grp];
+            load_words(codes + At<D>::k_at(k_at, mt, 0, j), x);
+            load_words(codes + At<D>::k_at(k_at, mt, 1, j), y);
+            const uint32_t px = params[(16 * mt + tg) * groups + grp], py = params[(16 * mt + tg + 2) * groups + grp];
             const uint32_t sx = twice_low(px), bx = twice_high(px), sy = twice_low(py), by = twice_high(py);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-              const uint32_t vx[4] = {fma_h2(pair<0>(x[w]), sx, bx), fma_h2(pair<1>(x[w]), sx, bx),
-                                      fma_h2(pair<2>(x[w]), sx, bx), fma_h2(pair<3>(x[w]), sx, bx)};
-              const uint32_t vy[4] = {fma_h2(pair<0>(y[w]), sy, by), fma_h2(pair<1>(y[w]), sy, by),
-                                      fma_h2(pair<2>(y[w]), sy, by), fma_h2(pair<3>(y[w]), sy, by)};
+              const uint32_t vx[4] = {fma_h2(masks.pair<0>(x[w]), sx, bx), fma_h2(masks.pair<1>(x[w]), sx, bx),
+                                      fma_h2(masks.pair<2>(x[w]), sx, bx), fma_h2(masks.pair<3>(x[w]), sx, bx)};
+              const uint32_t vy[4] = {fma_h2(masks.pair<0>(y[w]), sy, by), fma_h2(masks.pair<1>(y[w]), sy, by),
+                                      fma_h2(masks.pair<2>(y[w]), sy, by), fma_h2(masks.pair<3>(y[w]), sy, by)};
 #pragma unroll
               for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -331,7 +355,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           }
         }
       } else if (!skip) {
-        const int p0 = info.w * kTile;
+        const int p0 = info.w * kTokens;
         // exponents less the running maximum, plus the shift
         float lead = -INFINITY;
 #pragma unroll
@@ -339,7 +363,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           const float b0 = kShift - (mx[nt][0] == -INFINITY ? 0.f : mx[nt][0]);
           const float b1 = kShift - (mx[nt][1] == -INFINITY ? 0.f : mx[nt][1]);
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < kMTiles; ++mt) {
             sc[mt][nt][0] = fmaf(sc[mt][nt][0], fac[nt][0], b0);
             sc[mt][nt][1] = fmaf(sc[mt][nt][1], fac[nt][1], b1);
             sc[mt][nt][2] = fmaf(sc[mt][nt][2], fac[nt][0], b0);
@@ -347,21 +371,21 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           }
         }
         const int gone = info.z >> 17;
-        if (p0 + kTile - 1 > lim_min || gone) {
+        if (p0 + kTokens - 1 > lim_min || gone) {
           // tokens that some row does not see, or of a block that is not there
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < kMTiles; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (p0 + 16 * mt + tg + (e & 2) > lim[nt][e & 1] || (gone >> (paired ? mt : 0) & 1))
+                if (p0 + 16 * mt + tg + (e & 2) > lim[nt][e & 1] || (gone >> (16 * mt >> log2_step) & 1))
                   sc[mt][nt][e] = -INFINITY;
           // what the slots without a token hold must not meet the weights, 0 though they are
-          if (p0 + lane >= len || (gone >> (paired ? lane >> 4 : 0) & 1)) {
-            for (int k = 0; k < groups; ++k) params[lane * groups + k] = 0u;
-            fence_proxy_async_smem();
-          }
+          for (int t = lane; t < kTokens; t += 32)
+            if (p0 + t >= len || (gone >> (t >> log2_step) & 1))
+              for (int k = 0; k < groups; ++k) params[t * groups + k] = 0u;
+          fence_proxy_async_smem();
           __syncwarp();
         }
         bool empty = false;
@@ -369,7 +393,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         for (int nt = 0; nt < NT; ++nt) {
           empty |= mx[nt][0] == -INFINITY || mx[nt][1] == -INFINITY;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < kMTiles; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) lead = fmaxf(lead, sc[mt][nt][e]);
         }
@@ -380,7 +404,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           for (int nt = 0; nt < NT; ++nt) {
             float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int mt = 0; mt < kMTiles; ++mt) {
               m0 = fmaxf(m0, fmaxf(sc[mt][nt][0], sc[mt][nt][2]));
               m1 = fmaxf(m1, fmaxf(sc[mt][nt][1], sc[mt][nt][3]));
             }
@@ -405,45 +429,39 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
                 acc[j][nt][c + 2] *= f;
               }
 #pragma unroll
-              for (int mt = 0; mt < 2; ++mt) {
+              for (int mt = 0; mt < kMTiles; ++mt) {
                 sc[mt][nt][c] -= d;
                 sc[mt][nt][c + 2] -= d;
               }
             }
           }
         }
-        // weights and their sums; the weights transposed, as fp16
-        uint32_t pb[2][NT][2][Q2];
+        // O^T [D x 8 NT rows] += V^T w^T; lane g holds dimensions g * D/8 ...
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int mt = 0; mt < kMTiles; ++mt) {
+          // weights and their sums; the weights transposed, as fp16
+          uint32_t pb[NT][2][Q2];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int nt = 0; nt < NT; ++nt) {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2(sc[mt][nt][e]);
             sum_l[nt][0] += w[0] + w[2];
             sum_l[nt][1] += w[1] + w[3];
             const uint32_t x0 = pack_f16(w[0], w[1]), x1 = pack_f16(w[2], w[3]);
-            pb[mt][nt][0][0] = transpose8(x0);
-            pb[mt][nt][1][0] = transpose8(x1);
+            pb[nt][0][0] = transpose8(x0);
+            pb[nt][1][0] = transpose8(x1);
             if constexpr (F32) {
-              pb[mt][nt][0][1] = transpose8(rest_f16(x0, w[0], w[1]));
-              pb[mt][nt][1][1] = transpose8(rest_f16(x1, w[2], w[3]));
+              pb[nt][0][1] = transpose8(rest_f16(x0, w[0], w[1]));
+              pb[nt][1][1] = transpose8(rest_f16(x1, w[2], w[3]));
             }
           }
-        }
-
-        // O^T [D x 8 NT rows] += V^T w^T; lane g holds dimensions g * D/8 ...
-        const int grp = (g * (D / 8)) >> sa.log2_group;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
           constexpr int NW = D / 64;             // words of codes per token and lane
           uint32_t v[4][NW], pr[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int t = 16 * mt + 4 * tid + r;
-            load_words(codes + code_at<D>(t, g * (D / 16)), v[r]);
-            pr[r] = params[t * groups + grp];
+            load_words(codes + At<D>::v_at(v_at, mt, r), v[r]);
+            pr[r] = params[(16 * mt + 4 * tid + r) * groups + v_grp];
           }
           const uint32_t s01 = __byte_perm(pr[0], pr[1], 0x5410), b01 = __byte_perm(pr[0], pr[1], 0x7632);
           const uint32_t s23 = __byte_perm(pr[2], pr[3], 0x5410), b23 = __byte_perm(pr[2], pr[3], 0x7632);
@@ -452,10 +470,10 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
             // four dimensions of two tokens side by side
             const uint32_t sel = c & 1 ? 0x7632 : 0x5410;
             const uint32_t x = __byte_perm(v[0][c >> 1], v[1][c >> 1], sel), y = __byte_perm(v[2][c >> 1], v[3][c >> 1], sel);
-            const uint32_t vx[4] = {fma_h2(pair<0>(x), s01, b01), fma_h2(pair<1>(x), s01, b01),
-                                    fma_h2(pair<2>(x), s01, b01), fma_h2(pair<3>(x), s01, b01)};
-            const uint32_t vy[4] = {fma_h2(pair<0>(y), s23, b23), fma_h2(pair<1>(y), s23, b23),
-                                    fma_h2(pair<2>(y), s23, b23), fma_h2(pair<3>(y), s23, b23)};
+            const uint32_t vx[4] = {fma_h2(masks.pair<0>(x), s01, b01), fma_h2(masks.pair<1>(x), s01, b01),
+                                    fma_h2(masks.pair<2>(x), s01, b01), fma_h2(masks.pair<3>(x), s01, b01)};
+            const uint32_t vy[4] = {fma_h2(masks.pair<0>(y), s23, b23), fma_h2(masks.pair<1>(y), s23, b23),
+                                    fma_h2(masks.pair<2>(y), s23, b23), fma_h2(masks.pair<3>(y), s23, b23)};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -466,12 +484,12 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
                   // the matrix unit truncates its sums: over thousands of
                   // positions that would be a bias, so they are added here
                   float d[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816(d, a0, a1, a2, a3, pb[mt][nt][0][1], pb[mt][nt][1][1]);
-                  mma16816(d, a0, a1, a2, a3, pb[mt][nt][0][0], pb[mt][nt][1][0]);
+                  mma16816(d, a0, a1, a2, a3, pb[nt][0][1], pb[nt][1][1]);
+                  mma16816(d, a0, a1, a2, a3, pb[nt][0][0], pb[nt][1][0]);
 #pragma unroll
                   for (int e = 0; e < 4; ++e) o[e] += d[e];
                 } else {
-                  mma16816(o, a0, a1, a2, a3, pb[mt][nt][0][0], pb[mt][nt][1][0]);
+                  mma16816(o, a0, a1, a2, a3, pb[nt][0][0], pb[nt][1][0]);
                 }
               }
             }
@@ -571,7 +589,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
 template <int D, int NT, bool F32>
 lq_status launch_split(const SplitArgs& sa, const CUtensorMap& mk, const CUtensorMap& mv, int ctas, void* stream) {
   using C = Cfg<D, NT, F32>;
-  static_assert(C::halves(D / 32) >= 3 && C::smem(1) + 2048 <= 227 * 1024 && C::smem(D / 32) + 2048 <= 227 * 1024,
+  static_assert(C::halves(D / 32) >= 2 && C::smem(1) + 2048 <= 227 * 1024 && C::smem(D / 32) + 2048 <= 227 * 1024,
                 "shared memory");
   static_assert(C::halves(D / 32) * C::kHalfBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
   static_assert(C::kWarps * C::halves(D / 32) * C::kHalfBytes >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
@@ -672,7 +690,7 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
   const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;
   const int64_t bytes = num_blocks > 0 ? num_blocks * block_rows * 128 : 32768;
   CUtensorMap mk, mv;
-  const int box = (block_size < attn::kTile ? block_size : attn::kTile) * head_dim / 256;
+  const int box = (block_size < q4::kTokens ? block_size : q4::kTokens) * head_dim / 256;
   if (!attn::encode_cache(&mk, kc, bytes, box) || !attn::encode_cache(&mv, vc, bytes, box)) return LQ_ERR_CUDA;
   // eight query rows per pass over the codes, sixteen where the average request has more
   const bool few = ((total_q + batch - 1) / batch) * a.group <= 8;

@@ -1,6 +1,6 @@
 // Shared by the split kernels of the paged attention, which spread a batch's
 // work over all SMs in equal parts whatever its requests' lengths are (lq_attn_paged.cu
-// for the 8-bit cache, lq_attn_q4.cu for the 4-bit one): the list of 32-token tiles
+// for the 8-bit cache, lq_attn_q4.cu for the 4-bit one): the list of tiles
 // (request, tile of rows, kv head, tokens) and its division, a row's place, the joining
 // of pieces of rows in a CTA and between CTAs.  Internal to the library.
 #pragma once
@@ -10,7 +10,7 @@
 namespace lq {
 namespace attn {
 
-constexpr int kTile = 32;                      // tokens per tile
+constexpr int kTile = 32;                      // tokens per tile, where a kernel does not say otherwise
 
 // Floats of a piece: output rows, maxima, sums, their units.
 __host__ __device__ constexpr int piece_floats(int rows, int head_dim) { return rows * (head_dim + 3); }
@@ -24,15 +24,15 @@ struct Cursor {
   int len;
 };
 
-template <int ROWS>
+template <int ROWS, int TILE = kTile>
 __device__ __forceinline__ void enter(const Args& a, Cursor& c) {
   const Request r = load_request(a, c.i);
   c.len = r.len;
   c.nrt = (r.q_len * a.group + ROWS - 1) / ROWS;
-  c.nt = r.len > 0 ? (r.len + kTile - 1) / kTile : 1;
+  c.nt = r.len > 0 ? (r.len + TILE - 1) / TILE : 1;
 }
 
-template <int ROWS>
+template <int ROWS, int TILE = kTile>
 __device__ __forceinline__ void advance(const Args& a, Cursor& c) {
   if (++c.t < c.nt) return;
   c.t = 0;
@@ -43,7 +43,7 @@ __device__ __forceinline__ void advance(const Args& a, Cursor& c) {
   c.nrt = 0;
 #pragma unroll 1
   while (++c.i < a.batch) {
-    enter<ROWS>(a, c);
+    enter<ROWS, TILE>(a, c);
     if (c.nrt > 0) break;
   }
 }
@@ -100,7 +100,7 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f 
 // of the requests' tiles give the list's length; the CTAs, and in them the warps,
 // take equal parts (u0 and part_n).  pre: shared room for LQ_MAX_REQUESTS numbers,
 // wsum: for one per warp.  All threads come here together.
-template <int ROWS, int WARPS>
+template <int ROWS, int WARPS, int TILE = kTile>
 __device__ __forceinline__ int part_of_warp(const Args& a, long long* pre, long long* wsum, Cursor& ci) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto tiles_of = [&](int i) {
@@ -108,7 +108,7 @@ __device__ __forceinline__ int part_of_warp(const Args& a, long long* pre, long 
       raise_flag(a.status, LQ_DEV_RANGE);
     Cursor c;
     c.i = i;
-    enter<ROWS>(a, c);
+    enter<ROWS, TILE>(a, c);
     return (long long)c.nrt * a.kv_heads * c.nt;
   };
   auto scan = [&](long long x) {               // inclusive, over the warp
@@ -183,7 +183,7 @@ __device__ __forceinline__ int part_of_warp(const Args& a, long long* pre, long 
   }
   const int n = (int)(part_n < (1 << 29) ? part_n : (1 << 29));
   if (n > 0) {
-    enter<ROWS>(a, ci);
+    enter<ROWS, TILE>(a, ci);
     const long long rem = u0 - before;
     const long long hr = rem < INT_MAX ? (unsigned)rem / (unsigned)ci.nt : rem / ci.nt;    // row tile and head
     ci.t = (int)(rem - hr * ci.nt);

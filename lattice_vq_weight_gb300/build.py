@@ -22,7 +22,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ("lq_api.cu", "lq_quantize.cu", "lq_quantize_fmt.cu", "lq_quantize_dither.cu", "lq_gemv.cu", "lq_gemm.cu",
            "lq_rice.cu", "lq_calib.cu", "lq_kv.cu", "lq_kv_dither.cu", "lq_kv_rice.cu", "lq_kv_plan.cu", "lq_rope.cu",
            "lq_kv_paged.cu", "lq_attn_paged.cu",
-           "lq_attn_paged_tiles.cu", "lq_verify.cu", "lq_kv_q4.cu", "lq_attn_q4.cu", "lq_logprobs.cu")
+           "lq_attn_paged_tiles.cu", "lq_verify.cu", "lq_kv_q4.cu", "lq_attn_q4.cu", "lq_attn_q4_tiles.cu",
+           "lq_logprobs.cu")
 # Objects: one per source, except lq_kv_rice.cu, compiled once per (lattice,
 # norm format) pair so that its slow instantiations build in parallel.
 UNITS = tuple((s, s.replace(".cu", ".o"), ()) for s in SOURCES if s != "lq_kv_rice.cu") + tuple(

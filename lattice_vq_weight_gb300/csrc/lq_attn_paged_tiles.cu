@@ -43,13 +43,10 @@
 // Every wait is bounded (about a second of clock cycles); on expiry
 // LQ_DEV_TIMEOUT is recorded and the CTA winds down.
 #include "lq_attn_paged.cuh"
+#include "lq_attn_tiles.cuh"
 
 namespace lq {
 namespace attn {
-
-constexpr int kTileRows = 128;
-constexpr uint32_t kTopWeight = (15u + 15u) << 10;        // 2^(kShift + kLead) as fp16
-static_assert(kShift + kLead == 15.f, "the largest weight");
 
 // Which weights may go into a row's sum as weight / value scale: those of blocks
 // whose value scale is at least a floor.  With lv its log2 and lv >= mx - un - 60,
@@ -77,11 +74,10 @@ struct Floor {
 };
 
 template <int D>
-struct TileCfg {
-  static constexpr int T = D == 256 ? 1 : 2;                // row tiles per CTA
-  static constexpr int kRows = T * kTileRows;
-  static constexpr int BN = D == 256 ? 64 : 128;            // tokens per tile
-  static constexpr int kSub = D / 64;                       // 64-dimension sub-tiles
+struct TileCfg : TileShape<D> {
+  using TileShape<D>::T;
+  using TileShape<D>::BN;
+  using TileShape<D>::kSub;
   static constexpr int kQBytes = kTileRows * D * 2;         // of a row tile
   static constexpr int kCodeBytes = BN * D * 2;             // a K or V tile as fp16
   static constexpr int kRawBytes = BN * D;                  // a K or V tile's codes
@@ -108,107 +104,6 @@ struct TileArgs {
   int splits;                    // CTAs per pair of row tiles and kv head
 };
 
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-  // 128-byte swizzle, 8-row atoms of 1024 bytes one after the other
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t sub_stride) {
-  // the same atoms read along their rows: 64 columns per atom, the next 64
-  // sub_stride bytes further, the next 8 tokens 1024 bytes further
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((sub_stride >> 4) & 0x3FFFu) << 16 |
-         (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// Instruction descriptor: D f32, M = 128; A and B bf16 or f16; B along its rows when mn.
-template <int N, bool BF16, bool MN>
-struct Idesc {
-  static constexpr uint32_t v = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) |
-                                ((MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-                                ((uint32_t)(kTileRows >> 4) << 24);
-};
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               ::"r"(smem_addr(bar)) : "memory");
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
-}
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr) : "memory");
-}
-// The same without waiting, and the wait for all loads issued.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31]));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-// Bounded wait; false when the limit expired or another thread recorded that.
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* timeout) {
-  if (mbar_test(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_test(bar, parity)) {
-    if (*timeout) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *timeout = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
 // Two codes, placed by `sel`, as bf16 numbers.  0x4300 + (the low seven bits) is
 // 128 + those, and 0x4300 or 0x4380 is 128 or 256, as the sign bit is clear or
 // set: their difference is the code, exactly.
@@ -217,10 +112,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t codes, uint32_t sel) {
   const __nv_bfloat162 v =
       __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
 }
 
 // A row's weights of one tile from its scores: packed fp16 weights, the sum of
@@ -854,49 +745,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) attn_tiles_kernel(con
   if (threadIdx.x == 0 && timeout_flag) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 
-// Joins the pieces of rows whose positions were split: a warp per row, D / 32
-// neighbouring dimensions per lane.
-template <int D>
-__global__ void __launch_bounds__(256) attn_tiles_merge_kernel(const __grid_constant__ TileArgs ta) {
-  using C = TileCfg<D>;
-  constexpr int E = D / 32;
-  const Args& a = ta.a;
-  pdl_wait();
-  pdl_launch();
-  const int unit = blockIdx.x / (C::kRows / 8), row = (blockIdx.x % (C::kRows / 8)) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const Tag tag = a.meta[unit];
-  const int R = tag.rt * C::kRows + row, j = R / a.group;
-  if (!tag.valid || j >= tag.q_len) return;
-  const float* piece = a.part + ((int64_t)unit * ta.splits * C::kRows + row) * (D + 4);
-  constexpr int64_t next = (int64_t)C::kRows * (D + 4);
-  float M = -INFINITY, U = -INFINITY;
-  for (int p = 0; p < ta.splits; ++p) {
-    M = fmaxf(M, piece[p * next + D]);
-    U = fmaxf(U, piece[p * next + D + 2]);
-  }
-  float o[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < ta.splits; ++p) {
-    const float f = pow2(piece[p * next + D] - M);
-    l = fmaf(piece[p * next + D + 1], pow2(piece[p * next + D + 2] - U), l);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(piece + p * next + E * lane + e);
-      o[e] = fmaf(v.x, f, o[e]);
-      o[e + 1] = fmaf(v.y, f, o[e + 1]);
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l, back = unit_of(M, U);
-  const int64_t dst = (int64_t)(tag.q0 + j) * a.ldo + (int64_t)(tag.h * a.group + R - j * a.group) * D + E * lane;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + dst + e) =
-        __floats2bfloat162_rn(o[e] * inv * back, o[e + 1] * inv * back);
-}
-
 template <int D>
 lq_status launch_tiles(const TileArgs& ta, const TilePlan& plan, void* stream) {
   using C = TileCfg<D>;
@@ -910,7 +758,8 @@ lq_status launch_tiles(const TileArgs& ta, const TilePlan& plan, void* stream) {
   const lq_status st =
       serve::launch(kern, (unsigned)(plan.units * plan.splits), C::kThreads, C::kSmem, stream, ta);
   if (st != LQ_OK || plan.splits == 1) return st;
-  return serve::launch(attn_tiles_merge_kernel<D>, (unsigned)(plan.units * (C::kRows / 8)), 256, 0, stream, ta);
+  return serve::launch(attn_tiles_merge_kernel<D>, (unsigned)(plan.units * (C::kRows / 8)), 256, 0, stream,
+                       TileMergeArgs{ta.a, ta.splits});
 }
 
 TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms) {

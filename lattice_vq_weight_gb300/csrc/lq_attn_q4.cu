@@ -26,8 +26,8 @@
 // operand's order, 4 tid .. 4 tid + 3 in the tile's) and the lanes' reads of V
 // spread over the banks.
 #include "lq_attn_paged.cuh"
+#include "lq_attn_q4.cuh"
 #include "lq_attn_split.cuh"
-#include "lq_q4.cuh"
 
 namespace lq {
 namespace q4 {
@@ -38,10 +38,7 @@ constexpr int kTokens = 64;                    // tokens per tile
 constexpr int kMTiles = kTokens / 16;
 
 struct SplitArgs {
-  Args a;
-  const uint32_t* ks;        // (scale, base) pairs
-  const uint32_t* vs;
-  int log2_group;
+  CacheArgs ca;
   int halves;                // of a warp's ring
 };
 
@@ -65,11 +62,6 @@ struct Cfg {
   }
   static constexpr int smem(int groups) { return kWarps * halves(groups) * per_half(groups) + kRowBytes + 1024; }
 };
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
-}
 
 // Codes of a half lie in lines of 128 bytes whose 16-byte chunks are swizzled by the
 // line's number.  A lane reads at one offset (k_at, v_at) and others that differ from
@@ -113,7 +105,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, F32>::kThreads, 1)
 split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
              const __grid_constant__ SplitArgs sa) {
   using C = Cfg<D, NT, F32>;
-  const Args& a = sa.a;
+  const Args& a = sa.ca.a;
   constexpr int kWarps = C::kWarps, kRows = C::kRows;
   constexpr int KS = D / 16;                   // k steps of the scores, m tiles of the output
   constexpr int Q2 = F32 ? 2 : 1;              // fp16 terms of a query or weight
@@ -121,7 +113,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
   // (an offset, not a cast to and from a number, lets the compiler see shared memory)
   uint8_t* smem = q4_smem_raw + ((0u - smem_addr(q4_smem_raw)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tid = lane & 3;
-  const int S = sa.halves, groups = D >> sa.log2_group;
+  const int S = sa.halves, groups = D >> sa.ca.log2_group;
   const Masks masks;
   uint8_t* ring = smem + warp * S * C::kHalfBytes;
   uint8_t* after = smem + kWarps * S * C::kHalfBytes;
@@ -195,7 +187,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
         tma_load_2d(ring + s * C::kHalfBytes + lane * step * (D / 2), is_v ? &map_v : &map_k, bars + s, 0,
                     at_head * rows_per_block + ((off * (D / 2)) >> 7));
         bulk_load(scales + (s * kTokens + lane * step) * groups,
-                  (is_v ? sa.vs : sa.ks) + (((int64_t)at_head << a.log2_bs) + off) * groups, step * groups * 4, bars + s);
+                  (is_v ? sa.ca.vs : sa.ca.ks) + (((int64_t)at_head << a.log2_bs) + off) * groups, step * groups * 4, bars + s);
       }
       if (++qi < 2 * n && is_v) {
         advance<kRows, kTokens>(a, ci);
@@ -214,7 +206,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
     float sc[kMTiles][NT][4];                  // the tile's scores, then exponents
     const int tg = (g >> 1) * 4 + (g & 1);     // the token of row g of a product
     const uint32_t k_at = At<D>::k_at(tg, tid), v_at = At<D>::v_at(g, tid);
-    const int v_grp = (g * (D / 8)) >> sa.log2_group;
+    const int v_grp = (g * (D / 8)) >> sa.ca.log2_group;
     int s = 0;
     uint32_t ph = 1;
 
@@ -329,7 +321,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           constexpr int NW = D == 64 ? 2 : 4;          // words of codes per load, of one group
 #pragma unroll
           for (int j = 0; j < D / 32 / NW; ++j) {
-            const int grp = (tid * (D / 4) + 32 * j) >> sa.log2_group;
+            const int grp = (tid * (D / 4) + 32 * j) >> sa.ca.log2_group;
             uint32_t x[NW], y[NW];
             load_words(codes + At<D>::k_at(k_at, mt, 0, j), x);
             load_words(codes + At<D>::k_at(k_at, mt, 1, j), y);
@@ -587,7 +579,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
 }
 
 template <int D, int NT, bool F32>
-lq_status launch_split(const SplitArgs& sa, const CUtensorMap& mk, const CUtensorMap& mv, int ctas, void* stream) {
+lq_status launch_split(const CacheArgs& ca, const CUtensorMap& mk, const CUtensorMap& mv, int ctas, void* stream) {
   using C = Cfg<D, NT, F32>;
   static_assert(C::halves(D / 32) >= 2 && C::smem(1) + 2048 <= 227 * 1024 && C::smem(D / 32) + 2048 <= 227 * 1024,
                 "shared memory");
@@ -595,13 +587,12 @@ lq_status launch_split(const SplitArgs& sa, const CUtensorMap& mk, const CUtenso
   static_assert(C::kWarps * C::halves(D / 32) * C::kHalfBytes >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
   static_assert((2 + C::kWarps) * C::kPiece <= work_floats(D), "the pieces fit the workspace");
   auto kern = split_kernel<D, NT, F32>;
-  const int groups = D >> sa.log2_group, smem = C::smem(groups);
+  const int groups = D >> ca.log2_group, smem = C::smem(groups);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
     return LQ_ERR_CUDA;
   }
-  SplitArgs args = sa;
-  args.halves = C::halves(groups);
+  const SplitArgs args{ca, C::halves(groups)};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -616,13 +607,19 @@ lq_status launch_split(const SplitArgs& sa, const CUtensorMap& mk, const CUtenso
   if (e == cudaSuccess) {
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, attn_merge_kernel<D, NT, F32>, sa.a, ctas);
+    e = cudaLaunchKernelEx(&cfg, attn_merge_kernel<D, NT, F32>, ca.a, ctas);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return LQ_ERR_CUDA;
   }
   return check_launch();
+}
+
+// Whether the tensor-core kernel takes a bf16 call: by the query rows that an
+// average request has for each kv head.
+bool many_rows(int batch, int64_t total_q, int group, int head_dim) {
+  return (total_q + batch - 1) / batch * group > (head_dim == 256 ? 48 : 16);
 }
 
 }  // namespace q4
@@ -673,8 +670,8 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
     return LQ_ERR_SHAPE;
   const int sms = device_sm_count();
   if (sms <= 0) return LQ_ERR_CUDA;
-  q4::SplitArgs sa;
-  attn::Args& a = sa.a;
+  q4::CacheArgs ca;
+  attn::Args& a = ca.a;
   a = attn::Args{};
   a.q = q_dev; a.ldq = ldq; a.total_q = total_q; a.cu_q = cu_q_dev; a.kv_lens = kv_lens_dev; a.batch = batch;
   a.table = block_table_dev; a.ldt = table_stride; a.width = table_width; a.num_blocks = num_blocks;
@@ -683,8 +680,14 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
   a.meta = reinterpret_cast<attn::Tag*>(workspace_dev);
   const int ctas = attn::cta_count();
   a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + attn::meta_bytes(ctas));
-  sa.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); sa.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
-  sa.log2_group = serve::log2_of(group_size);
+  ca.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); ca.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
+  ca.log2_group = serve::log2_of(group_size);
+  ca.kc = k_cache_dev; ca.vc = v_cache_dev;
+  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, head_dim))
+    return q4::launch_tiles(ca, head_dim,
+                            attn::plan_tiles(batch, total_q, a.group, kv_heads, head_dim,
+                                             (int64_t)table_width * block_size, ctas),
+                            stream);
   // a pool without blocks: no copy is issued, any valid map will do
   const void* kc = num_blocks > 0 ? (const void*)k_cache_dev : workspace_dev;
   const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;
@@ -695,13 +698,13 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
   // eight query rows per pass over the codes, sixteen where the average request has more
   const bool few = ((total_q + batch - 1) / batch) * a.group <= 8;
   if (dtype == LQ_F32) {
-    if (head_dim == 64) return q4::launch_split<64, 1, true>(sa, mk, mv, ctas, stream);
-    if (head_dim == 128) return q4::launch_split<128, 1, true>(sa, mk, mv, ctas, stream);
-    return q4::launch_split<256, 1, true>(sa, mk, mv, ctas, stream);
+    if (head_dim == 64) return q4::launch_split<64, 1, true>(ca, mk, mv, ctas, stream);
+    if (head_dim == 128) return q4::launch_split<128, 1, true>(ca, mk, mv, ctas, stream);
+    return q4::launch_split<256, 1, true>(ca, mk, mv, ctas, stream);
   }
-  if (head_dim == 256) return q4::launch_split<256, 1, false>(sa, mk, mv, ctas, stream);
-  if (head_dim == 64) return few ? q4::launch_split<64, 1, false>(sa, mk, mv, ctas, stream)
-                                 : q4::launch_split<64, 2, false>(sa, mk, mv, ctas, stream);
-  return few ? q4::launch_split<128, 1, false>(sa, mk, mv, ctas, stream)
-             : q4::launch_split<128, 2, false>(sa, mk, mv, ctas, stream);
+  if (head_dim == 256) return q4::launch_split<256, 1, false>(ca, mk, mv, ctas, stream);
+  if (head_dim == 64) return few ? q4::launch_split<64, 1, false>(ca, mk, mv, ctas, stream)
+                                 : q4::launch_split<64, 2, false>(ca, mk, mv, ctas, stream);
+  return few ? q4::launch_split<128, 1, false>(ca, mk, mv, ctas, stream)
+             : q4::launch_split<128, 2, false>(ca, mk, mv, ctas, stream);
 }

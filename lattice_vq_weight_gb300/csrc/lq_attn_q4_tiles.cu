@@ -1,0 +1,681 @@
+// Paged attention over the 4-bit cache for many query rows per kv head (prompts and
+// chunks of them), on the 5th-generation tensor cores.
+//
+// The formulas are those of lq_attn_q4.cu.  With hundreds of rows per code the
+// matrix products bound the work (4 head_dim flops per row and position), so here
+// a CTA takes 256 query rows of one kv head as two row tiles (one for head_dim 256)
+// and walks the positions they see in tiles of 128 (64):
+//     S = Q K^T       tcgen05.mma in fp16, both operands in shared memory, S in TMEM
+//     W = 2^(x - max) by one thread per row, from TMEM and back: the fp16
+//                     weights take the columns of the scores
+//     O += W V        tcgen05.mma in fp16 with W from TMEM, O in TMEM
+// One warp fetches codes, scales and bases by untiled bulk copies, up to two half
+// tiles (K, V) ahead; warps 0..3 turn them into fp16 values in two stages of shared
+// memory; four warps per row tile hold its rows' maxima and sums, and one issues its
+// products.  The values are what the cache stands for, exactly, so the softmax knows
+// nothing of scales: a weight is one fma and one exponential.  A word of eight codes
+// becomes pairs (0, 4), (1, 5), (2, 6), (3, 7) of dimensions, and is left in that order:
+// queries are brought into it when they are read, outputs out of it when they are
+// written.  bf16 queries are exact in fp16 after a power of two per row.
+//
+// The two row tiles run half a period apart, so that one's products run under the
+// other's exponentials, and share every tile of values.  Scores are overwritten only
+// after the products that read the weights there have completed.  The running maximum
+// may lag by 2^7, so that a row's weights are made in one pass and O is rescaled only
+// when the maximum really moves.  bf16 only: the tensor core's accumulator truncates,
+// 6e-5 of the output after 30000 positions (measured), which fp32 outputs would show.
+// Few row tiles would leave SMs idle: then several CTAs share one, a range of the
+// positions each, and a second kernel joins their outputs in the order of the positions.
+//
+// Every wait is bounded (about a second of clock cycles); on expiry
+// LQ_DEV_TIMEOUT is recorded and the CTA winds down.
+#include "lq_attn_paged.cuh"
+#include "lq_attn_q4.cuh"
+#include "lq_attn_tiles.cuh"
+
+namespace lq {
+namespace q4 {
+
+using namespace attn;
+
+template <int D>
+struct TileCfg : TileShape<D> {
+  using TileShape<D>::T;
+  using TileShape<D>::BN;
+  using TileShape<D>::kSub;
+  static constexpr int kQBytes = kTileRows * D * 2;         // of a row tile
+  static constexpr int kValueBytes = BN * D * 2;            // a K or V tile as fp16
+  static constexpr int kRawBytes = BN * D / 2;              // a K or V tile's codes
+  static constexpr int kParamBytes = BN * (D / 32) * 4;     // and its scales and bases, at most
+  static constexpr int kSmem = T * kQBytes + 4 * kValueBytes + 2 * kRawBytes + 2 * kParamBytes + 1024;
+  static constexpr uint32_t kCols = 512;
+  static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
+  static constexpr int kMmaWarp = 4 + 4 * T;                // and the next, one per row tile
+  static constexpr int kFetchWarp = kMmaWarp + T;
+  static constexpr int kThreads = 32 * (8 + 4 * T);         // whole groups of four warps
+  // Registers per thread: the launch gives every warp 65536 / 512 = 128 (T = 2)
+  // and the groups then divide those up, 80 + 2 x 184 + 64 = 4 x 128.
+  static constexpr bool kSplitRegs = T == 2;
+  static constexpr int kConvertRegs = 80, kSoftmaxRegs = 184, kIssueRegs = 64;
+  static_assert(!kSplitRegs || kConvertRegs + 2 * kSoftmaxRegs + kIssueRegs <= 4 * 128, "the launch's registers");
+  // tokens that the 128 converting threads take in one pass (16 codes each), and
+  // passes per tile
+  static constexpr int kPassRows = 2048 / D;
+  static constexpr int kPasses = BN / kPassRows;
+};
+
+struct TileArgs {
+  CacheArgs ca;
+  int splits;                    // CTAs per pair of row tiles and kv head
+};
+
+// A row's weights of one tile from its scores: packed fp16 weights and their sum;
+// returns the largest weight's bits, or more (positive fp16 numbers are in the order of
+// their bits, with infinity and NaN above, and take three-way integer maxima two at a
+// time).  The exponent of a token is score * fac + base.
+template <int BN>
+__device__ __forceinline__ uint32_t row_weights(uint32_t tmem, float fac, float base, uint32_t (&w)[BN / 2], float& l) {
+  uint32_t top = 0;
+  uint32_t s[2][32];
+  const float2 k2 = make_float2(fac, fac), d2 = make_float2(base, base);
+  float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+  tmem_ld32_async(tmem, s[0]);
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t (&x32)[32] = s[c & 1];
+    tmem_wait_ld(x32);
+    if (c + 1 < BN / 32) tmem_ld32_async(tmem + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float2 x = fma2(make_float2(__uint_as_float(x32[2 * e]), __uint_as_float(x32[2 * e + 1])), k2, d2);
+      x = make_float2(ex2(x.x), ex2(x.y));
+      if (e & 1) sum1 = add2(sum1, x);
+      else sum0 = add2(sum0, x);
+      w[16 * c + e] = pack_f16(x.x, x.y);
+      if (e & 1) top = __vimax3_u16x2(top, w[16 * c + e - 1], w[16 * c + e]);
+    }
+  }
+  sum0 = add2(sum0, sum1);
+  l += sum0.x + sum0.y;
+  return max(top >> 16, top & 0xFFFFu);
+}
+
+// The tiles that the above does not serve, few of a unit: tokens that a row does
+// not see (beyond vis0, or in a block that is gone), rows whose maximum moves.  Two
+// short loops, the largest exponent and then the weights: code that runs so seldom
+// comes from far away.
+template <int BN>
+__device__ __forceinline__ float row_top(uint32_t tmem, float fac, uint32_t gone, int vis0) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x32[32];
+    tmem_ld32(tmem + 32 * c, x32);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int g = 2 * c + half, vis = (gone >> g & 1) ? -1 : vis0 - 16 * g;      // tokens 0 .. vis are seen
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, e > vis ? -INFINITY : __uint_as_float(x32[16 * half + e]) * fac);
+    }
+  }
+  return top;
+}
+template <int BN>
+__device__ __forceinline__ void store_weights(uint32_t tmem, float fac, float base, uint32_t gone, int vis0, float& l) {
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x32[32], w[16];
+    tmem_ld32(tmem + 32 * c, x32);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int g = 2 * c + half, vis = (gone >> g & 1) ? -1 : vis0 - 16 * g;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x0 = ex2(2 * e > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + 2 * e]), fac, base));
+        const float x1 = ex2(2 * e + 1 > vis ? -INFINITY : fmaf(__uint_as_float(x32[16 * half + 2 * e + 1]), fac, base));
+        sum0 += x0;
+        sum1 += x1;
+        w[8 * half + e] = pack_f16(x0, x1);
+      }
+      l += sum0 + sum1;
+    }
+    tmem_st16(tmem + 16 * c, w);                            // over scores read before
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __grid_constant__ TileArgs ta) {
+  using C = TileCfg<D>;
+  constexpr int BN = C::BN, T = C::T;
+  const Args& a = ta.ca.a;
+  extern __shared__ uint8_t q4_tiles_smem_raw[];
+  uint8_t* smem = q4_tiles_smem_raw + ((0u - smem_addr(q4_tiles_smem_raw)) & 1023u);
+  uint8_t* sq = smem;                                       // the query rows
+  uint8_t* sk = sq + T * C::kQBytes;                        // two stages each
+  uint8_t* sv = sk + 2 * C::kValueBytes;
+  uint8_t* raw = sv + 2 * C::kValueBytes;                   // codes as fetched, K and V
+  uint8_t* params = raw + 2 * C::kRawBytes;                 // (scale, base) pairs, K and V
+  __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
+  __shared__ uint64_t raw_full[2], raw_free[2];             // K, V
+  __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], turn[T][2], drain;
+  __shared__ uint32_t tmem_base;
+  __shared__ int timeout_flag, found[2];
+  __shared__ int wsum[C::kThreads / 32];
+  volatile int* timeout = &timeout_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = D >> ta.ca.log2_group;
+
+  pdl_wait();
+  pdl_launch();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init1(&raw_full[i], 1);
+      mbar_init1(&raw_free[i], 4);                          // one arrival per converting warp
+      mbar_init1(&k_full[i], 4);
+      mbar_init1(&v_full[i], 4);
+      mbar_init1(&k_free[i], T);                            // the row tiles' products that read the stage are done
+      mbar_init1(&v_free[i], T);
+    }
+    for (int t = 0; t < T; ++t) {
+      mbar_init1(&s_full[t], 1);                            // scores computed
+      mbar_init1(&p_full[t], 4);                            // one arrival per softmax warp
+      mbar_init1(&o_done[t], 1);                            // values added: O readable, the weights read
+      mbar_init1(&q_full[t], 4);
+      mbar_init1(&turn[t][0], 1);                           // scores issued
+      mbar_init1(&turn[t][1], 1);
+    }
+    mbar_init1(&drain, T);
+    mbar_init_fence();
+    timeout_flag = 0;
+    found[0] = -1;
+  }
+
+  // rows that no request owns
+  {
+    const int64_t end = max(a.cu_q[a.batch], 0), cols = (int64_t)a.q_heads * D;
+    for (int64_t t = end + blockIdx.x; t < a.total_q; t += gridDim.x)
+      for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) {
+        reinterpret_cast<uint16_t*>(a.out)[t * a.ldo + c] = 0;
+      }
+  }
+
+  // this CTA's request and row tile, the last rows first: they see the most
+  const int split = blockIdx.x % ta.splits, unit = blockIdx.x / ta.splits;
+  const int h = unit % a.kv_heads, item = unit / a.kv_heads;
+  {
+    const int per = (a.batch + C::kThreads - 1) / C::kThreads;
+    const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
+    auto tiles_of = [&](int i) {
+      const Request r = load_request(a, i);
+      return (r.q_len * a.group + C::kRows - 1) / C::kRows;
+    };
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) {
+      if (blockIdx.x == 0 && (int64_t)a.kv_lens[i] > ((int64_t)a.width << a.log2_bs))
+        raise_flag(a.status, LQ_DEV_RANGE);
+      sum += tiles_of(i);
+    }
+    int inc = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) inc += wsum[w];
+    int begin = inc - sum;
+    if (item >= begin && item < inc) {
+      for (int i = i0; i < i1; ++i) {
+        const int n = tiles_of(i);
+        if (item < begin + n) {
+          found[0] = i;
+          found[1] = begin + n - 1 - item;
+          break;
+        }
+        begin += n;
+      }
+    }
+    __syncthreads();
+  }
+  if (found[0] < 0) {                                       // fewer row tiles than CTAs
+    if (ta.splits > 1 && split == 0 && threadIdx.x == 0) a.meta[unit].valid = 0;
+    return;
+  }
+  const int req = found[0], row0 = found[1] * C::kRows;
+  const Request r = load_request(a, req);
+  const int rows = r.q_len * a.group;
+  // tiles of the tokens that a row tile's last row sees; none if it has no rows
+  auto tiles_seen = [&](int t) {
+    if (row0 + t * kTileRows >= rows) return 0;
+    const int last = min(row0 + (t + 1) * kTileRows, rows) - 1;
+    const int seen = min(r.len, r.shown + last / a.group + 1);
+    return seen > 0 ? (seen + BN - 1) / BN : 0;
+  };
+  const int all0 = tiles_seen(0), all1 = T > 1 ? tiles_seen(1) : 0, all = max(all0, all1);
+  // this CTA's tiles: `first` and the ones after it
+  const int first = (int)((int64_t)all * split / ta.splits), past = (int)((int64_t)all * (split + 1) / ta.splits);
+  const int n0 = max(0, min(all0, past) - first), n1 = max(0, min(all1, past) - first), tiles = max(n0, n1);
+  const int seen = min(r.len, past * BN);                   // tokens fetched end here
+  if (ta.splits > 1 && split == 0 && threadIdx.x == 0) {
+    Tag tag = {};
+    tag.i = req; tag.h = h; tag.rt = found[1]; tag.q0 = r.q0; tag.q_len = r.q_len; tag.valid = 1;
+    a.meta[unit] = tag;
+  }
+  const int32_t* table = a.table + (int64_t)req * a.ldt;
+
+  if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_addr(&tmem_base)), "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  // columns: the row tiles' scores, then their outputs
+  const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + T * BN;
+
+  if (warp < 4) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kConvertRegs));
+    // ------------------------------------------------------------ codes to fp16
+    // 16 codes per thread and pass.  The eight lanes of a shared-memory phase write
+    // chunks 2 q (+ 1) of two neighbouring tokens' lines, whose swizzles keep them off
+    // each other's banks; what they read is contiguous.
+    const Masks masks;
+    const int t = threadIdx.x, q = t & 3, sub = (t >> 3) & (C::kSub - 1);
+    const int r0 = (t >> 2 & 1) + 2 * (t / (8 * C::kSub));
+    const int grp = (64 * sub + 16 * q) >> ta.ca.log2_group;
+    const uint32_t to0 = sub * BN * 128 + r0 * 128 + (((2 * q) ^ (r0 & 7)) << 4), to1 = to0 ^ 16;
+    // lim: the tile's tokens that are there; others are zeros, whatever their slots hold
+    auto convert = [&](int v, uint8_t* dst, int lim, uint64_t* full) {
+      const uint8_t* src = raw + v * C::kRawBytes + r0 * (D / 2) + sub * 32 + q * 8;
+      const uint32_t* par = reinterpret_cast<const uint32_t*>(params + v * C::kParamBytes) + r0 * groups + grp;
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src + p * C::kPassRows * (D / 2));
+        uint32_t pr = par[p * C::kPassRows * groups];
+        if (p * C::kPassRows + r0 >= lim) pr = 0u;
+        const uint32_t s = twice_low(pr), b = twice_high(pr);
+        uint8_t* line = dst + p * C::kPassRows * 128;
+        *reinterpret_cast<uint4*>(line + to0) =
+            make_uint4(fma_h2(masks.pair<0>(x.x), s, b), fma_h2(masks.pair<1>(x.x), s, b),
+                       fma_h2(masks.pair<2>(x.x), s, b), fma_h2(masks.pair<3>(x.x), s, b));
+        *reinterpret_cast<uint4*>(line + to1) =
+            make_uint4(fma_h2(masks.pair<0>(x.y), s, b), fma_h2(masks.pair<1>(x.y), s, b),
+                       fma_h2(masks.pair<2>(x.y), s, b), fma_h2(masks.pair<3>(x.y), s, b));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        arrive(&raw_free[v]);
+        arrive(full);
+      }
+    };
+    for (int j = 0; j < tiles; ++j) {
+      const int st = j & 1, lim = seen - (first + j) * BN;
+      const uint32_t before = (uint32_t)(j / 2 + 1) & 1;    // the stage's previous use
+      bool ok = wait_on(&raw_full[0], (uint32_t)j & 1, timeout);
+      if (j >= 2) ok = ok && wait_on(&k_free[st], before, timeout);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      convert(0, sk + st * C::kValueBytes, lim, &k_full[st]);
+      ok = wait_on(&raw_full[1], (uint32_t)j & 1, timeout);
+      if (j >= 2) ok = ok && wait_on(&v_free[st], before, timeout);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      convert(1, sv + st * C::kValueBytes, lim, &v_full[st]);
+    }
+  } else if (warp >= C::kMmaWarp) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+    if (warp == C::kFetchWarp) {
+      // ------------------------------------------------------------ codes from the cache
+      // lane g: the g-th part of the tile, a block or BN tokens of one
+      const int step = min(1 << a.log2_bs, BN), parts = BN / step;
+      auto look_up = [&](int j) {
+        const int pos = (first + j) * BN + step * lane;
+        return lane < parts && pos < seen ? table[pos >> a.log2_bs] : -1;
+      };
+      int blk = look_up(0), issued = 0;
+      for (int j = 0; j < tiles; ++j) {
+        const int pos = (first + j) * BN + step * lane;
+        const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
+        const bool lost = !ok && lane < parts && pos < seen;
+        if (lost) raise_flag(a.status, LQ_DEV_RANGE);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * step * (D / 2 + 4 * groups);
+        const int64_t row = (((int64_t)blk * a.kv_heads + h) << a.log2_bs) + (pos & ((1 << a.log2_bs) - 1));
+        blk = look_up(j + 1);
+        bool go = true;
+        for (int v = 0; v < 2 && go; ++v) {
+          if (j > 0) go = __all_sync(0xffffffffu, wait_on(&raw_free[v], (uint32_t)(j - 1) & 1, timeout));
+          if (!go) break;
+          uint8_t* codes = raw + v * C::kRawBytes + lane * step * (D / 2);
+          uint32_t* par = reinterpret_cast<uint32_t*>(params + v * C::kParamBytes) + lane * step * groups;
+          if (lost) {                                       // a block that is not there: zeros
+            for (int i = 0; i < step * groups; ++i) par[i] = 0u;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(&raw_full[v], bytes);
+          __syncwarp();
+          if (ok) {
+            bulk_load(codes, (v ? ta.ca.vc : ta.ca.kc) + row * (D / 2), step * (D / 2), &raw_full[v]);
+            bulk_load(par, (v ? ta.ca.vs : ta.ca.ks) + row * groups, step * groups * 4, &raw_full[v]);
+          }
+          ++issued;
+        }
+        if (!go) break;
+      }
+      // after a timeout: let the copies in flight land before the CTA ends
+      if (*timeout)
+        for (int q = max(0, issued - 2); q < issued; ++q)
+          mbar_wait_bounded(&raw_full[q & 1], (uint32_t)(q >> 1) & 1, kWaitCycles / 8);
+    } else if (warp < C::kFetchWarp) {
+      // ------------------------------------------------------------ products
+      // A warp per row tile: the products of one then run while the other's warp
+      // waits (one warp for both, in line: 3950 clocks a step, 2050 of them
+      // products).  The whole warp runs the loop, so that descriptors are uniform
+      // values; one elected lane issues.
+      const int t = warp - C::kMmaWarp, n = t == 0 ? n0 : n1;
+      const uint64_t dq = desc_k_major(smem_addr(sq + t * C::kQBytes)), dk = desc_k_major(smem_addr(sk));
+      const uint64_t dv = desc_mn_major(smem_addr(sv), C::kSub > 1 ? BN * 128 : 1024);
+      const uint32_t my_s = tmem_s + t * BN, my_o = tmem_o + t * D;
+      auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+      // scores of tile j; past this row tile's last, the other's codes are let go
+      auto scores = [&](int j) {
+        if (j >= tiles) return true;
+        const int st = j & 1;
+        bool ok = wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout);
+        if (j < n) {
+          if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
+          // they overwrite the weights of the tile before
+          else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
+        }
+        if (!all(ok)) return false;
+        tc_after();
+        if (elect()) {
+          if (j < n) {
+            const uint64_t kd = dk + (uint64_t)(st * C::kValueBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(my_s, dq + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4),
+                     kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, false, false>::v, k > 0);
+            mma_commit(&s_full[t]);
+            mma_commit(&k_free[st]);
+            arrive(&turn[t][st]);
+          } else {
+            arrive(&k_free[st]);
+          }
+        }
+        __syncwarp();
+        return true;
+      };
+      auto add_values = [&](int j) {
+        const int st = j & 1;
+        bool ok = wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout);
+        if (j < n) ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
+        // In turn, values and next scores of one row tile, then of the other: when
+        // both had weights ready together, they would stay in step and neither's
+        // exponentials run under the other's products.  (Neither can be two tiles
+        // ahead here: a parity tells.  The turn passes when the scores have been
+        // issued: passed before, the two warps' products interleave and the row
+        // tile that is ahead loses its lead, 252 us to 242.)
+        if (T > 1 && t == 0 && j < min(n, n1)) ok = ok && wait_on(&turn[T - 1][st], (uint32_t)(j >> 1) & 1, timeout);
+        if (T > 1 && t == 1 && j < n && j + 1 < n0) ok = ok && wait_on(&turn[0][st ^ 1], (uint32_t)((j + 1) >> 1) & 1, timeout);
+        if (!all(ok)) return false;
+        tc_after();
+        if (elect()) {
+          if (j < n) {
+            const uint64_t vd = dv + (uint64_t)(st * C::kValueBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              mma_ts(my_o, my_s + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
+            mma_commit(&o_done[t]);
+            mma_commit(&v_free[st]);
+          } else {
+            arrive(&v_free[st]);
+          }
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = scores(0);
+      for (int j = 0; j < tiles && ok; ++j) ok = add_values(j) && scores(j + 1);
+    }
+  } else {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;                          // row tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t my_s = tmem_s + lanes + t * BN, my_o = tmem_o + lanes + t * D;
+    const int R0 = row0 + t * kTileRows, R = R0 + row, j_tok = R / a.group;
+    const int n = t == 0 ? n0 : n1;
+    const bool mine = R < rows;
+    const int head = h * a.group + R - j_tok * a.group;
+    const int lim = mine ? min(r.shown + j_tok, r.len - 1) : r.len - 1;     // last position the row sees
+    const int lim_min = min(r.shown + R0 / a.group, r.len - 1);           // of the tile's first row
+
+    // The warp's query rows go to shared memory as they are, D / 8 lanes to a
+    // row; rows past the request's are zeros.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+    uint8_t* my_line = sq + t * C::kQBytes + row * 128;
+    auto chunk_of = [&](int c) {                            // 16-byte part c of this thread's row
+      return reinterpret_cast<uint4*>(my_line + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4));
+    };
+    auto line_of = [&](int r32, int c) {                    // 16-byte part c of the warp's row
+      const int rr = (warp & 3) * 32 + r32;
+      return sq + t * C::kQBytes + (c >> 3) * kTileRows * 128 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+    };
+    {
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q);
+      if (mine) src += (int64_t)(r.q0 + j_tok) * a.ldq + (int64_t)head * D;
+      const uint32_t have = __ballot_sync(0xffffffffu, mine);
+      const int c = lane & (kLanes - 1);
+#pragma unroll 4
+      for (int pass = 0; pass < kLanes; ++pass) {
+        const int from = pass * kAtOnce + lane / kLanes;
+        const uint16_t* p =
+            reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+        copy16(line_of(from, c), p + 8 * c, have >> from & 1 ? 16 : 0);
+      }
+    }
+
+    // lane g < BN / 16: whether the tile's g-th 16 tokens lie in a block that is not
+    // there, a tile ahead
+    bool lost = false;
+    auto look_up = [&](int j) {
+      const int pos = (first + j) * BN + 16 * lane;
+      lost = lane < BN / 16 && pos < seen && (unsigned)table[pos >> a.log2_bs] >= (unsigned long long)a.num_blocks;
+    };
+    if (n > 0) look_up(0);
+
+    // To fp16 in place, each word of eight dimensions in the values' order, after a
+    // power of two that brings the row's largest to [2^13, 2^14).
+    float fac;
+    {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      uint32_t top = 0;                                     // of the two halves' magnitudes
+#pragma unroll 8
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *chunk_of(c);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+      }
+      top = max(top >> 16, top & 0xFFFFu);
+      const int ex = min(126, max(-116, 140 - (int)(top >> 7)));
+      const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+      fac = a.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *chunk_of(c);
+        const auto low = [&](uint32_t v) { return __uint_as_float(v << 16) * up; };
+        const auto high = [&](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u) * up; };
+        *chunk_of(c) = make_uint4(pack_f16(low(x.x), low(x.z)), pack_f16(high(x.x), high(x.z)),
+                                  pack_f16(low(x.y), low(x.w)), pack_f16(high(x.y), high(x.w)));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(&q_full[t]);
+    }
+    float mx = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t gone = __ballot_sync(0xffffffffu, lost);
+      if (j + 1 < n) look_up(j + 1);
+      const int vis0 = lim - (first + j) * BN;
+      const bool masked = (first + j + 1) * BN - 1 > lim_min || gone != 0;
+      ok = __all_sync(0xffffffffu, wait_on(&s_full[t], (uint32_t)j & 1, timeout));
+      if (!ok) break;
+      tc_after();
+      __syncwarp();
+      bool common = !masked && !__any_sync(0xffffffffu, mx == -INFINITY);
+      if (common) {
+        uint32_t w[BN / 2];
+        float sum = l;
+        const uint32_t top = row_weights<BN>(my_s, fac, kShift - mx, w, sum);
+        common = !__any_sync(0xffffffffu, top > kTopWeight);
+        if (common) {
+          l = sum;
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) tmem_st16(my_s + 16 * c, w + 16 * c);
+        }
+      }
+      if (!common) {
+        // where the maximum moves, what there is so far shrinks
+        const float top = row_top<BN>(my_s, fac, gone, vis0);
+        const bool moves = mx == -INFINITY ? top != -INFINITY : top > mx + kLead;
+        const float to = moves ? ceilf(top) : mx, f = moves ? pow2(mx - to) : 1.f;
+        l *= f;
+        mx = to;
+        if (j > 0 && __any_sync(0xffffffffu, moves)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(my_o + 32 * c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(my_o + 32 * c, o);
+            tmem_st16(my_o + 32 * c + 16, o + 16);
+          }
+        }
+        store_weights<BN>(my_s, fac, kShift - (mx == -INFINITY ? 0.f : mx), gone, vis0, l);
+      }
+      tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) arrive(&p_full[t]);
+    }
+
+    // Outputs, by way of the rows of shared memory where the queries were (the
+    // products with them are done): a warp's stores then cover whole lines.
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(n - 1) & 1, timeout));
+    tc_after();
+    __syncwarp();
+    if (ok) {
+      const bool whole = ta.splits == 1;
+      const uint32_t rows_out = whole ? __ballot_sync(0xffffffffu, mine) : 0xffffffffu;
+      // with the positions split: the row's sums as they are
+      float* piece = a.part + ((int64_t)blockIdx.x * C::kRows + t * kTileRows + row) * (D + 4);
+      uint8_t* dst = reinterpret_cast<uint8_t*>(
+          whole ? reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D
+                : reinterpret_cast<uint16_t*>(piece));
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // 2 D bytes of each row: all of it as bf16, or half of it
+#pragma unroll 1
+      for (int part = 0; part < (whole ? 1 : 2); ++part) {
+#pragma unroll 1
+        for (int c = 0; c < (whole ? D / 32 : D / 64); ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(my_o + part * (D / 2) + 32 * c, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          // columns 0, 2, 4, 6 of eight are dimensions 0 .. 3, columns 1, 3, 5, 7 the others
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int at = 8 * e + 4 * (q & 1) + (q >> 1);
+                const __nv_bfloat162 b =
+                    __floats2bfloat162_rn(__uint_as_float(o[at]) * inv, __uint_as_float(o[at + 2]) * inv);
+                u[q] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              *chunk_of(4 * c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = 8 * (e >> 1) + (e & 1);
+              *chunk_of(8 * c + e) = make_uint4(o[at], o[at + 2], o[at + 4], o[at + 6]);
+            }
+          }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int pass = 0; pass < kLanes; ++pass) {
+          const int from = pass * kAtOnce + lane / kLanes, c = lane & (kLanes - 1);
+          uint8_t* p = reinterpret_cast<uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
+          if (rows_out >> from & 1)
+            *reinterpret_cast<uint4*>(p + part * 2 * D + 16 * c) = *reinterpret_cast<const uint4*>(line_of(from, c));
+        }
+        __syncwarp();
+      }
+      if (!whole) {
+        piece[D] = mx;
+        piece[D + 1] = l;
+        piece[D + 2] = mx - kShift;                         // the unit of the sum: 2^that
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_before();
+  __syncthreads();
+  if (timeout_flag && warp >= C::kMmaWarp && warp < C::kFetchWarp) {
+    // products may still be in flight: all have completed once this arrives
+    if (elect()) mma_commit(&drain);
+    __syncwarp();
+  }
+  if (warp == C::kMmaWarp) {
+    if (timeout_flag) mbar_wait_bounded(&drain, 0, kWaitCycles);
+    __syncwarp();
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kCols));
+  }
+  if (threadIdx.x == 0 && timeout_flag) raise_flag(a.status, LQ_DEV_TIMEOUT);
+}
+
+template <int D>
+lq_status launch(const TileArgs& ta, const TilePlan& plan, void* stream) {
+  using C = TileCfg<D>;
+  static_assert(C::kSmem + 1536 <= 227 * 1024, "shared memory");
+  static_assert(C::kRows * (D + 4) <= work_floats(D), "a CTA's piece fits its SM's share of the workspace");
+  auto kern = tiles_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return LQ_ERR_CUDA;
+  }
+  const lq_status st = serve::launch(kern, (unsigned)(plan.units * plan.splits), C::kThreads, C::kSmem, stream, ta);
+  if (st != LQ_OK || plan.splits == 1) return st;
+  return serve::launch(attn_tiles_merge_kernel<D>, (unsigned)(plan.units * (C::kRows / 8)), 256, 0, stream,
+                       TileMergeArgs{ta.ca.a, ta.splits});
+}
+
+lq_status launch_tiles(const CacheArgs& ca, int head_dim, const TilePlan& plan, void* stream) {
+  if (plan.units * plan.splits > INT32_MAX) return LQ_ERR_SHAPE;
+  TileArgs ta;
+  ta.ca = ca;
+  ta.splits = plan.splits;
+  switch (head_dim) {
+    case 64: return launch<64>(ta, plan, stream);
+    case 128: return launch<128>(ta, plan, stream);
+    default: return launch<256>(ta, plan, stream);
+  }
+}
+
+}  // namespace q4
+}  // namespace lq

@@ -9,20 +9,26 @@
 // the order of (d descending, token ascending): that of the log probabilities as
 // they are given, in which logits that differ by less than d's last place are equal.
 //
-// A cluster of up to eight CTAs per row reads the row once: each CTA copies its
-// share to shared memory in pieces (untiled bulk copies; the few elements before and
-// after the 16-byte boundaries by ordinary loads) and takes maxima as they arrive, the
+// Rows are read once.  A CTA, or a cluster of up to eight where a row is longer than
+// one SM's shared memory or there are few rows, copies its share of a row to shared
+// memory in four pieces (untiled bulk copies) and takes maxima as they arrive; the
 // CTAs agree on the row's maximum, and everything else, whose terms hang on it, comes
-// from shared memory.  The exponentials, one fma, two additions, the rank's comparison
-// and the unpacking make about 8 instructions an element, so rows stay bound by HBM as
-// long as other CTAs of the SM load meanwhile.  Sums go through fixed trees: equal
-// calls give equal bits.
+// from shared memory: about 11 instructions an element for the exponentials, sums and
+// the rank's comparison.  CTAs stay for row after row: as soon as a piece has been read
+// for the last time, the same piece of the next row is copied over it, so that the
+// loads run under the exponentials.  A cluster waits for itself once per row: the
+// maxima of a row and the results of the row before cross together, and a row's results
+// are put together by its CTAs in turn.  Sums go through fixed trees: equal calls give
+// equal bits.
 //
 // Alternatives: the k-th largest of 32 maxima, each over every 32nd 16-byte chunk of
 // the share, is a bound that at least k elements reach and few others do; those are
 // listed on the way and ranked by counting.  Where more reach it than there is room
 // for (equal logits, large ones in step with the chunks), the k are taken one after
-// the other instead.
+// the other instead, from the row itself.
+//
+// A row starts at any element: chunks at its ends are copied whole where that stays
+// inside the matrix, and slots that are not the row's count as -inf.
 #include "lq_device.cuh"
 #include "lq_host.h"
 #include "lq_serve.cuh"
@@ -34,12 +40,12 @@
 namespace lq {
 namespace score {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxTop = LQ_MAX_ALTERNATIVES, kMaxCluster = 8;
-constexpr int kPieces = 8;                     // copies that a share is split into
-constexpr int kRoom = 1024;                    // candidates that are listed
+constexpr int kPieces = 4;                     // of a share
+constexpr int kRoom = 512;                     // candidates that are listed
 constexpr int kByRank = 256;                   // and ordered by counting
-constexpr int kMostBytes = 192 * 1024;         // of a share in shared memory at once
+constexpr int kMostBytes = 208 * 1024;         // of a share in shared memory at once
 constexpr long long kWaitCycles = 2000000000ll;
 typedef unsigned long long u64;
 
@@ -57,6 +63,7 @@ struct Args {
   int cluster;
   int64_t share;             // elements of a row per CTA
   int segment;               // of those in shared memory at once
+  int per_piece;             // chunks
 };
 
 // A value and its token as one number, larger for the ones that come first.
@@ -126,37 +133,47 @@ __device__ __forceinline__ void put(uint32_t to, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void copy_in(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
-// What a CTA finds in its share, for the cluster's first one.
-struct Found {
-  float l, s;
-  int before, pad;
-  u64 top[kMaxTop];
+// A segment of a CTA's share of a row: n elements from token `base` on, in `chunks`
+// chunks of 16 bytes whose first `skew` slots and last ones may not be the row's.
+struct View {
+  const uint8_t* src;        // of the first chunk, at a 16-byte boundary
+  int64_t base;
+  int n, skew, chunks;
 };
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__ Args a) {
   constexpr int E = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4;
-  extern __shared__ __align__(16) uint8_t image[];
-  __shared__ uint64_t bars[kPieces];
+  constexpr int kBatch = BF16 ? 2 : 4;         // chunks that a thread works on at a time
+  extern __shared__ __align__(16) uint8_t image_bytes[];
+  uint4* image = reinterpret_cast<uint4*>(image_bytes);
+  __shared__ uint64_t full[kPieces], empty[kPieces];
   __shared__ float maxima[kWarps][32];
   __shared__ float sums[kWarps][2];
   __shared__ int counts[kWarps];
-  __shared__ float tops[kMaxCluster];          // the CTAs' maxima
+  __shared__ float tops[2][kMaxCluster];       // the CTAs' maxima, of this row and the next
   __shared__ float bound;                      // of the candidates, a logit
   __shared__ int listed, timeout;
   __shared__ u64 list[kRoom], best[kMaxTop], round_best[kWarps];
-  __shared__ Found found[kMaxCluster];
+  __shared__ float4 found[2][kMaxCluster];     // the CTAs' sums and counts
+  __shared__ u64 keys[2][kMaxCluster * kMaxTop];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = a.cluster, rank = ctas > 1 ? (int)cluster_rank() : 0;
-  const int64_t row = blockIdx.x / ctas;
+  const int64_t clusters = gridDim.x / ctas, row0 = blockIdx.x / ctas;
 
   if (tid == 0) {
-    for (int p = 0; p < kPieces; ++p) mbar_init1(bars + p, 1);
+    for (int p = 0; p < kPieces; ++p) {
+      mbar_init1(full + p, 1);
+      mbar_init1(empty + p, kWarps);
+    }
     mbar_init_fence();
     timeout = 0;
   }
@@ -165,315 +182,400 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
   pdl_launch();
   __syncthreads();
 
-  const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x) + row * a.ld * kSize;
+  const uint8_t* all = reinterpret_cast<const uint8_t*>(a.x);
+  const uint8_t* all_end = all + ((a.rows - 1) * a.ld + a.vocab) * kSize;
   const int64_t v0 = min(a.vocab, rank * a.share), v1 = min(a.vocab, v0 + a.share);
   const int segments = v1 > v0 ? (int)((v1 - v0 + a.segment - 1) / a.segment) : 1;
 
-  // A segment: n elements from token base on, in 16-byte chunks of which the first
-  // `skew` elements and those past the end are -inf.
-  int64_t base = 0;
-  int n = 0, skew = 0, chunks = 0, body = 0, per_piece = 0;
-  uint32_t phase = 0;
-  auto load = [&](int segment) {
-    base = v0 + (int64_t)segment * a.segment;
-    n = (int)min((int64_t)a.segment, v1 - base);
-    const uint8_t* src = x + base * kSize;
-    const int head = min(n, (int)((0u - (uint32_t)reinterpret_cast<uintptr_t>(src)) & 15u) / kSize);
-    skew = head > 0 ? E - head : 0;
-    body = (n - head) / E;                     // whole chunks
-    chunks = (skew + n + E - 1) / E;
-    per_piece = (body + kPieces - 1) / kPieces;
-    const int first = skew > 0;
-    if (tid < kPieces) {
-      const int c0 = min(body, tid * per_piece), c1 = min(body, c0 + per_piece);
-      mbar_expect_tx(bars + tid, (c1 - c0) * 16);
-      if (c1 > c0) copy_in(image + (first + c0) * 16, src + head * kSize + c0 * 16, (c1 - c0) * 16, bars + tid);
-    }
-    // what lies outside the boundaries: first and last chunk
-    if (warp == 1) {
-      const uint32_t none = BF16 ? 0xFF80u : 0xFF800000u;
-      const auto set = [&](int slot, uint32_t v) {
-        if constexpr (BF16) reinterpret_cast<uint16_t*>(image)[slot] = (uint16_t)v;
-        else reinterpret_cast<uint32_t*>(image)[slot] = v;
-      };
-      const auto get = [&](int i) -> uint32_t {
-        if constexpr (BF16) return reinterpret_cast<const uint16_t*>(src)[i];
-        else return reinterpret_cast<const uint32_t*>(src)[i];
-      };
-      if (first && lane < E) set(lane, lane >= skew && lane - skew < n ? get(lane - skew) : none);
-      const int slot = (first + body) * E + lane;           // after the body
-      if (lane < E && slot < chunks * E) set(slot, slot - skew < n ? get(slot - skew) : none);
-    }
-    __syncthreads();
+  auto view = [&](int64_t row, int segment) {
+    View w;
+    w.base = v0 + (int64_t)segment * a.segment;
+    w.n = (int)min((int64_t)a.segment, v1 - w.base);
+    const uint8_t* src = all + (row * a.ld + w.base) * kSize;
+    const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(src) & 15u;
+    w.src = src - low;
+    w.skew = w.n > 0 ? (int)low / kSize : 0;
+    w.chunks = (w.skew + w.n + E - 1) / E;
+    return w;
   };
-  // Runs f(chunk, its 16 bytes) over this thread's chunks as their pieces arrive.
-  auto each = [&](auto f) {
-    const int first = skew > 0;
+  // Warp 0 copies piece p; its barrier completes a phase even if there is nothing to
+  // copy.  The matrix's own first and last chunk, where not all of it is inside, come by
+  // single loads.
+  auto start = [&](const View& w, int p) {
+    int c0 = min(w.chunks, p * a.per_piece), c1 = min(w.chunks, c0 + a.per_piece);
+    const bool single0 = c0 == 0 && c1 > 0 && w.src < all;
+    const bool single1 = c1 == w.chunks && c1 > c0 && w.src + (int64_t)w.chunks * 16 > all_end;
+    if (single0 || single1) {
+      const int slot = (lane < E && single0 ? 0 : w.chunks - 1) * E + (lane & (E - 1));
+      if (lane < 2 * E && (lane < E ? single0 : single1) && (unsigned)(slot - w.skew) < (unsigned)w.n) {
+        if constexpr (BF16)
+          reinterpret_cast<uint16_t*>(image)[slot] = reinterpret_cast<const uint16_t*>(w.src)[slot];
+        else
+          reinterpret_cast<uint32_t*>(image)[slot] = reinterpret_cast<const uint32_t*>(w.src)[slot];
+      }
+      fence_proxy_async_smem();                // before the copy that comes here next
+      __syncwarp();
+      c0 += single0;
+      c1 = max(c0, c1 - (single1 && (c1 > c0)));
+    }
+    if (lane == 0) {
+      mbar_expect_tx(full + p, (c1 - c0) * 16);
+      if (c1 > c0) copy_in(image + c0, w.src + (int64_t)c0 * 16, (c1 - c0) * 16, full + p);
+    }
+  };
+  auto wait_for = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait_bounded(bar, parity, kWaitCycles)) timeout = 1;
+  };
+  // The values of chunks c, c + kThreads, ...; -inf for slots that are not the row's.
+  auto values = [&](const View& w, int c, auto& v) {
+    constexpr int B = sizeof(v) / sizeof(v[0]);
+    uint4 u[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) u[b] = image[c + b * kThreads];
+#pragma unroll
+    for (int b = 0; b < B; ++b) unpack<BF16>(u[b], v[b]);
+    if (c == 0 || c + (B - 1) * kThreads == w.chunks - 1) {
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((unsigned)((c + b * kThreads) * E + e - w.skew) >= (unsigned)w.n) v[b][e] = -INFINITY;
+    }
+  };
+  // Runs f(c, batch) over this thread's chunks of piece p, several at a time.
+  auto each = [&](const View& w, int p, auto f) {
+    const int c1 = min(w.chunks, (p + 1) * a.per_piece);
+    int c = p * a.per_piece + tid;
+#pragma unroll 1
+    for (; c + (kBatch - 1) * kThreads < c1; c += kBatch * kThreads) {
+      float v[kBatch][E];
+      values(w, c, v);
+      f(c, v);
+    }
+#pragma unroll 1
+    for (; c < c1; c += kThreads) {
+      float v[1][E];
+      values(w, c, v);
+      f(c, v);
+    }
+  };
+  // The largest logit of this thread's chunks, as they arrive.
+  auto largest = [&](const View& w, uint32_t parity) {
+    float m = -INFINITY;
 #pragma unroll 1
     for (int p = 0; p < kPieces; ++p) {
-      const int c0 = p == 0 ? 0 : first + min(body, p * per_piece);
-      const int c1 = p == kPieces - 1 ? chunks : first + min(body, (p + 1) * per_piece);
-      if (c0 >= c1) continue;
-      if (!mbar_wait_bounded(bars + p, phase, kWaitCycles)) {
-        timeout = 1;
-        break;
-      }
-#pragma unroll 4
-      for (int c = c0 + ((tid - c0) & (kThreads - 1)); c < c1; c += kThreads)
-        f(c, reinterpret_cast<const uint4*>(image)[c]);
-    }
-  };
-  // The largest logit of this thread's chunks.
-  auto largest = [&]() {
-    float m = -INFINITY;
-    each([&](int, const uint4& w) {
-      float v[E];
-      unpack<BF16>(w, v);
+      wait_for(full + p, parity);
+      each(w, p, [&](int, auto& v) {
+        constexpr int B = sizeof(v) / sizeof(v[0]);
+        float h[B];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) m = fmaxf(m, fmaxf(v[e], v[e + 1]));
-    });
+        for (int b = 0; b < B; ++b) {
+          h[b] = fmaxf(v[b][0], v[b][1]);
+#pragma unroll
+          for (int e = 2; e < E; e += 2) h[b] = fmaxf(h[b], fmaxf(v[b][e], v[b][e + 1]));
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) m = fmaxf(m, h[b]);
+      });
+    }
     return m;
   };
-  // From the threads' maxima the CTA's, and the bound under its candidates.
+  // From the threads' maxima the CTA's (in warp 0), and the bound under its candidates.
   auto bound_of = [&](float mine) {
     maxima[warp][lane] = mine;
     __syncthreads();
     float m = -INFINITY;
     if (warp == 0) {
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, maxima[w][lane]);
-      if (a.top > 0) {
-        int ahead = 0;                         // lanes whose maximum comes before this one's
-#pragma unroll 8
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) m = fmaxf(m, maxima[q][lane]);
+      int ahead = 0;                           // lanes whose maximum comes before this one's
+      if (a.top > 1) {
+#pragma unroll
         for (int o = 0; o < 32; ++o) {
           const float y = __shfl_sync(0xffffffffu, m, o);
-          ahead += y > m || (y == m && o < lane);
+          ahead += (y > m) | ((y == m) & (o < lane));
         }
         if (ahead == a.top - 1) bound = m;
       }
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (a.top == 1 && lane == 0) bound = m;
     }
-    return m;                                  // in warp 0
+    return m;
   };
 
-  // the row's maximum
-  float mine = -INFINITY;
-  for (int g = 0; g < segments; ++g) {
-    if (g > 0) {
-      fence_proxy_async_smem();
-      __syncthreads();
-      phase ^= 1;
+  // The row before, which is finished once the cluster has met again.
+  int64_t last_row = -1;
+  int last_token = -1;
+  float last_m = 0.f, last_dt = 0.f;
+  auto finish = [&](int slot) {
+    float l = 0.f, s = 0.f;
+    int before = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r < ctas) {
+        const float4 f = found[slot][r];
+        l += f.x;
+        s += f.y;
+        before += __float_as_int(f.z);
+      }
     }
-    load(g);
-    mine = fmaxf(mine, largest());
-  }
-  float m = bound_of(mine);
-  if (ctas > 1) {
-    cluster_wait();
-    if (warp == 0 && lane < ctas) put(peer(tops + rank, lane), m);
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    if (tid == 0) tops[0] = m;
-    __syncthreads();
-  }
-  m = tops[0];
-  for (int r = 1; r < ctas; ++r) m = fmaxf(m, tops[r]);
-  const float zero = m == -INFINITY ? 0.f : m;
-
-  const int32_t token = a.tokens[row];
-  const bool given = token >= 0 && token < a.vocab;
-  const float dt = given ? at<BF16>(x, token) - zero : INFINITY;
-  const float dt_after = given ? after(dt) : INFINITY;              // d > dt is d >= dt_after
-
-  float2 l2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
-  int before = 0, have = 0;                    // have: alternatives found in earlier segments
-  for (int g = 0; g < segments; ++g) {
-    if (segments > 1) {                        // the share again
-      fence_proxy_async_smem();
-      __syncthreads();
-      phase ^= 1;
-      load(g);
-      bound_of(largest());
+    const bool bad = !(l < INFINITY);          // NaN: one among the logits, or +inf less itself
+    const bool given = last_token >= 0 && last_token < a.vocab;
+    const float log_l = l > 0.f ? logf(l) : 0.f;
+    if (tid == kThreads - 1) {
+      if (bad) raise_flag(a.status, LQ_DEV_NONFINITE);
+      else if (last_m == -INFINITY) raise_flag(a.status, LQ_DEV_RANGE);
+      if (last_token >= a.vocab) raise_flag(a.status, LQ_DEV_RANGE);
+      a.logprobs[last_row] = bad ? NAN : given ? last_dt - log_l : 0.f;
+      if (a.entropy != nullptr) a.entropy[last_row] = bad ? NAN : l > 0.f ? log_l - s / l : 0.f;
+      if (a.ranks != nullptr) a.ranks[last_row] = bad || !given ? -1 : before;
     }
-    if (tid < have) list[tid] = best[tid];
-    if (tid == 0) listed = have;
-    __syncthreads();
-    const float least = a.top > 0 ? bound - zero : INFINITY;
-    const int64_t first = base - skew;         // token of the image's first slot
-    each([&](int c, const uint4& w) {
-      float v[E];
-      unpack<BF16>(w, v);
-      const int64_t t0 = first + (int64_t)c * E;
-      const float2 shift = make_float2(-zero, -zero), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
-      float high = -INFINITY;
-      // all of the chunk before the token, or all after it; the chunk that holds it and
-      // those with slots that are no tokens are looked at one by one
-      const bool apart = (token >= t0 && token < t0 + E) || c == 0 || c == chunks - 1;
-      const float from = t0 < token ? dt : dt_after;
-      int more = 0;
+    if (tid < a.top * ctas) {
+      // an alternative's place: how many of every CTA's, which are in order, come before it
+      const u64 key = keys[slot][tid];
+      int ahead[kMaxCluster];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        float2 d = add2(make_float2(v[e], v[e + 1]), shift);
-        more += (d.x >= from) + (d.y >= from);
-        v[e] = d.x;
-        v[e + 1] = d.y;
-        high = fmaxf(high, fmaxf(d.x, d.y));
-        d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));       // -inf: no term, not 0 times itself
-        float2 y = mul2(d, log2e);
-        y = make_float2(ex2(y.x), ex2(y.y));
-        l2 = add2(l2, y);
-        s2 = fma2(y, d, s2);
-      }
-      if (apart) {
-        more = 0;
+      for (int r = 0; r < kMaxCluster; ++r) ahead[r] = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int64_t t = t0 + e;
-          more += t >= base && t < base + n && (v[e] >= dt_after || (v[e] == dt && t < token));
+      for (int step = kMaxTop; step; step >>= 1)
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          const int to = ahead[r] + step;
+          if (r < ctas && to <= a.top && keys[slot][r * a.top + to - 1] > key) ahead[r] = to;
         }
-      }
-      before += more;
-      if (high >= least) {
+      int place = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int64_t t = t0 + e;
-          if (v[e] >= least && t >= base && t < base + n) {
-            const int to = atomicAdd(&listed, 1);
-            if (to < kRoom) list[to] = key_of(v[e], (uint32_t)t);
-          }
-        }
+      for (int r = 0; r < kMaxCluster; ++r) place += ahead[r];
+      if (bad ? tid < a.top : key != 0 && place < a.top) {
+        const int64_t to = last_row * a.top + (bad ? tid : place);
+        a.top_tokens[to] = bad ? -1 : (int32_t)(0xFFFFFFFFu - (uint32_t)key);
+        a.top_logprobs[to] = bad ? NAN : value_of(key) - log_l;
       }
-    });
-    __syncthreads();
-    if (a.top > 0) {
-      const int count = listed, k = min((int64_t)a.top, (int64_t)have + n);
-      if (count <= kByRank) {
-        const u64 key = tid < count ? list[tid] : 0;
-        int ahead = 0;
-#pragma unroll 8
-        for (int i = 0; i < count; ++i) ahead += list[i] > key;
+    }
+  };
+
+  int use = 0;                                 // copies of whole segments so far
+  if (segments == 1 && warp == 0) {
+    const View w = view(row0, 0);
+    for (int p = 0; p < kPieces; ++p) start(w, p);
+  }
+  if (ctas > 1) cluster_wait();
+  int it = 0;
+  for (int64_t row = row0; row < a.rows; row += clusters, ++it) {
+    const int32_t token = a.tokens[row];
+    const bool given = token >= 0 && token < a.vocab;
+    const float xt = given ? at<BF16>(all + row * a.ld * kSize, token) : 0.f;
+    // segment g, once everyone has read what was there; its phase
+    View w = view(row, 0);
+    auto load = [&](int g) {
+      if (segments > 1) {
         __syncthreads();
-        if (tid < count && ahead < k) best[ahead] = key;
-      } else {
-        // one after the other: the largest key below the last, of the list or, where it
-        // has overflowed, of the earlier segments' and the whole segment
-        u64 last = ~0ull;
-        const int old = count <= kRoom ? count : have;
-        u64 taken = 0;
-        for (int i = 0; i < k; ++i) {
-          u64 top = 0;
-          for (int j = tid; j < old; j += kThreads)
-            if (list[j] < last && list[j] > top) top = list[j];
-          if (count > kRoom)
-            each([&](int c, const uint4& w) {
-              float v[E];
-              unpack<BF16>(w, v);
+        w = view(row, g);
+        if (warp == 0)
+          for (int p = 0; p < kPieces; ++p) start(w, p);
+      }
+      return (uint32_t)use++ & 1u;
+    };
+    // the row's maximum
+    uint32_t parity = 0;
+    float mine = -INFINITY;
+    for (int g = 0; g < segments; ++g) {
+      parity = load(g);
+      mine = fmaxf(mine, largest(w, parity));
+    }
+    float m = bound_of(mine);
+    if (ctas > 1) {
+      if (warp == 0 && lane < ctas) put(peer(&tops[it & 1][rank], lane), m);
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      if (tid == 0) tops[it & 1][0] = m;
+      __syncthreads();
+    }
+    m = tops[it & 1][0];
+#pragma unroll
+    for (int r = 1; r < kMaxCluster; ++r)
+      if (r < ctas) m = fmaxf(m, tops[it & 1][r]);
+    if (it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
+    const float zero = m == -INFINITY ? 0.f : m;
+    const float dt = given ? xt - zero : INFINITY;
+    const float dt_after = given ? after(dt) : INFINITY;            // d > dt is d >= dt_after
+
+    float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, s2[2] = {l2[0], l2[0]};
+    int before = 0, have = 0;                  // have: alternatives found in earlier segments
+    for (int g = 0; g < segments; ++g) {
+      if (segments > 1) {                      // the share again
+        parity = load(g);
+        bound_of(largest(w, parity));
+      }
+      if (tid < have) list[tid] = best[tid];
+      if (tid == 0) listed = have;
+      __syncthreads();
+      const float least = a.top > 0 ? bound - zero : INFINITY;
+      // the token's slot of the image, or one before or behind all
+      const int64_t far = token - w.base + w.skew;
+      const int slot = far < 0 ? -1 : far < w.chunks * E ? (int)far : w.chunks * E;
+      const float2 shift = make_float2(-zero, -zero), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
+      // The rank by whole chunks before and behind the token: the slots of the chunk that
+      // holds it and of those at the ends, some of them no tokens, are counted one by one,
+      // one per lane, and what the loop below counts for them is taken off.
+      if (warp == kWarps - 1 && lane < 3 * E && w.chunks > 0) {
+        const int which = lane / E, c = which == 0 ? 0 : which == 1 ? w.chunks - 1 : slot / E;
+        // each of them once
+        if (which == 0 || (which == 1 && c > 0) || (which == 2 && slot >= 0 && c > 0 && c < w.chunks - 1)) {
+          const int at_slot = c * E + lane % E;
+          const bool in = (unsigned)(at_slot - w.skew) < (unsigned)w.n;
+          const float d = (in ? at<BF16>(image, at_slot) : -INFINITY) - zero;
+          before += (in & ((d >= dt_after) | ((d == dt) & (at_slot < slot)))) - (int)(d >= (c * E < slot ? dt : dt_after));
+        }
+        __syncwarp(0xffffffffu >> (32 - 3 * E));
+      }
+      const View next = view(row + clusters, 0);
+      const bool more = segments == 1 && row + clusters < a.rows;
+#pragma unroll 1
+      for (int p = 0; p < kPieces; ++p) {
+        each(w, p, [&](int c, auto& v) {
+          constexpr int B = sizeof(v) / sizeof(v[0]);
+          float high = -INFINITY;
+          int ahead[B];
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            const float from = (c + b * kThreads) * E < slot ? dt : dt_after;
+            ahead[b] = 0;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              float2 d = add2(make_float2(v[b][e], v[b][e + 1]), shift);
+              ahead[b] += d.x >= from;
+              ahead[b] += d.y >= from;
+              v[b][e] = d.x;
+              v[b][e + 1] = d.y;
+              high = fmaxf(high, fmaxf(d.x, d.y));
+              d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));   // -inf: no term, not 0 times itself
+              float2 y = mul2(d, log2e);
+              y = make_float2(ex2(y.x), ex2(y.y));
+              l2[b & 1] = add2(l2[b & 1], y);
+              s2[b & 1] = fma2(y, d, s2[b & 1]);
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < B; ++b) before += ahead[b];
+          if (high >= least) {
+#pragma unroll
+            for (int b = 0; b < B; ++b)
 #pragma unroll
               for (int e = 0; e < E; ++e) {
-                const int64_t t = first + (int64_t)c * E + e;
-                const u64 key = key_of(v[e] - zero, (uint32_t)t);
-                if (t >= base && t < base + n && key < last && key > top) top = key;
+                const int i = (c + b * kThreads) * E + e - w.skew;
+                if (v[b][e] >= least && (unsigned)i < (unsigned)w.n) {
+                  const int to = atomicAdd(&listed, 1);
+                  if (to < kRoom) list[to] = key_of(v[b][e], (uint32_t)(w.base + i));
+                }
               }
-            });
-          for (int o = 16; o; o >>= 1) {
-            const u64 y = __shfl_xor_sync(0xffffffffu, top, o);
-            top = y > top ? y : top;
           }
-          if (lane == 0) round_best[warp] = top;
-          __syncthreads();
-          for (int w = 0; w < kWarps; ++w) top = round_best[w] > top ? round_best[w] : top;
-          __syncthreads();
-          last = top;
-          if (tid == i) taken = top;
+        });
+        __syncwarp();
+        if (lane == 0) arrive(empty + p);
+        if (more && warp == 0 && p > 0) {      // the piece before, once all have read it
+          wait_for(empty + p - 1, (uint32_t)it & 1u);
+          start(next, p - 1);
         }
-        if (tid < k) best[tid] = taken;
       }
-      have = k;
+      if (more && warp == 0) {
+        wait_for(empty + kPieces - 1, (uint32_t)it & 1u);
+        start(next, kPieces - 1);
+      }
       __syncthreads();
+      if (a.top > 0) {
+        const int count = listed, k = (int)min((int64_t)a.top, (int64_t)have + w.n);
+        if (count <= kByRank) {
+          if (warp <= (count - 1) >> 5) {
+            const u64 key = tid < count ? list[tid] : 0;
+            int ahead = 0;
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) ahead += list[i] > key;
+            if (tid < count && ahead < k) best[ahead] = key;
+          }
+        } else {
+          // one after the other: the largest key below the last, of the list or, where it
+          // has overflowed, of the earlier segments' and the whole segment
+          u64 last = ~0ull, taken = 0;
+          const int old = count <= kRoom ? count : have;
+          const uint8_t* src = all + (row * a.ld + w.base) * kSize;
+          for (int i = 0; i < k; ++i) {
+            u64 top = 0;
+            for (int j = tid; j < old; j += kThreads)
+              if (list[j] < last && list[j] > top) top = list[j];
+            if (count > kRoom)
+              for (int j = tid; j < w.n; j += kThreads) {
+                const u64 key = key_of(at<BF16>(src, j) - zero, (uint32_t)(w.base + j));
+                if (key < last && key > top) top = key;
+              }
+            for (int o = 16; o; o >>= 1) {
+              const u64 y = __shfl_xor_sync(0xffffffffu, top, o);
+              top = y > top ? y : top;
+            }
+            if (lane == 0) round_best[warp] = top;
+            __syncthreads();
+            for (int q = 0; q < kWarps; ++q) top = round_best[q] > top ? round_best[q] : top;
+            __syncthreads();
+            last = top;
+            if (tid == i) taken = top;
+          }
+          if (tid < k) best[tid] = taken;
+        }
+        have = k;
+        __syncthreads();
+      }
     }
-  }
 
-  // sums over the CTA, then over the cluster, in a fixed order
-  float l = l2.x + l2.y, s = s2.x + s2.y;
-  for (int o = 16; o; o >>= 1) {
-    l += __shfl_xor_sync(0xffffffffu, l, o);
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) {
-    sums[warp][0] = l;
-    sums[warp][1] = s;
-    counts[warp] = before;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    l = s = 0.f;
-    before = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      l += sums[w][0];
-      s += sums[w][1];
-      before += counts[w];
+    // sums over the CTA in a fixed order, to the one of the cluster whose turn it is
+    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), s = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+    before = __reduce_add_sync(0xffffffffu, before);
+    for (int o = 16; o; o >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      s += __shfl_xor_sync(0xffffffffu, s, o);
     }
-    Found* to = found + rank;
-    if (ctas > 1) {
-      if (lane == 0) {
-        put(peer(&to->l, 0), l);
-        put(peer(&to->s, 0), s);
-        put(peer(&to->before, 0), __int_as_float(before));
-      }
-      if (lane < a.top) put(peer(&to->top[lane], 0), lane < have ? best[lane] : (u64)0);
-    } else {
-      if (lane == 0) {
-        to->l = l;
-        to->s = s;
-        to->before = before;
-      }
-      if (lane < a.top) to->top[lane] = lane < have ? best[lane] : 0;
+    if (lane == 0) {
+      sums[warp][0] = l;
+      sums[warp][1] = s;
+      counts[warp] = before;
     }
+    __syncthreads();
+    if (warp == 0) {
+      l = lane < kWarps ? sums[lane][0] : 0.f;
+      s = lane < kWarps ? sums[lane][1] : 0.f;
+      before = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[lane] : 0);
+      for (int o = kWarps / 2; o; o >>= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+      }
+      const int turn = it % ctas;
+      const u64 key = lane < have ? best[lane] : 0;
+      if (ctas > 1) {
+        if (lane == 0) {
+          const uint32_t to = peer(&found[it & 1][rank], turn);
+          put(to, l);
+          put(to + 4, s);
+          put(to + 8, __int_as_float(before));
+        }
+        if (lane < a.top) put(peer(&keys[it & 1][rank * a.top + lane], turn), key);
+      } else {
+        if (lane == 0) found[it & 1][0] = make_float4(l, s, __int_as_float(before), 0.f);
+        if (lane < a.top) keys[it & 1][lane] = key;
+      }
+    }
+    last_row = row;
+    last_token = token;
+    last_m = m;
+    last_dt = dt;
   }
   if (ctas > 1) {
     cluster_arrive();
-    if (rank != 0) {
-      if (tid == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
-      return;
-    }
     cluster_wait();
   } else {
     __syncthreads();
   }
-  l = s = 0.f;
-  before = 0;
-  for (int r = 0; r < ctas; ++r) {
-    l += found[r].l;
-    s += found[r].s;
-    before += found[r].before;
-  }
-  const bool bad = !(l < INFINITY);            // NaN: one among the logits, or +inf less itself
-  const float log_l = l > 0.f ? logf(l) : 0.f;
-  if (tid == 0) {
-    if (timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
-    if (bad) raise_flag(a.status, LQ_DEV_NONFINITE);
-    else if (m == -INFINITY) raise_flag(a.status, LQ_DEV_RANGE);
-    if (token >= a.vocab) raise_flag(a.status, LQ_DEV_RANGE);
-    a.logprobs[row] = bad ? NAN : given ? dt - log_l : 0.f;
-    if (a.entropy != nullptr) a.entropy[row] = bad ? NAN : l > 0.f ? log_l - s / l : 0.f;
-    if (a.ranks != nullptr) a.ranks[row] = bad || !given ? -1 : before;
-  }
-  if (tid < a.top * ctas) {
-    // an alternative's place: how many of all CTAs' lists come before it
-    const u64 key = found[tid / a.top].top[tid % a.top];
-    int ahead = 0;
-    for (int r = 0; r < ctas; ++r)
-      for (int i = 0; i < a.top; ++i) ahead += found[r].top[i] > key;
-    if (key != 0 && ahead < a.top) {
-      a.top_tokens[row * a.top + ahead] = bad ? -1 : (int32_t)(0xFFFFFFFFu - (uint32_t)key);
-      a.top_logprobs[row * a.top + ahead] = bad ? NAN : value_of(key) - log_l;
-    }
-  }
-  if (bad && tid < a.top) {                    // (keys of NaN say nothing)
-    a.top_tokens[row * a.top + tid] = -1;
-    a.top_logprobs[row * a.top + tid] = NAN;
-  }
+  if (it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
+  if (tid == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 
 }  // namespace score
@@ -504,22 +606,28 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   a.top_logprobs = top_logprobs_dev; a.status = dev_status_dev;
   const int sms = device_sm_count();
   if (sms <= 0) return LQ_ERR_CUDA;
-  // As few CTAs per row as keep several shares on an SM, more where the rows alone
-  // would leave SMs idle.
+  // As few CTAs per row as hold it in shared memory, more where the rows alone would
+  // leave SMs idle.
   const int64_t esize = dtype == LQ_BF16 ? 2 : 4, bytes = vocab * esize;
   int ctas = 1;
   while (ctas < score::kMaxCluster &&
-         (bytes / ctas > 52 * 1024 || (rows * ctas < 2 * sms && bytes / ctas > 8 * 1024)))
+         (bytes / ctas > score::kMostBytes - 16 || (rows * ctas < sms && bytes / ctas > 8 * 1024)))
     ctas *= 2;
   a.cluster = ctas;
   a.share = (vocab + ctas - 1) / ctas;
-  a.segment = (int)(a.share < score::kMostBytes / esize ? a.share : score::kMostBytes / esize);
-  const int smem = (int)(a.segment * esize) / 16 * 16 + 48;          // chunks at both ends may be partial
+  const int64_t most = (score::kMostBytes - 32) / esize;
+  a.segment = (int)(a.share < most ? a.share : most);
+  const int chunks = ((int)(a.segment * esize) + 15) / 16 + 1;       // those at both ends may be partial
+  a.per_piece = (chunks + score::kPieces - 1) / score::kPieces;
+  const int smem = chunks * 16;
   const auto kernel = dtype == LQ_BF16 ? score::score_kernel<true> : score::score_kernel<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kMostBytes + 48) !=
-      cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kMostBytes) != cudaSuccess) {
     cudaGetLastError();
     return LQ_ERR_CUDA;
   }
-  return serve::launch(kernel, (unsigned)(rows * ctas), score::kThreads, smem, stream, a, (unsigned)ctas);
+  // a cluster stays for row after row once there are more rows than fit
+  int per_sm = (228 * 1024) / (smem + 16 * 1024);
+  per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
+  const int64_t resident = (int64_t)sms * per_sm / ctas, clusters = rows < resident ? rows : resident;
+  return serve::launch(kernel, (unsigned)(clusters * ctas), score::kThreads, smem, stream, a, (unsigned)ctas);
 }

@@ -58,14 +58,29 @@ def test_sizes(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n", [150, 1000])
-def test_many_rows(dtype, n):
+@pytest.mark.parametrize("n,vocab", [(150, 515), (1000, 515), (900, 4001), (400, 9999)])
+def test_many_rows(dtype, n, vocab):
+    """More rows than fit the GPU at once, at odd addresses."""
     torch, L = cuda()
     rng = np.random.default_rng(n)
-    x, tokens = rows(torch, rng, n, 515, dtype), rng.integers(-1, 515, n)
+    x, tokens = rows(torch, rng, n, vocab, dtype), rng.integers(-1, vocab, n)
     got, st = call(torch, L, x, tokens, 4)
     assert st == 0
     check(got, x.float().cpu().numpy(), tokens, 4)
+
+
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 786433), ("bf16", 1000003), ("f32", 393217), ("f32", 900001)])
+def test_rows_longer_than_shared_memory(dtype, vocab):
+    """Shares in two or three segments, the last of them one token or more; all equal, and the largest in the last."""
+    torch, L = cuda()
+    rng = np.random.default_rng(vocab)
+    x = rows(torch, rng, 3, vocab, dtype)
+    x[1] = 1.5
+    x[2, vocab - 9:] = 30.0
+    tokens = [vocab // 3, vocab - 1, vocab - 5]
+    got, st = call(torch, L, x, tokens, 7)
+    assert st == 0
+    check(got, x.float().cpu().numpy(), tokens, 7)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

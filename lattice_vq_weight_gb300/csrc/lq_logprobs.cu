@@ -40,13 +40,17 @@
 namespace lq {
 namespace score {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;               // and a warp that copies and finishes rows
 constexpr int kMaxTop = LQ_MAX_ALTERNATIVES, kMaxCluster = 8;
-constexpr int kPieces = 4;                     // of a share
+#ifndef PCS
+#define PCS 6
+#endif
+constexpr int kPieces = PCS;                   // of a share
 constexpr int kRoom = 512;                     // candidates that are listed
 constexpr int kByRank = 256;                   // and ordered by counting
 constexpr int kMostBytes = 208 * 1024;         // of a share in shared memory at once
 constexpr long long kWaitCycles = 2000000000ll;
+constexpr float kHuge = 3.40282347e38f;        // the largest number
 typedef unsigned long long u64;
 
 struct Args {
@@ -76,11 +80,6 @@ __device__ __forceinline__ float value_of(u64 key) {
   const uint32_t b = (uint32_t)(key >> 32);
   return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
 }
-// The number after x (x <= 0).
-__device__ __forceinline__ float after(float x) {
-  return x == 0.f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(x) - 1u);
-}
-
 template <bool BF16>
 __device__ __forceinline__ float at(const void* p, int64_t i) {
   if constexpr (BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
@@ -113,6 +112,16 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return z;
 }
 
+// 1 where x is above 0 (by 2^-127 or more), else 0, and where x is 0, k.
+__device__ __forceinline__ float step_of(float x, float k) {
+  float y;
+  asm("fma.rn.sat.f32 %0, %1, 0f7F000000, %2;" : "=f"(y) : "f"(x), "f"(k));        // 2^127
+  return y;
+}
+
+// Barrier of the warps that compute.
+__device__ __forceinline__ void sync_workers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
@@ -141,6 +150,11 @@ __device__ __forceinline__ void copy_in(void* dst, const void* src, uint32_t byt
                ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 // A segment of a CTA's share of a row: n elements from token `base` on, in `chunks`
 // chunks of 16 bytes whose first `skew` slots and last ones may not be the row's.
 struct View {
@@ -150,9 +164,8 @@ struct View {
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_constant__ Args a) {
   constexpr int E = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4;
-  constexpr int kBatch = BF16 ? 2 : 4;         // chunks that a thread works on at a time
   extern __shared__ __align__(16) uint8_t image_bytes[];
   uint4* image = reinterpret_cast<uint4*>(image_bytes);
   __shared__ uint64_t full[kPieces], empty[kPieces];
@@ -198,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
     w.chunks = (w.skew + w.n + E - 1) / E;
     return w;
   };
-  // Warp 0 copies piece p; its barrier completes a phase even if there is nothing to
+  // The last warp copies piece p; its barrier completes a phase even if there is nothing to
   // copy.  The matrix's own first and last chunk, where not all of it is inside, come by
   // single loads.
   auto start = [&](const View& w, int p) {
@@ -226,42 +239,52 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
     if (!mbar_wait_bounded(bar, parity, kWaitCycles)) timeout = 1;
   };
-  // The values of chunks c, c + kThreads, ...; -inf for slots that are not the row's.
-  auto values = [&](const View& w, int c, auto& v) {
-    constexpr int B = sizeof(v) / sizeof(v[0]);
+  // Runs f(c, values) over this thread's chunks of piece p, several at a time: the values
+  // of chunks c, c + kThreads, ..., -inf for slots that are not the row's (edges: there
+  // may be such ones).
+  auto some = [&](const View& w, int c, auto edges, auto batch, auto& f) {
+    constexpr int B = decltype(batch)::value;
     uint4 u[B];
+    float v[B][E];
 #pragma unroll
     for (int b = 0; b < B; ++b) u[b] = image[c + b * kThreads];
 #pragma unroll
     for (int b = 0; b < B; ++b) unpack<BF16>(u[b], v[b]);
-    if (c == 0 || c + (B - 1) * kThreads == w.chunks - 1) {
+    if constexpr (decltype(edges)::value) {
 #pragma unroll
-      for (int b = 0; b < B; ++b)
+      for (int b = 0; b < B; ++b) {
+        const int from = (c + b * kThreads) * E - w.skew;
+        if (from < 0 || from + E > w.n) {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if ((unsigned)((c + b * kThreads) * E + e - w.skew) >= (unsigned)w.n) v[b][e] = -INFINITY;
+          for (int e = 0; e < E; ++e)
+            if ((unsigned)(from + e) >= (unsigned)w.n) v[b][e] = -INFINITY;
+        }
+      }
     }
+    f(c, v);
   };
-  // Runs f(c, batch) over this thread's chunks of piece p, several at a time.
-  auto each = [&](const View& w, int p, auto f) {
+  auto piece = [&](const View& w, int p, auto edges, auto& f) {
+    constexpr int B = BF16 ? 2 : 4;
     const int c1 = min(w.chunks, (p + 1) * a.per_piece);
     int c = p * a.per_piece + tid;
 #pragma unroll 1
-    for (; c + (kBatch - 1) * kThreads < c1; c += kBatch * kThreads) {
-      float v[kBatch][E];
-      values(w, c, v);
-      f(c, v);
+    for (; c + (B - 1) * kThreads < c1; c += B * kThreads) some(w, c, edges, Int<B>(), f);
+    if constexpr (B > 2) {
+      if (c + kThreads < c1) {
+        some(w, c, edges, Int<2>(), f);
+        c += 2 * kThreads;
+      }
     }
-#pragma unroll 1
-    for (; c < c1; c += kThreads) {
-      float v[1][E];
-      values(w, c, v);
-      f(c, v);
-    }
+    if (c < c1) some(w, c, edges, Int<1>(), f);
+  };
+  auto each = [&](const View& w, int p, auto f) {
+    if (p == 0 || (p + 1) * a.per_piece >= w.chunks) piece(w, p, Int<1>(), f);
+    else piece(w, p, Int<0>(), f);
   };
   // The largest logit of this thread's chunks, as they arrive.
   auto largest = [&](const View& w, uint32_t parity) {
     float m = -INFINITY;
+    if (warp == kWarps) return m;
 #pragma unroll 1
     for (int p = 0; p < kPieces; ++p) {
       wait_for(full + p, parity);
@@ -282,8 +305,9 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
   };
   // From the threads' maxima the CTA's (in warp 0), and the bound under its candidates.
   auto bound_of = [&](float mine) {
+    if (warp == kWarps) return mine;
     maxima[warp][lane] = mine;
-    __syncthreads();
+    sync_workers();
     float m = -INFINITY;
     if (warp == 0) {
 #pragma unroll
@@ -303,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
     return m;
   };
 
-  // The row before, which is finished once the cluster has met again.
+  // The row before, which the last warp finishes once the cluster has met again.
   int64_t last_row = -1;
   int last_token = -1;
   float last_m = 0.f, last_dt = 0.f;
@@ -322,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
     const bool bad = !(l < INFINITY);          // NaN: one among the logits, or +inf less itself
     const bool given = last_token >= 0 && last_token < a.vocab;
     const float log_l = l > 0.f ? logf(l) : 0.f;
-    if (tid == kThreads - 1) {
+    if (lane == 0) {
       if (bad) raise_flag(a.status, LQ_DEV_NONFINITE);
       else if (last_m == -INFINITY) raise_flag(a.status, LQ_DEV_RANGE);
       if (last_token >= a.vocab) raise_flag(a.status, LQ_DEV_RANGE);
@@ -330,9 +354,9 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
       if (a.entropy != nullptr) a.entropy[last_row] = bad ? NAN : l > 0.f ? log_l - s / l : 0.f;
       if (a.ranks != nullptr) a.ranks[last_row] = bad || !given ? -1 : before;
     }
-    if (tid < a.top * ctas) {
+    for (int i = lane; i < a.top * ctas; i += 32) {
       // an alternative's place: how many of every CTA's, which are in order, come before it
-      const u64 key = keys[slot][tid];
+      const u64 key = keys[slot][i];
       int ahead[kMaxCluster];
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) ahead[r] = 0;
@@ -346,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
       int place = 0;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) place += ahead[r];
-      if (bad ? tid < a.top : key != 0 && place < a.top) {
-        const int64_t to = last_row * a.top + (bad ? tid : place);
+      if (bad ? i < a.top : key != 0 && place < a.top) {
+        const int64_t to = last_row * a.top + (bad ? i : place);
         a.top_tokens[to] = bad ? -1 : (int32_t)(0xFFFFFFFFu - (uint32_t)key);
         a.top_logprobs[to] = bad ? NAN : value_of(key) - log_l;
       }
@@ -355,23 +379,31 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
   };
 
   int use = 0;                                 // copies of whole segments so far
-  if (segments == 1 && warp == 0) {
+  if (segments == 1 && warp == kWarps) {
     const View w = view(row0, 0);
     for (int p = 0; p < kPieces; ++p) start(w, p);
   }
   if (ctas > 1) cluster_wait();
   int it = 0;
+  auto logit_of = [&](int64_t row, int32_t token) {
+    return token >= 0 && token < a.vocab ? at<BF16>(all + row * a.ld * kSize, token) : 0.f;
+  };
+  int32_t next_token = a.tokens[row0];
+  float next_xt = logit_of(row0, next_token);
   for (int64_t row = row0; row < a.rows; row += clusters, ++it) {
-    const int32_t token = a.tokens[row];
+    // the next row's token and logit are fetched under this row's work
+    const int32_t token = next_token;
     const bool given = token >= 0 && token < a.vocab;
-    const float xt = given ? at<BF16>(all + row * a.ld * kSize, token) : 0.f;
+    const float xt = next_xt;
+    const bool more = row + clusters < a.rows;
+    if (more) next_token = a.tokens[row + clusters];
     // segment g, once everyone has read what was there; its phase
     View w = view(row, 0);
     auto load = [&](int g) {
       if (segments > 1) {
         __syncthreads();
         w = view(row, g);
-        if (warp == 0)
+        if (warp == kWarps)
           for (int p = 0; p < kPieces; ++p) start(w, p);
       }
       return (uint32_t)use++ & 1u;
@@ -396,26 +428,41 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
 #pragma unroll
     for (int r = 1; r < kMaxCluster; ++r)
       if (r < ctas) m = fmaxf(m, tops[it & 1][r]);
-    if (it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
+    if (warp == kWarps && it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
     const float zero = m == -INFINITY ? 0.f : m;
-    const float dt = given ? xt - zero : INFINITY;
-    const float dt_after = given ? after(dt) : INFINITY;            // d > dt is d >= dt_after
+    const float dt = given ? xt - zero : kHuge;
+    // Counting by step_of needs differences of 2^-127 or more, and tokens above the least
+    // number: other rows' ranks are counted one by one.
+    const bool odd_rank = given && (fabsf(zero) < 8.4703295e-22f || dt <= -kHuge);         // 2^-70
 
     float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, s2[2] = {l2[0], l2[0]};
-    int before = 0, have = 0;                  // have: alternatives found in earlier segments
+    float2 n2[2] = {l2[0], l2[0]};             // elements before the token
+    float before = 0.f;                        // and what they are off by
+    int have = 0, odd = 0;                     // alternatives found in earlier segments
     for (int g = 0; g < segments; ++g) {
       if (segments > 1) {                      // the share again
         parity = load(g);
         bound_of(largest(w, parity));
       }
+      if (g == 0 && more) next_xt = logit_of(row + clusters, next_token);
+      if (warp == kWarps) {
+        if (segments == 1 && more) {
+          const View next = view(row + clusters, 0);
+          for (int p = 0; p < kPieces; ++p) {
+            wait_for(empty + p, (uint32_t)it & 1u);         // all have read the piece
+            start(next, p);
+          }
+        }
+        continue;
+      }
       if (tid < have) list[tid] = best[tid];
       if (tid == 0) listed = have;
-      __syncthreads();
+      sync_workers();
       const float least = a.top > 0 ? bound - zero : INFINITY;
       // the token's slot of the image, or one before or behind all
       const int64_t far = token - w.base + w.skew;
       const int slot = far < 0 ? -1 : far < w.chunks * E ? (int)far : w.chunks * E;
-      const float2 shift = make_float2(-zero, -zero), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
+      const float2 shift = make_float2(-zero, -zero), token_at = make_float2(-dt, -dt), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
       // The rank by whole chunks before and behind the token: the slots of the chunk that
       // holds it and of those at the ends, some of them no tokens, are counted one by one,
       // one per lane, and what the loop below counts for them is taken off.
@@ -426,42 +473,41 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
           const int at_slot = c * E + lane % E;
           const bool in = (unsigned)(at_slot - w.skew) < (unsigned)w.n;
           const float d = (in ? at<BF16>(image, at_slot) : -INFINITY) - zero;
-          before += (in & ((d >= dt_after) | ((d == dt) & (at_slot < slot)))) - (int)(d >= (c * E < slot ? dt : dt_after));
+          const float ahead = step_of(max_nan(d, -kHuge) - dt, c * E < slot ? 1.f : 0.f);
+          before += (float)(in & ((d > dt) | ((d == dt) & (at_slot < slot)))) - ahead;
         }
-        __syncwarp(0xffffffffu >> (32 - 3 * E));
       }
-      const View next = view(row + clusters, 0);
-      const bool more = segments == 1 && row + clusters < a.rows;
 #pragma unroll 1
       for (int p = 0; p < kPieces; ++p) {
         each(w, p, [&](int c, auto& v) {
           constexpr int B = sizeof(v) / sizeof(v[0]);
-          float high = -INFINITY;
-          int ahead[B];
+          float high[B];
 #pragma unroll
           for (int b = 0; b < B; ++b) {
-            const float from = (c + b * kThreads) * E < slot ? dt : dt_after;
-            ahead[b] = 0;
+            const float equal = (c + b * kThreads) * E < slot ? 1.f : 0.f;
+            high[b] = -INFINITY;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
               float2 d = add2(make_float2(v[b][e], v[b][e + 1]), shift);
-              ahead[b] += d.x >= from;
-              ahead[b] += d.y >= from;
               v[b][e] = d.x;
               v[b][e + 1] = d.y;
-              high = fmaxf(high, fmaxf(d.x, d.y));
-              d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));   // -inf: no term, not 0 times itself
+              high[b] = fmaxf(high[b], fmaxf(d.x, d.y));
+              d = make_float2(max_nan(d.x, -kHuge), max_nan(d.y, -kHuge));   // -inf: no term, not 0 times itself
+              const float2 over = add2(d, token_at);
+              n2[b & 1] = add2(n2[b & 1], make_float2(step_of(over.x, equal), step_of(over.y, equal)));
               float2 y = mul2(d, log2e);
               y = make_float2(ex2(y.x), ex2(y.y));
               l2[b & 1] = add2(l2[b & 1], y);
               s2[b & 1] = fma2(y, d, s2[b & 1]);
             }
           }
+          float highest = high[0];
 #pragma unroll
-          for (int b = 0; b < B; ++b) before += ahead[b];
-          if (high >= least) {
+          for (int b = 1; b < B; ++b) highest = fmaxf(highest, high[b]);
+          if (highest >= least) {
 #pragma unroll
-            for (int b = 0; b < B; ++b)
+            for (int b = 0; b < B; ++b) {
+              if (high[b] < least) continue;
 #pragma unroll
               for (int e = 0; e < E; ++e) {
                 const int i = (c + b * kThreads) * E + e - w.skew;
@@ -470,20 +516,20 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
                   if (to < kRoom) list[to] = key_of(v[b][e], (uint32_t)(w.base + i));
                 }
               }
+            }
           }
         });
         __syncwarp();
         if (lane == 0) arrive(empty + p);
-        if (more && warp == 0 && p > 0) {      // the piece before, once all have read it
-          wait_for(empty + p - 1, (uint32_t)it & 1u);
-          start(next, p - 1);
+      }
+      if (odd_rank) {
+        const uint8_t* src = all + (row * a.ld + w.base) * kSize;
+        for (int j = tid; j < w.n; j += kThreads) {
+          const float d = at<BF16>(src, j) - zero;
+          odd += (d > dt) | ((d == dt) & (w.base + j < token));
         }
       }
-      if (more && warp == 0) {
-        wait_for(empty + kPieces - 1, (uint32_t)it & 1u);
-        start(next, kPieces - 1);
-      }
-      __syncthreads();
+      sync_workers();
       if (a.top > 0) {
         const int count = listed, k = (int)min((int64_t)a.top, (int64_t)have + w.n);
         if (count <= kByRank) {
@@ -514,36 +560,40 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
               top = y > top ? y : top;
             }
             if (lane == 0) round_best[warp] = top;
-            __syncthreads();
+            sync_workers();
             for (int q = 0; q < kWarps; ++q) top = round_best[q] > top ? round_best[q] : top;
-            __syncthreads();
+            sync_workers();
             last = top;
             if (tid == i) taken = top;
           }
           if (tid < k) best[tid] = taken;
         }
         have = k;
-        __syncthreads();
+        sync_workers();
       }
     }
 
     // sums over the CTA in a fixed order, to the one of the cluster whose turn it is
-    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), s = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-    before = __reduce_add_sync(0xffffffffu, before);
-    for (int o = 16; o; o >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (warp < kWarps) {
+      // (whole numbers: at most 2^20 of a thread's, and 2^24 in all)
+      int n = (int)((n2[0].x + n2[0].y) + (n2[1].x + n2[1].y) + before);
+      if (odd_rank) n = odd;
+      float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), s = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+      n = __reduce_add_sync(0xffffffffu, n);
+      for (int o = 16; o; o >>= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+      }
+      if (lane == 0) {
+        sums[warp][0] = l;
+        sums[warp][1] = s;
+        counts[warp] = n;
+      }
+      sync_workers();
     }
-    if (lane == 0) {
-      sums[warp][0] = l;
-      sums[warp][1] = s;
-      counts[warp] = before;
-    }
-    __syncthreads();
     if (warp == 0) {
-      l = lane < kWarps ? sums[lane][0] : 0.f;
-      s = lane < kWarps ? sums[lane][1] : 0.f;
-      before = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[lane] : 0);
+      float l = lane < kWarps ? sums[lane][0] : 0.f, s = lane < kWarps ? sums[lane][1] : 0.f;
+      const int n = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[lane] : 0);
       for (int o = kWarps / 2; o; o >>= 1) {
         l += __shfl_xor_sync(0xffffffffu, l, o);
         s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -555,11 +605,11 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
           const uint32_t to = peer(&found[it & 1][rank], turn);
           put(to, l);
           put(to + 4, s);
-          put(to + 8, __int_as_float(before));
+          put(to + 8, __int_as_float(n));
         }
         if (lane < a.top) put(peer(&keys[it & 1][rank * a.top + lane], turn), key);
       } else {
-        if (lane == 0) found[it & 1][0] = make_float4(l, s, __int_as_float(before), 0.f);
+        if (lane == 0) found[it & 1][0] = make_float4(l, s, __int_as_float(n), 0.f);
         if (lane < a.top) keys[it & 1][lane] = key;
       }
     }
@@ -574,7 +624,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
   } else {
     __syncthreads();
   }
-  if (it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
+  if (warp == kWarps && it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
   if (tid == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 
@@ -629,5 +679,5 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   int per_sm = (228 * 1024) / (smem + 16 * 1024);
   per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
   const int64_t resident = (int64_t)sms * per_sm / ctas, clusters = rows < resident ? rows : resident;
-  return serve::launch(kernel, (unsigned)(clusters * ctas), score::kThreads, smem, stream, a, (unsigned)ctas);
+  return serve::launch(kernel, (unsigned)(clusters * ctas), score::kThreads + 32, smem, stream, a, (unsigned)ctas);
 }

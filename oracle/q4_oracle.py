@@ -90,13 +90,15 @@ def token_logprobs(logits, tokens, top):
     top_logprobs = np.zeros((n, top))
     for i in range(n):
         x = np.asarray(logits[i], dtype=np.float64)
-        m = x.max()
-        lse = m + math.log(np.exp(x - m).sum()) if m > -math.inf else 0.0
+        m = x.max() if x.max() > -math.inf else 0.0
+        with np.errstate(over="ignore"):
+            d = x.astype(np.float32) - np.float32(m)
+        order = sorted(range(vocab), key=lambda v: (-d[v], v))
+        x = x - m                          # (a sum with m itself would lose a small logarithm beside a large m)
+        total = np.exp(x).sum()
+        lse = math.log(total) if total > 0 else 0.0
         p = np.exp(x - lse)
         entropy[i] = -sum(float(a) * float(b - lse) for a, b in zip(p, x) if a > 0)
-        with np.errstate(over="ignore"):
-            d = x.astype(np.float32) - np.float32(m if m > -math.inf else 0.0)
-        order = sorted(range(vocab), key=lambda v: (-d[v], v))
         top_tokens[i] = order[:top]
         top_logprobs[i] = x[order[:top]] - lse
         t = int(tokens[i])

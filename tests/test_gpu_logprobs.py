@@ -154,6 +154,27 @@ def test_masked_tokens(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [90, 30001])
+def test_ranks_at_the_ends_of_the_range(dtype, vocab):
+    """Masks of the type's lowest value beside -inf, logits all within 2^-100 of one another, a largest logit of 0."""
+    torch, L = cuda()
+    rng = np.random.default_rng(vocab)
+    x = rows(torch, rng, 5, vocab, dtype)
+    low = torch.finfo(x.dtype).min
+    x[0, ::2], x[0, 1::3] = -float("inf"), low
+    x[1, 1:] = low
+    x[2] *= 2.0 ** -104
+    x[3] = -x[3].abs()
+    x[3, 7] = 0
+    x[4, :] = low
+    x[4, 5] = -float("inf")
+    for tokens in ([4, 3, 8, 7, 5], [7, 9, 50, 60, 6], [1, 0, 11, 12, 0]):
+        got, st = call(torch, L, x, tokens, 3)
+        assert st == 0
+        check(got, x.float().cpu().numpy(), tokens, 3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("where", [0, 777, 20000])
 def test_non_finite_logits_stay_in_their_row(dtype, bad, where):

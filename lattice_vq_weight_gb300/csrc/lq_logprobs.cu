@@ -13,10 +13,12 @@
 // one SM's shared memory or there are few rows, copies its share of a row to shared
 // memory in four pieces (untiled bulk copies) and takes maxima as they arrive; the
 // CTAs agree on the row's maximum, and everything else, whose terms hang on it, comes
-// from shared memory: about 11 instructions an element for the exponentials, sums and
-// the rank's comparison.  CTAs stay for row after row: as soon as a piece has been read
-// for the last time, the same piece of the next row is copied over it, so that the
-// loads run under the exponentials.  A cluster waits for itself once per row: the
+// from shared memory: 7 to 8 instructions an element for the exponential, the sums and
+// the rank's comparison (by saturating products: as compare and count it was the pipe of
+// compares and integers that bound the kernel, 135 us for 2047 rows of 50001 to 106).
+// CTAs stay for row after row: as soon as a piece has been read for the last time, a warp
+// of its own copies the same piece of the next row over it, so that the loads run under
+// the exponentials, and finishes the row before.  A cluster waits for itself once per row: the
 // maxima of a row and the results of the row before cross together, and a row's results
 // are put together by its CTAs in turn.  Sums go through fixed trees: equal calls give
 // equal bits.
@@ -42,10 +44,7 @@ namespace score {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;               // and a warp that copies and finishes rows
 constexpr int kMaxTop = LQ_MAX_ALTERNATIVES, kMaxCluster = 8;
-#ifndef PCS
-#define PCS 6
-#endif
-constexpr int kPieces = PCS;                   // of a share
+constexpr int kPieces = 4;                   // of a share
 constexpr int kRoom = 512;                     // candidates that are listed
 constexpr int kByRank = 256;                   // and ordered by counting
 constexpr int kMostBytes = 208 * 1024;         // of a share in shared memory at once
@@ -119,8 +118,10 @@ __device__ __forceinline__ float step_of(float x, float k) {
   return y;
 }
 
-// Barrier of the warps that compute.
+// Barrier of the warps that compute, and one that the last warp comes to without waiting.
 __device__ __forceinline__ void sync_workers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void sync_listed() { asm volatile("bar.sync 2, %0;" ::"n"(kThreads + 32) : "memory"); }
+__device__ __forceinline__ void arrive_listed() { asm volatile("bar.arrive 2, %0;" ::"n"(kThreads + 32) : "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -164,14 +165,14 @@ struct View {
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_constant__ Args a) {
   constexpr int E = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4;
   extern __shared__ __align__(16) uint8_t image_bytes[];
   uint4* image = reinterpret_cast<uint4*>(image_bytes);
   __shared__ uint64_t full[kPieces], empty[kPieces];
-  __shared__ float maxima[kWarps][32];
-  __shared__ float sums[kWarps][2];
-  __shared__ int counts[kWarps];
+  __shared__ float maxima[kWarps + 1][32];
+  __shared__ float sums[kWarps + 1][2];
+  __shared__ int counts[kWarps + 1];
   __shared__ float tops[2][kMaxCluster];       // the CTAs' maxima, of this row and the next
   __shared__ float bound;                      // of the candidates, a logit
   __shared__ int listed, timeout;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
       mbar_init1(empty + p, kWarps);
     }
     mbar_init_fence();
-    timeout = 0;
+    timeout = listed = 0;
   }
   if (ctas > 1) cluster_arrive();              // the others' shared memory is there once all have come here
   pdl_wait();
@@ -239,52 +240,49 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
     if (!mbar_wait_bounded(bar, parity, kWaitCycles)) timeout = 1;
   };
-  // Runs f(c, values) over this thread's chunks of piece p, several at a time: the values
-  // of chunks c, c + kThreads, ..., -inf for slots that are not the row's (edges: there
-  // may be such ones).
-  auto some = [&](const View& w, int c, auto edges, auto batch, auto& f) {
-    constexpr int B = decltype(batch)::value;
-    uint4 u[B];
-    float v[B][E];
-#pragma unroll
-    for (int b = 0; b < B; ++b) u[b] = image[c + b * kThreads];
-#pragma unroll
-    for (int b = 0; b < B; ++b) unpack<BF16>(u[b], v[b]);
-    if constexpr (decltype(edges)::value) {
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const int from = (c + b * kThreads) * E - w.skew;
-        if (from < 0 || from + E > w.n) {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if ((unsigned)(from + e) >= (unsigned)w.n) v[b][e] = -INFINITY;
-        }
-      }
-    }
-    f(c, v);
-  };
-  auto piece = [&](const View& w, int p, auto edges, auto& f) {
-    constexpr int B = BF16 ? 2 : 4;
-    const int c1 = min(w.chunks, (p + 1) * a.per_piece);
-    int c = p * a.per_piece + tid;
-#pragma unroll 1
-    for (; c + (B - 1) * kThreads < c1; c += B * kThreads) some(w, c, edges, Int<B>(), f);
-    if constexpr (B > 2) {
-      if (c + kThreads < c1) {
-        some(w, c, edges, Int<2>(), f);
-        c += 2 * kThreads;
-      }
-    }
-    if (c < c1) some(w, c, edges, Int<1>(), f);
-  };
+  // Runs f(c, values of chunks c, c + kThreads, ...) over this thread's chunks of piece p,
+  // several at a time, whole warps together (chunks past the piece: -inf).  The share's
+  // first and last chunk, some of whose slots may not be the row's, are left out: the last
+  // warp looks after them.
   auto each = [&](const View& w, int p, auto f) {
-    if (p == 0 || (p + 1) * a.per_piece >= w.chunks) piece(w, p, Int<1>(), f);
-    else piece(w, p, Int<0>(), f);
+    constexpr int B = BF16 ? 2 : 4;
+    const int c1 = min(w.chunks - 1, (p + 1) * a.per_piece);
+    int c = max(1, p * a.per_piece) + warp * 32;            // lane 0's
+#pragma unroll 1
+    for (; c + 31 + (B - 1) * kThreads < c1; c += B * kThreads) {
+      uint4 u[B];
+      float v[B][E];
+#pragma unroll
+      for (int b = 0; b < B; ++b) u[b] = image[c + lane + b * kThreads];
+#pragma unroll
+      for (int b = 0; b < B; ++b) unpack<BF16>(u[b], v[b]);
+      f(c, v);
+    }
+    constexpr uint32_t none = BF16 ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll 1
+    for (; c < c1; c += kThreads) {
+      uint4 u = make_uint4(none, none, none, none);
+      if (c + lane < c1) u = image[c + lane];
+      float v[1][E];
+      unpack<BF16>(u, v[0]);
+      f(c, v);
+    }
+  };
+  // The slot of the first or last chunk that a lane of the last warp looks after, -1 if
+  // none: E lanes for each.
+  auto edge_slot = [&](const View& w) {
+    const int c = lane < E ? 0 : w.chunks - 1, slot = c * E + (lane & (E - 1));
+    const bool mine = lane < 2 * E && w.chunks > 0 && (lane < E || c > 0);
+    return mine && (unsigned)(slot - w.skew) < (unsigned)w.n ? slot : -1;
   };
   // The largest logit of this thread's chunks, as they arrive.
   auto largest = [&](const View& w, uint32_t parity) {
     float m = -INFINITY;
-    if (warp == kWarps) return m;
+    if (warp == kWarps) {
+      for (int p = 0; p < kPieces; ++p) wait_for(full + p, parity);
+      const int slot = edge_slot(w);
+      return slot >= 0 ? at<BF16>(image, slot) : m;
+    }
 #pragma unroll 1
     for (int p = 0; p < kPieces; ++p) {
       wait_for(full + p, parity);
@@ -305,13 +303,12 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
   };
   // From the threads' maxima the CTA's (in warp 0), and the bound under its candidates.
   auto bound_of = [&](float mine) {
-    if (warp == kWarps) return mine;
     maxima[warp][lane] = mine;
-    sync_workers();
+    __syncthreads();
     float m = -INFINITY;
     if (warp == 0) {
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q) m = fmaxf(m, maxima[q][lane]);
+      for (int q = 0; q <= kWarps; ++q) m = fmaxf(m, maxima[q][lane]);
       int ahead = 0;                           // lanes whose maximum comes before this one's
       if (a.top > 1) {
 #pragma unroll
@@ -445,7 +442,34 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
         bound_of(largest(w, parity));
       }
       if (g == 0 && more) next_xt = logit_of(row + clusters, next_token);
+      if (segments > 1) __syncthreads();       // the bound
+      const float least = a.top > 0 ? bound - zero : INFINITY;
+      // the token's slot of the image, or one before or behind all
+      const int64_t far = token - w.base + w.skew;
+      const int slot = far < 0 ? -1 : far < w.chunks * E ? (int)far : w.chunks * E;
+      auto note = [&](float d, int at_slot) {  // a candidate
+        const int to = atomicAdd(&listed, 1);
+        if (to < kRoom) list[to] = key_of(d, (uint32_t)(w.base + at_slot - w.skew));
+      };
       if (warp == kWarps) {
+        // The chunks at the ends, a slot per lane; and the rank by whole chunks before and
+        // behind the token, which the workers count, is not that of the slots of the chunk
+        // that holds it: they are counted one by one, what the workers count taken off.
+        const int edge = edge_slot(w), c = slot / E;
+        if (edge >= 0) {
+          const float d = at<BF16>(image, edge) - zero, dc = max_nan(d, -kHuge), y = ex2(dc * 1.4426950408889634f);
+          l2[0].x += y;
+          s2[0].x = fmaf(y, dc, s2[0].x);
+          before += (float)((d > dt) | ((d == dt) & (edge < slot)));
+          if (d >= least) note(d, edge);
+        }
+        if (slot >= 0 && c > 0 && c < w.chunks - 1 && lane < E) {
+          const float d = at<BF16>(image, c * E + lane) - zero;
+          before += (float)((d > dt) | ((d == dt) & (c * E + lane < slot)));
+          before -= step_of(max_nan(d, -kHuge) - dt, c * E < slot ? 1.f : 0.f);
+        }
+        __syncwarp();
+        arrive_listed();
         if (segments == 1 && more) {
           const View next = view(row + clusters, 0);
           for (int p = 0; p < kPieces; ++p) {
@@ -455,43 +479,20 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
         }
         continue;
       }
-      if (tid < have) list[tid] = best[tid];
-      if (tid == 0) listed = have;
-      sync_workers();
-      const float least = a.top > 0 ? bound - zero : INFINITY;
-      // the token's slot of the image, or one before or behind all
-      const int64_t far = token - w.base + w.skew;
-      const int slot = far < 0 ? -1 : far < w.chunks * E ? (int)far : w.chunks * E;
       const float2 shift = make_float2(-zero, -zero), token_at = make_float2(-dt, -dt), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
-      // The rank by whole chunks before and behind the token: the slots of the chunk that
-      // holds it and of those at the ends, some of them no tokens, are counted one by one,
-      // one per lane, and what the loop below counts for them is taken off.
-      if (warp == kWarps - 1 && lane < 3 * E && w.chunks > 0) {
-        const int which = lane / E, c = which == 0 ? 0 : which == 1 ? w.chunks - 1 : slot / E;
-        // each of them once
-        if (which == 0 || (which == 1 && c > 0) || (which == 2 && slot >= 0 && c > 0 && c < w.chunks - 1)) {
-          const int at_slot = c * E + lane % E;
-          const bool in = (unsigned)(at_slot - w.skew) < (unsigned)w.n;
-          const float d = (in ? at<BF16>(image, at_slot) : -INFINITY) - zero;
-          const float ahead = step_of(max_nan(d, -kHuge) - dt, c * E < slot ? 1.f : 0.f);
-          before += (float)(in & ((d > dt) | ((d == dt) & (at_slot < slot)))) - ahead;
-        }
-      }
 #pragma unroll 1
       for (int p = 0; p < kPieces; ++p) {
+        const int c1 = min(w.chunks - 1, (p + 1) * a.per_piece);
         each(w, p, [&](int c, auto& v) {
           constexpr int B = sizeof(v) / sizeof(v[0]);
-          float high[B];
+          float high = -INFINITY;
 #pragma unroll
           for (int b = 0; b < B; ++b) {
-            const float equal = (c + b * kThreads) * E < slot ? 1.f : 0.f;
-            high[b] = -INFINITY;
+            const float equal = (c + lane + b * kThreads) * E < slot ? 1.f : 0.f;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
               float2 d = add2(make_float2(v[b][e], v[b][e + 1]), shift);
-              v[b][e] = d.x;
-              v[b][e + 1] = d.y;
-              high[b] = fmaxf(high[b], fmaxf(d.x, d.y));
+              high = fmaxf(high, fmaxf(d.x, d.y));
               d = make_float2(max_nan(d.x, -kHuge), max_nan(d.y, -kHuge));   // -inf: no term, not 0 times itself
               const float2 over = add2(d, token_at);
               n2[b & 1] = add2(n2[b & 1], make_float2(step_of(over.x, equal), step_of(over.y, equal)));
@@ -501,21 +502,12 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
               s2[b & 1] = fma2(y, d, s2[b & 1]);
             }
           }
-          float highest = high[0];
-#pragma unroll
-          for (int b = 1; b < B; ++b) highest = fmaxf(highest, high[b]);
-          if (highest >= least) {
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-              if (high[b] < least) continue;
-#pragma unroll
-              for (int e = 0; e < E; ++e) {
-                const int i = (c + b * kThreads) * E + e - w.skew;
-                if (v[b][e] >= least && (unsigned)i < (unsigned)w.n) {
-                  const int to = atomicAdd(&listed, 1);
-                  if (to < kRoom) list[to] = key_of(v[b][e], (uint32_t)(w.base + i));
-                }
-              }
+          // lanes with candidates, seldom: the warp looks at one's slots together
+          for (uint32_t hit = __ballot_sync(0xffffffffu, high >= least); hit; hit &= hit - 1) {
+            const int chunk = c + __ffs(hit) - 1 + lane / E * kThreads, to = chunk * E + lane % E;
+            if (lane < B * E && chunk < c1) {
+              const float d = at<BF16>(image, to) - zero;
+              if (d >= least) note(d, to);
             }
           }
         });
@@ -529,7 +521,7 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
           odd += (d > dt) | ((d == dt) & (w.base + j < token));
         }
       }
-      sync_workers();
+      sync_listed();
       if (a.top > 0) {
         const int count = listed, k = (int)min((int64_t)a.top, (int64_t)have + w.n);
         if (count <= kByRank) {
@@ -570,11 +562,15 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
         }
         have = k;
         sync_workers();
+        // the next list begins with these, if it is one of the same row
+        const int keep = g + 1 < segments ? have : 0;
+        if (tid < keep) list[tid] = best[tid];
+        if (tid == 0) listed = keep;
       }
     }
 
     // sums over the CTA in a fixed order, to the one of the cluster whose turn it is
-    if (warp < kWarps) {
+    {
       // (whole numbers: at most 2^20 of a thread's, and 2^24 in all)
       int n = (int)((n2[0].x + n2[0].y) + (n2[1].x + n2[1].y) + before);
       if (odd_rank) n = odd;
@@ -589,12 +585,12 @@ __global__ void __launch_bounds__(kThreads + 32) score_kernel(const __grid_const
         sums[warp][1] = s;
         counts[warp] = n;
       }
-      sync_workers();
+      __syncthreads();
     }
     if (warp == 0) {
-      float l = lane < kWarps ? sums[lane][0] : 0.f, s = lane < kWarps ? sums[lane][1] : 0.f;
-      const int n = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[lane] : 0);
-      for (int o = kWarps / 2; o; o >>= 1) {
+      float l = lane <= kWarps ? sums[lane][0] : 0.f, s = lane <= kWarps ? sums[lane][1] : 0.f;
+      const int n = __reduce_add_sync(0xffffffffu, lane <= kWarps ? counts[lane] : 0);
+      for (int o = 16; o; o >>= 1) {
         l += __shfl_xor_sync(0xffffffffu, l, o);
         s += __shfl_xor_sync(0xffffffffu, s, o);
       }
@@ -668,7 +664,10 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   const int64_t most = (score::kMostBytes - 32) / esize;
   a.segment = (int)(a.share < most ? a.share : most);
   const int chunks = ((int)(a.segment * esize) + 15) / 16 + 1;       // those at both ends may be partial
+  // pieces of whole batches: chunks one at a time take twice as long
+  const int unit = score::kThreads * (dtype == LQ_BF16 ? 2 : 4);
   a.per_piece = (chunks + score::kPieces - 1) / score::kPieces;
+  if (a.per_piece > unit / 2) a.per_piece = (a.per_piece + unit - 1) / unit * unit;
   const int smem = chunks * 16;
   const auto kernel = dtype == LQ_BF16 ? score::score_kernel<true> : score::score_kernel<false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kMostBytes) != cudaSuccess) {

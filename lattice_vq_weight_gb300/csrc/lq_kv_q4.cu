@@ -29,92 +29,136 @@ struct AppendArgs {
   uint32_t* scales[2];       // (scale, base) pairs
   const int64_t* slots;
   int64_t tokens, slots_in_cache;
-  int kv_heads, dim, log2_bs, log2_group;
+  int kv_heads, log2_dim, log2_bs, log2_group;
   int32_t* status;
 };
 
+// Eight values as they are in memory: 16 bytes, or 32.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if constexpr (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+  uint4 w[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load8(const void* p, int64_t i) {
+  Raw<BF16> r;
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
+  r.w[0] = q[0];
+  if constexpr (!BF16) r.w[1] = q[1];
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Raw<BF16>& r, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < (BF16 ? 1 : 2); ++k) {
+    const uint32_t u[4] = {r.w[k].x, r.w[k].y, r.w[k].z, r.w[k].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(u[e] << 16);
-      v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      if constexpr (BF16) {
+        v[2 * e] = __uint_as_float(u[e] << 16);
+        v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      } else {
+        v[4 * k + e] = __uint_as_float(u[e]);
+      }
     }
+  }
+}
+// Whether one of them is beyond kMost or not a number, by the order of the bits.
+template <bool BF16>
+__device__ __forceinline__ bool beyond(const Raw<BF16>& r) {
+  if constexpr (BF16) {
+    const uint32_t m = 0x7FFF7FFFu, top = __vmaxu2(__vimax3_u16x2(r.w[0].x & m, r.w[0].y & m, r.w[0].z & m), r.w[0].w & m);
+    return max(top >> 16, top & 0xFFFFu) > (__float_as_uint(kMost) >> 16);
   } else {
-    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const uint32_t m = 0x7FFFFFFFu;
+    const uint32_t top = max(__vimax3_u32(__vimax3_u32(r.w[0].x & m, r.w[0].y & m, r.w[0].z & m), r.w[0].w & m, r.w[1].x & m),
+                             __vimax3_u32(r.w[1].y & m, r.w[1].z & m, r.w[1].w & m));
+    return top > __float_as_uint(kMost);
   }
 }
 
-// A warp per token and cache, eight values per lane and step: a lane's codes are
-// one word, a group G / 8 neighbouring lanes.
+// A warp per token and cache, eight values per lane and step: a lane's codes are one
+// word, a group G / 8 neighbouring lanes.  The loads of kUnroll steps are in flight at
+// once (one after the other, the write and read-back of 13 944 tokens took 76 us).
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+  constexpr int kUnroll = BF16 ? 4 : 2;
   pdl_wait();
   pdl_launch();
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int words = a.dim / 8, per_row = a.kv_heads * words, span = 1 << (a.log2_group - 3);
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < 2 * a.tokens; u += warps) {
-    const int64_t t = u >> 1, slot = a.slots[t];
+  const int log2_words = a.log2_dim - 3, log2_span = a.log2_group - 3, span = 1 << log2_span;
+  const int per_row = a.kv_heads << log2_words;
+  int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  int64_t slot = u < 2 * a.tokens ? a.slots[u >> 1] : -1;
+  for (; u < 2 * a.tokens; u += warps) {
+    const int64_t t = u >> 1, here = slot;
     const int which = (int)(u & 1);
-    if (slot < 0) continue;
-    if (slot >= a.slots_in_cache) {
+    slot = u + warps < 2 * a.tokens ? a.slots[(u + warps) >> 1] : -1;
+    if (here < 0) continue;
+    if (here >= a.slots_in_cache) {
       if (lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
       continue;
     }
-    const int64_t first = ((slot >> a.log2_bs) * a.kv_heads << a.log2_bs) + (slot & ((1 << a.log2_bs) - 1));
-    for (int c0 = 0; c0 < per_row; c0 += 32) {
-      const int c = c0 + lane;
-      const bool in = c < per_row;
-      float v[8];
+    const int64_t first = ((here >> a.log2_bs) * a.kv_heads << a.log2_bs) + (here & ((1 << a.log2_bs) - 1));
+    const void* x = which ? a.x[1] : a.x[0];
+    const int64_t row = t * (which ? a.ld[1] : a.ld[0]);
+    uint32_t* codes = which ? a.codes[1] : a.codes[0];
+    uint32_t* scales = which ? a.scales[1] : a.scales[0];
+    for (int c0 = lane; c0 - lane < per_row; c0 += 32 * kUnroll) {
+      Raw<BF16> raw[kUnroll];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      if (in) load8<BF16>(a.x[which], t * a.ld[which] + 8 * c, v);
-      float low = INFINITY, high = -INFINITY;
-      bool odd = false, far = false;
+      for (int i = 0; i < kUnroll; ++i) {
+        raw[i].w[0] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (!BF16) raw[i].w[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (c0 + 32 * i < per_row) raw[i] = load8<BF16>(x, row + 8 * (c0 + 32 * i));
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (!(fabsf(v[e]) <= kMost)) {
-          if (fabsf(v[e]) < INFINITY) {
-            far = true;
-            v[e] = copysignf(kMost, v[e]);
-          } else {
-            odd = true;
-            v[e] = 0.f;
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + 32 * i;
+        if (c - lane >= per_row) break;
+        float v[8];
+        unpack8<BF16>(raw[i], v);
+        if (beyond<BF16>(raw[i])) {            // seldom
+          for (int e = 0; e < 8; ++e) {
+            if (fabsf(v[e]) < INFINITY) {
+              if (fabsf(v[e]) > kMost) raise_flag(a.status, LQ_DEV_RANGE);
+              v[e] = fminf(fmaxf(v[e], -kMost), kMost);
+            } else {
+              raise_flag(a.status, LQ_DEV_NONFINITE);
+              v[e] = 0.f;
+            }
           }
         }
-        low = fminf(low, v[e]);
-        high = fmaxf(high, v[e]);
-      }
-      if (odd) raise_flag(a.status, LQ_DEV_NONFINITE);
-      if (far) raise_flag(a.status, LQ_DEV_RANGE);
-      for (int o = 1; o < span; o <<= 1) {
-        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-      }
-      const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(high, low), 15.f));
-      const float sf = __half2float(s);
-      const __half b = __float2half_rn(__fsub_rn(low, 16.f * sf));
-      const float bf = __half2float(b), r = sf > 0.f ? __frcp_rn(sf) : 0.f;
-      uint32_t word = 0;
+        float low = fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
+        float high = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+        for (int o = 1; o < span; o <<= 1) {
+          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+          high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        }
+        const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(high, low), 15.f));
+        const float sf = __half2float(s);
+        const __half b = __float2half_rn(__fsub_rn(low, 16.f * sf));
+        const float bf = __half2float(b), r = sf > 0.f ? __frcp_rn(sf) : 0.f;
+        // (x - b) r cut to 16 .. 31 and rounded: added to 1.5 2^23 its low four bits are the
+        // code (where s is 0 it is 0, and cut to 16)
+        const float2 minus = make_float2(-bf, -bf), r2 = make_float2(r, r), magic = make_float2(12582912.f, 12582912.f);
+        uint32_t word = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float q = rintf(__fmul_rn(__fsub_rn(v[e], bf), r)) - 16.f;
-        word |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (4 * e);
-      }
-      if (in) {
-        const int h = c / words, w = c - h * words;
-        const int64_t row = first + ((int64_t)h << a.log2_bs);
-        a.codes[which][row * words + w] = word;
-        if ((w & (span - 1)) == 0)
-          a.scales[which][row * (words / span) + w / span] =
-              (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(b) << 16;
+        for (int e = 0; e < 8; e += 2) {
+          float2 q = mul2(add2(make_float2(v[e], v[e + 1]), minus), r2);
+          q = make_float2(fminf(fmaxf(q.x, 16.f), 31.f), fminf(fmaxf(q.y, 16.f), 31.f));
+          q = add2(q, magic);
+          word |= (__float_as_uint(q.x) & 15u) << (4 * e);
+          word |= (__float_as_uint(q.y) & 15u) << (4 * e + 4);
+        }
+        if (c < per_row) {
+          const int h = c >> log2_words, w = c & ((1 << log2_words) - 1);
+          const int64_t at = first + ((int64_t)h << a.log2_bs);
+          codes[(at << log2_words) + w] = word;
+          if ((w & (span - 1)) == 0)
+            scales[(at << (log2_words - log2_span)) + (w >> log2_span)] =
+                (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(b) << 16;
+        }
       }
     }
   }
@@ -126,46 +170,63 @@ struct GatherArgs {
   const uint32_t* scales[2];
   void* out[2];
   int64_t n, slots_in_cache;
-  int kv_heads, dim, log2_bs, log2_group;
+  int kv_heads, log2_dim, log2_bs, log2_group;
   int32_t* status;
 };
 
-// A warp per slot and cache, a word of codes per lane and step.
+// A warp per slot and cache, 16 bytes of output per lane and step: a word of codes for
+// bf16, half of one for fp32; the loads of kUnroll steps in flight at once.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) gather_kernel(GatherArgs a) {
+  constexpr int kUnroll = 4;
   pdl_wait();
   pdl_launch();
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int words = a.dim / 8, per_row = a.kv_heads * words, span = 1 << (a.log2_group - 3);
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < 2 * a.n; u += warps) {
-    const int64_t slot = a.slots[u >> 1];
+  // steps of a vector: 8 or 4 values each
+  const int log2_steps = a.log2_dim - (BF16 ? 3 : 2), log2_words = a.log2_dim - 3;
+  const int log2_groups = a.log2_dim - a.log2_group, per_row = a.kv_heads << log2_steps;
+  int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  int64_t next = u < 2 * a.n ? a.slots[u >> 1] : -1;
+  for (; u < 2 * a.n; u += warps) {
+    const int64_t slot = next;
     const int which = (int)(u & 1);
+    next = u + warps < 2 * a.n ? a.slots[(u + warps) >> 1] : -1;
     const bool ok = slot >= 0 && slot < a.slots_in_cache;
     if (slot >= a.slots_in_cache && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
     const int64_t first = ((slot >> a.log2_bs) * a.kv_heads << a.log2_bs) + (slot & ((1 << a.log2_bs) - 1));
-    for (int c = lane; c < per_row; c += 32) {
-      float v[8];
+    const uint32_t* codes = which ? a.codes[1] : a.codes[0];
+    const uint32_t* scales = which ? a.scales[1] : a.scales[0];
+    uint4* out = reinterpret_cast<uint4*>(which ? a.out[1] : a.out[0]) + (u >> 1) * per_row;
+    for (int c0 = lane; c0 < per_row; c0 += 32 * kUnroll) {
+      uint32_t word[kUnroll], pr[kUnroll];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      if (ok) {
-        const int h = c / words, w = c - h * words;
-        const int64_t row = first + ((int64_t)h << a.log2_bs);
-        values8(a.codes[which][row * words + w], a.scales[which][row * (words / span) + w / span], v);
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + 32 * i, h = c >> log2_steps, k = c & ((1 << log2_steps) - 1);
+        word[i] = pr[i] = 0u;                  // scale and base 0: zeros
+        if (ok && c < per_row) {
+          const int64_t at = first + ((int64_t)h << a.log2_bs);
+          word[i] = codes[(at << log2_words) + (BF16 ? k : k >> 1)];
+          pr[i] = scales[(at << log2_groups) + (k >> (log2_steps - log2_groups))];
+        }
       }
-      const int64_t at = (u >> 1) * per_row + c;
-      if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + 32 * i;
+        if (c >= per_row) break;
+        float v[8];
+        values8(word[i], pr[i], v);
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-          o[e] = *reinterpret_cast<const uint32_t*>(&p);
+          if constexpr (BF16) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            o[e] = *reinterpret_cast<const uint32_t*>(&p);
+          } else {
+            o[e] = __float_as_uint(c & 1 ? v[e + 4] : v[e]);
+          }
         }
-        reinterpret_cast<uint4*>(a.out[which])[at] = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        float4* out = reinterpret_cast<float4*>(a.out[which]) + 2 * at;
-        out[0] = make_float4(v[0], v[1], v[2], v[3]);
-        out[1] = make_float4(v[4], v[5], v[6], v[7]);
+        out[c] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -215,7 +276,7 @@ extern "C" lq_status lq_kv_append_q4(const void* k_dev, int64_t ldk, const void*
   a.codes[0] = reinterpret_cast<uint32_t*>(k_cache_dev); a.codes[1] = reinterpret_cast<uint32_t*>(v_cache_dev);
   a.scales[0] = reinterpret_cast<uint32_t*>(k_scales_dev); a.scales[1] = reinterpret_cast<uint32_t*>(v_scales_dev);
   a.slots = slots_dev; a.tokens = tokens; a.slots_in_cache = num_blocks * block_size;
-  a.kv_heads = kv_heads; a.dim = head_dim; a.log2_bs = serve::log2_of(block_size);
+  a.kv_heads = kv_heads; a.log2_dim = serve::log2_of(head_dim); a.log2_bs = serve::log2_of(block_size);
   a.log2_group = serve::log2_of(group_size); a.status = dev_status_dev;
   int64_t grid = (2 * tokens + 7) / 8;
   if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
@@ -247,7 +308,7 @@ extern "C" lq_status lq_kv_gather_q4(const int64_t* slots_dev, int64_t n, const 
   a.scales[0] = reinterpret_cast<const uint32_t*>(k_scales_dev);
   a.scales[1] = reinterpret_cast<const uint32_t*>(v_scales_dev);
   a.out[0] = k_out_dev; a.out[1] = v_out_dev; a.n = n; a.slots_in_cache = num_blocks * block_size;
-  a.kv_heads = kv_heads; a.dim = head_dim; a.log2_bs = serve::log2_of(block_size);
+  a.kv_heads = kv_heads; a.log2_dim = serve::log2_of(head_dim); a.log2_bs = serve::log2_of(block_size);
   a.log2_group = serve::log2_of(group_size); a.status = dev_status_dev;
   int64_t grid = (2 * n + 7) / 8;
   if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;

@@ -79,14 +79,14 @@ __device__ __forceinline__ bool beyond(const Raw<BF16>& r) {
 // A warp per token and cache, eight values per lane and step: a lane's codes are one
 // word, a group G / 8 neighbouring lanes.  The loads of kUnroll steps are in flight at
 // once (one after the other, the write and read-back of 13 944 tokens took 76 us).
-template <bool BF16>
+template <bool BF16, int GROUP>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
-  constexpr int kUnroll = BF16 ? 4 : 2;
+  constexpr int kUnroll = BF16 ? 4 : 2, span = GROUP / 8, log2_span = span == 4 ? 2 : span == 8 ? 3 : 4;
   pdl_wait();
   pdl_launch();
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int log2_words = a.log2_dim - 3, log2_span = a.log2_group - 3, span = 1 << log2_span;
+  const int log2_words = a.log2_dim - 3;
   const int per_row = a.kv_heads << log2_words;
   int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   int64_t slot = u < 2 * a.tokens ? a.slots[u >> 1] : -1;
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     const int64_t first = ((here >> a.log2_bs) * a.kv_heads << a.log2_bs) + (here & ((1 << a.log2_bs) - 1));
     const void* x = which ? a.x[1] : a.x[0];
     const int64_t row = t * (which ? a.ld[1] : a.ld[0]);
-    uint32_t* codes = which ? a.codes[1] : a.codes[0];
-    uint32_t* scales = which ? a.scales[1] : a.scales[0];
+    uint32_t* codes = (which ? a.codes[1] : a.codes[0]) + (first << log2_words);
+    uint32_t* scales = (which ? a.scales[1] : a.scales[0]) + (first << (log2_words - log2_span));
     for (int c0 = lane; c0 - lane < per_row; c0 += 32 * kUnroll) {
       Raw<BF16> raw[kUnroll];
 #pragma unroll
@@ -131,32 +131,42 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
         }
         float low = fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
         float high = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-        for (int o = 1; o < span; o <<= 1) {
-          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-          high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        if constexpr (BF16) {
+          // (bf16 numbers both: they cross together)
+          __nv_bfloat162 both = __floats2bfloat162_rn(low, -high);
+#pragma unroll
+          for (int o = 1; o < span; o <<= 1) both = __hmin2(both, __shfl_xor_sync(0xffffffffu, both, o));
+          low = __low2float(both);
+          high = -__high2float(both);
+        } else {
+#pragma unroll
+          for (int o = 1; o < span; o <<= 1) {
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+            high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+          }
         }
         const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(high, low), 15.f));
         const float sf = __half2float(s);
         const __half b = __float2half_rn(__fsub_rn(low, 16.f * sf));
         const float bf = __half2float(b), r = sf > 0.f ? __frcp_rn(sf) : 0.f;
-        // (x - b) r cut to 16 .. 31 and rounded: added to 1.5 2^23 its low four bits are the
-        // code (where s is 0 it is 0, and cut to 16)
-        const float2 minus = make_float2(-bf, -bf), r2 = make_float2(r, r), magic = make_float2(12582912.f, 12582912.f);
+        // (x - b) r rounded: the last places of its sum with 1.5 2^23 (it is below 2^17: a
+        // group is at least a last place of its values wide, and b off by 2^-12 of itself)
+        // (The products one by one: the packed product and sum would become one fma, which
+        // does not round the product.)
+        const float2 minus = make_float2(-bf, -bf), magic = make_float2(12582912.f, 12582912.f);
         uint32_t word = 0;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          float2 q = mul2(add2(make_float2(v[e], v[e + 1]), minus), r2);
-          q = make_float2(fminf(fmaxf(q.x, 16.f), 31.f), fminf(fmaxf(q.y, 16.f), 31.f));
-          q = add2(q, magic);
-          word |= (__float_as_uint(q.x) & 15u) << (4 * e);
-          word |= (__float_as_uint(q.y) & 15u) << (4 * e + 4);
+          const float2 d = add2(make_float2(v[e], v[e + 1]), minus);
+          const float2 q = add2(make_float2(__fmul_rn(d.x, r), __fmul_rn(d.y, r)), magic);
+          word += (uint32_t)__vimin_s32_relu(__float_as_int(q.x) - 0x4B400010, 15) << (4 * e);
+          word += (uint32_t)__vimin_s32_relu(__float_as_int(q.y) - 0x4B400010, 15) << (4 * e + 4);
         }
         if (c < per_row) {
           const int h = c >> log2_words, w = c & ((1 << log2_words) - 1);
-          const int64_t at = first + ((int64_t)h << a.log2_bs);
-          codes[(at << log2_words) + w] = word;
+          codes[(h << (a.log2_bs + log2_words)) + w] = word;
           if ((w & (span - 1)) == 0)
-            scales[(at << (log2_words - log2_span)) + (w >> log2_span)] =
+            scales[(h << (a.log2_bs + log2_words - log2_span)) + (w >> log2_span)] =
                 (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(b) << 16;
         }
       }
@@ -195,8 +205,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(GatherArgs a) {
     const bool ok = slot >= 0 && slot < a.slots_in_cache;
     if (slot >= a.slots_in_cache && lane == 0) raise_flag(a.status, LQ_DEV_RANGE);
     const int64_t first = ((slot >> a.log2_bs) * a.kv_heads << a.log2_bs) + (slot & ((1 << a.log2_bs) - 1));
-    const uint32_t* codes = which ? a.codes[1] : a.codes[0];
-    const uint32_t* scales = which ? a.scales[1] : a.scales[0];
+    const uint32_t* codes = (which ? a.codes[1] : a.codes[0]) + (first << log2_words);
+    const uint32_t* scales = (which ? a.scales[1] : a.scales[0]) + (first << log2_groups);
     uint4* out = reinterpret_cast<uint4*>(which ? a.out[1] : a.out[0]) + (u >> 1) * per_row;
     for (int c0 = lane; c0 < per_row; c0 += 32 * kUnroll) {
       uint32_t word[kUnroll], pr[kUnroll];
@@ -205,26 +215,36 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(GatherArgs a) {
         const int c = c0 + 32 * i, h = c >> log2_steps, k = c & ((1 << log2_steps) - 1);
         word[i] = pr[i] = 0u;                  // scale and base 0: zeros
         if (ok && c < per_row) {
-          const int64_t at = first + ((int64_t)h << a.log2_bs);
-          word[i] = codes[(at << log2_words) + (BF16 ? k : k >> 1)];
-          pr[i] = scales[(at << log2_groups) + (k >> (log2_steps - log2_groups))];
+          word[i] = codes[(h << (a.log2_bs + log2_words)) + (BF16 ? k : k >> 1)];
+          pr[i] = scales[(h << (a.log2_bs + log2_groups)) + (k >> (log2_steps - log2_groups))];
         }
       }
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         const int c = c0 + 32 * i;
         if (c >= per_row) break;
-        float v[8];
-        values8(word[i], pr[i], v);
         uint32_t o[4];
+        if constexpr (BF16) {
+          float v[8];
+          values8(word[i], pr[i], v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (BF16) {
+          for (int e = 0; e < 4; ++e) {
             const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
             o[e] = *reinterpret_cast<const uint32_t*>(&p);
-          } else {
-            o[e] = __float_as_uint(c & 1 ? v[e + 4] : v[e]);
           }
+        } else {
+          // four codes of the word's half: 0 and 2 below 1 and 3
+          const uint32_t half = __byte_perm(word[i], 0u, c & 1 ? 0x4432 : 0x4410);
+          const uint32_t w = half + (half & 0xFFF0u) * 4096u;
+          const uint32_t s = twice_low(pr[i]), b = twice_high(pr[i]);
+          const uint32_t x = fma_h2(((w << 6) & 0x03C003C0u) | 0x4C004C00u, s, b);
+          const uint32_t y = fma_h2(((w >> 2) & 0x03C003C0u) | 0x4C004C00u, s, b);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+          const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&y));
+          o[0] = __float_as_uint(f.x);
+          o[1] = __float_as_uint(f.y);
+          o[2] = __float_as_uint(g.x);
+          o[3] = __float_as_uint(g.y);
         }
         out[c] = make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -280,8 +300,10 @@ extern "C" lq_status lq_kv_append_q4(const void* k_dev, int64_t ldk, const void*
   a.log2_group = serve::log2_of(group_size); a.status = dev_status_dev;
   int64_t grid = (2 * tokens + 7) / 8;
   if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
-  return dtype == LQ_BF16 ? serve::launch(q4::append_kernel<true>, (unsigned)grid, q4::kThreads, 0, stream, a)
-                          : serve::launch(q4::append_kernel<false>, (unsigned)grid, q4::kThreads, 0, stream, a);
+  void (*const kernels[2][3])(q4::AppendArgs) = {
+      {q4::append_kernel<false, 32>, q4::append_kernel<false, 64>, q4::append_kernel<false, 128>},
+      {q4::append_kernel<true, 32>, q4::append_kernel<true, 64>, q4::append_kernel<true, 128>}};
+  return serve::launch(kernels[dtype == LQ_BF16][a.log2_group - 5], (unsigned)grid, q4::kThreads, 0, stream, a);
 }
 
 extern "C" lq_status lq_kv_gather_q4(const int64_t* slots_dev, int64_t n, const uint8_t* k_cache_dev,

@@ -583,7 +583,7 @@ lq_status launch_split(const CacheArgs& ca, const CUtensorMap& mk, const CUtenso
   using C = Cfg<D, NT, F32>;
   static_assert(C::halves(D / 32) >= 2 && C::smem(1) + 2048 <= 227 * 1024 && C::smem(D / 32) + 2048 <= 227 * 1024,
                 "shared memory");
-  static_assert(C::halves(D / 32) * C::kHalfBytes >= C::kPiece * 4, "a warp's last piece fits its ring");
+  static_assert(C::halves(D / 32) * C::kHalfBytes >= C::kRows * D * 4, "a warp's last piece fits its ring");
   static_assert(C::kWarps * C::halves(D / 32) * C::kHalfBytes >= LQ_MAX_REQUESTS * 8, "the prefix sums fit the rings");
   static_assert((2 + C::kWarps) * C::kPiece <= work_floats(D), "the pieces fit the workspace");
   auto kern = split_kernel<D, NT, F32>;
@@ -619,7 +619,7 @@ lq_status launch_split(const CacheArgs& ca, const CUtensorMap& mk, const CUtenso
 // Whether the tensor-core kernel takes a bf16 call: by the query rows that an
 // average request has for each kv head.
 bool many_rows(int batch, int64_t total_q, int group, int head_dim) {
-  return (total_q + batch - 1) / batch * group > (head_dim == 256 ? 48 : 16);
+  return batch > 0 && (total_q + batch - 1) / batch * group > (head_dim == 256 ? 16 : 16);
 }
 
 }  // namespace q4
@@ -629,7 +629,14 @@ using namespace lq;
 
 extern "C" size_t lq_attention_paged_q4_workspace_size(int batch, int64_t total_q, int q_heads, int kv_heads,
                                                        int head_dim) {
-  return lq_attention_paged_workspace_size(batch, total_q, q_heads, kv_heads, head_dim);
+  if (batch < 0 || batch > LQ_MAX_REQUESTS || total_q < 0 || total_q > INT32_MAX || kv_heads <= 0 || q_heads <= 0 ||
+      q_heads % kv_heads != 0 || q_heads > 1024 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  const int ctas = attn::cta_count();
+  const size_t split = attn::meta_bytes(ctas) + (size_t)ctas * attn::work_floats(head_dim) * sizeof(float);
+  if (!q4::many_rows(batch, total_q, q_heads / kv_heads, head_dim)) return split;
+  const size_t tiles = q4::tiles_workspace(batch, total_q, q_heads, kv_heads, head_dim, ctas);
+  return split > tiles ? split : tiles;
 }
 
 extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int dtype, int64_t total_q,
@@ -683,11 +690,13 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
   ca.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); ca.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
   ca.log2_group = serve::log2_of(group_size);
   ca.kc = k_cache_dev; ca.vc = v_cache_dev;
-  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, head_dim))
+  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, head_dim)) {
+    a.part = reinterpret_cast<float*>(workspace_dev);
     return q4::launch_tiles(ca, head_dim,
-                            attn::plan_tiles(batch, total_q, a.group, kv_heads, head_dim,
-                                             (int64_t)table_width * block_size, ctas),
+                            q4::plan_tiles(batch, total_q, a.group, kv_heads, head_dim,
+                                           (int64_t)table_width * block_size, ctas),
                             stream);
+  }
   // a pool without blocks: no copy is issued, any valid map will do
   const void* kc = num_blocks > 0 ? (const void*)k_cache_dev : workspace_dev;
   const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;

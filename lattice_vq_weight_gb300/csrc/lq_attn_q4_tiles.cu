@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     __syncthreads();
   }
   if (found[0] < 0) {                                       // fewer row tiles than CTAs
-    if (ta.splits > 1 && split == 0 && threadIdx.x == 0) a.meta[unit].valid = 0;
     return;
   }
   const int req = found[0], row0 = found[1] * C::kRows;
@@ -257,11 +256,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   const int first = (int)((int64_t)all * split / ta.splits), past = (int)((int64_t)all * (split + 1) / ta.splits);
   const int n0 = max(0, min(all0, past) - first), n1 = max(0, min(all1, past) - first), tiles = max(n0, n1);
   const int seen = min(r.len, past * BN);                   // tokens fetched end here
-  if (ta.splits > 1 && split == 0 && threadIdx.x == 0) {
-    Tag tag = {};
-    tag.i = req; tag.h = h; tag.rt = found[1]; tag.q0 = r.q0; tag.q_len = r.q_len; tag.valid = 1;
-    a.meta[unit] = tag;
-  }
   const int32_t* table = a.table + (int64_t)req * a.ldt;
 
   if (warp == C::kMmaWarp) {
@@ -572,9 +566,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     __syncwarp();
     if (ok) {
       const bool whole = ta.splits == 1;
-      const uint32_t rows_out = whole ? __ballot_sync(0xffffffffu, mine) : 0xffffffffu;
+      const uint32_t rows_out = __ballot_sync(0xffffffffu, mine);
       // with the positions split: the row's sums as they are
-      float* piece = a.part + ((int64_t)blockIdx.x * C::kRows + t * kTileRows + row) * (D + 4);
+      float* piece = a.part + (((int64_t)split * a.total_q + r.q0 + j_tok) * a.q_heads + head) * (D + 4);
       uint8_t* dst = reinterpret_cast<uint8_t*>(
           whole ? reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D
                 : reinterpret_cast<uint16_t*>(piece));
@@ -624,10 +618,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         }
         __syncwarp();
       }
-      if (!whole) {
+      if (!whole && mine) {
         piece[D] = mx;
         piece[D + 1] = l;
-        piece[D + 2] = mx - kShift;                         // the unit of the sum: 2^that
       }
     }
   }
@@ -649,11 +642,49 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   if (threadIdx.x == 0 && timeout_flag) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 
+// Joins what the CTAs that share a row's positions left of it: a warp per row, D / 32
+// neighbouring dimensions per lane.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ TileArgs ta) {
+  constexpr int E = D / 32;
+  const Args& a = ta.ca.a;
+  pdl_wait();
+  pdl_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), tokens = min((int64_t)a.cu_q[a.batch], a.total_q);
+  const int64_t token = row / a.q_heads;
+  if (token >= tokens) return;                              // no request's: zeros already
+  const float* piece = a.part + row * (D + 4);
+  const int64_t next = a.total_q * a.q_heads * (D + 4);
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int p = 0; p < ta.splits; ++p) M = fmaxf(M, piece[p * next + D]);
+  float o[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < ta.splits; ++p) {
+    const float m = piece[p * next + D], f = m == M ? 1.f : pow2(m - M);
+    l = fmaf(piece[p * next + D + 1], f, l);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(piece + p * next + E * lane + e);
+      o[e] = fmaf(v.x, f, o[e]);
+      o[e + 1] = fmaf(v.y, f, o[e + 1]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t dst = token * a.ldo + (row - token * a.q_heads) * D + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + dst + e) =
+        __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+}
+
 template <int D>
 lq_status launch(const TileArgs& ta, const TilePlan& plan, void* stream) {
   using C = TileCfg<D>;
   static_assert(C::kSmem + 1536 <= 227 * 1024, "shared memory");
-  static_assert(C::kRows * (D + 4) <= work_floats(D), "a CTA's piece fits its SM's share of the workspace");
   auto kern = tiles_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
     cudaGetLastError();
@@ -661,8 +692,43 @@ lq_status launch(const TileArgs& ta, const TilePlan& plan, void* stream) {
   }
   const lq_status st = serve::launch(kern, (unsigned)(plan.units * plan.splits), C::kThreads, C::kSmem, stream, ta);
   if (st != LQ_OK || plan.splits == 1) return st;
-  return serve::launch(attn_tiles_merge_kernel<D>, (unsigned)(plan.units * (C::kRows / 8)), 256, 0, stream,
-                       TileMergeArgs{ta.ca.a, ta.splits});
+  const int64_t rows = ta.ca.a.total_q * ta.ca.a.q_heads;
+  return serve::launch(merge_kernel<D>, (unsigned)((rows + 7) / 8), 256, 0, stream, ta);
+}
+
+// Units: row tiles of a request's rows, at least `group` of them, rounded up.
+static int64_t units_of(int batch, int64_t total_q, int group, int kv_heads, int head_dim) {
+  const int rows = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;
+  const int64_t requests = batch < total_q ? batch : total_q;
+  return ((total_q * group - requests) / rows + requests) * kv_heads;
+}
+// CTAs per SM that shared units may make.
+constexpr int kMostWaves = 4;
+static int64_t most_splits(int64_t units, int sms) {
+  const int64_t n = units > 0 ? (int64_t)kMostWaves * sms / units : 1;
+  return n > 1 ? n : 1;
+}
+
+TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms) {
+  const int bn = head_dim == 256 ? TileCfg<256>::BN : TileCfg<128>::BN;
+  TilePlan p;
+  p.units = units_of(batch, total_q, group, kv_heads, head_dim);
+  // Parts so that every SM has one, and of the longest request's positions no part is
+  // longer than kPart tiles (what one part costs beside them, about 9 us, is 8 tiles):
+  // the batch's requests may be of any lengths, and the longest one ends last.
+  constexpr int kPart = 24;
+  const int64_t tiles = (most_tokens + bn - 1) / bn, fill = p.units > 0 ? sms / p.units : 1;
+  int64_t splits = (tiles + kPart - 1) / kPart;
+  if (splits < fill) splits = fill;
+  if (splits > tiles / 4) splits = tiles / 4;               // of at least four tiles each
+  if (splits > most_splits(p.units, sms)) splits = most_splits(p.units, sms);
+  p.splits = splits > 1 ? (int)splits : 1;
+  return p;
+}
+
+size_t tiles_workspace(int batch, int64_t total_q, int q_heads, int kv_heads, int head_dim, int sms) {
+  const int64_t splits = most_splits(units_of(batch, total_q, q_heads / kv_heads, kv_heads, head_dim), sms);
+  return splits > 1 ? (size_t)splits * total_q * q_heads * (head_dim + 4) * sizeof(float) : 0;
 }
 
 lq_status launch_tiles(const CacheArgs& ca, int head_dim, const TilePlan& plan, void* stream) {

@@ -716,7 +716,7 @@ TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int hea
   // Parts so that every SM has one, and of the longest request's positions no part is
   // longer than kPart tiles (what one part costs beside them, about 9 us, is 8 tiles):
   // the batch's requests may be of any lengths, and the longest one ends last.
-  constexpr int kPart = 24;
+  constexpr int kPart = 48;
   const int64_t tiles = (most_tokens + bn - 1) / bn, fill = p.units > 0 ? sms / p.units : 1;
   int64_t splits = (tiles + kPart - 1) / kPart;
   if (splits < fill) splits = fill;

@@ -759,10 +759,10 @@ def lq_verify_draft(draft_tokens, draft_lens, target_probs, draft_probs, u_accep
 LQ_MAX_ALTERNATIVES = 32
 
 
-def _run(call: str, device: int, *args) -> None:
+def _run(call: str, device: int, args) -> None:
     """The library's call with `device` as the current one: kernels are launched there."""
     import torch
-    fn = getattr(_get_lib(), call)
+    fn = getattr(_LIB or _get_lib(), call)
     if device == torch.cuda.current_device():
         st = fn(*args)
     else:
@@ -775,20 +775,19 @@ def _run(call: str, device: int, *args) -> None:
 def _cache_q4(call, k_cache, k_scales, v_cache, v_scales):
     """(num_blocks, kv_heads, block_size, head_dim, group_size) of a 4-bit cache's four tensors, checked."""
     import torch
-    u8, f16, shape = torch.uint8, torch.float16, k_cache.shape
+    u8, f16, shape, per_group = torch.uint8, torch.float16, k_cache.shape, k_scales.shape
     if len(shape) != 4:
         raise ValueError(f"{call}: k_cache: want [num_blocks x kv_heads x block_size x head_dim / 2], got {tuple(shape)}")
-    groups = k_scales.shape[3] if k_scales.dim() == 5 else 0
-    if groups <= 0 or 2 * shape[3] % groups:
-        raise ValueError(f"{call}: k_scales: want [num_blocks x kv_heads x block_size x groups x 2] with groups that "
-                         f"divide head_dim {2 * shape[3]}, got {tuple(k_scales.shape)}")
-    per_group = (*shape[:3], groups, 2)
+    nb, hk, bs, half = shape
+    groups = per_group[3] if len(per_group) == 5 else 0
+    if groups <= 0 or 2 * half % groups or per_group != (nb, hk, bs, groups, 2):
+        raise ValueError(f"{call}: k_scales: want [{nb} x {hk} x {bs} x groups x 2] with groups that divide head_dim "
+                         f"{2 * half}, got {tuple(per_group)}")
     if not (_is(k_cache, u8, shape) and _is(v_cache, u8, shape) and _is(k_scales, f16, per_group)
             and _is(v_scales, f16, per_group)):
         _explain(call, (("k_cache", k_cache, u8, shape), ("v_cache", v_cache, u8, shape),
                         ("k_scales", k_scales, f16, per_group), ("v_scales", v_scales, f16, per_group)))
-    d = 2 * shape[3]
-    return (*shape[:3], d, d // groups)
+    return nb, hk, bs, 2 * half, 2 * half // groups
 
 
 def paged_cache_q4(num_blocks: int, kv_heads: int, block_size: int, head_dim: int, group_size: int, device):
@@ -814,9 +813,9 @@ def lq_kv_append_q4(k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_statu
     if not _is(slots, torch.int64, (n,)):
         _explain("lq_kv_append_q4", (("slots", slots, torch.int64, (n,)),))
     dev = _one_device("lq_kv_append_q4", k, v, slots, k_cache, k_scales, v_cache, v_scales, dev_status)
-    _run("lq_kv_append_q4", dev, k.data_ptr(), _heads("k", k), v.data_ptr(), _heads("v", v), _dtype_id(k), n,
-         slots.data_ptr(), k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk,
-         d, group, _addr(dev_status), _stream_of(dev, stream))
+    _run("lq_kv_append_q4", dev, (k.data_ptr(), _heads("k", k), v.data_ptr(), _heads("v", v), _dtype_id(k), n,
+          slots.data_ptr(), k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), nb, bs, hk,
+          d, group, _addr(dev_status), _stream_of(dev, stream)))
 
 
 def lq_kv_gather_q4(slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status=None, stream=None) -> None:
@@ -828,9 +827,9 @@ def lq_kv_gather_q4(slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, d
         _explain("lq_kv_gather_q4", (("slots", slots, torch.int64, (n,)), ("k_out", k_out, dt, shape),
                                      ("v_out", v_out, dt, shape)))
     dev = _one_device("lq_kv_gather_q4", slots, k_cache, k_scales, v_cache, v_scales, k_out, v_out, dev_status)
-    _run("lq_kv_gather_q4", dev, slots.data_ptr(), n, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
-         v_scales.data_ptr(), nb, bs, hk, d, group, k_out.data_ptr(), v_out.data_ptr(), _dtype_id(k_out),
-         _addr(dev_status), _stream_of(dev, stream))
+    _run("lq_kv_gather_q4", dev, (slots.data_ptr(), n, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
+          v_scales.data_ptr(), nb, bs, hk, d, group, k_out.data_ptr(), v_out.data_ptr(), _dtype_id(k_out),
+          _addr(dev_status), _stream_of(dev, stream)))
 
 
 def lq_attention_paged_q4_workspace_size(batch: int, total_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -855,10 +854,10 @@ def lq_attention_paged_q4(q, cu_q, kv_lens, block_table, k_cache, k_scales, v_ca
     stride, width = _table("lq_attention_paged_q4", block_table, b)
     dev = _one_device("lq_attention_paged_q4", q, cu_q, kv_lens, block_table, k_cache, k_scales, v_cache, v_scales, out,
                       workspace, dev_status)
-    _run("lq_attention_paged_q4", dev, q.data_ptr(), ldq, _dtype_id(q), total, cu_q.data_ptr(), kv_lens.data_ptr(), b,
-         block_table.data_ptr(), stride, width, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
-         v_scales.data_ptr(), nb, bs, hq, hk, d, group, d ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), ldo,
-         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(dev_status), _stream_of(dev, stream))
+    _run("lq_attention_paged_q4", dev, (q.data_ptr(), ldq, _dtype_id(q), total, cu_q.data_ptr(), kv_lens.data_ptr(), b,
+          block_table.data_ptr(), stride, width, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
+          v_scales.data_ptr(), nb, bs, hq, hk, d, group, d ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), ldo,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(dev_status), _stream_of(dev, stream)))
 
 
 def lq_token_logprobs(logits, tokens, logprobs, entropy=None, ranks=None, top_tokens=None, top_logprobs=None,
@@ -883,9 +882,9 @@ def lq_token_logprobs(logits, tokens, logprobs, entropy=None, ranks=None, top_to
             ("top_logprobs", top_logprobs, f32, (rows, top))))
     dev = _one_device("lq_token_logprobs", logits, tokens, logprobs, entropy, ranks, top_tokens, top_logprobs,
                       dev_status)
-    _run("lq_token_logprobs", dev, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _dtype_id(logits), rows,
-         vocab, tokens.data_ptr(), logprobs.data_ptr(), _addr(entropy), _addr(ranks), top, _addr(top_tokens),
-         _addr(top_logprobs), _addr(dev_status), _stream_of(dev, stream))
+    _run("lq_token_logprobs", dev, (logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _dtype_id(logits), rows,
+          vocab, tokens.data_ptr(), logprobs.data_ptr(), _addr(entropy), _addr(ranks), top, _addr(top_tokens),
+          _addr(top_logprobs), _addr(dev_status), _stream_of(dev, stream)))
 
 
 # ------------------------------------------------------------------ allocating helpers

@@ -9,8 +9,8 @@
 //     W = 2^(x - max) by one thread per row, from TMEM and back: the fp16
 //                     weights take the columns of the scores
 //     O += W V        tcgen05.mma in fp16 with W from TMEM, O in TMEM
-// One warp fetches codes, scales and bases by untiled bulk copies, up to two half
-// tiles (K, V) ahead; warps 0..3 turn them into fp16 values in two stages of shared
+// One warp fetches codes, scales and bases by untiled bulk copies, up to three half
+// tiles (K, V, K, ...) ahead; warps 0..3 turn them into fp16 values in two stages of shared
 // memory; four warps per row tile hold its rows' maxima and sums, and one issues its
 // products.  The values are what the cache stands for, exactly, so the softmax knows
 // nothing of scales: a weight is one fma and one exponential.  A word of eight codes
@@ -24,8 +24,18 @@
 // may lag by 2^7, so that a row's weights are made in one pass and O is rescaled only
 // when the maximum really moves.  bf16 only: the tensor core's accumulator truncates,
 // 6e-5 of the output after 30000 positions (measured), which fp32 outputs would show.
-// Few row tiles would leave SMs idle: then several CTAs share one, a range of the
-// positions each, and a second kernel joins their outputs in the order of the positions.
+//
+// What bounds it, head_dim 128 (prompt chunks of 1900 tokens over 2300 to 5400, 226 us):
+// a step of 128 tokens takes 3350 clocks, in which the products of both row tiles run
+// one after the other without a gap, 1650 clocks for the values and next scores of a
+// tile where the tensor core's rate would be 1024.  Their operands come from shared
+// memory at its 128 bytes a clock for the scores, and the conversions (2100 clocks a
+// step, beside them) write there too: 296 KB a step, 2300 clocks.  A row's weights take
+// 1000 clocks of that period, under the other tile's products.
+//
+// Few row tiles, or requests much longer than others, would leave SMs idle: then several
+// CTAs share a tile's positions, a range each, and a second kernel joins their outputs
+// by row, in the order of the positions.
 //
 // Every wait is bounded (about a second of clock cycles); on expiry
 // LQ_DEV_TIMEOUT is recorded and the CTA winds down.
@@ -47,7 +57,11 @@ struct TileCfg : TileShape<D> {
   static constexpr int kValueBytes = BN * D * 2;            // a K or V tile as fp16
   static constexpr int kRawBytes = BN * D / 2;              // a K or V tile's codes
   static constexpr int kParamBytes = BN * (D / 32) * 4;     // and its scales and bases, at most
-  static constexpr int kSmem = T * kQBytes + 4 * kValueBytes + 2 * kRawBytes + 2 * kParamBytes + 1024;
+  // Half tiles as fetched, K and V in turn: from a slot's last read to the next data in it
+  // 2200 clocks pass, which with one slot each for K and V the conversions waited for
+  // (drafts at head_dim 256: 86 to 84 us with three).
+  static constexpr int kRaw = 3;
+  static constexpr int kSmem = T * kQBytes + 4 * kValueBytes + kRaw * (kRawBytes + kParamBytes) + 1024;
   static constexpr uint32_t kCols = 512;
   static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
   static constexpr int kMmaWarp = 4 + 4 * T;                // and the next, one per row tile
@@ -154,10 +168,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   uint8_t* sq = smem;                                       // the query rows
   uint8_t* sk = sq + T * C::kQBytes;                        // two stages each
   uint8_t* sv = sk + 2 * C::kValueBytes;
-  uint8_t* raw = sv + 2 * C::kValueBytes;                   // codes as fetched, K and V
-  uint8_t* params = raw + 2 * C::kRawBytes;                 // (scale, base) pairs, K and V
+  uint8_t* raw = sv + 2 * C::kValueBytes;                   // codes as fetched
+  uint8_t* params = raw + C::kRaw * C::kRawBytes;           // and their (scale, base) pairs
   __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
-  __shared__ uint64_t raw_full[2], raw_free[2];             // K, V
+  __shared__ uint64_t raw_full[C::kRaw], raw_free[C::kRaw];
   __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], turn[T][2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[2];
@@ -169,9 +183,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   pdl_wait();
   pdl_launch();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kRaw; ++i) {
       mbar_init1(&raw_full[i], 1);
       mbar_init1(&raw_free[i], 4);                          // one arrival per converting warp
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init1(&k_full[i], 4);
       mbar_init1(&v_full[i], 4);
       mbar_init1(&k_free[i], T);                            // the row tiles' products that read the stage are done
@@ -281,9 +297,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     const int grp = (64 * sub + 16 * q) >> ta.ca.log2_group;
     const uint32_t to0 = sub * BN * 128 + r0 * 128 + (((2 * q) ^ (r0 & 7)) << 4), to1 = to0 ^ 16;
     // lim: the tile's tokens that are there; others are zeros, whatever their slots hold
-    auto convert = [&](int v, uint8_t* dst, int lim, uint64_t* full) {
-      const uint8_t* src = raw + v * C::kRawBytes + r0 * (D / 2) + sub * 32 + q * 8;
-      const uint32_t* par = reinterpret_cast<const uint32_t*>(params + v * C::kParamBytes) + r0 * groups + grp;
+    int slot = 0;                                           // of the next half tile, and its phase
+    uint32_t phase = 0;
+    auto convert = [&](uint8_t* dst, int lim, uint64_t* full) {
+      const uint8_t* src = raw + slot * C::kRawBytes + r0 * (D / 2) + sub * 32 + q * 8;
+      const uint32_t* par = reinterpret_cast<const uint32_t*>(params + slot * C::kParamBytes) + r0 * groups + grp;
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
         const uint2 x = *reinterpret_cast<const uint2*>(src + p * C::kPassRows * (D / 2));
@@ -301,21 +319,25 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive(&raw_free[v]);
+        arrive(&raw_free[slot]);
         arrive(full);
+      }
+      if (++slot == C::kRaw) {
+        slot = 0;
+        phase ^= 1;
       }
     };
     for (int j = 0; j < tiles; ++j) {
       const int st = j & 1, lim = seen - (first + j) * BN;
       const uint32_t before = (uint32_t)(j / 2 + 1) & 1;    // the stage's previous use
-      bool ok = wait_on(&raw_full[0], (uint32_t)j & 1, timeout);
+      bool ok = wait_on(&raw_full[slot], phase, timeout);
       if (j >= 2) ok = ok && wait_on(&k_free[st], before, timeout);
       if (!__all_sync(0xffffffffu, ok)) break;
-      convert(0, sk + st * C::kValueBytes, lim, &k_full[st]);
-      ok = wait_on(&raw_full[1], (uint32_t)j & 1, timeout);
+      convert(sk + st * C::kValueBytes, lim, &k_full[st]);
+      ok = wait_on(&raw_full[slot], phase, timeout);
       if (j >= 2) ok = ok && wait_on(&v_free[st], before, timeout);
       if (!__all_sync(0xffffffffu, ok)) break;
-      convert(1, sv + st * C::kValueBytes, lim, &v_full[st]);
+      convert(sv + st * C::kValueBytes, lim, &v_full[st]);
     }
   } else if (warp >= C::kMmaWarp) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
@@ -327,7 +349,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         const int pos = (first + j) * BN + step * lane;
         return lane < parts && pos < seen ? table[pos >> a.log2_bs] : -1;
       };
-      int blk = look_up(0), issued = 0;
+      int blk = look_up(0), issued = 0, slot = 0;
+      uint32_t phase = 1;                                   // of the slot's last read
       for (int j = 0; j < tiles; ++j) {
         const int pos = (first + j) * BN + step * lane;
         const bool ok = (unsigned)blk < (unsigned long long)a.num_blocks;
@@ -338,29 +361,33 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         blk = look_up(j + 1);
         bool go = true;
         for (int v = 0; v < 2 && go; ++v) {
-          if (j > 0) go = __all_sync(0xffffffffu, wait_on(&raw_free[v], (uint32_t)(j - 1) & 1, timeout));
+          if (issued >= C::kRaw) go = __all_sync(0xffffffffu, wait_on(&raw_free[slot], phase, timeout));
           if (!go) break;
-          uint8_t* codes = raw + v * C::kRawBytes + lane * step * (D / 2);
-          uint32_t* par = reinterpret_cast<uint32_t*>(params + v * C::kParamBytes) + lane * step * groups;
+          uint8_t* codes = raw + slot * C::kRawBytes + lane * step * (D / 2);
+          uint32_t* par = reinterpret_cast<uint32_t*>(params + slot * C::kParamBytes) + lane * step * groups;
           if (lost) {                                       // a block that is not there: zeros
             for (int i = 0; i < step * groups; ++i) par[i] = 0u;
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_expect_tx(&raw_full[v], bytes);
+          if (lane == 0) mbar_expect_tx(&raw_full[slot], bytes);
           __syncwarp();
           if (ok) {
-            bulk_load(codes, (v ? ta.ca.vc : ta.ca.kc) + row * (D / 2), step * (D / 2), &raw_full[v]);
-            bulk_load(par, (v ? ta.ca.vs : ta.ca.ks) + row * groups, step * groups * 4, &raw_full[v]);
+            bulk_load(codes, (v ? ta.ca.vc : ta.ca.kc) + row * (D / 2), step * (D / 2), &raw_full[slot]);
+            bulk_load(par, (v ? ta.ca.vs : ta.ca.ks) + row * groups, step * groups * 4, &raw_full[slot]);
           }
           ++issued;
+          if (++slot == C::kRaw) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
         if (!go) break;
       }
       // after a timeout: let the copies in flight land before the CTA ends
       if (*timeout)
-        for (int q = max(0, issued - 2); q < issued; ++q)
-          mbar_wait_bounded(&raw_full[q & 1], (uint32_t)(q >> 1) & 1, kWaitCycles / 8);
+        for (int q = max(0, issued - C::kRaw); q < issued; ++q)
+          mbar_wait_bounded(&raw_full[q % C::kRaw], (uint32_t)(q / C::kRaw) & 1, kWaitCycles / 8);
     } else if (warp < C::kFetchWarp) {
       // ------------------------------------------------------------ products
       // A warp per row tile: the products of one then run while the other's warp

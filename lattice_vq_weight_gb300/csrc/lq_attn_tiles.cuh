@@ -1,8 +1,7 @@
 // Shared by the kernels of the paged attention for many query rows, on the
 // 5th-generation tensor cores (lq_attn_paged_tiles.cu for the 8-bit cache,
 // lq_attn_q4_tiles.cu for the 4-bit one): shapes of the tiles, descriptors and
-// instructions, bounded waits, the joining of rows whose positions were split.
-// Internal to the library.
+// instructions, bounded waits.  Internal to the library.
 #pragma once
 
 #include "lq_attn_paged.cuh"
@@ -125,54 +124,6 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
-}
-
-struct TileMergeArgs {
-  Args a;
-  int splits;                    // CTAs per pair of row tiles and kv head
-};
-
-// Joins the pieces of rows whose positions were split: a warp per row, D / 32
-// neighbouring dimensions per lane.
-template <int D>
-__global__ void __launch_bounds__(256) attn_tiles_merge_kernel(const __grid_constant__ TileMergeArgs ta) {
-  using C = TileShape<D>;
-  constexpr int E = D / 32;
-  const Args& a = ta.a;
-  pdl_wait();
-  pdl_launch();
-  const int unit = blockIdx.x / (C::kRows / 8), row = (blockIdx.x % (C::kRows / 8)) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const Tag tag = a.meta[unit];
-  const int R = tag.rt * C::kRows + row, j = R / a.group;
-  if (!tag.valid || j >= tag.q_len) return;
-  const float* piece = a.part + ((int64_t)unit * ta.splits * C::kRows + row) * (D + 4);
-  constexpr int64_t next = (int64_t)C::kRows * (D + 4);
-  float M = -INFINITY, U = -INFINITY;
-  for (int p = 0; p < ta.splits; ++p) {
-    M = fmaxf(M, piece[p * next + D]);
-    U = fmaxf(U, piece[p * next + D + 2]);
-  }
-  float o[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < ta.splits; ++p) {
-    const float f = pow2(piece[p * next + D] - M);
-    l = fmaf(piece[p * next + D + 1], pow2(piece[p * next + D + 2] - U), l);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(piece + p * next + E * lane + e);
-      o[e] = fmaf(v.x, f, o[e]);
-      o[e + 1] = fmaf(v.y, f, o[e + 1]);
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l, back = unit_of(M, U);
-  const int64_t dst = (int64_t)(tag.q0 + j) * a.ldo + (int64_t)(tag.h * a.group + R - j * a.group) * D + E * lane;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + dst + e) =
-        __floats2bfloat162_rn(o[e] * inv * back, o[e + 1] * inv * back);
 }
 
 }  // namespace attn

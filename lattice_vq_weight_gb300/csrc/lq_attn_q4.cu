@@ -700,13 +700,8 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
   ca.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); ca.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
   ca.log2_group = serve::log2_of(group_size);
   ca.kc = k_cache_dev; ca.vc = v_cache_dev;
-  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, head_dim)) {
-    a.part = reinterpret_cast<float*>(workspace_dev);
-    return q4::launch_tiles(ca, head_dim,
-                            q4::plan_tiles(batch, total_q, a.group, kv_heads, head_dim,
-                                           (int64_t)table_width * block_size, ctas),
-                            stream);
-  }
+  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, head_dim))
+    return q4::launch_tiles(ca, head_dim, (int64_t)table_width * block_size, ctas, workspace_dev, stream);
   // a pool without blocks: no copy is issued, any valid map will do
   const void* kc = num_blocks > 0 ? (const void*)k_cache_dev : workspace_dev;
   const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;

@@ -25,14 +25,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
-// The kernel for many query rows (lq_attn_q4_tiles.cu): its units of work, pairs of
-// row tiles of a kv head (at most so many), and the CTAs that share one's positions.
-// most_tokens: positions that any request can have.
-attn::TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens,
-                          int sms);
-// Its workspace: what the CTAs that share a row leave of it.
+// The kernel for many query rows (lq_attn_q4_tiles.cu); most_tokens: positions that any
+// request can have.
+lq_status launch_tiles(const CacheArgs& ca, int head_dim, int64_t most_tokens, int sms, void* workspace, void* stream);
+// Its workspace: what the CTAs that share a row leave of it, and where.
 size_t tiles_workspace(int batch, int64_t total_q, int q_heads, int kv_heads, int head_dim, int sms);
-lq_status launch_tiles(const CacheArgs& ca, int head_dim, const attn::TilePlan& plan, void* stream);
 
 }  // namespace q4
 }  // namespace lq

@@ -34,8 +34,12 @@
 // 1000 clocks of that period, under the other tile's products.
 //
 // Few row tiles, or requests much longer than others, would leave SMs idle: then several
-// CTAs share a tile's positions, a range each, and a second kernel joins their outputs
-// by row, in the order of the positions.
+// CTAs share a unit's positions (a pair of row tiles and a kv head), a range each, and a
+// second kernel joins their outputs by row, in the order of the positions.  How many share
+// a unit follows from the lengths, which only the device knows: no range is longer than P
+// tiles, and every CTA finds the same P before it looks up its own range, as the one of
+// some hundred that promises the earliest end.  (24 requests of 500 to 12000 tokens at
+// head_dim 256: the same number of CTAs for every unit 80 us, by length @@ us.)
 //
 // Every wait is bounded (about a second of clock cycles); on expiry
 // LQ_DEV_TIMEOUT is recorded and the CTA winds down.
@@ -80,8 +84,13 @@ struct TileCfg : TileShape<D> {
 
 struct TileArgs {
   CacheArgs ca;
-  int splits;                    // CTAs per pair of row tiles and kv head
+  // Where CTAs may share a unit: the units of a kv head at most (0: they do not), and the
+  // rows of a CTA's piece
+  int items, stride, ctas, sms;
+  int2* places;                  // of every query row: its first piece's row, and how many CTAs share it
 };
+// What a CTA costs beside its tiles, in tiles (9 us), and how many shares are tried.
+constexpr int kFixedTiles = 8, kMostShares = 128;
 
 // A row's weights of one tile from its scores: packed fp16 weights and their sum;
 // returns the largest weight's bits, or more (positive fp16 numbers are in the order of
@@ -174,8 +183,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   __shared__ uint64_t raw_full[C::kRaw], raw_free[C::kRaw];
   __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], turn[T][2], drain;
   __shared__ uint32_t tmem_base;
-  __shared__ int timeout_flag, found[2];
+  __shared__ int timeout_flag, found[5];                    // request, row tile, kv head; share, shares
   __shared__ int wsum[C::kThreads / 32];
+  __shared__ unsigned long long best[C::kThreads / 32];
   volatile int* timeout = &timeout_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = D >> ta.ca.log2_group;
@@ -217,20 +227,22 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   }
 
   // this CTA's request and row tile, the last rows first: they see the most
-  const int split = blockIdx.x % ta.splits, unit = blockIdx.x / ta.splits;
-  const int h = unit % a.kv_heads, item = unit / a.kv_heads;
+  auto tiles_of = [&](const Request& r, int row0, int n_rows) {     // of the tokens that the last of the rows sees
+    const int rows = r.q_len * a.group;
+    if (row0 >= rows) return 0;
+    const int last = min(row0 + n_rows, rows) - 1;
+    const int seen = min(r.len, r.shown + last / a.group + 1);
+    return seen > 0 ? (seen + BN - 1) / BN : 0;
+  };
   {
     const int per = (a.batch + C::kThreads - 1) / C::kThreads;
     const int i0 = min(a.batch, (int)threadIdx.x * per), i1 = min(a.batch, i0 + per);
-    auto tiles_of = [&](int i) {
-      const Request r = load_request(a, i);
-      return (r.q_len * a.group + C::kRows - 1) / C::kRows;
-    };
+    auto items_of = [&](const Request& r) { return (r.q_len * a.group + C::kRows - 1) / C::kRows; };
     int sum = 0;
     for (int i = i0; i < i1; ++i) {
       if (blockIdx.x == 0 && (int64_t)a.kv_lens[i] > ((int64_t)a.width << a.log2_bs))
         raise_flag(a.status, LQ_DEV_RANGE);
-      sum += tiles_of(i);
+      sum += items_of(load_request(a, i));
     }
     int inc = sum;
     for (int o = 1; o < 32; o <<= 1) {
@@ -239,37 +251,106 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) inc += wsum[w];
+    int total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w < warp) inc += wsum[w];
+      total += wsum[w];
+    }
     int begin = inc - sum;
-    if (item >= begin && item < inc) {
+    if (ta.items == 0) {
+      const int h = blockIdx.x % a.kv_heads, item = blockIdx.x / a.kv_heads;
+      if (item >= begin && item < inc) {
+        for (int i = i0; i < i1; ++i) {
+          const int n = items_of(load_request(a, i));
+          if (item < begin + n) {
+            found[0] = i;
+            found[1] = begin + n - 1 - item;
+            found[2] = h;
+            found[3] = 0;
+            found[4] = 1;
+            break;
+          }
+          begin += n;
+        }
+      }
+    } else {
+      // every item's tiles, request and row tile, where the query rows will be
+      int* const item_tiles = reinterpret_cast<int*>(sq);
+      int* const item_req = item_tiles + ta.items;
+      int* const item_at = item_req + ta.items;
       for (int i = i0; i < i1; ++i) {
-        const int n = tiles_of(i);
-        if (item < begin + n) {
-          found[0] = i;
-          found[1] = begin + n - 1 - item;
-          break;
+        const Request r = load_request(a, i);
+        const int n = items_of(r);
+        for (int k = 0; k < n && begin + k < ta.items; ++k) {
+          item_tiles[begin + k] = tiles_of(r, (n - 1 - k) * C::kRows, C::kRows);
+          item_req[begin + k] = i;
+          item_at[begin + k] = n - 1 - k;
         }
         begin += n;
+      }
+      __syncthreads();
+      total = min(total, ta.items);
+      int longest = 0;
+      for (int i = lane; i < total; i += 32) longest = max(longest, item_tiles[i]);
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      // P such that the longest item makes j ranges: the end is that of the last wave of
+      // CTAs, each as long as its longest, and of the rows' joining
+      unsigned long long least = ~0ull;
+      for (int j = 1 + warp; j <= kMostShares && (j == 1 || j * a.kv_heads <= (int)gridDim.x); j += C::kThreads / 32) {
+        const int P = max(4, (longest + j - 1) / j);
+        int count = 0;
+        for (int i = lane; i < total; i += 32) count += max(1, (item_tiles[i] + P - 1) / P);
+        count = __reduce_add_sync(0xffffffffu, count) * a.kv_heads;
+        if (count > (int)gridDim.x) continue;
+        const unsigned long long cost = (unsigned long long)((count + ta.sms - 1) / ta.sms) * (kFixedTiles + P) * 8 + j;
+        least = min(least, cost << 32 | (unsigned)P);
+      }
+      if (lane == 0) best[warp] = least;
+      __syncthreads();
+      if (warp == 0) {
+        least = lane < C::kThreads / 32 ? best[lane] : ~0ull;
+        for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        const int P = (int)(least & 0x7FFFFFFFu);
+        int before = 0;
+        for (int at32 = 0; at32 < total && before <= (int)blockIdx.x; at32 += 32) {
+          const int i = at32 + lane, shares = i < total ? max(1, (item_tiles[i] + P - 1) / P) : 0;
+          int end = shares * a.kv_heads;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += x;
+          }
+          end += before;
+          const int at = (int)blockIdx.x - (end - shares * a.kv_heads);
+          if (at >= 0 && (int)blockIdx.x < end) {
+            found[0] = item_req[i];
+            found[1] = item_at[i];
+            found[2] = at / shares;
+            found[3] = at % shares;
+            found[4] = shares;
+          }
+          before = __shfl_sync(0xffffffffu, end, 31);
+        }
       }
     }
     __syncthreads();
   }
-  if (found[0] < 0) {                                       // fewer row tiles than CTAs
+  if (found[0] < 0) {                                       // fewer units than CTAs
     return;
   }
-  const int req = found[0], row0 = found[1] * C::kRows;
+  const int req = found[0], row0 = found[1] * C::kRows, h = found[2], share = found[3], shares = found[4];
   const Request r = load_request(a, req);
   const int rows = r.q_len * a.group;
-  // tiles of the tokens that a row tile's last row sees; none if it has no rows
-  auto tiles_seen = [&](int t) {
-    if (row0 + t * kTileRows >= rows) return 0;
-    const int last = min(row0 + (t + 1) * kTileRows, rows) - 1;
-    const int seen = min(r.len, r.shown + last / a.group + 1);
-    return seen > 0 ? (seen + BN - 1) / BN : 0;
-  };
-  const int all0 = tiles_seen(0), all1 = T > 1 ? tiles_seen(1) : 0, all = max(all0, all1);
+  const int all0 = tiles_of(r, row0, kTileRows), all1 = T > 1 ? tiles_of(r, row0 + kTileRows, kTileRows) : 0;
+  const int all = max(all0, all1);
+  if (ta.items > 0 && share == 0) {                         // where the rows' pieces are
+    for (int i = threadIdx.x; i < C::kRows && row0 + i < rows; i += C::kThreads) {
+      const int j = (row0 + i) / a.group;
+      ta.places[(int64_t)(r.q0 + j) * a.q_heads + h * a.group + row0 + i - j * a.group] =
+          make_int2((int)blockIdx.x * ta.stride + i, shares);
+    }
+  }
   // this CTA's tiles: `first` and the ones after it
-  const int first = (int)((int64_t)all * split / ta.splits), past = (int)((int64_t)all * (split + 1) / ta.splits);
+  const int first = (int)((int64_t)all * share / shares), past = (int)((int64_t)all * (share + 1) / shares);
   const int n0 = max(0, min(all0, past) - first), n1 = max(0, min(all1, past) - first), tiles = max(n0, n1);
   const int seen = min(r.len, past * BN);                   // tokens fetched end here
   const int32_t* table = a.table + (int64_t)req * a.ldt;
@@ -592,10 +673,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     tc_after();
     __syncwarp();
     if (ok) {
-      const bool whole = ta.splits == 1;
+      const bool whole = shares == 1;
       const uint32_t rows_out = __ballot_sync(0xffffffffu, mine);
       // with the positions split: the row's sums as they are
-      float* piece = a.part + (((int64_t)split * a.total_q + r.q0 + j_tok) * a.q_heads + head) * (D + 4);
+      float* piece = a.part + ((int64_t)blockIdx.x * ta.stride + R - row0) * (D + 4);
       uint8_t* dst = reinterpret_cast<uint8_t*>(
           whole ? reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + j_tok) * a.ldo + (int64_t)head * D
                 : reinterpret_cast<uint16_t*>(piece));
@@ -681,16 +762,19 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tile
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), tokens = min((int64_t)a.cu_q[a.batch], a.total_q);
   const int64_t token = row / a.q_heads;
   if (token >= tokens) return;                              // no request's: zeros already
-  const float* piece = a.part + row * (D + 4);
-  const int64_t next = a.total_q * a.q_heads * (D + 4);
+  const int2 place = ta.places[row];
+  // one CTA's already (or of no request, in offsets that are not in order)
+  if (place.y <= 1 || place.y > ta.ctas || place.x < 0 || place.x >= (ta.ctas - place.y + 1) * ta.stride) return;
+  const float* piece = a.part + (int64_t)place.x * (D + 4);
+  const int64_t next = (int64_t)ta.stride * (D + 4);
   float M = -INFINITY;
 #pragma unroll 4
-  for (int p = 0; p < ta.splits; ++p) M = fmaxf(M, piece[p * next + D]);
+  for (int p = 0; p < place.y; ++p) M = fmaxf(M, piece[p * next + D]);
   float o[E], l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-  for (int p = 0; p < ta.splits; ++p) {
+  for (int p = 0; p < place.y; ++p) {
     const float m = piece[p * next + D], f = m == M ? 1.f : pow2(m - M);
     l = fmaf(piece[p * next + D + 1], f, l);
 #pragma unroll
@@ -709,7 +793,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tile
 }
 
 template <int D>
-lq_status launch(const TileArgs& ta, const TilePlan& plan, void* stream) {
+lq_status launch(const TileArgs& ta, void* stream) {
   using C = TileCfg<D>;
   static_assert(C::kSmem + 1536 <= 227 * 1024, "shared memory");
   auto kern = tiles_kernel<D>;
@@ -717,56 +801,58 @@ lq_status launch(const TileArgs& ta, const TilePlan& plan, void* stream) {
     cudaGetLastError();
     return LQ_ERR_CUDA;
   }
-  const lq_status st = serve::launch(kern, (unsigned)(plan.units * plan.splits), C::kThreads, C::kSmem, stream, ta);
-  if (st != LQ_OK || plan.splits == 1) return st;
+  const lq_status st = serve::launch(kern, (unsigned)ta.ctas, C::kThreads, C::kSmem, stream, ta);
+  if (st != LQ_OK || ta.items == 0) return st;
   const int64_t rows = ta.ca.a.total_q * ta.ca.a.q_heads;
   return serve::launch(merge_kernel<D>, (unsigned)((rows + 7) / 8), 256, 0, stream, ta);
 }
 
-// Units: row tiles of a request's rows, at least `group` of them, rounded up.
-static int64_t units_of(int batch, int64_t total_q, int group, int kv_heads, int head_dim) {
+// Row tiles, or pairs of them, of a request's rows, at least `group` of them, rounded up.
+static int64_t items_of(int batch, int64_t total_q, int group, int head_dim) {
   const int rows = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;
   const int64_t requests = batch < total_q ? batch : total_q;
-  return ((total_q * group - requests) / rows + requests) * kv_heads;
+  return (total_q * group - requests) / rows + requests;
 }
-// CTAs per SM that shared units may make.
-constexpr int kMostWaves = 4;
-static int64_t most_splits(int64_t units, int sms) {
-  const int64_t n = units > 0 ? (int64_t)kMostWaves * sms / units : 1;
-  return n > 1 ? n : 1;
+// CTAs per SM where they may share units: two for each unit, so that a wave is at least
+// two thirds full whatever their number is, and four at most; 0: a unit is one CTA's.
+static int waves_of(int64_t units, int sms) {
+  const int64_t n = (2 * units + sms - 1) / sms;
+  return n <= 4 ? (int)n : 0;
 }
-
-TilePlan plan_tiles(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms) {
-  const int bn = head_dim == 256 ? TileCfg<256>::BN : TileCfg<128>::BN;
-  TilePlan p;
-  p.units = units_of(batch, total_q, group, kv_heads, head_dim);
-  // Parts so that every SM has one, and of the longest request's positions no part is
-  // longer than kPart tiles (what one part costs beside them, about 9 us, is 8 tiles):
-  // the batch's requests may be of any lengths, and the longest one ends last.
-  constexpr int kPart = 48;
-  const int64_t tiles = (most_tokens + bn - 1) / bn, fill = p.units > 0 ? sms / p.units : 1;
-  int64_t splits = (tiles + kPart - 1) / kPart;
-  if (splits < fill) splits = fill;
-  if (splits > tiles / 4) splits = tiles / 4;               // of at least four tiles each
-  if (splits > most_splits(p.units, sms)) splits = most_splits(p.units, sms);
-  p.splits = splits > 1 ? (int)splits : 1;
-  return p;
+// A CTA's piece has as many rows as a request can have.
+static int stride_of(int64_t total_q, int group, int head_dim) {
+  const int rows = head_dim == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows;
+  return total_q * group < rows ? (int)(total_q * group) : rows;
 }
 
 size_t tiles_workspace(int batch, int64_t total_q, int q_heads, int kv_heads, int head_dim, int sms) {
-  const int64_t splits = most_splits(units_of(batch, total_q, q_heads / kv_heads, kv_heads, head_dim), sms);
-  return splits > 1 ? (size_t)splits * total_q * q_heads * (head_dim + 4) * sizeof(float) : 0;
+  const int group = q_heads / kv_heads, waves = waves_of(items_of(batch, total_q, group, head_dim) * kv_heads, sms);
+  if (waves == 0) return 0;
+  const size_t places = ((size_t)total_q * q_heads * sizeof(int2) + 15) & ~(size_t)15;
+  return places + (size_t)waves * sms * stride_of(total_q, group, head_dim) * (head_dim + 4) * sizeof(float);
 }
 
-lq_status launch_tiles(const CacheArgs& ca, int head_dim, const TilePlan& plan, void* stream) {
-  if (plan.units * plan.splits > INT32_MAX) return LQ_ERR_SHAPE;
+lq_status launch_tiles(const CacheArgs& ca, int head_dim, int64_t most_tokens, int sms, void* workspace, void* stream) {
+  const Args& a = ca.a;
+  const int64_t items = items_of(a.batch, a.total_q, a.group, head_dim);
+  const int bn = head_dim == 256 ? TileCfg<256>::BN : TileCfg<128>::BN;
+  // (no unit is shared that has fewer than eight tiles)
+  const int waves = most_tokens >= 8 * bn ? waves_of(items * a.kv_heads, sms) : 0;
+  const int64_t ctas = waves > 0 ? (int64_t)waves * sms : items * a.kv_heads;
+  if (ctas > INT32_MAX) return LQ_ERR_SHAPE;
   TileArgs ta;
   ta.ca = ca;
-  ta.splits = plan.splits;
+  ta.items = waves > 0 ? (int)items : 0;
+  ta.ctas = (int)ctas;
+  ta.sms = sms;
+  ta.stride = stride_of(a.total_q, a.group, head_dim);
+  ta.places = reinterpret_cast<int2*>(workspace);
+  ta.ca.a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
+                                          (((size_t)a.total_q * a.q_heads * sizeof(int2) + 15) & ~(size_t)15));
   switch (head_dim) {
-    case 64: return launch<64>(ta, plan, stream);
-    case 128: return launch<128>(ta, plan, stream);
-    default: return launch<256>(ta, plan, stream);
+    case 64: return launch<64>(ta, stream);
+    case 128: return launch<128>(ta, stream);
+    default: return launch<256>(ta, stream);
   }
 }
 

@@ -67,18 +67,25 @@ struct TileCfg : TileShape<D> {
   static constexpr int kRaw = 3;
   static constexpr int kSmem = T * kQBytes + 4 * kValueBytes + kRaw * (kRawBytes + kParamBytes) + 1024;
   static constexpr uint32_t kCols = 512;
-  static_assert(T * (BN + D) <= (int)kCols, "S and O fit TMEM");
+  // Columns for scores: one row tile has two buffers, so that the next tile's scores are
+  // there when a tile's weights are done; with two row tiles each is the other's gap.
+  static constexpr int kBufs = T == 1 ? 2 : 1;
+  // and for its query rows, which the products would read again for every tile
+  static constexpr bool kQueriesInTmem = T == 1;
+  static_assert(T * (kBufs * BN + D) + (kQueriesInTmem ? D / 2 : 0) <= (int)kCols, "S, O and the queries fit TMEM");
   static constexpr int kMmaWarp = 4 + 4 * T;                // and the next, one per row tile
   static constexpr int kFetchWarp = kMmaWarp + T;
-  static constexpr int kThreads = 32 * (8 + 4 * T);         // whole groups of four warps
+  static constexpr int kMoreWarp = kMmaWarp + 4;            // with one row tile, four more that convert
+  static constexpr int kConvertWarps = T == 1 ? 8 : 4;
+  static constexpr int kThreads = 512;                      // whole groups of four warps
+  static_assert(kThreads == 32 * (4 + 4 * T + kConvertWarps), "four warps fetch and issue");
   // Registers per thread: the launch gives every warp 65536 / 512 = 128 (T = 2)
   // and the groups then divide those up, 80 + 2 x 184 + 64 = 4 x 128.
   static constexpr bool kSplitRegs = T == 2;
   static constexpr int kConvertRegs = 80, kSoftmaxRegs = 184, kIssueRegs = 64;
   static_assert(!kSplitRegs || kConvertRegs + 2 * kSoftmaxRegs + kIssueRegs <= 4 * 128, "the launch's registers");
-  // tokens that the 128 converting threads take in one pass (16 codes each), and
-  // passes per tile
-  static constexpr int kPassRows = 2048 / D;
+  // tokens that the converting threads take in one pass (16 codes each), and passes per tile
+  static constexpr int kPassRows = 32 * kConvertWarps * 16 / D;
   static constexpr int kPasses = BN / kPassRows;
 };
 
@@ -181,7 +188,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   uint8_t* params = raw + C::kRaw * C::kRawBytes;           // and their (scale, base) pairs
   __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
   __shared__ uint64_t raw_full[C::kRaw], raw_free[C::kRaw];
-  __shared__ uint64_t s_full[T], p_full[T], o_done[T], q_full[T], turn[T][2], drain;
+  constexpr int B = C::kBufs;
+  __shared__ uint64_t s_full[T][B], p_full[T][B], o_done[T], q_full[T], turn[T][2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[5];                    // request, row tile, kv head; share, shares
   __shared__ int wsum[C::kThreads / 32];
@@ -195,17 +203,19 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kRaw; ++i) {
       mbar_init1(&raw_full[i], 1);
-      mbar_init1(&raw_free[i], 4);                          // one arrival per converting warp
+      mbar_init1(&raw_free[i], C::kConvertWarps);           // one arrival per converting warp
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init1(&k_full[i], 4);
-      mbar_init1(&v_full[i], 4);
+      mbar_init1(&k_full[i], C::kConvertWarps);
+      mbar_init1(&v_full[i], C::kConvertWarps);
       mbar_init1(&k_free[i], T);                            // the row tiles' products that read the stage are done
       mbar_init1(&v_free[i], T);
     }
     for (int t = 0; t < T; ++t) {
-      mbar_init1(&s_full[t], 1);                            // scores computed
-      mbar_init1(&p_full[t], 4);                            // one arrival per softmax warp
+      for (int b = 0; b < B; ++b) {
+        mbar_init1(&s_full[t][b], 1);                       // scores computed
+        mbar_init1(&p_full[t][b], 4);                       // one arrival per softmax warp
+      }
       mbar_init1(&o_done[t], 1);                            // values added: O readable, the weights read
       mbar_init1(&q_full[t], 4);
       mbar_init1(&turn[t][0], 1);                           // scores issued
@@ -215,15 +225,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     mbar_init_fence();
     timeout_flag = 0;
     found[0] = -1;
-  }
-
-  // rows that no request owns
-  {
-    const int64_t end = max(a.cu_q[a.batch], 0), cols = (int64_t)a.q_heads * D;
-    for (int64_t t = end + blockIdx.x; t < a.total_q; t += gridDim.x)
-      for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) {
-        reinterpret_cast<uint16_t*>(a.out)[t * a.ldo + c] = 0;
-      }
   }
 
   // this CTA's request and row tile, the last rows first: they see the most
@@ -334,6 +335,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     }
     __syncthreads();
   }
+  // rows that no request owns
+  {
+    const int64_t end = max(a.cu_q[a.batch], 0), cols = (int64_t)a.q_heads * D;
+    for (int64_t t = end + blockIdx.x; t < a.total_q; t += gridDim.x)
+      for (int64_t c = threadIdx.x; c < cols; c += C::kThreads) {
+        reinterpret_cast<uint16_t*>(a.out)[t * a.ldo + c] = 0;
+      }
+  }
   if (found[0] < 0) {                                       // fewer units than CTAs
     return;
   }
@@ -363,17 +372,20 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   tc_before();
   __syncthreads();
   tc_after();
-  // columns: the row tiles' scores, then their outputs
-  const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + T * BN;
+  // columns: the row tiles' scores, then their outputs, then query rows
+  const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + T * B * BN, tmem_q = tmem_o + T * D;
+  // tile j's buffer for scores, and the parity of the buffer's barriers
+  auto buf_of = [](int j) { return B == 2 ? j & 1 : 0; };
+  auto parity_of = [](int j) { return (uint32_t)(B == 2 ? j >> 1 : j) & 1; };
 
-  if (warp < 4) {
+  if (warp < 4 || warp >= C::kMoreWarp) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kConvertRegs));
     // ------------------------------------------------------------ codes to fp16
     // 16 codes per thread and pass.  The eight lanes of a shared-memory phase write
     // chunks 2 q (+ 1) of two neighbouring tokens' lines, whose swizzles keep them off
     // each other's banks; what they read is contiguous.
     const Masks masks;
-    const int t = threadIdx.x, q = t & 3, sub = (t >> 3) & (C::kSub - 1);
+    const int t = threadIdx.x - (warp < 4 ? 0 : 32 * (C::kMoreWarp - 4)), q = t & 3, sub = (t >> 3) & (C::kSub - 1);
     const int r0 = (t >> 2 & 1) + 2 * (t / (8 * C::kSub));
     const int grp = (64 * sub + 16 * q) >> ta.ca.log2_group;
     const uint32_t to0 = sub * BN * 128 + r0 * 128 + (((2 * q) ^ (r0 & 7)) << 4), to1 = to0 ^ 16;
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       const int t = warp - C::kMmaWarp, n = t == 0 ? n0 : n1;
       const uint64_t dq = desc_k_major(smem_addr(sq + t * C::kQBytes)), dk = desc_k_major(smem_addr(sk));
       const uint64_t dv = desc_mn_major(smem_addr(sv), C::kSub > 1 ? BN * 128 : 1024);
-      const uint32_t my_s = tmem_s + t * BN, my_o = tmem_o + t * D;
+      const uint32_t my_s = tmem_s + t * B * BN, my_o = tmem_o + t * D;
       auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
       // scores of tile j; past this row tile's last, the other's codes are let go
       auto scores = [&](int j) {
@@ -487,8 +499,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         bool ok = wait_on(&k_full[st], (uint32_t)(j >> 1) & 1, timeout);
         if (j < n) {
           if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
-          // they overwrite the weights of the tile before
-          else ok = ok && wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout);
+          // they overwrite the weights of the buffer's last tile
+          else if (j >= B) ok = ok && wait_on(&o_done[t], (uint32_t)(j - B) & 1, timeout);
         }
         if (!all(ok)) return false;
         tc_after();
@@ -496,10 +508,15 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
           if (j < n) {
             const uint64_t kd = dk + (uint64_t)(st * C::kValueBytes >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(my_s, dq + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4),
-                     kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4), Idesc<BN, false, false>::v, k > 0);
-            mma_commit(&s_full[t]);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t kk = kd + (((k >> 2) * BN * 128 + (k & 3) * 32) >> 4);
+              if constexpr (C::kQueriesInTmem)
+                mma_ts(my_s + buf_of(j) * BN, tmem_q + k * 8, kk, Idesc<BN, false, false>::v, k > 0);
+              else
+                mma_ss(my_s + buf_of(j) * BN, dq + (((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4), kk,
+                       Idesc<BN, false, false>::v, k > 0);
+            }
+            mma_commit(&s_full[t][buf_of(j)]);
             mma_commit(&k_free[st]);
             arrive(&turn[t][st]);
           } else {
@@ -512,7 +529,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       auto add_values = [&](int j) {
         const int st = j & 1;
         bool ok = wait_on(&v_full[st], (uint32_t)(j >> 1) & 1, timeout);
-        if (j < n) ok = ok && wait_on(&p_full[t], (uint32_t)j & 1, timeout);
+        if (j < n) ok = ok && wait_on(&p_full[t][buf_of(j)], parity_of(j), timeout);
         // In turn, values and next scores of one row tile, then of the other: when
         // both had weights ready together, they would stay in step and neither's
         // exponentials run under the other's products.  (Neither can be two tiles
@@ -528,7 +545,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
             const uint64_t vd = dv + (uint64_t)(st * C::kValueBytes >> 4);
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
-              mma_ts(my_o, my_s + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
+              mma_ts(my_o, my_s + buf_of(j) * BN + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
             mma_commit(&o_done[t]);
             mma_commit(&v_free[st]);
           } else {
@@ -539,7 +556,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         return true;
       };
       bool ok = scores(0);
-      for (int j = 0; j < tiles && ok; ++j) ok = add_values(j) && scores(j + 1);
+      for (int j = 0; j < tiles && ok; ++j)
+        ok = B == 2 ? scores(j + 1) && add_values(j) : add_values(j) && scores(j + 1);
     }
   } else {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
@@ -547,7 +565,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     const int t = (warp - 4) >> 2;                          // row tile
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t my_s = tmem_s + lanes + t * BN, my_o = tmem_o + lanes + t * D;
+    const uint32_t tile_s = tmem_s + lanes + t * B * BN, my_o = tmem_o + lanes + t * D;
     const int R0 = row0 + t * kTileRows, R = R0 + row, j_tok = R / a.group;
     const int n = t == 0 ? n0 : n1;
     const bool mine = R < rows;
@@ -589,7 +607,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
     };
     if (n > 0) look_up(0);
 
-    // To fp16 in place, each word of eight dimensions in the values' order, after a
+    // To fp16, in place or in tensor memory, each word of eight dimensions in the values' order, after a
     // power of two that brings the row's largest to [2^13, 2^14).
     float fac;
     {
@@ -606,15 +624,30 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       const int ex = min(126, max(-116, 140 - (int)(top >> 7)));
       const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
       fac = a.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = *chunk_of(c);
+      const auto halves = [&](const uint4& x) {
         const auto low = [&](uint32_t v) { return __uint_as_float(v << 16) * up; };
         const auto high = [&](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u) * up; };
-        *chunk_of(c) = make_uint4(pack_f16(low(x.x), low(x.z)), pack_f16(high(x.x), high(x.z)),
-                                  pack_f16(low(x.y), low(x.w)), pack_f16(high(x.y), high(x.w)));
+        return make_uint4(pack_f16(low(x.x), low(x.z)), pack_f16(high(x.x), high(x.z)), pack_f16(low(x.y), low(x.w)),
+                          pack_f16(high(x.y), high(x.w)));
+      };
+      if constexpr (C::kQueriesInTmem) {
+#pragma unroll 2
+        for (int c = 0; c < D / 8; c += 4) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 x = halves(*chunk_of(c + e));
+            w[4 * e] = x.x; w[4 * e + 1] = x.y; w[4 * e + 2] = x.z; w[4 * e + 3] = x.w;
+          }
+          tmem_st16(tmem_q + lanes + 4 * c, w);
+        }
+        tmem_wait_st();
+        tc_before();
+      } else {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) *chunk_of(c) = halves(*chunk_of(c));
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive(&q_full[t]);
     }
@@ -625,7 +658,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       if (j + 1 < n) look_up(j + 1);
       const int vis0 = lim - (first + j) * BN;
       const bool masked = (first + j + 1) * BN - 1 > lim_min || gone != 0;
-      ok = __all_sync(0xffffffffu, wait_on(&s_full[t], (uint32_t)j & 1, timeout));
+      const uint32_t my_s = tile_s + buf_of(j) * BN;
+      ok = __all_sync(0xffffffffu, wait_on(&s_full[t][buf_of(j)], parity_of(j), timeout));
       if (!ok) break;
       tc_after();
       __syncwarp();
@@ -649,6 +683,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         l *= f;
         mx = to;
         if (j > 0 && __any_sync(0xffffffffu, moves)) {
+          if (B == 2) {                                     // (one buffer: these scores came after the last values)
+            ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout));
+            if (!ok) break;
+            tc_after();
+            __syncwarp();
+          }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -664,17 +704,20 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       tmem_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) arrive(&p_full[t]);
+      if (lane == 0) arrive(&p_full[t][buf_of(j)]);
     }
 
     // Outputs, by way of the rows of shared memory where the queries were (the
     // products with them are done): a warp's stores then cover whole lines.
+    // (With two buffers the values of the tile before may be under way too: a parity
+    // tells one phase from the next only.)
+    if (B == 2 && ok && n > 1) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)n & 1, timeout));
     if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(n - 1) & 1, timeout));
     tc_after();
     __syncwarp();
-    if (ok) {
+    const uint32_t rows_out = __ballot_sync(0xffffffffu, mine);
+    if (ok && rows_out) {
       const bool whole = shares == 1;
-      const uint32_t rows_out = __ballot_sync(0xffffffffu, mine);
       // with the positions split: the row's sums as they are
       float* piece = a.part + ((int64_t)blockIdx.x * ta.stride + R - row0) * (D + 4);
       uint8_t* dst = reinterpret_cast<uint8_t*>(

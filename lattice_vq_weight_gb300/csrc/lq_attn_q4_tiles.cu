@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       if (mine) src += (int64_t)(r.q0 + j_tok) * a.ldq + (int64_t)head * D;
       const uint32_t have = __ballot_sync(0xffffffffu, mine);
       const int c = lane & (kLanes - 1);
-#pragma unroll 4
+#pragma unroll 8
       for (int pass = 0; pass < kLanes; ++pass) {
         const int from = pass * kAtOnce + lane / kLanes;
         const uint16_t* p =
@@ -759,13 +759,21 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
           }
         }
         __syncwarp();
-#pragma unroll 4
-        for (int pass = 0; pass < kLanes; ++pass) {
-          const int from = pass * kAtOnce + lane / kLanes, c = lane & (kLanes - 1);
-          uint8_t* p = reinterpret_cast<uint8_t*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
-          if (rows_out >> from & 1)
-            *reinterpret_cast<uint4*>(p + part * 2 * D + 16 * c) = *reinterpret_cast<const uint4*>(line_of(from, c));
+        // (reads of eight passes first: the compiler keeps them behind the stores before)
+#pragma unroll 1
+        for (int pass = 0; pass < kLanes; pass += 8) {
+          const int c = lane & (kLanes - 1);
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(line_of((pass + i) * kAtOnce + lane / kLanes, c));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int from = (pass + i) * kAtOnce + lane / kLanes;
+            uint8_t* p = reinterpret_cast<uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
+            if (rows_out >> from & 1) *reinterpret_cast<uint4*>(p + part * 2 * D + 16 * c) = x[i];
+          }
         }
         __syncwarp();
       }

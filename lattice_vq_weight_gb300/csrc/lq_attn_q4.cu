@@ -622,14 +622,14 @@ lq_status launch_split(const CacheArgs& ca, const CUtensorMap& mk, const CUtenso
 // heads of one to four query heads, this kernel's time against the split kernel's at
 // 16 / 24 / 32 / 48 / 64 rows, in us:
 //   head_dim                      64                   128                        256
-//   16 requests of 4000  64: 27/41/41/57/70    77: 37/62/62/84/109     130: 83/116/155/216/293
-//   one of 32000 tokens  39: 22/27/27/34/41    49: 29/38/38/48/59      100: 50/63/80/108/140
-//   one of 4000 tokens   17: 13/13/13/14/17    21: 16/17/17/21/21       28: 20/26/26/30/35
-//   24 of 500 to 12000  112: 37/59/60/81/101  135: 58/93/95/130/159    222: 123/168/211/305/395
+//   16 requests of 4000  55: 27/41/41/56/70    65: 37/62/62/84/109      83: 83/116/155/215/293
+//   one of 32000 tokens  41: 21/27/27/34/41    44: 29/38/38/48/59       59: 50/63/80/108/139
+//   one of 4000 tokens   21: 13/13/13/14/17    23: 16/17/17/21/21       31: 19/26/26/30/35
+//   24 of 500 to 12000   96: 36/59/60/81/101  114: 58/92/95/130/159    144: 123/167/211/305/397
 // (Passes of 32 rows, queries in shared memory, were no better than two of 16: 69 us to
 // 62 for 32 rows of 16 requests of 4000, head_dim 128.)
 bool many_rows(int batch, int64_t total_q, int group, int head_dim) {
-  return batch > 0 && (total_q + batch - 1) / batch * group > (head_dim == 64 ? 56 : head_dim == 128 ? 48 : 32);
+  return batch > 0 && (total_q + batch - 1) / batch * group > (head_dim == 64 ? 48 : head_dim == 128 ? 32 : 16);
 }
 
 }  // namespace q4

@@ -33,13 +33,20 @@
 // step, beside them) write there too: 296 KB a step, 2300 clocks.  A row's weights take
 // 1000 clocks of that period, under the other tile's products.
 //
+// At head_dim 256 there is one row tile, two buffers of scores instead, and the queries
+// lie in tensor memory.  A step of 64 tokens takes 2200 clocks: the 16 products of the
+// scores are issued over 1000, then those of the values, and the next scores wait 950
+// for these to complete (a third buffer does not fit); the conversions take 1900 beside
+// them.  Before and after its tiles a CTA spends 9 us on the lengths, its queries and its
+// outputs (24 requests of 500 to 12000 tokens, 24 to 40 rows each: 50 us).
+//
 // Few row tiles, or requests much longer than others, would leave SMs idle: then several
 // CTAs share a unit's positions (a pair of row tiles and a kv head), a range each, and a
 // second kernel joins their outputs by row, in the order of the positions.  How many share
 // a unit follows from the lengths, which only the device knows: no range is longer than P
 // tiles, and every CTA finds the same P before it looks up its own range, as the one of
 // some hundred that promises the earliest end.  (24 requests of 500 to 12000 tokens at
-// head_dim 256: the same number of CTAs for every unit 80 us, by length @@ us.)
+// head_dim 256: the same number of CTAs for every unit 80 us, by length 60.)
 //
 // Every wait is bounded (about a second of clock cycles); on expiry
 // LQ_DEV_TIMEOUT is recorded and the CTA winds down.
@@ -63,7 +70,7 @@ struct TileCfg : TileShape<D> {
   static constexpr int kParamBytes = BN * (D / 32) * 4;     // and its scales and bases, at most
   // Half tiles as fetched, K and V in turn: from a slot's last read to the next data in it
   // 2200 clocks pass, which with one slot each for K and V the conversions waited for
-  // (drafts at head_dim 256: 86 to 84 us with three).
+  // (head_dim 256: 86 to 84 us with three; nine are no faster).
   static constexpr int kRaw = 3;
   static constexpr int kSmem = T * kQBytes + 4 * kValueBytes + kRaw * (kRawBytes + kParamBytes) + 1024;
   static constexpr uint32_t kCols = 512;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         for (int i = lane; i < total; i += 32) count += max(1, (item_tiles[i] + P - 1) / P);
         count = __reduce_add_sync(0xffffffffu, count) * a.kv_heads;
         if (count > (int)gridDim.x) continue;
-        const unsigned long long cost = (unsigned long long)((count + ta.sms - 1) / ta.sms) * (kFixedTiles + P) * 8 + j;
+        const unsigned long long waves = (count + ta.sms - 1) / ta.sms, cost = waves * (kFixedTiles + P) * 8 + j;
         least = min(least, cost << 32 | (unsigned)P);
       }
       if (lane == 0) best[warp] = least;

@@ -323,3 +323,54 @@ def test_replayed_graphs(dtype, q_len):
         torch.cuda.synchronize()
         for s, _, out in cases:
             check(out, reference(s), dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hk", [(8, 2), (4, 4)])
+def test_requests_of_very_different_lengths(d, hq, hk):
+    """Long requests beside short and empty ones, enough query rows for the tensor-core kernel: how many CTAs share a
+    request follows from the lengths, which change under a captured graph.  Bytes around the workspace stay."""
+    torch, L = cuda()
+    reqs = [(9000, 37), (0, 3), (1, 150), (64, 17), (0, 0), (700, 300), (129, 1), (2500, 90), (65, 65)]
+    s = build(torch, np.random.default_rng(d + hq), reqs, hq, hk, 16, d, 32, "bf16")
+    dev = {n: to_dev(torch, s[n]) for n in ("cu", "lens", "table", *CACHE)}
+    out = torch.full(tuple(s["q"].shape), float("nan"), dtype=s["q"].dtype, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    size = L.lq_attention_paged_q4_workspace_size(len(reqs), s["q"].shape[0], hq, hk, d)
+    guarded = torch.full((size + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    work = guarded[4096:4096 + size]
+    work.fill_(0xFF)
+
+    def call():
+        L.lq_attention_paged_q4(s["q"], dev["cu"], dev["lens"], dev["table"], *(dev[n] for n in CACHE), out, work,
+                                dev_status=st)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens in ([n for n, _ in reqs], [40, 0, 1, 30, 0, 333, 129, 2400, 64], [8, 0, 1, 0, 0, 7, 2, 5, 1]):
+        s["lens"] = np.array(lens, np.int32)
+        dev["lens"].copy_(to_dev(torch, s["lens"]))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, reference(s), "bf16")
+    assert int(st) == 0
+    assert bool((guarded[:4096] == 0xA5).all()) and bool((guarded[4096 + size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [2, 70])
+def test_maxima_that_rise(dtype, d, q_len):
+    """Keys that grow with their position: the running maximum moves again and again."""
+    torch, L = cuda()
+    reqs = [(3001, q_len), (700, q_len)]
+    s = build(torch, np.random.default_rng(31), reqs, 4, 2, 16, d, 64, dtype, q_size=8.0)
+    for i, (n, _) in enumerate(reqs):
+        size = np.linspace(0.02, 1.0, n) ** 2
+        for p in range(n):
+            s["ks"][s["table"][i, p // 16], :, p % 16] = (s["ks"][s["table"][i, p // 16], :, p % 16].astype(np.float64)
+                                                           * size[p]).astype(np.float16)
+    check(run(torch, L, s), reference(s), dtype)

@@ -36,6 +36,7 @@
 #include "lq_serve.cuh"
 #include "lq_tma.cuh"
 
+#include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -44,10 +45,12 @@ namespace score {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;               // and a warp that copies and finishes rows
 constexpr int kMaxTop = LQ_MAX_ALTERNATIVES, kMaxCluster = 8;
-constexpr int kPieces = 4;                   // of a share
+constexpr int kPieces = 4;                     // of a share
 constexpr int kRoom = 512;                     // candidates that are listed
 constexpr int kByRank = 256;                   // and ordered by counting
 constexpr int kMostBytes = 208 * 1024;         // of a share in shared memory at once
+// What a row costs beside its elements, in elements of a CTA's: 6 us, at 29 elements a ns.
+constexpr int kFixed = 176 * 1024;
 constexpr long long kWaitCycles = 2000000000ll;
 constexpr float kHuge = 3.40282347e38f;        // the largest number
 typedef unsigned long long u64;
@@ -479,7 +482,8 @@ __global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_co
         }
         continue;
       }
-      const float2 shift = make_float2(-zero, -zero), token_at = make_float2(-dt, -dt), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
+      const float2 shift = make_float2(-zero, -zero), token_at = make_float2(-dt, -dt);
+      const float2 log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
 #pragma unroll 1
       for (int p = 0; p < kPieces; ++p) {
         const int c1 = min(w.chunks - 1, (p + 1) * a.per_piece);
@@ -624,6 +628,41 @@ __global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_co
   if (tid == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 
+// The kernels may use all of the shared memory that a share can take.
+bool prepare() {
+  for (auto kernel : {score_kernel<true>, score_kernel<false>})
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+  return true;
+}
+
+// Clusters of so many CTAs that the current device holds at once, one CTA per SM (fewer
+// than the SMs allow: a cluster lies within one of their groups); 0 on an error.
+int most_clusters(int ctas) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];
+  int device = 0, n = 0;
+  if (cudaGetDevice(&device) == cudaSuccess && device < kDevices && (n = known[device][ctas].load()) > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads + 32);
+  cfg.dynamicSmemBytes = kMostBytes;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, score_kernel<true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (device < kDevices) known[device][ctas].store(n);
+  return n;
+}
+
 }  // namespace score
 }  // namespace lq
 
@@ -646,19 +685,31 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   if (top > 0 && (top_tokens_dev == nullptr || top_logprobs_dev == nullptr || !aligned4(top_tokens_dev) ||
                   !aligned4(top_logprobs_dev)))
     return LQ_ERR_ARG;
+  if (!score::prepare()) return LQ_ERR_CUDA;
   score::Args a;
   a.x = logits_dev; a.ld = ld; a.rows = rows; a.vocab = vocab; a.tokens = tokens_dev; a.logprobs = logprobs_dev;
   a.entropy = entropy_dev; a.ranks = ranks_dev; a.top = top; a.top_tokens = top_tokens_dev;
   a.top_logprobs = top_logprobs_dev; a.status = dev_status_dev;
   const int sms = device_sm_count();
   if (sms <= 0) return LQ_ERR_CUDA;
-  // As few CTAs per row as hold it in shared memory, more where the rows alone would
-  // leave SMs idle.
+  // CTAs per row: enough to hold it in shared memory, and of those the number that ends
+  // first, by the rows that a cluster takes one after the other.  (96 rows of 32000: one
+  // CTA each 8.9 us, two 16.6; 33 of 50001: four each 8.7, eight 23.)
   const int64_t esize = dtype == LQ_BF16 ? 2 : 4, bytes = vocab * esize;
-  int ctas = 1;
-  while (ctas < score::kMaxCluster &&
-         (bytes / ctas > score::kMostBytes - 16 || (rows * ctas < sms && bytes / ctas > 8 * 1024)))
-    ctas *= 2;
+  int ctas = 0, at_once = 0;
+  int64_t least = INT64_MAX;
+  for (int c = 1; c <= score::kMaxCluster && (c == 1 || bytes / c >= 4096); ++c) {
+    if (c < score::kMaxCluster && bytes / c > score::kMostBytes - 16) continue;
+    const int clusters = c == 1 ? sms : score::most_clusters(c);
+    if (clusters <= 0) continue;
+    const int64_t cost = (rows + clusters - 1) / clusters * (vocab / c + score::kFixed);
+    if (cost < least) {
+      least = cost;
+      ctas = c;
+      at_once = clusters;
+    }
+  }
+  if (ctas == 0) return LQ_ERR_CUDA;
   a.cluster = ctas;
   a.share = (vocab + ctas - 1) / ctas;
   const int64_t most = (score::kMostBytes - 32) / esize;
@@ -670,13 +721,9 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   if (a.per_piece > unit / 2) a.per_piece = (a.per_piece + unit - 1) / unit * unit;
   const int smem = chunks * 16;
   const auto kernel = dtype == LQ_BF16 ? score::score_kernel<true> : score::score_kernel<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kMostBytes) != cudaSuccess) {
-    cudaGetLastError();
-    return LQ_ERR_CUDA;
-  }
   // a cluster stays for row after row once there are more rows than fit
   int per_sm = (228 * 1024) / (smem + 16 * 1024);
   per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
-  const int64_t resident = (int64_t)sms * per_sm / ctas, clusters = rows < resident ? rows : resident;
+  const int64_t resident = (int64_t)at_once * per_sm, clusters = rows < resident ? rows : resident;
   return serve::launch(kernel, (unsigned)(clusters * ctas), score::kThreads + 32, smem, stream, a, (unsigned)ctas);
 }

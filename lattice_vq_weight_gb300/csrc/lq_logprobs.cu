@@ -49,8 +49,7 @@ constexpr int kPieces = 4;                     // of a share
 constexpr int kRoom = 512;                     // candidates that are listed
 constexpr int kByRank = 256;                   // and ordered by counting
 constexpr int kMostBytes = 208 * 1024;         // of a share in shared memory at once
-// What a row costs beside its elements, in elements of a CTA's: 6 us, at 29 elements a ns.
-constexpr int kFixed = 176 * 1024;
+constexpr int kFixed = 64 * 1024;              // what a row costs beside its elements, in elements of a CTA's
 constexpr long long kWaitCycles = 2000000000ll;
 constexpr float kHuge = 3.40282347e38f;        // the largest number
 typedef unsigned long long u64;
@@ -694,15 +693,28 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   if (sms <= 0) return LQ_ERR_CUDA;
   // CTAs per row: enough to hold it in shared memory, and of those the number that ends
   // first, by the rows that a cluster takes one after the other.  (96 rows of 32000: one
-  // CTA each 8.9 us, two 16.6; 33 of 50001: four each 8.7, eight 23.)
-  const int64_t esize = dtype == LQ_BF16 ? 2 : 4, bytes = vocab * esize;
+  // CTA each 8.9 us, two 16.6; 33 of 50001: four each 8.7, eight 23.  Three, 400 rows of
+  // 128256 in fp32: 100 us against four's 68.)
+  const int64_t esize = dtype == LQ_BF16 ? 2 : 4, bytes = vocab * esize, most = (score::kMostBytes - 32) / esize;
+  auto divide = [&](int c) {                   // among c CTAs; pieces of whole batches: chunks one at a time take
+    a.cluster = c;                             // twice as long
+    a.share = (vocab + c - 1) / c;
+    a.segment = (int)(a.share < most ? a.share : most);
+    const int chunks = ((int)(a.segment * esize) + 15) / 16 + 1;     // those at both ends may be partial
+    const int unit = score::kThreads * (dtype == LQ_BF16 ? 2 : 4);
+    a.per_piece = (chunks + score::kPieces - 1) / score::kPieces;
+    if (a.per_piece > unit / 2) a.per_piece = (a.per_piece + unit - 1) / unit * unit;
+    return chunks;
+  };
   int ctas = 0, at_once = 0;
   int64_t least = INT64_MAX;
-  for (int c = 1; c <= score::kMaxCluster && (c == 1 || bytes / c >= 4096); ++c) {
+  for (int c = 1; c <= score::kMaxCluster && (c == 1 || bytes / c >= 4096); c *= 2) {
     if (c < score::kMaxCluster && bytes / c > score::kMostBytes - 16) continue;
     const int clusters = c == 1 ? sms : score::most_clusters(c);
     if (clusters <= 0) continue;
-    const int64_t cost = (rows + clusters - 1) / clusters * (vocab / c + score::kFixed);
+    divide(c);
+    const int64_t elements = (int64_t)a.per_piece * score::kPieces * (16 / esize);
+    const int64_t cost = (rows + clusters - 1) / clusters * (elements + score::kFixed);
     if (cost < least) {
       least = cost;
       ctas = c;
@@ -710,15 +722,7 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
     }
   }
   if (ctas == 0) return LQ_ERR_CUDA;
-  a.cluster = ctas;
-  a.share = (vocab + ctas - 1) / ctas;
-  const int64_t most = (score::kMostBytes - 32) / esize;
-  a.segment = (int)(a.share < most ? a.share : most);
-  const int chunks = ((int)(a.segment * esize) + 15) / 16 + 1;       // those at both ends may be partial
-  // pieces of whole batches: chunks one at a time take twice as long
-  const int unit = score::kThreads * (dtype == LQ_BF16 ? 2 : 4);
-  a.per_piece = (chunks + score::kPieces - 1) / score::kPieces;
-  if (a.per_piece > unit / 2) a.per_piece = (a.per_piece + unit - 1) / unit * unit;
+  const int chunks = divide(ctas);
   const int smem = chunks * 16;
   const auto kernel = dtype == LQ_BF16 ? score::score_kernel<true> : score::score_kernel<false>;
   // a cluster stays for row after row once there are more rows than fit

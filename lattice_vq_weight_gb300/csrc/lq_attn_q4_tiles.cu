@@ -38,7 +38,7 @@
 // scores are issued over 1000, then those of the values, and the next scores wait 950
 // for these to complete (a third buffer does not fit); the conversions take 1900 beside
 // them.  Before and after its tiles a CTA spends 9 us on the lengths, its queries and its
-// outputs (24 requests of 500 to 12000 tokens, 24 to 40 rows each: 50 us).
+// outputs (24 requests of 500 to 12000 tokens, 24 to 40 rows each: 48 us).
 //
 // Few row tiles, or requests much longer than others, would leave SMs idle: then several
 // CTAs share a unit's positions (a pair of row tiles and a kv head), a range each, and a
@@ -301,27 +301,33 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       int longest = 0;
       for (int i = lane; i < total; i += 32) longest = max(longest, item_tiles[i]);
       longest = __reduce_max_sync(0xffffffffu, longest);
-      // P such that the longest item makes j ranges: the end is that of the last wave of
-      // CTAs, each as long as its longest, and of the rows' joining
+      // Ranges per tile, 1 / P, such that the longest item makes j ranges, each of four tiles or
+      // more; and an item's ranges.  (Every CTA has the same numbers: their last place may be
+      // off.  With divisions of whole numbers this took 4200 clocks, so 2900.)
+      auto ranges_of = [](int tiles, float density) { return max(1, (int)ceilf(fmaf((float)tiles, density, -1e-3f))); };
+      // the end is that of the last wave of CTAs, each as long as its longest, and of the
+      // rows' joining
       unsigned long long least = ~0ull;
+      const float per_sm = 1.f / (float)ta.sms;
       for (int j = 1 + warp; j <= kMostShares && (j == 1 || j * a.kv_heads <= (int)gridDim.x); j += C::kThreads / 32) {
-        const int P = max(4, (longest + j - 1) / j);
+        const float density = fminf(0.25f, __fdividef((float)j, (float)max(1, longest)));
         int count = 0;
-        for (int i = lane; i < total; i += 32) count += max(1, (item_tiles[i] + P - 1) / P);
+        for (int i = lane; i < total; i += 32) count += ranges_of(item_tiles[i], density);
         count = __reduce_add_sync(0xffffffffu, count) * a.kv_heads;
-        if (count > (int)gridDim.x) continue;
-        const unsigned long long waves = (count + ta.sms - 1) / ta.sms, cost = waves * (kFixedTiles + P) * 8 + j;
-        least = min(least, cost << 32 | (unsigned)P);
+        if (j > 1 && count > (int)gridDim.x) continue;
+        const float waves = ceilf((float)count * per_sm - 1e-3f);
+        const float cost = waves * ((float)kFixedTiles + __fdividef(1.f, density)) + 0.125f * (float)j;
+        least = min(least, (unsigned long long)__float_as_uint(cost) << 32 | __float_as_uint(density));
       }
       if (lane == 0) best[warp] = least;
       __syncthreads();
       if (warp == 0) {
         least = lane < C::kThreads / 32 ? best[lane] : ~0ull;
         for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        const int P = (int)(least & 0x7FFFFFFFu);
+        const float density = __uint_as_float((uint32_t)least);
         int before = 0;
         for (int at32 = 0; at32 < total && before <= (int)blockIdx.x; at32 += 32) {
-          const int i = at32 + lane, shares = i < total ? max(1, (item_tiles[i] + P - 1) / P) : 0;
+          const int i = at32 + lane, shares = i < total ? ranges_of(item_tiles[i], density) : 0;
           int end = shares * a.kv_heads;
           for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, end, o);

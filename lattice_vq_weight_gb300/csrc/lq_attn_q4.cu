@@ -626,10 +626,18 @@ lq_status launch_split(const CacheArgs& ca, const CUtensorMap& mk, const CUtenso
 //   one of 32000 tokens  41: 21/27/27/34/41    44: 29/38/38/48/59       59: 50/63/80/108/139
 //   one of 4000 tokens   21: 13/13/13/14/17    23: 16/17/17/21/21       31: 19/26/26/30/35
 //   24 of 500 to 12000   96: 36/59/60/81/101  114: 58/92/95/130/159    144: 123/167/211/305/397
+// With more units than CTAs can share, its 9 us beside a unit's tiles show where contexts
+// are short, of which the host knows a bound:
+//   256 requests of 300  149: 39/60/61/81/103 180: 66/97/97/139/171    190: 140/188/240/337/422
+//   256 of 1000          248: 82/144/148/204/272  291: 128/223/224/318/422  360: 326/470/617/861/1157
 // (Passes of 32 rows, queries in shared memory, were no better than two of 16: 69 us to
 // 62 for 32 rows of 16 requests of 4000, head_dim 128.)
-bool many_rows(int batch, int64_t total_q, int group, int head_dim) {
-  return batch > 0 && (total_q + batch - 1) / batch * group > (head_dim == 64 ? 48 : head_dim == 128 ? 32 : 16);
+bool many_rows(int batch, int64_t total_q, int group, int kv_heads, int head_dim, int64_t most_tokens, int sms) {
+  if (batch <= 0) return false;
+  const int64_t rows = (total_q + batch - 1) / batch * group;
+  if (rows <= (head_dim == 64 ? 48 : head_dim == 128 ? 32 : 16)) return false;
+  if (rows > (head_dim == 64 ? 64 : head_dim == 128 ? 48 : 24)) return true;
+  return (int64_t)batch * kv_heads <= 4 * sms || most_tokens >= (head_dim == 256 ? 320 : 704);
 }
 
 }  // namespace q4
@@ -644,7 +652,7 @@ extern "C" size_t lq_attention_paged_q4_workspace_size(int batch, int64_t total_
     return 0;
   const int ctas = attn::cta_count();
   const size_t split = attn::meta_bytes(ctas) + (size_t)ctas * attn::work_floats(head_dim) * sizeof(float);
-  if (!q4::many_rows(batch, total_q, q_heads / kv_heads, head_dim)) return split;
+  if (!q4::many_rows(batch, total_q, q_heads / kv_heads, kv_heads, head_dim, INT64_MAX, ctas)) return split;
   const size_t tiles = q4::tiles_workspace(batch, total_q, q_heads, kv_heads, head_dim, ctas);
   return split > tiles ? split : tiles;
 }
@@ -700,8 +708,9 @@ extern "C" lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int d
   ca.ks = reinterpret_cast<const uint32_t*>(k_scales_dev); ca.vs = reinterpret_cast<const uint32_t*>(v_scales_dev);
   ca.log2_group = serve::log2_of(group_size);
   ca.kc = k_cache_dev; ca.vc = v_cache_dev;
-  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, head_dim))
-    return q4::launch_tiles(ca, head_dim, (int64_t)table_width * block_size, ctas, workspace_dev, stream);
+  const int64_t most_tokens = (int64_t)table_width * block_size;
+  if (dtype == LQ_BF16 && q4::many_rows(batch, total_q, a.group, kv_heads, head_dim, most_tokens, ctas))
+    return q4::launch_tiles(ca, head_dim, most_tokens, ctas, workspace_dev, stream);
   // a pool without blocks: no copy is issued, any valid map will do
   const void* kc = num_blocks > 0 ? (const void*)k_cache_dev : workspace_dev;
   const void* vc = num_blocks > 0 ? (const void*)v_cache_dev : workspace_dev;

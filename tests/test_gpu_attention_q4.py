@@ -374,3 +374,18 @@ def test_maxima_that_rise(dtype, d, q_len):
             s["ks"][s["table"][i, p // 16], :, p % 16] = (s["ks"][s["table"][i, p // 16], :, p % 16].astype(np.float64)
                                                            * size[p]).astype(np.float16)
     check(run(torch, L, s), reference(s), dtype)
+
+
+@pytest.mark.parametrize("d,q_len", [(64, 14), (128, 10), (256, 5)])
+@pytest.mark.parametrize("length", [40, 750])
+def test_many_requests_with_some_rows(d, q_len, length):
+    """More requests than CTAs can share, rows between the two kernels' ranges, short contexts and longer ones."""
+    torch, L = cuda()
+    rng = np.random.default_rng(d + length)
+    reqs = [(int(n), q_len) for n in rng.integers(1, length, 170)]
+    s = build(torch, rng, reqs, 16, 4, 16, d, 64, "bf16")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(torch, L, s, st)
+    assert int(st) == 0
+    seen = [i for i in range(0, len(reqs) * q_len, 37)]
+    check(got, reference(s), "bf16", seen)

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per stage
   __shared__ uint64_t raw_full[C::kRaw], raw_free[C::kRaw];
   constexpr int B = C::kBufs;
-  __shared__ uint64_t s_full[T][B], p_full[T][B], o_done[T], q_full[T], turn[T][2], drain;
+  __shared__ uint64_t s_full[T][B], p_full[T][B], o_done[T][B], q_full[T], turn[T][2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int timeout_flag, found[5];                    // request, row tile, kv head; share, shares
   __shared__ int wsum[C::kThreads / 32];
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       for (int b = 0; b < B; ++b) {
         mbar_init1(&s_full[t][b], 1);                       // scores computed
         mbar_init1(&p_full[t][b], 4);                       // one arrival per softmax warp
+        mbar_init1(&o_done[t][b], 1);                       // values added: O readable, the weights read
       }
-      mbar_init1(&o_done[t], 1);                            // values added: O readable, the weights read
       mbar_init1(&q_full[t], 4);
       mbar_init1(&turn[t][0], 1);                           // scores issued
       mbar_init1(&turn[t][1], 1);
@@ -387,7 +387,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
   tc_after();
   // columns: the row tiles' scores, then their outputs, then query rows
   const uint32_t tmem_s = tmem_base, tmem_o = tmem_base + T * B * BN, tmem_q = tmem_o + T * D;
-  // tile j's buffer for scores, and the parity of the buffer's barriers
+  // Tile j's buffer for scores, and the parity of the buffer's barriers.  A parity tells a
+  // phase from the next only, so a wait for a phase comes neither when the phase after it may
+  // have completed too nor while the one before it may be missing.  Each buffer has its own
+  // o_done for that: after tile j's phase comes that of tile j + B, whose weights are announced
+  // only after the last wait for tile j; and tile j - B's had completed when the scores of
+  // tile j were issued, which whoever waits for tile j's values has issued or waited for.
   auto buf_of = [](int j) { return B == 2 ? j & 1 : 0; };
   auto parity_of = [](int j) { return (uint32_t)(B == 2 ? j >> 1 : j) & 1; };
 
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         if (j < n) {
           if (j == 0) ok = ok && wait_on(&q_full[t], 0, timeout);
           // they overwrite the weights of the buffer's last tile
-          else if (j >= B) ok = ok && wait_on(&o_done[t], (uint32_t)(j - B) & 1, timeout);
+          else if (j >= B) ok = ok && wait_on(&o_done[t][buf_of(j - B)], parity_of(j - B), timeout);
         }
         if (!all(ok)) return false;
         tc_after();
@@ -559,7 +564,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
               mma_ts(my_o, my_s + buf_of(j) * BN + k * 8, vd + (k * 2048 >> 4), Idesc<D, false, true>::v, j > 0 || k > 0);
-            mma_commit(&o_done[t]);
+            mma_commit(&o_done[t][buf_of(j)]);
             mma_commit(&v_free[st]);
           } else {
             arrive(&v_free[st]);
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
         mx = to;
         if (j > 0 && __any_sync(0xffffffffu, moves)) {
           if (B == 2) {                                     // (one buffer: these scores came after the last values)
-            ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(j - 1) & 1, timeout));
+            ok = __all_sync(0xffffffffu, wait_on(&o_done[t][buf_of(j - 1)], parity_of(j - 1), timeout));
             if (!ok) break;
             tc_after();
             __syncwarp();
@@ -722,10 +727,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
 
     // Outputs, by way of the rows of shared memory where the queries were (the
     // products with them are done): a warp's stores then cover whole lines.
-    // (With two buffers the values of the tile before may be under way too: a parity
-    // tells one phase from the next only.)
-    if (B == 2 && ok && n > 1) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)n & 1, timeout));
-    if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done[t], (uint32_t)(n - 1) & 1, timeout));
+    // (Products complete in their order: the last tile's values are there, so all are.)
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_on(&o_done[t][buf_of(n - 1)], parity_of(n - 1), timeout));
     tc_after();
     __syncwarp();
     const uint32_t rows_out = __ballot_sync(0xffffffffu, mine);

@@ -226,6 +226,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ 
           // tid * D/4 ...; a power of two per row brings them into fp16's range
           const Request r = load_request(a, info.x);
           len = r.len;
+          __syncwarp();                        // every lane has read the segment before's
           if (lane == 0) asked[warp] = make_int2(r.q0, r.q_len);
           lim_min = INT_MAX;
 #pragma unroll

@@ -33,6 +33,7 @@
 // inside the matrix, and slots that are not the row's count as -inf.
 #include "lq_device.cuh"
 #include "lq_host.h"
+#include "lq_logprobs_plan.h"
 #include "lq_serve.cuh"
 #include "lq_tma.cuh"
 
@@ -43,18 +44,15 @@
 namespace lq {
 namespace score {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;               // and a warp that copies and finishes rows
-constexpr int kMaxTop = LQ_MAX_ALTERNATIVES, kMaxCluster = 8;
-constexpr int kPieces = 4;                     // of a share
+constexpr int kWarps = kThreads / 32;          // and a warp that copies and finishes rows
+constexpr int kMaxTop = LQ_MAX_ALTERNATIVES;
 constexpr int kRoom = 512;                     // candidates that are listed
 constexpr int kByRank = 256;                   // and ordered by counting
-constexpr int kMostBytes = 208 * 1024;         // of a share in shared memory at once
-constexpr int kFixed = 64 * 1024;              // what a row costs beside its elements, in elements of a CTA's
 constexpr long long kWaitCycles = 2000000000ll;
 constexpr float kHuge = 3.40282347e38f;        // the largest number
 typedef unsigned long long u64;
 
-struct Args {
+struct Args : Division {
   const void* x;
   int64_t ld, rows, vocab;
   const int32_t* tokens;
@@ -65,10 +63,6 @@ struct Args {
   int32_t* top_tokens;
   float* top_logprobs;
   int32_t* status;
-  int cluster;
-  int64_t share;             // elements of a row per CTA
-  int segment;               // of those in shared memory at once
-  int per_piece;             // chunks
 };
 
 // A value and its token as one number, larger for the ones that come first.
@@ -691,43 +685,12 @@ extern "C" lq_status lq_token_logprobs(const void* logits_dev, int64_t ld, int d
   a.top_logprobs = top_logprobs_dev; a.status = dev_status_dev;
   const int sms = device_sm_count();
   if (sms <= 0) return LQ_ERR_CUDA;
-  // CTAs per row: enough to hold it in shared memory, and of those the number that ends
-  // first, by the rows that a cluster takes one after the other.  (96 rows of 32000: one
-  // CTA each 8.9 us, two 16.6; 33 of 50001: four each 8.7, eight 23.  Three, 400 rows of
-  // 128256 in fp32: 100 us against four's 68.)
-  const int64_t esize = dtype == LQ_BF16 ? 2 : 4, bytes = vocab * esize, most = (score::kMostBytes - 32) / esize;
-  auto divide = [&](int c) {                   // among c CTAs; pieces of whole batches: chunks one at a time take
-    a.cluster = c;                             // twice as long
-    a.share = (vocab + c - 1) / c;
-    a.segment = (int)(a.share < most ? a.share : most);
-    const int chunks = ((int)(a.segment * esize) + 15) / 16 + 1;     // those at both ends may be partial
-    const int unit = score::kThreads * (dtype == LQ_BF16 ? 2 : 4);
-    a.per_piece = (chunks + score::kPieces - 1) / score::kPieces;
-    if (a.per_piece > unit / 2) a.per_piece = (a.per_piece + unit - 1) / unit * unit;
-    return chunks;
-  };
-  int ctas = 0, at_once = 0;
-  int64_t least = INT64_MAX;
-  for (int c = 1; c <= score::kMaxCluster && (c == 1 || bytes / c >= 4096); c *= 2) {
-    if (c < score::kMaxCluster && bytes / c > score::kMostBytes - 16) continue;
-    const int clusters = c == 1 ? sms : score::most_clusters(c);
-    if (clusters <= 0) continue;
-    divide(c);
-    const int64_t elements = (int64_t)a.per_piece * score::kPieces * (16 / esize);
-    const int64_t cost = (rows + clusters - 1) / clusters * (elements + score::kFixed);
-    if (cost < least) {
-      least = cost;
-      ctas = c;
-      at_once = clusters;
-    }
-  }
-  if (ctas == 0) return LQ_ERR_CUDA;
-  const int chunks = divide(ctas);
-  const int smem = chunks * 16;
+  score::Plan plan;
+  if (!score::make_plan(rows, vocab, dtype == LQ_BF16 ? 2 : 4,
+                        [&](int c) { return c == 1 ? sms : score::most_clusters(c); }, &plan))
+    return LQ_ERR_CUDA;
+  static_cast<score::Division&>(a) = plan.d;
   const auto kernel = dtype == LQ_BF16 ? score::score_kernel<true> : score::score_kernel<false>;
-  // a cluster stays for row after row once there are more rows than fit
-  int per_sm = (228 * 1024) / (smem + 16 * 1024);
-  per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
-  const int64_t resident = (int64_t)at_once * per_sm, clusters = rows < resident ? rows : resident;
-  return serve::launch(kernel, (unsigned)(clusters * ctas), score::kThreads + 32, smem, stream, a, (unsigned)ctas);
+  return serve::launch(kernel, (unsigned)(plan.clusters * plan.d.cluster), score::kThreads + 32, plan.d.chunks * 16, stream,
+                       a, (unsigned)plan.d.cluster);
 }

@@ -46,7 +46,8 @@ inline Division divide(int64_t vocab, int esize, int cluster) {
 // those the number that ends first, by the rows that a cluster takes one after the other.
 // (96 rows of 32000: one CTA each 8.9 us, two 16.6; 33 of 50001: four each 8.7, eight 23.
 // Three, 400 rows of 128256 in fp32: 100 us against four's 68.)  at_once(c): clusters of c
-// CTAs that the device holds, 0 if none; false if there is no such c.
+// CTAs that the device holds, one CTA per SM (two need more registers than there are), 0 if
+// none; false if there is no such c.
 template <typename AtOnce>
 bool make_plan(int64_t rows, int64_t vocab, int esize, AtOnce at_once, Plan* plan) {
   int64_t least = INT64_MAX;
@@ -60,10 +61,7 @@ bool make_plan(int64_t rows, int64_t vocab, int esize, AtOnce at_once, Plan* pla
     if (cost < least) {
       least = cost;
       plan->d = d;
-      // a cluster stays for row after row once there are more rows than fit
-      int per_sm = (228 * 1024) / (d.chunks * 16 + 16 * 1024);
-      per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
-      plan->clusters = rows < clusters * per_sm ? rows : clusters * per_sm;
+      plan->clusters = rows < clusters ? rows : clusters;   // each stays for row after row
     }
   }
   return least < INT64_MAX;

@@ -65,3 +65,10 @@ def test_a_share_stays_in_shared_memory_where_a_cluster_can_hold_the_row(plans):
     for (rows, vocab, esize), (ctas, share, segment, *_) in plans(list(calls())):
         if segment < share:
             assert ctas == 8 and -(-vocab // 8) * esize > MOST, (rows, vocab, esize)
+
+
+def test_no_more_clusters_than_the_device_holds(plans):
+    """A CTA has 17 warps of 94 registers a thread and more: two do not fit an SM, however small their shares are.
+    Those past the first round would start cold, where a resident one has its next row under way."""
+    for (rows, *_), (ctas, *_, clusters) in plans(list(calls())):
+        assert clusters == min(rows, CLUSTERS[ctas])

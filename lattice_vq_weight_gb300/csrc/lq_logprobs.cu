@@ -208,6 +208,17 @@ __global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_co
     w.chunks = (w.skew + w.n + E - 1) / E;
     return w;
   };
+  // Every wait is bounded (about a second of clock cycles).  A thread whose wait has run out
+  // waits no more, lets no piece go and starts no copy, so that the CTA's rows, garbage now,
+  // soon come to their end and no piece is copied whose last copy is still under way.
+  bool waited = true;                          // until then
+  auto wait_for = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait_bounded(bar, parity, waited ? kWaitCycles : 0)) {
+      timeout = 1;
+      waited = false;
+    }
+  };
+  int started = 0;                             // copies, by the last warp's lane 0: of piece 0, 1, ... in turn
   // The last warp copies piece p; its barrier completes a phase even if there is nothing to
   // copy.  The matrix's own first and last chunk, where not all of it is inside, come by
   // single loads.
@@ -228,13 +239,11 @@ __global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_co
       c0 += single0;
       c1 = max(c0, c1 - (single1 && (c1 > c0)));
     }
-    if (lane == 0) {
+    if (lane == 0 && waited) {
+      ++started;
       mbar_expect_tx(full + p, (c1 - c0) * 16);
       if (c1 > c0) copy_in(image + c0, w.src + (int64_t)c0 * 16, (c1 - c0) * 16, full + p);
     }
-  };
-  auto wait_for = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait_bounded(bar, parity, kWaitCycles)) timeout = 1;
   };
   // Runs f(c, values of chunks c, c + kThreads, ...) over this thread's chunks of piece p,
   // several at a time, whole warps together (chunks past the piece: -inf).  The share's
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_co
           }
         });
         __syncwarp();
-        if (lane == 0) arrive(empty + p);
+        if (lane == 0 && waited) arrive(empty + p);
       }
       if (odd_rank) {
         const uint8_t* src = all + (row * a.ld + w.base) * kSize;
@@ -618,6 +627,13 @@ __global__ void __launch_bounds__(kThreads + 32, 1) score_kernel(const __grid_co
     __syncthreads();
   }
   if (warp == kWarps && it > 0 && (it - 1) % ctas == rank) finish((it - 1) & 1);
+  if (warp == kWarps && lane == 0 && timeout) {
+    // let the last copy of each piece land before the CTA ends
+    for (int p = 0; p < kPieces; ++p) {
+      const int copies = (started + kPieces - 1 - p) / kPieces;
+      if (copies > 0) mbar_wait_bounded(full + p, (uint32_t)(copies - 1) & 1u, kWaitCycles / 8);
+    }
+  }
   if (tid == 0 && timeout) raise_flag(a.status, LQ_DEV_TIMEOUT);
 }
 

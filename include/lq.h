@@ -757,9 +757,11 @@ lq_status lq_verify_draft(const int32_t* draft_tokens_dev, const int32_t* draft_
  * of a vector becomes
  *     s = fp16((max x - min x) / 15),  b = fp16(min x - 16 s),
  *     code = rint((x - b) (1 / s)) - 16, cut to 0 .. 15;  0 where s is 0,
- * so codes and scales depend on the group alone.  A value is off by at most half a
- * step s / 2, a little more where fp16 rounds s, b or the value itself: groups
- * whose values differ by less than 2^-24 become one value.
+ * so codes and scales depend on the group alone.  A value v is off by at most
+ *     max(s / 2, 2^-11 (|min x| + 31 s)) + 2^-11 |v| + 2^-20:
+ * half a step, or where that is more (|min x| of about a thousand s and up) the
+ * rounding of b and s to fp16, and its own.  Groups whose values differ by no more
+ * than 15 2^-25 become one value.
  *   k_dev, v_dev    [tokens x kv_heads x head_dim] of type dtype, token strides ldk,
  *                   ldv (a multiple of 16 bytes)
  *   slots_dev       int64 [tokens]; negative: the token is left out.  No slot

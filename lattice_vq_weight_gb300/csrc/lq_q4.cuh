@@ -8,8 +8,9 @@
 // one logic operation puts two codes into place and one packed fp16 fma makes
 // their values, which are then exact operands of the matrix products.  The price
 // is a base that reaches past the least value by 16 steps: its rounding, up to
-// 2^-12 (|least| + 16 s), shifts the grid by a few thousandths of a step, and
-// codes are chosen on the grid as stored.
+// 2^-11 (|least| + 16 s), shifts the grid.  Near zero that is a hundredth of a step, for
+// |least| of a thousand steps half of one, and beyond that codes are cut at the grid's
+// ends.  Codes are chosen on the grid as stored.
 #pragma once
 
 #include <cstdint>

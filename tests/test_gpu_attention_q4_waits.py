@@ -1,4 +1,5 @@
-"""The 4-bit attention's tensor-core kernel at every small number of tiles: no wait gives up, whoever is first."""
+"""The 4-bit attention's tensor-core kernel at every small number of tiles (no wait gives up, whoever is first) and in a
+batch of many requests."""
 import numpy as np
 import pytest
 
@@ -30,3 +31,19 @@ def test_no_wait_gives_up(d, tiles):
         assert torch.equal(out, first)
     assert int(st) == 0
     check(first, reference(s), "bf16", range(2 * rows))
+
+
+@pytest.mark.parametrize("d,q_len", [(128, 10), (256, 5)])
+def test_every_row_of_many_requests(d, q_len):
+    """More requests than CTAs can share, one of them long: every row of every request."""
+    torch, L = cuda()
+    rng = np.random.default_rng(d)
+    reqs = [(int(n), q_len) for n in rng.integers(1, 400, 90)] + [(6000, q_len)]
+    s = build(torch, rng, reqs, 16, 4, 16, d, 64, "bf16")
+    dev = {n: to_dev(torch, s[n]) for n in ("cu", "lens", "table", *CACHE)}
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(s["q"], float("nan"))
+    L.lq_attention_paged_q4(s["q"], dev["cu"], dev["lens"], dev["table"], *(dev[n] for n in CACHE), out,
+                            workspace(torch, L, s), dev_status=st)
+    assert int(st) == 0
+    check(out, reference(s), "bf16")

@@ -24,3 +24,17 @@ def test_rows_that_just_fill_the_shared_memory(dtype, ctas, more):
     got, st = call(torch, L, x, tokens, 5)
     assert st == 0
     check(got, x.float().cpu().numpy(), tokens, 5)
+
+
+def test_rows_far_into_a_matrix():
+    """Rows whose elements and bytes lie past 2^32, as columns of a wide buffer."""
+    torch, L = cuda()
+    vocab, ld = 5001, (1 << 30) + 3
+    rng = np.random.default_rng(8)
+    buf = torch.empty((4 * ld + vocab,), dtype=torch.bfloat16, device="cuda")      # 8.6 GB
+    x = buf.as_strided((5, vocab), (ld, 1))
+    x.copy_(rows(torch, rng, 5, vocab, "bf16"))
+    tokens = rng.integers(0, vocab, 5)
+    got, st = call(torch, L, x, tokens, 6)
+    assert st == 0
+    check(got, x.float().cpu().numpy(), tokens, 6)

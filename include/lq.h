@@ -788,12 +788,14 @@ size_t lq_attention_paged_q4_workspace_size(int batch, int64_t total_q, int q_he
 /*
  * lq_attention_paged over the 4-bit cache: the same arguments but for the cache and
  * its group_size, the same masks, zeros and status bits.  The values, exact fp16
- * numbers, are the operands of the products; scores and sums are fp32, outputs are
- * rounded once.  The softmax weights of a bf16 call are rounded to fp16 (11 bits,
- * fewer below 2^-22 of the row's largest), its sum of weights uses them unrounded;
- * those of an fp32 call carry 22 bits and are added in fp32.  Equal calls give equal
- * bits.  Slots that hold no token of a request may hold anything; the scales and
- * bases of its tokens are finite (as lq_kv_append_q4 writes them).
+ * numbers, are the operands of the products; scores are fp32, outputs are rounded
+ * once.  The softmax weights of a bf16 call are rounded to fp16: 11 bits, fewer below
+ * 2^-22 of the row's largest; its sum of weights uses them unrounded in fp32, and its
+ * sums of values stay in the matrix unit, whose additions truncate (6e-5 of the output
+ * after 30000 positions).  Queries and weights of an fp32 call carry 22 bits, its sums
+ * are added in fp32.  Equal calls give equal bits.  Slots that hold no token of a
+ * request may hold anything; the scales and bases of its tokens are finite (as
+ * lq_kv_append_q4 writes them).
  */
 lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int dtype, int64_t total_q, const int32_t* cu_q_dev,
                                 const int32_t* kv_lens_dev, int batch, const int32_t* block_table_dev,
@@ -823,7 +825,8 @@ lq_status lq_attention_paged_q4(const void* q_dev, int64_t ldq, int dtype, int64
  *   dev_status_dev  LQ_DEV_NONFINITE: NaN or +inf in a row (its floats NaN, its
  *                   tokens and rank -1); LQ_DEV_RANGE: a token past the vocabulary
  *                   (as if none were given), or a row of -inf alone (logprobs -inf,
- *                   entropy 0)
+ *                   entropy 0); LQ_DEV_TIMEOUT: a bounded wait expired (outputs
+ *                   unspecified)
  * vocab <= 2^24, rows <= 2^24.
  */
 #define LQ_MAX_ALTERNATIVES 32

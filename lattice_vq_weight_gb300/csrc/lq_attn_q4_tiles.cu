@@ -38,7 +38,7 @@
 // scores are issued over 1000, then those of the values, and the next scores wait 950
 // for these to complete (a third buffer does not fit); the conversions take 1900 beside
 // them.  Before and after its tiles a CTA spends 9 us on the lengths, its queries and its
-// outputs (24 requests of 500 to 12000 tokens, 24 to 40 rows each: 48 us).
+// outputs (24 requests of 500 to 12000 tokens, 24 to 40 rows each: 48.5 us of GPU time).
 //
 // Few row tiles, or requests much longer than others, would leave SMs idle: then several
 // CTAs share a unit's positions (a pair of row tiles and a kv head), a range each, and a
@@ -103,7 +103,9 @@ struct TileArgs {
   int items, stride, ctas, sms;
   int2* places;                  // of every query row: its first piece's row, and how many CTAs share it
 };
-// What a CTA costs beside its tiles, in tiles (9 us), and how many shares are tried.
+// What a CTA costs beside its tiles, in tiles, and how many shares are tried.  (Measured at
+// head_dim 256, 9 us in steps of 2200 clocks, and taken for the others too, whose steps of
+// 3350 clocks make it 13 us.)
 constexpr int kFixedTiles = 8, kMostShares = 128;
 
 // A row's weights of one tile from its scores: packed fp16 weights and their sum;
@@ -301,9 +303,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) tiles_kernel(const __
       int longest = 0;
       for (int i = lane; i < total; i += 32) longest = max(longest, item_tiles[i]);
       longest = __reduce_max_sync(0xffffffffu, longest);
-      // Ranges per tile, 1 / P, such that the longest item makes j ranges, each of four tiles or
-      // more; and an item's ranges.  (Every CTA has the same numbers: their last place may be
-      // off.  With divisions of whole numbers this took 4200 clocks, so 2900.)
+      // Ranges per tile, 1 / P, such that the longest item makes j ranges, at most one for every
+      // four tiles; and an item's ranges, rounded up (five tiles: two and three).  (Every CTA
+      // has the same numbers: their last place may be off.  With divisions of whole numbers
+      // this took 4200 clocks, so 2900.)
       auto ranges_of = [](int tiles, float density) { return max(1, (int)ceilf(fmaf((float)tiles, density, -1e-3f))); };
       // the end is that of the last wave of CTAs, each as long as its longest, and of the
       // rows' joining
@@ -881,7 +884,9 @@ static int64_t items_of(int batch, int64_t total_q, int group, int head_dim) {
   return (total_q * group - requests) / rows + requests;
 }
 // CTAs per SM where they may share units: two for each unit, so that a wave is at least
-// two thirds full whatever their number is, and four at most; 0: a unit is one CTA's.
+// two thirds full whatever their number is, and four at most; 0: a unit is one CTA's, and
+// as long as its request is.  (37 requests of 500 tokens and one of 60000, five query tokens
+// each of 8 heads for 8 kv heads of 128: 750 us, all of them the long one's.)
 static int waves_of(int64_t units, int sms) {
   const int64_t n = (2 * units + sms - 1) / sms;
   return n <= 4 ? (int)n : 0;

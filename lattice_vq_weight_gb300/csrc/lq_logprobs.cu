@@ -9,7 +9,9 @@
 // the order of (d descending, token ascending): that of the log probabilities as
 // they are given, in which logits that differ by less than d's last place are equal.
 //
-// Rows are read once.  A CTA, or a cluster of up to eight where a row is longer than
+// A row is read once where a cluster's shared memory holds it (longer ones, in segments,
+// twice; ranks among logits within 2^-70 of 0 or against masked tokens, and an overflowing
+// list of candidates, read the row again).  A CTA, or a cluster of up to eight where a row is longer than
 // one SM's shared memory or there are few rows, copies its share of a row to shared
 // memory in four pieces (untiled bulk copies) and takes maxima as they arrive; the
 // CTAs agree on the row's maximum, and everything else, whose terms hang on it, comes
@@ -26,8 +28,9 @@
 // Alternatives: the k-th largest of 32 maxima, each over every 32nd 16-byte chunk of
 // the share, is a bound that at least k elements reach and few others do; those are
 // listed on the way and ranked by counting.  Where more reach it than there is room
-// for (equal logits, large ones in step with the chunks), the k are taken one after
-// the other instead, from the row itself.
+// for (equal logits, large ones in step with the chunks, rows of which a mask leaves so few
+// that the bound is -inf), the k are taken one after the other instead, from the row itself:
+// 96 rows of 128256 with 20 alternatives take 22 us, with all but 30 tokens masked 450.
 //
 // A row starts at any element: chunks at its ends are copied whole where that stays
 // inside the matrix, and slots that are not the row's count as -inf.
@@ -146,11 +149,6 @@ __device__ __forceinline__ void copy_in(void* dst, const void* src, uint32_t byt
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
-
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
 
 // A segment of a CTA's share of a row: n elements from token `base` on, in `chunks`
 // chunks of 16 bytes whose first `skew` slots and last ones may not be the row's.
